@@ -15,6 +15,7 @@
 
 #include "../../include/zr.h"
 #include "../../include/zr_testing.h"
+#include "zr_checks.h"
 #include "zr_launch.h"
 #include "zr_plan.h"
 
@@ -28,48 +29,6 @@ bool op_ok(int op) { return op >= OP_ADD && op <= OP_DIV; }
 bool needs_a(int op, int which) { return which == 1 && (op == OP_MUL || op == OP_DIV); }
 bool needs_b(int op, int which) {
   return (which == 0 && (op == OP_MUL || op == OP_DIV)) || (which == 1 && op == OP_DIV);
-}
-
-// Byte interval [lo, hi) touched by a tensor (empty when numel == 0).
-struct Span {
-  uintptr_t lo = 0, hi = 0;
-};
-Span span_of(const void* p, int64_t extent, int es = 4) {
-  Span s;
-  if (p && extent > 0) {
-    s.lo = reinterpret_cast<uintptr_t>(p);
-    s.hi = s.lo + uintptr_t(extent) * uintptr_t(es);
-  }
-  return s;
-}
-bool overlaps(const Span& x, const Span& y) {
-  return x.hi > x.lo && y.hi > y.lo && x.lo < y.hi && y.lo < x.hi;
-}
-
-// Sufficient condition for a strided view to address every element once:
-// sorted by stride, each stride exceeds the extent of all smaller dims.
-bool non_overlapping(const TDesc& t) {
-  int idx[kMaxDims];
-  int m = 0;
-  for (int i = 0; i < t.nd; ++i)
-    if (t.size[i] > 1) idx[m++] = i;
-  std::sort(idx, idx + m, [&](int x, int y) { return t.stride[x] < t.stride[y]; });
-  int64_t reach = 0;  // largest offset reachable with the dims seen so far
-  for (int i = 0; i < m; ++i) {
-    const int d = idx[i];
-    if (t.stride[d] <= reach) return false;
-    reach += (t.size[d] - 1) * t.stride[d];
-  }
-  return true;
-}
-
-bool same_layout(const TDesc& x, const TDesc& y) {
-  if (x.ptr != y.ptr || x.nd != y.nd) return false;
-  for (int i = 0; i < x.nd; ++i) {
-    if (x.size[i] != y.size[i]) return false;
-    if (x.size[i] > 1 && x.stride[i] != y.stride[i]) return false;
-  }
-  return true;
 }
 
 bool is_reduced(const TDesc& x, int n, const int64_t* out_size) {
@@ -93,29 +52,6 @@ TDesc dense_desc(const float* p, int nd, const int64_t* size) {
   contiguous_strides(nd, t.size, t.stride);
   t.extent = n;
   return t;
-}
-
-int check_device_ptr(const void* p) {
-  if (p == nullptr) return ZR_ERR_NULL;
-  cudaPointerAttributes at;
-  const cudaError_t e = cudaPointerGetAttributes(&at, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return ZR_ERR_DEVICE;
-  }
-  if (at.type == cudaMemoryTypeUnregistered) return ZR_ERR_DEVICE;
-  // Pinned host memory is used through the same address only (unified
-  // addressing maps it there); a different device alias is refused.
-  if (at.type == cudaMemoryTypeHost && at.devicePointer != p) return ZR_ERR_DEVICE;
-  if (at.type == cudaMemoryTypeDevice) {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-      cudaGetLastError();
-      return ZR_ERR_DEVICE;
-    }
-    if (at.device != dev) return ZR_ERR_DEVICE;
-  }
-  return ZR_OK;
 }
 
 // ------------------------------------------------------------------ forward
@@ -437,8 +373,6 @@ int plan_sum(const zr_tensor& tin, int32_t ndo, const int64_t* so, float* out, S
   return ZR_OK;
 }
 
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? ZR_OK : ZR_ERR_CUDA; }
-
 // Launch (or, with dry, only guard-check) the kernels of a backward plan.
 int launch_bwd_set(const BwdSet& S, int op, void* workspace, cudaStream_t st, bool dry) {
   if (S.direct) return cuda_status(launch_bwd_direct(op, S.want, S.eb, st, dry));
@@ -465,15 +399,6 @@ int launch_sum_set(const SumSet& S, void* workspace, cudaStream_t st, bool dry) 
   rb.comb.partial = rb.plan.partial;
   return cuda_status(launch_reduce(OP_ADD, 2, rb, st, dry));
 }
-
-int copy_json(const std::string& s, char* buf, size_t len) {
-  if (!buf || len == 0) return ZR_ERR_NULL;
-  const size_t m = std::min(len - 1, s.size());
-  std::memcpy(buf, s.data(), m);
-  buf[m] = '\0';
-  return ZR_OK;
-}
-
 
 // Plan descriptions (JSON) shared by the test hooks and the trace.
 std::string fwd_json(const FwdSet& S) {
@@ -511,21 +436,6 @@ std::string sum_json(const SumSet& S) {
   if (S.empty) return "{\"kernel\":\"none\"}";
   if (S.copy) return "{\"plans\":[" + describe_ew(S.eb) + "],\"ws_query\":0}";
   return "{\"plans\":[" + describe_red(S.rb) + "],\"ws_query\":" + std::to_string(S.ws_query) + "}";
-}
-
-// ZR_TRACE set (and not "0"): every forward, backward, sum-to-shape and
-// unary call that is about to launch writes one line "zr_trace <entry> <plan JSON>" to
-// stderr.  Read once per process.
-bool trace_on() {
-  static const bool on = [] {
-    const char* e = std::getenv("ZR_TRACE");
-    return e != nullptr && e[0] != '\0' && !(e[0] == '0' && e[1] == '\0');
-  }();
-  return on;
-}
-
-void trace(const char* entry, const std::string& json) {
-  std::fprintf(stderr, "zr_trace %s %s\n", entry, json.c_str());
 }
 
 }  // namespace
@@ -813,6 +723,7 @@ const char* zr_status_string(int status) {
   switch (status) {
     case ZR_OK: return "ZR_OK";
     case ZR_ERR_DTYPE: return "ZR_ERR_DTYPE: unknown element type";
+    case ZR_ERR_VALUE: return "ZR_ERR_VALUE: a scalar argument is outside its range";
     case ZR_ERR_NULL: return "ZR_ERR_NULL: required pointer is NULL or op code unknown";
     case ZR_ERR_RANK: return "ZR_ERR_RANK: ndim < 0 or ndim > 8";
     case ZR_ERR_SHAPE: return "ZR_ERR_SHAPE: shapes not broadcastable or wrong grad_out shape";

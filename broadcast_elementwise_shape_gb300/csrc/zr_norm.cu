@@ -1,0 +1,320 @@
+// zr_norm.cu — layer norm's C entry points: checks, plan and launches.
+#include "zr_norm.h"
+
+#include "zr_checks.h"
+#include "zr_launch.h"
+
+namespace zr {
+namespace {
+
+struct NormSet {
+  int es = 4, vec = 1;
+  bool empty = false;        // no rows
+  NormPlan p;
+  TDesc in[2], out, gamma, beta;
+  size_t ws = 0;
+};
+
+// gamma or beta: rank 1 of `dim` elements, or absent (no data).
+int read_affine(const zr_tensor& t, int64_t dim, TDesc* d) {
+  if (t.data == nullptr) {
+    *d = TDesc{};
+    return ZR_OK;
+  }
+  const int rc = read_tensor(t, d);
+  if (rc) return rc;
+  return d->nd == 1 && d->size[0] == dim ? ZR_OK : ZR_ERR_SHAPE;
+}
+
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes) == 0; }
+
+template <int VEC, typename F>
+void norm_cases(F f) {
+#define ZR_NORM_CASE(G_, NI_) f(uint32_t(G_), uint32_t(NI_));
+  ZR_NORM_CASES(VEC)
+#undef ZR_NORM_CASE
+}
+
+// Fewest lanes whose registers hold the row: 8 lanes only for rows that a
+// warp's single access would leave half empty.
+void pick_group(NormPlan* p, int vec) {
+  p->group = p->ni = 0;
+  uint64_t best = ~uint64_t(0);
+  auto see = [&](uint32_t g, uint32_t ni) {
+    const uint64_t cols = uint64_t(g) * ni * vec;
+    if (cols < p->dim || (g == 8 && p->dim > 16u * uint32_t(vec > 1 ? vec : 4))) return;
+    const uint64_t cost = uint64_t(g) * 1000 + ni;
+    if (cost < best) { best = cost; p->group = g; p->ni = ni; }
+  };
+  if (vec == 1) norm_cases<1>(see);
+  else if (vec == 4) norm_cases<4>(see);
+  else norm_cases<8>(see);
+}
+
+// Rows and access width over the input slots 0 .. nin-1 and the output.
+int plan_rows(NormSet* S, int nin, const void* out) {
+  NormPlan& p = S->p;
+  const int n = S->in[0].nd;
+  const int64_t dim = S->in[0].size[n - 1];
+  if (dim >= (int64_t(1) << 31)) return ZR_ERR_SIZE;
+  int64_t st[kProbSlots][kMaxDims] = {};
+  for (int d = 0; d < n - 1; ++d) {
+    for (int k = 0; k < nin; ++k) st[k][d] = S->in[k].stride[d];
+    st[kSlotOut][d] = S->out.stride[d];
+  }
+  const uint32_t active = (nin == 2 ? 3u : 1u) | (out ? 1u << kSlotOut : 0u);
+  Prob P;
+  // -1: the row index stays row-major, as mean and rstd are stored.
+  int rc = coalesce(n - 1, S->in[0].size, st, active, -1, &P);
+  if (rc) return rc;
+  uint64_t nrow = 1;
+  p.rows.n = P.n;
+  for (int i = 0; i < P.n; ++i) {
+    const int d = P.n - 1 - i;
+    if (P.size[d] >= (int64_t(1) << 32)) return ZR_ERR_SIZE;
+    p.rows.div[i] = make_fastdiv(uint32_t(P.size[d]));
+    for (int k = 0; k < kMaxOperands; ++k) p.rows.stride[k][i] = P.st[k][d];
+    nrow *= uint64_t(P.size[d]);
+    if (nrow >= (uint64_t(1) << 31)) return ZR_ERR_SIZE;  // grid and row index
+  }
+  p.nrow = uint32_t(nrow);
+  p.dim = uint32_t(dim);
+  p.inv_dim = 1.f / float(dim);
+  const int V = 16 / S->es;
+  bool wide = dim % V == 0;
+  auto look = [&](const TDesc& t, int slot, const void* ptr) {
+    p.inner_stride[slot] = dim == 1 ? 0 : t.stride[n - 1];
+    if (p.inner_stride[slot] != 1 || !aligned(ptr, 16)) wide = false;
+    for (int i = 0; i < P.n; ++i)
+      if (p.rows.stride[slot][i] % V != 0) wide = false;
+  };
+  for (int k = 0; k < nin; ++k) look(S->in[k], k, S->in[k].ptr);
+  if (out) look(S->out, kSlotOut, out);
+  S->vec = wide ? V : 1;
+  p.gamma = S->gamma.ptr;
+  p.beta = S->beta.ptr;
+  p.gamma_stride = S->gamma.nd ? S->gamma.stride[0] : 0;
+  p.beta_stride = S->beta.nd ? S->beta.stride[0] : 0;
+  p.affine_vec = (!p.gamma || (p.gamma_stride == 1 && aligned(p.gamma, 16))) &&
+                 (!p.beta || (p.beta_stride == 1 && aligned(p.beta, 16)));
+  pick_group(&p, S->vec);
+  return ZR_OK;
+}
+
+// Outputs may not meet one another or any input, except that `out` may be an
+// input exactly.
+int check_spans(const NormSet& S, int nin, const void* out, const Span* small, int nsmall) {
+  const Span so = span_of(out, S.out.extent, S.es);
+  for (int k = 0; k < nin; ++k)
+    if (overlaps(so, span_of(S.in[k].ptr, S.in[k].extent, S.es)) && !same_layout(S.in[k], S.out))
+      return ZR_ERR_LAYOUT;
+  const Span ga = span_of(S.gamma.ptr, S.gamma.extent, S.es);
+  const Span be = span_of(S.beta.ptr, S.beta.extent, S.es);
+  if (overlaps(so, ga) || overlaps(so, be)) return ZR_ERR_LAYOUT;
+  for (int i = 0; i < nsmall; ++i) {
+    if (overlaps(small[i], so) || overlaps(small[i], ga) || overlaps(small[i], be))
+      return ZR_ERR_LAYOUT;
+    for (int k = 0; k < nin; ++k)
+      if (overlaps(small[i], span_of(S.in[k].ptr, S.in[k].extent, S.es))) return ZR_ERR_LAYOUT;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(small[i], small[j])) return ZR_ERR_LAYOUT;
+  }
+  return ZR_OK;
+}
+
+std::string norm_json(const NormSet& S, const char* what) {
+  if (S.empty) return "{\"kernel\":\"none\"}";
+  return std::string("{\"kernel\":\"") + what + (S.p.group ? "\"" : "_long\"") +
+         ",\"vec\":" + std::to_string(S.vec) + ",\"rows\":" + std::to_string(S.p.nrow) +
+         ",\"dim\":" + std::to_string(S.p.dim) + ",\"group\":" + std::to_string(S.p.group) +
+         ",\"ni\":" + std::to_string(S.p.ni) + ",\"n_cta\":" + std::to_string(S.p.n_cta) +
+         ",\"ws\":" + std::to_string(S.ws) + "}";
+}
+
+int plan_norm_fwd(zr_dtype dtype, const zr_tensor& x, const zr_tensor& gamma, const zr_tensor& beta,
+                  float eps, void* y, const int64_t* y_strides, float* mean, float* rstd,
+                  NormSet* S) {
+  if (dtype != ZR_F32 && dtype != ZR_BF16) return ZR_ERR_DTYPE;
+  S->es = dtype == ZR_BF16 ? 2 : 4;
+  S->p = NormPlan{};
+  int rc = read_tensor(x, &S->in[0]);
+  if (rc) return rc;
+  const int n = S->in[0].nd;
+  if (n < 1) return ZR_ERR_RANK;
+  const int64_t dim = S->in[0].size[n - 1];
+  if (dim < 1) return ZR_ERR_SHAPE;
+  if (!(eps >= 0.f) || eps > 3.4028234663852886e38f) return ZR_ERR_VALUE;
+  if ((rc = read_affine(gamma, dim, &S->gamma))) return rc;
+  if ((rc = read_affine(beta, dim, &S->beta))) return rc;
+  if ((rc = read_tensor(zr_tensor{y, n, S->in[0].size, y_strides}, &S->out))) return rc;
+  if (S->in[0].numel == 0) {
+    S->empty = true;
+    return ZR_OK;
+  }
+  if (!S->in[0].ptr || !y) return ZR_ERR_NULL;
+  if (!non_overlapping(S->out)) return ZR_ERR_LAYOUT;
+  const int64_t rows = S->in[0].numel / dim;
+  const Span small[2] = {span_of(mean, mean ? rows : 0), span_of(rstd, rstd ? rows : 0)};
+  if ((rc = check_spans(*S, 1, y, small, 2))) return rc;
+  NormPlan& p = S->p;
+  p.in[0] = S->in[0].ptr;
+  p.out = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.eps = eps;
+  if ((rc = plan_rows(S, 1, y))) return rc;
+  const uint32_t rpb = p.group ? kNormThreads / p.group : 1;
+  p.n_cta = (p.nrow + rpb - 1) / rpb;
+  return ZR_OK;
+}
+
+int plan_norm_bwd(zr_dtype dtype, const zr_tensor& g, const zr_tensor& x, const zr_tensor& gamma,
+                  const float* mean, const float* rstd, void* gx, const int64_t* gx_strides,
+                  void* ggamma, void* gbeta, NormSet* S) {
+  if (dtype != ZR_F32 && dtype != ZR_BF16) return ZR_ERR_DTYPE;
+  S->es = dtype == ZR_BF16 ? 2 : 4;
+  S->p = NormPlan{};
+  int rc = read_tensor(g, &S->in[0]);
+  if (rc) return rc;
+  if ((rc = read_tensor(x, &S->in[1]))) return rc;
+  const int n = S->in[0].nd;
+  if (n < 1) return ZR_ERR_RANK;
+  if (S->in[1].nd != n) return ZR_ERR_SHAPE;
+  for (int d = 0; d < n; ++d)
+    if (S->in[1].size[d] != S->in[0].size[d]) return ZR_ERR_SHAPE;
+  const int64_t dim = S->in[0].size[n - 1];
+  if (dim < 1) return ZR_ERR_SHAPE;
+  if ((rc = read_affine(gamma, dim, &S->gamma))) return rc;
+  S->beta = TDesc{};
+  if ((rc = read_tensor(zr_tensor{gx, n, S->in[0].size, gx_strides}, &S->out))) return rc;
+  NormPlan& p = S->p;
+  p.want_gamma = ggamma != nullptr;
+  p.want_beta = gbeta != nullptr;
+  if (S->in[0].numel == 0) {
+    S->empty = true;
+    return ZR_OK;
+  }
+  if (!S->in[0].ptr || !S->in[1].ptr || !mean || !rstd) return ZR_ERR_NULL;
+  if (gx && !non_overlapping(S->out)) return ZR_ERR_LAYOUT;
+  const int64_t rows = S->in[0].numel / dim;
+  const Span small[2] = {span_of(ggamma, ggamma ? dim : 0, S->es), span_of(gbeta, gbeta ? dim : 0, S->es)};
+  if ((rc = check_spans(*S, 2, gx, small, 2))) return rc;
+  for (const float* st : {mean, rstd}) {
+    const Span ss = span_of(st, rows);
+    if (overlaps(ss, span_of(gx, S->out.extent, S->es)) || overlaps(ss, small[0]) ||
+        overlaps(ss, small[1]))
+      return ZR_ERR_LAYOUT;
+  }
+  p.in[0] = S->in[0].ptr;
+  p.in[1] = S->in[1].ptr;
+  p.out = gx;
+  p.mean_in = mean;
+  p.rstd_in = rstd;
+  if ((rc = plan_rows(S, 2, gx))) return rc;
+  const bool sums = p.want_gamma || p.want_beta;
+  if (p.group) {
+    // Persistent over rows: the column sums stay in registers.
+    const uint32_t rpb = p.group > 32 ? 1 : kNormBwdThreads / p.group;
+    const uint32_t need = (p.nrow + rpb - 1) / rpb;
+    const uint32_t cols = p.ni * uint32_t(S->vec);
+    const uint32_t per_sm = p.group > 32 ? (cols > 16 ? 1 : 2) : (cols > 16 ? 3 : 4);
+    p.n_cta = std::min<uint32_t>(need, kSms * per_sm);
+  } else {
+    // k_norm_sums: rows split so that the column blocks fill the GPU, at
+    // least 64 rows to a split.
+    const uint32_t cb = (p.dim + kNormSumCols - 1) / kNormSumCols;
+    const uint32_t want = (kSms * 8 + cb - 1) / cb;
+    p.n_cta = std::max<uint32_t>(1, std::min<uint32_t>(want, p.nrow / 64));
+  }
+  if (sums) S->ws = size_t(p.n_cta) * (p.want_gamma + p.want_beta) * size_t(dim) * sizeof(float);
+  return ZR_OK;
+}
+
+}  // namespace
+}  // namespace zr
+
+using namespace zr;
+
+extern "C" {
+
+int zr_layer_norm_fwd(zr_dtype dtype, zr_tensor x, zr_tensor gamma, zr_tensor beta, float eps,
+                      void* y, const int64_t* y_strides, float* mean, float* rstd,
+                      zr_stream_t stream) {
+  NormSet S;
+  int rc = plan_norm_fwd(dtype, x, gamma, beta, eps, y, y_strides, mean, rstd, &S);
+  if (rc || S.empty) return rc;
+  if (trace_on()) trace("zr_layer_norm_fwd", norm_json(S, "norm_fwd"));
+  const void* need[6] = {S.p.in[0], y, S.p.gamma, S.p.beta, mean, rstd};
+  for (const void* q : need)
+    if (q && (rc = check_device_ptr(q))) return rc;
+  return cuda_status(launch_norm_fwd(S.p, S.es, S.vec, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int zr_layer_norm_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor x, zr_tensor gamma,
+                      const float* mean, const float* rstd, void* grad_x,
+                      const int64_t* grad_x_strides, void* grad_gamma, void* grad_beta,
+                      void* workspace, size_t* workspace_bytes, zr_stream_t stream) {
+  if (!workspace_bytes) return ZR_ERR_NULL;
+  NormSet S;
+  int rc = plan_norm_bwd(dtype, grad_out, x, gamma, mean, rstd, grad_x, grad_x_strides, grad_gamma,
+                         grad_beta, &S);
+  if (rc) return rc;
+  if (!workspace) {
+    *workspace_bytes = S.ws;
+    return ZR_OK;
+  }
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t dim = S.in[0].nd ? size_t(S.in[0].size[S.in[0].nd - 1]) : 0;
+  if (S.empty) {
+    for (void* q : {grad_gamma, grad_beta}) {
+      if (!q) continue;
+      if ((rc = check_device_ptr(q))) return rc;
+      if ((rc = cuda_status(cudaMemsetAsync(q, 0, dim * S.es, st)))) return rc;
+    }
+    return ZR_OK;
+  }
+  if (!grad_x && !grad_gamma && !grad_beta) return ZR_OK;
+  if (*workspace_bytes < S.ws) return ZR_ERR_WORKSPACE;
+  if (S.ws) {
+    if (!aligned(workspace, 16)) return ZR_ERR_WORKSPACE;
+    const Span sw = span_of(workspace, int64_t(S.ws), 1);
+    for (int k = 0; k < 2; ++k)
+      if (overlaps(sw, span_of(S.in[k].ptr, S.in[k].extent, S.es))) return ZR_ERR_LAYOUT;
+    if (overlaps(sw, span_of(grad_x, S.out.extent, S.es))) return ZR_ERR_LAYOUT;
+  }
+  if (trace_on()) trace("zr_layer_norm_bwd", norm_json(S, "norm_bwd"));
+  const void* need[9] = {S.p.in[0], S.p.in[1], S.p.gamma, mean, rstd, grad_x, grad_gamma, grad_beta,
+                         S.ws ? workspace : nullptr};
+  for (const void* q : need)
+    if (q && (rc = check_device_ptr(q))) return rc;
+  NormPlan& p = S.p;
+  p.partial = S.ws ? static_cast<float*>(workspace) : nullptr;
+  if ((rc = cuda_status(launch_norm_bwd(p, S.es, S.vec, st)))) return rc;
+  if (!p.partial) return ZR_OK;
+  CombinePlan c{};
+  c.partial = p.partial;
+  c.nout = uint64_t(p.want_gamma + p.want_beta) * p.dim;
+  c.split = p.want_gamma ? p.dim : c.nout;
+  c.nslots = p.n_cta;
+  c.out = static_cast<float*>(grad_gamma ? grad_gamma : grad_beta);
+  c.out2 = static_cast<float*>(grad_beta);
+  c.scale = 1.f;
+  return cuda_status(S.es == 2 ? launch_combine_bf16(c, st) : launch_combine_f32(c, st));
+}
+
+int zr_test_describe_layer_norm(zr_dtype dtype, zr_tensor grad_out, zr_tensor x, char* buf,
+                                size_t len) {
+  NormSet S;
+  const float* one = reinterpret_cast<const float*>(uintptr_t(16));
+  void* a = reinterpret_cast<void*>(uintptr_t(1) << 60);
+  void* b = reinterpret_cast<void*>((uintptr_t(1) << 60) + (uintptr_t(1) << 50));
+  void* o = reinterpret_cast<void*>(uintptr_t(1) << 61);
+  const zr_tensor none{nullptr, 0, nullptr, nullptr};
+  const int rc = grad_out.data == nullptr
+                     ? plan_norm_fwd(dtype, x, none, none, 0.f, o, nullptr, nullptr, nullptr, &S)
+                     : plan_norm_bwd(dtype, grad_out, x, none, one, one, o, nullptr, a, b, &S);
+  if (rc) return rc;
+  return copy_json(norm_json(S, grad_out.data ? "norm_bwd" : "norm_fwd"), buf, len);
+}
+
+}  // extern "C"

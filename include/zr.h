@@ -83,7 +83,8 @@ typedef enum {
   ZR_ERR_DEVICE = -6,    /* pointer not addressable by the current device      */
   ZR_ERR_WORKSPACE = -7, /* workspace smaller than required                    */
   ZR_ERR_CUDA = -8,      /* a CUDA call or kernel launch failed                */
-  ZR_ERR_DTYPE = -9      /* unknown element type (the _t entry points)         */
+  ZR_ERR_DTYPE = -9,     /* unknown element type (the _t entry points)         */
+  ZR_ERR_VALUE = -10     /* a scalar argument is outside its range             */
 } zr_status;
 
 /*
@@ -379,6 +380,80 @@ int zr_unary_fwd_t(zr_dtype dtype, zr_unary op, float alpha, zr_tensor x, void* 
 /* zr_unary_bwd on `dtype` storage, with the same accuracy as zr_unary_fwd_t. */
 int zr_unary_bwd_t(zr_dtype dtype, zr_unary op, float alpha, zr_tensor grad_out, zr_tensor x,
                    void* grad_x, const int64_t* grad_x_strides, zr_stream_t stream);
+
+/*
+ * Layer norm over the last dim (the book's OpLayerNorm).  Per row of D
+ * elements: mean = sum(x) / D, rstd = 1 / sqrt(sum((x - mean)^2) / D + eps),
+ *   y = (x - mean) * rstd * gamma + beta.
+ * Arithmetic, sums and statistics are binary32 on either storage; y is rounded
+ * once.
+ *
+ * zr_layer_norm_fwd
+ *   x           rank 1 to 8, any strides; D = the last size, >= 1.
+ *   gamma, beta rank 1 of D elements, any stride, x's element type; with
+ *               data == NULL, 1 and 0.
+ *   eps         finite, >= 0 (else ZR_ERR_VALUE).
+ *   y           x's shape in y_strides (NULL: dense row-major).  It may alias
+ *               x exactly (same layout); other overlap is ZR_ERR_LAYOUT.
+ *   mean, rstd  float per row, dense in the order of the leading dims; either
+ *               may be NULL (not kept).
+ * A row of equal values has rstd = 1 / sqrt(eps) (infinite for eps = 0, and
+ * its y NaN).  No rows: nothing is launched.  Errors as zr_binary_fwd, plus
+ * ZR_ERR_DTYPE, ZR_ERR_VALUE.
+ *
+ * zr_layer_norm_bwd — with xh = (x - mean) * rstd and q = grad_out * gamma:
+ *   grad_x = rstd * (q - sum(q) / D - xh * sum(q * xh) / D),
+ *   grad_gamma = sum over rows of grad_out * xh,
+ *   grad_beta  = sum over rows of grad_out.
+ *   grad_out, x same shape, any strides;  mean, rstd: the forward's.
+ *   grad_x      in grad_x_strides (NULL: dense), may alias grad_out or x
+ *               exactly; grad_gamma, grad_beta dense.  Any may be NULL.
+ *   workspace   as zr_binary_bwd: NULL queries the size (partial column sums).
+ * Column sums are added in an order fixed by the shape (no atomics).  No rows:
+ * grad_gamma and grad_beta become zero.
+ */
+int zr_layer_norm_fwd(zr_dtype dtype, zr_tensor x, zr_tensor gamma, zr_tensor beta, float eps,
+                      void* y, const int64_t* y_strides, float* mean, float* rstd,
+                      zr_stream_t stream);
+int zr_layer_norm_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor x, zr_tensor gamma,
+                      const float* mean, const float* rstd, void* grad_x,
+                      const int64_t* grad_x_strides, void* grad_gamma, void* grad_beta,
+                      void* workspace, size_t* workspace_bytes, zr_stream_t stream);
+
+/*
+ * Dropout with the residual addition that follows it (the book's Dropout):
+ *   out[i] = residual[i] + (keep(i) ? x[i] * (1 / (1 - p)) : 0),
+ * and its gradient for x, keep(i) ? grad_out[i] * (1 / (1 - p)) : 0 (the
+ * residual's gradient is grad_out itself).  The mask is never stored: element
+ * i, counted row-major over the shape whatever the strides, is kept when word
+ * i mod 4 of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, SC 2011) at
+ * counter (c, c >> 32, 0, 0), c = offset + *device_offset + i / 4, under the
+ * key (seed, seed >> 32), is at least round(p * 2^32).  A call uses the
+ * counters [c0, c0 + ceil(n / 4)): advance the offset by that much for the
+ * next one.
+ *   rng.device_offset  device memory (8-byte aligned) read when the kernel
+ *               runs, or NULL: a captured graph that advances it draws a new
+ *               mask at each replay.
+ *   p           in [0, 1] (else ZR_ERR_VALUE); 0 keeps, 1 drops every element.
+ *               A dropped element adds 0 whatever x holds there (infinities
+ *               and NaN included).
+ *   residual    x's shape, any strides; data == NULL: none (0).
+ *   out         x's shape in out_strides (NULL: dense); it may alias x or the
+ *               residual exactly.
+ * One binary32 multiplication and one addition per element, rounded once to
+ * the storage type.  Errors as zr_binary_fwd, plus ZR_ERR_DTYPE and
+ * ZR_ERR_VALUE.
+ */
+typedef struct {
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* device_offset;
+} zr_rng;
+
+int zr_dropout_fwd(zr_dtype dtype, zr_tensor x, zr_tensor residual, double p, zr_rng rng, void* out,
+                   const int64_t* out_strides, zr_stream_t stream);
+int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, void* grad_x,
+                   const int64_t* grad_x_strides, zr_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* zr_status_string(int status);

@@ -49,6 +49,12 @@ int zr_test_dry_run_chain_bwd(zr_op op1, zr_op op2, zr_tensor grad_out, zr_tenso
                               zr_tensor c, const float* grad_a, const float* grad_b,
                               const float* grad_c);
 
+/* The plan of zr_layer_norm_fwd on x (grad_out.data == NULL) or of
+ * zr_layer_norm_bwd on (grad_out, x), with dense outputs and every gradient
+ * requested. */
+int zr_test_describe_layer_norm(zr_dtype dtype, zr_tensor grad_out, zr_tensor x, char* buf,
+                                size_t len);
+
 /* Plan a call and run the launch-time operand checks without launching:
  * ZR_OK, an argument error, or ZR_ERR_CUDA if a kernel would read an operand
  * the plan does not provide. */
