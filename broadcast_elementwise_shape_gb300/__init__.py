@@ -17,6 +17,8 @@ Entry points mirror the C names:
   ``zr_layer_norm_bwd(grad_out, x, gamma, mean, rstd) -> (grad_x, grad_gamma, grad_beta)``
 * ``zr_dropout_fwd(x, p, seed, offset, residual=None) -> out`` and
   ``zr_dropout_bwd(grad_out, p, seed, offset) -> grad_x``
+* ``zr_linear_xent_fwd(x, w, labels, reduction) -> (loss, lse)`` and
+  ``zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction) -> (grad_x, grad_w)``
 
 ``op`` is one of ``"add" "sub" "mul" "div"`` or the ``ZR_*`` integer codes.
 """
@@ -92,13 +94,17 @@ def lib() -> ctypes.CDLL:
                                         vp, vp, szp, vp]
         L.zr_dropout_fwd.argtypes = [c_int, ZrTensor, ZrTensor, ctypes.c_double, ZrRng, vp, i64p, vp]
         L.zr_dropout_bwd.argtypes = [c_int, ZrTensor, ctypes.c_double, ZrRng, vp, i64p, vp]
+        L.zr_linear_xent_fwd.argtypes = [c_int, ZrTensor, ZrTensor, c_int, ZrTensor,
+                                         ctypes.c_int64, c_int, vp, vp, vp, szp, vp]
+        L.zr_linear_xent_bwd.argtypes = [c_int, vp, ZrTensor, ZrTensor, c_int, ZrTensor,
+                                         ctypes.c_int64, c_int, vp, vp, vp, vp, szp, vp]
         L.zr_status_string.argtypes = [c_int]
         L.zr_status_string.restype = ctypes.c_char_p
         for f in ("zr_broadcast_shape", "zr_binary_fwd", "zr_binary_bwd", "zr_sum_to_shape",
                   "zr_chain_fwd", "zr_chain_bwd", "zr_binary_bwd_ex", "zr_unary_fwd", "zr_unary_bwd",
                   "zr_binary_fwd_t", "zr_binary_bwd_t", "zr_sum_to_shape_t", "zr_unary_fwd_t",
                   "zr_unary_bwd_t", "zr_layer_norm_fwd", "zr_layer_norm_bwd", "zr_dropout_fwd",
-                  "zr_dropout_bwd"):
+                  "zr_dropout_bwd", "zr_linear_xent_fwd", "zr_linear_xent_bwd"):
             getattr(L, f).restype = c_int
         _lib = L
     return _lib
@@ -490,3 +496,89 @@ def zr_dropout_bwd(grad_out, p, seed, offset=0, grad_x=None, device_offset=None)
                               _i64(grad_x.stride()), _stream(grad_out))
     _check(rc, "zr_dropout_bwd")
     return grad_x
+
+
+REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
+
+
+def _labels(labels, x):
+    """(index type, descriptor, what it keeps alive) of a label tensor."""
+    import torch
+    if labels.dtype not in (torch.int32, torch.int64):
+        raise TypeError("labels must be int32 or int64")
+    _shape_is(labels, x.shape[:-1], "labels")
+    if labels.numel() > 0 and not labels.is_cuda:
+        raise ValueError("zr operands must be CUDA tensors")
+    sizes, strides = _i64(labels.shape), _i64(labels.stride())
+    return (1 if labels.dtype == torch.int64 else 0,
+            ZrTensor(_ptr(labels), labels.dim(), sizes, strides), (sizes, strides, labels))
+
+
+def _reduction(reduction):
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
+    return REDUCTIONS[reduction]
+
+
+def zr_linear_xent_fwd(x, w, labels, reduction="mean", ignore_index=-100, workspace=None):
+    """(loss, lse) of the softmax cross entropy of logits x w^T, which are
+    never stored: x [..., D], w [V, D], labels x's leading shape.  loss is a
+    float32 scalar, or per row with reduction "none"; lse (float32 per row) is
+    what the backward takes."""
+    import torch
+    dt = _dtype_of(x, w)
+    red = _reduction(reduction)
+    it, dl, kl = _labels(labels, x)
+    lead = x.shape[:-1]
+    loss = torch.empty(lead if red == 0 else (), dtype=torch.float32, device=x.device)
+    lse = torch.empty(lead, dtype=torch.float32, device=x.device)
+    dx, kx = _desc(x)
+    dw, kw = _desc(w)
+    args = (dt, dx, dw, it, dl, int(ignore_index), red, _ptr(loss), _ptr(lse))
+    L = lib()
+    nbytes = ctypes.c_size_t(0)
+    _check(L.zr_linear_xent_fwd(*args, None, ctypes.byref(nbytes), None),
+           "zr_linear_xent_fwd (workspace query)")
+    if workspace is None or workspace.numel() < nbytes.value:
+        workspace = _workspace(nbytes.value, x.device)
+    nbytes = ctypes.c_size_t(workspace.numel())
+    rc = L.zr_linear_xent_fwd(*args, workspace.data_ptr(), ctypes.byref(nbytes), _stream(x))
+    _check(rc, "zr_linear_xent_fwd")
+    return loss, lse
+
+
+def zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction="mean", ignore_index=-100,
+                       want=(True, True), grads=(None, None), workspace=None):
+    """(grad_x, grad_w) of zr_linear_xent_fwd's loss given grad_loss (float32,
+    the loss's shape) and the forward's lse.  ``grads`` may hold preallocated
+    contiguous outputs."""
+    import torch
+    dt = _dtype_of(x, w, *grads)
+    red = _reduction(reduction)
+    it, dl, kl = _labels(labels, x)
+    for t, what, n in ((grad_loss, "grad_loss", labels.numel() if red == 0 else 1),
+                       (lse, "lse", labels.numel())):
+        if t.dtype != torch.float32:
+            raise TypeError(f"{what} must be float32")
+        if t.numel() != n:
+            raise ValueError(f"{what} has {t.numel()} elements, expected {n}")
+        _dense(t, what)
+    gs = [g if g is not None else (torch.empty(t.shape, dtype=t.dtype, device=t.device) if k else None)
+          for g, t, k in zip(grads, (x, w), want)]
+    for g, t, what in zip(gs, (x, w), ("grad_x", "grad_w")):
+        _shape_is(g, t.shape, what)
+        _dense(g, what)
+    dx, kx = _desc(x)
+    dw, kw = _desc(w)
+    args = (dt, _ptr(grad_loss), dx, dw, it, dl, int(ignore_index), red, _ptr(lse), _ptr(gs[0]),
+            _ptr(gs[1]))
+    L = lib()
+    nbytes = ctypes.c_size_t(0)
+    _check(L.zr_linear_xent_bwd(*args, None, ctypes.byref(nbytes), None),
+           "zr_linear_xent_bwd (workspace query)")
+    if workspace is None or workspace.numel() < nbytes.value:
+        workspace = _workspace(nbytes.value, x.device)
+    nbytes = ctypes.c_size_t(workspace.numel())
+    rc = L.zr_linear_xent_bwd(*args, workspace.data_ptr(), ctypes.byref(nbytes), _stream(x))
+    _check(rc, "zr_linear_xent_bwd")
+    return gs[0], gs[1]

@@ -1,0 +1,570 @@
+// zr_gemm.cuh — persistent tcgen05 product with fused epilogues (sm_103a).
+//
+// A tile is 128 rows per CTA by up to 256 columns, k in blocks of 64.  Warp 8
+// brings operand blocks by TMA (128-byte swizzle) through a ring in shared
+// memory, warp 9 issues the tensor-core instructions, and warps 0-7 run the
+// epilogue: 32 rows (TMEM lanes) and half the columns each.  The accumulator
+// is double-buffered in TMEM (2 x 256 columns), so one tile's epilogue
+// overlaps the next one's products.  With CG = 2 a cluster of two CTAs shares
+// a tile of 256 rows: each loads its own 128 rows of A and half of B's
+// columns, and the pair's tensor cores read both halves, which cuts the
+// operand traffic from L2 by a third.
+//
+// Every wait has a limit (kWaitNs).  When one runs out, the CTA sets its
+// abort flag, all its roles leave their loops, in-flight copies get time to
+// land before TMEM is freed, and the epilogue fills the CTA's remaining tiles
+// with NaN: a failure shows in the results, nothing hangs.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "zr_gemm.h"
+#include "zr_kernels.cuh"
+
+namespace zr {
+
+constexpr int kGemmThreads = 320;      // 8 epilogue warps, producer, issuer
+constexpr uint32_t kGemmM = 128;       // rows per CTA
+constexpr uint32_t kGemmK = 64;        // k per block (128 bytes)
+constexpr uint32_t kABytes = kGemmM * kGemmK * 2;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+template <int CG>
+struct GemmCfg {
+  static constexpr uint32_t kBBytes = 256 / CG * kGemmK * 2;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = CG == 1 ? 4 : 6;
+  static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;  // + alignment
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint64_t timer_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// ------------------------------------------------------------------ mbarrier
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase of the given parity; false when the CTA has aborted or
+// the limit ran out (which aborts it).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t t0 = timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try(bar, parity)) return true;
+    if (*abort) return false;
+    if (timer_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+// The address of `local` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
+}
+
+// ------------------------------------------------------------------ TMA, tcgen05
+template <int CG>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                         int y, int z) {
+  if constexpr (CG == 1) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+  if constexpr (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 1) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// Arrives on `bar` (of both CTAs of a pair) once the instructions issued so
+// far are done.
+template <int CG>
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  if constexpr (CG == 1) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  } else {
+    const uint16_t both = 3;
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"(both)
+        : "memory");
+  }
+}
+// 32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tc_load32(uint32_t addr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle.  Both kinds of block
+// hold 128-byte rows in groups of 8 (1024 bytes apart, the stride offset).
+// K-major: a row is one m or n with 64 k.  MN-major: a row is one k with 64 m
+// or n, and further 64-wide columns of rows follow after 8192 bytes (64 k
+// rows; the leading offset).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t mn_major) {
+  uint64_t d = uint64_t((addr & 0x3FFFFu) >> 4);
+  d |= uint64_t(mn_major ? 8192 >> 4 : 1) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+
+struct GemmTile {
+  uint32_t prob, mt, nt;
+};
+__device__ __forceinline__ GemmTile gemm_tile(const GemmPlan& p, uint32_t t) {
+  GemmTile g;
+  g.prob = t >= p.tiles0 ? 1u : 0u;
+  const uint32_t l = t - (g.prob ? p.tiles0 : 0u);
+  const GemmProblem& q = p.pr[g.prob];
+  if (p.m_fast) {
+    g.nt = l / q.m_tiles;
+    g.mt = l - g.nt * q.m_tiles;
+  } else {
+    g.mt = l / q.n_tiles;
+    g.nt = l - g.mt * q.n_tiles;
+  }
+  return g;
+}
+
+// Pairs of parts (a, b) in the order they are added: smallest products first,
+// so that the sum is small until the last, largest pair (parts 0, 0).
+__device__ __forceinline__ void gemm_combo(uint32_t n_combo, uint32_t i, int* a, int* b) {
+  if (n_combo == 1) {
+    *a = *b = 0;
+    return;
+  }
+  const uint32_t pa = 0x001012u, pb = 0x010210u;  // hex digit i, lowest first
+  *a = int((pa >> (4 * i)) & 3u);
+  *b = int((pb >> (4 * i)) & 3u);
+}
+
+// ------------------------------------------------------------------ epilogues
+
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float qnan() { return __uint_as_float(0x7FFFFFFFu); }
+
+__device__ __forceinline__ int64_t xent_label(const void* labels, int64_t stride, uint32_t i64,
+                                              uint32_t row) {
+  return i64 ? static_cast<const int64_t*>(labels)[int64_t(row) * stride]
+             : int64_t(static_cast<const int32_t*>(labels)[int64_t(row) * stride]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Where one epilogue warp's lane stands: row `row` (live: inside the product),
+// columns [c0, c1) of the tile, tile column 0 = column n0.
+struct EpiPos {
+  uint32_t row, n0, c0, c1, tmem, nt, half;
+  bool live, ok;
+};
+
+// Running maximum and sum of exponentials over the lane's columns, in one
+// walk: a chunk's maximum rescales the sum once.
+__device__ __forceinline__ void epi_lse(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
+  const int64_t label =
+      e.live ? xent_label(p.labels, p.label_stride, p.label_i64, e.row) : int64_t(-1);
+  const int64_t at = label - int64_t(e.n0);  // column of the label in this tile
+  float m = -INFINITY, s = 0.f;
+  for (uint32_t c = e.c0; c < e.c1; c += 32) {
+    if (e.n0 + c >= q.n) break;
+    float v[32];
+    __syncwarp();
+    tc_load32(e.tmem + c, v);
+    if (e.n0 + c + 32 > q.n) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (e.n0 + c + i >= q.n) v[i] = -INFINITY;
+    }
+    if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 32 && e.live)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (e.live && at == int64_t(c) + i) p.at[e.row] = e.ok ? v[i] : qnan();
+    }
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
+    const float mn = fmaxf(m, top);
+    const float ms = mn == -INFINITY ? 0.f : mn * kLog2e;
+    s *= ex2(__fmaf_rn(m, kLog2e, -ms));
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) add[i & 3] += ex2(__fmaf_rn(v[i], kLog2e, -ms));
+    s += (add[0] + add[1]) + (add[2] + add[3]);
+    m = mn;
+  }
+  if (e.live)
+    p.partial[uint64_t(e.row) * (2 * q.n_tiles) + 2 * e.nt + e.half] =
+        e.ok ? make_float2(m, s) : make_float2(0.f, qnan());
+}
+
+// G = scale * (exp(l - lse) - [column is the label]).  G is the operand of
+// the two gradient products, so it is stored as their operand type: rounded
+// once to bfloat16 (2^-9 relative per element, the size of the rounding of
+// the bfloat16 results that average over it), or, for binary32 tensors, as
+// three bfloat16 parts that hold it to 2^-24.
+__device__ __forceinline__ void epi_grad(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
+  float scale = 0.f, lse2 = 0.f;
+  int64_t at = -1;
+  bool out = true;  // the row is left out: zeros, whatever its products are
+  if (e.live) {
+    const int32_t lab = p.label32[e.row];
+    out = lab == -1;
+    scale = p.scale[e.row];
+    lse2 = p.lse[e.row] * kLog2e;
+    at = int64_t(lab) - p.label_base - int64_t(e.n0);
+  }
+  for (uint32_t c = e.c0; c < e.c1; c += 32) {
+    if (e.n0 + c >= q.n) break;
+    float v[32];
+    __syncwarp();
+    tc_load32(e.tmem + c, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = scale * ex2(__fmaf_rn(v[i], kLog2e, -lse2));
+    if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 32)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (at == int64_t(c) + i) v[i] -= scale;
+    }
+    if (out || !e.ok) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = e.ok ? 0.f : qnan();
+    }
+    if (!e.live) continue;
+    // Rows of G are padded to a multiple of 64 columns: whole 16-byte stores.
+    uint16_t* g = p.g + int64_t(e.row) * p.ldg + e.n0 + c;
+    for (uint32_t part = 0; part < p.n_part; ++part, g += p.g_part) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (e.n0 + c + 8 * i >= q.n) break;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float& x = v[8 * i + 2 * j];
+          float& y = v[8 * i + 2 * j + 1];
+          w[j] = pack_bf16(x, y);
+          x -= __uint_as_float(w[j] << 16);
+          y -= __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint4*>(g + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void epi_out(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
+  for (uint32_t c = e.c0; c < e.c1; c += 32) {
+    const uint32_t n = e.n0 + c;
+    if (n >= q.n) break;
+    float v[32];
+    __syncwarp();
+    tc_load32(e.tmem + c, v);
+    if (!e.ok) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = qnan();
+    }
+    if (!e.live) continue;
+    const bool whole = q.vec && n + 32 <= q.n;
+    float* acc = q.acc + int64_t(e.row) * q.lda + n;
+    if (q.acc_in) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        if (whole) {
+          const float4 o = *reinterpret_cast<const float4*>(acc + i);
+          v[i] += o.x; v[i + 1] += o.y; v[i + 2] += o.z; v[i + 3] += o.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + i + j < q.n) v[i + j] += acc[i + j];
+        }
+      }
+    }
+    if (q.acc_out || p.es == 4) {
+      float* o = q.acc_out ? acc : static_cast<float*>(q.out) + int64_t(e.row) * q.ldo + n;
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        if (whole) {
+          *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + i + j < q.n) o[i + j] = v[i + j];
+        }
+      }
+    } else {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(q.out) + int64_t(e.row) * q.ldo + n;
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        if (whole) {
+          *reinterpret_cast<uint4*>(o + i) =
+              make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                         pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (n + i + j < q.n) o[i + j] = __float2bfloat16_rn(v[i + j]);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <int EPI, int CG>
+__global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant__ GemmPlan p) {
+  using Cfg = GemmCfg<CG>;
+  constexpr int S = Cfg::kStages;
+  extern __shared__ uint8_t s_raw[];
+  __shared__ uint64_t s_full[S], s_empty[S], s_tfull[2], s_tempty[2];
+  __shared__ uint32_t s_tmem, s_abort;
+  pdl_trigger();
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0 : cluster_rank();
+  const uint32_t ring = (smem_u32(s_raw) + 1023u) & ~1023u;
+  volatile uint32_t* abort = &s_abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_tfull[i]), 1);
+      mbar_init(smem_u32(&s_tempty[i]), 8 * CG);
+    }
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) tmem_alloc<CG>(smem_u32(&s_tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;
+  pdl_wait();
+
+  if (warp == 8 && lane == 0) {
+    // Producer: this CTA's rows of A and its share of B's columns.
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (uint32_t t = first; t < p.tiles && ok; t += step) {
+      const GemmTile g = gemm_tile(p, t);
+      const GemmProblem& q = p.pr[g.prob];
+      const uint32_t tnc = q.tn / CG;
+      const int m0 = int((g.mt * CG + rank) * kGemmM);
+      const int n0 = int(g.nt * q.tn + rank * tnc);
+      const uint32_t nb = q.b_mn ? (tnc + 63) / 64 * 8192 : tnc * 128;
+      for (uint32_t c = 0; c < p.n_combo && ok; ++c) {
+        int pa, pb;
+        gemm_combo(p.n_combo, c, &pa, &pb);
+        for (uint32_t kb = 0; kb < q.n_kb; ++kb) {
+          if (!mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort)) { ok = false; break; }
+          const uint32_t local = smem_u32(&s_full[stage]);
+          if (rank == 0) mbar_expect(local, (kABytes + nb) * CG);
+          const uint32_t bar = CG == 1 ? local : cluster_addr(local, 0);
+          const uint32_t sa = ring + stage * Cfg::kStageBytes, sb = sa + kABytes;
+          const int k0 = int(kb * kGemmK);
+          if (q.a_mn) {
+            tma_load<CG>(sa, &q.a, bar, m0, k0, pa);
+            tma_load<CG>(sa + 8192, &q.a, bar, m0 + 64, k0, pa);
+          } else {
+            tma_load<CG>(sa, &q.a, bar, k0, m0, pa);
+          }
+          if (q.b_mn) {
+            for (uint32_t j = 0; j < tnc; j += 64)
+              tma_load<CG>(sb + j * 128, &q.b, bar, n0 + int(j), k0, pb);
+          } else {
+            tma_load<CG>(sb, &q.b, bar, k0, n0, pb);
+          }
+          if (++stage == S) { stage = 0; phase ^= 1; }
+        }
+      }
+    }
+    // Every slot is read before the CTA may end (and its peer's signals are in).
+    for (int i = 0; i < S && ok; ++i) {
+      ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort);
+      if (++stage == S) { stage = 0; phase ^= 1; }
+    }
+  } else if (warp == 9 && lane == 0 && rank == 0) {
+    // Issuer.
+    uint32_t stage = 0, phase = 0, it = 0;
+    bool ok = true;
+    for (uint32_t t = first; t < p.tiles && ok; t += step, ++it) {
+      const GemmTile g = gemm_tile(p, t);
+      const GemmProblem& q = p.pr[g.prob];
+      const uint32_t buf = it & 1;
+      // D binary32, A and B bfloat16, their majors, N / 8, M / 16.
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (q.a_mn << 15) | (q.b_mn << 16) |
+                             ((q.tn >> 3) << 17) | (uint32_t(kGemmM * CG / 16) << 24);
+      const uint32_t ka = q.a_mn ? 2048 >> 4 : 32 >> 4, kb16 = q.b_mn ? 2048 >> 4 : 32 >> 4;
+      if (!mbar_wait(smem_u32(&s_tempty[buf]), ((it >> 1) & 1) ^ 1, abort)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * 256;
+      const uint32_t nk = q.n_kb * p.n_combo;
+      for (uint32_t kb = 0; kb < nk; ++kb) {
+        if (!mbar_wait(smem_u32(&s_full[stage]), phase, abort)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t sa = ring + stage * Cfg::kStageBytes;
+        const uint64_t da = operand_desc(sa, q.a_mn), db = operand_desc(sa + kABytes, q.b_mn);
+#pragma unroll
+        for (uint32_t j = 0; j < kGemmK / 16; ++j)
+          tc_mma<CG>(d, da + j * ka, db + j * kb16, idesc, (kb | j) != 0);
+        tc_commit<CG>(smem_u32(&s_empty[stage]));
+        if (++stage == S) { stage = 0; phase ^= 1; }
+      }
+      if (ok) tc_commit<CG>(smem_u32(&s_tfull[buf]));
+    }
+  } else if (warp < 8) {
+    uint32_t it = 0;
+    bool ok = true;
+    const uint32_t quad = warp & 3, half = warp >> 2;
+    for (uint32_t t = first; t < p.tiles; t += step, ++it) {
+      const GemmTile g = gemm_tile(p, t);
+      const GemmProblem& q = p.pr[g.prob];
+      const uint32_t buf = it & 1;
+      ok = ok && mbar_wait(smem_u32(&s_tfull[buf]), (it >> 1) & 1, abort);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc_fence_after();
+      EpiPos e;
+      e.row = (g.mt * CG + rank) * kGemmM + quad * 32 + lane;
+      e.live = e.row < q.m;
+      e.n0 = g.nt * q.tn;
+      e.c0 = half * (q.tn / 2);
+      e.c1 = e.c0 + q.tn / 2;
+      e.tmem = tmem + (quad << 21) + buf * 256;
+      e.nt = g.nt;
+      e.half = half;
+      e.ok = ok;
+      if constexpr (EPI == kEpiLse) epi_lse(p, q, e);
+      else if constexpr (EPI == kEpiGrad) epi_grad(p, q, e);
+      else epi_out(p, q, e);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&s_tempty[buf]);
+        mbar_arrive_cluster(CG == 1 ? bar : cluster_addr(bar, 0));
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort) {
+    // Copies and products still in flight land within this time.
+    const uint64_t t0 = timer_ns();
+    while (timer_ns() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_free<CG>(tmem, 512);
+}
+
+}  // namespace zr

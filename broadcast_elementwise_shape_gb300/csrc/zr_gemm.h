@@ -1,0 +1,61 @@
+// zr_gemm.h — plan of the tensor-core products behind the cross entropy of a
+// linear head, and its launchers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace zr {
+
+// One product out[m, n] = sum_k A[m, k] B[n, k] of bfloat16 operands, binary32
+// accumulation.  Each operand is a 3-d tensor map over (inner, outer, part):
+// K-major operands have k as the inner (contiguous) dim, MN-major ones m or n.
+// Parts are the pieces of a binary32 operand (zr_xent.cu): the product runs
+// over n_combo pairs of parts.
+struct GemmProblem {
+  CUtensorMap a, b;
+  uint32_t m, n, k;
+  uint32_t a_mn, b_mn;       // 1: MN-major
+  uint32_t tn;               // tile width, a multiple of 64, <= 256
+  uint32_t m_tiles, n_tiles, n_kb;  // n_kb: 64-wide k blocks
+  // Epilogue kEpiOut: out = [acc_in +] product, in `es` bytes per element
+  // with row stride ldo; or to the binary32 array acc when acc_out.
+  void* out;
+  float* acc;
+  int64_t ldo, lda;
+  uint32_t acc_in, acc_out, vec;
+};
+
+enum GemmEpilogue : int {
+  kEpiLse = 0,   // per row and half tile: maximum and sum of exponentials
+  kEpiGrad = 1,  // scale * (exp(product - lse) - [column == label]) as bfloat16 parts
+  kEpiOut = 2    // the product itself
+};
+
+struct GemmPlan {
+  GemmProblem pr[2];
+  uint32_t n_prob, n_combo;
+  uint32_t tiles0, tiles;    // tiles of problem 0, of both
+  uint32_t m_fast;           // consecutive tiles walk m first
+  uint32_t es;               // kEpiOut: bytes per output element
+  // kEpiLse
+  const void* labels;        // label of row r: labels[r * label_stride]
+  int64_t label_stride;
+  uint32_t label_i64;
+  float2* partial;           // [m][2 * n_tiles] (maximum, sum)
+  float* at;                 // [m] product at the label
+  // kEpiGrad
+  const float* lse;          // [m]
+  const float* scale;        // [m]
+  const int32_t* label32;    // [m], -1: the row is left out
+  int64_t label_base;        // column 0 of this product is this label
+  uint16_t* g;               // [n_part][m][ldg]
+  int64_t ldg, g_part;
+  uint32_t n_part;
+};
+
+// grid: CTAs (a multiple of cg); cg: CTAs per cluster, 1 or 2.
+cudaError_t launch_gemm(int epi, int cg, const GemmPlan& p, unsigned grid, cudaStream_t s);
+
+}  // namespace zr

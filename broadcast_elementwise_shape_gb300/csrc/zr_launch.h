@@ -64,9 +64,10 @@ inline cudaError_t launch_k_cluster(void (*kernel)(KArgs...), unsigned grid, uns
 }
 
 // Kernels whose dynamic shared memory may exceed the default 48 KB limit:
-// raise_smem_limit sets the kernel's limit to the most a CTA may use, once
-// per kernel and device (remembered in a small table under a lock).
-inline cudaError_t raise_smem_limit(const void* kernel) {
+// raise_smem_limit sets the kernel's limit to `bytes` (the most a CTA may use,
+// for kernels without static shared memory), once per kernel and device
+// (remembered in a small table under a lock).
+inline cudaError_t raise_smem_limit(const void* kernel, int bytes = 227 * 1024) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -75,7 +76,7 @@ inline cudaError_t raise_smem_limit(const void* kernel) {
   std::lock_guard<std::mutex> lock(mu);
   for (const auto& d : done)
     if (d.first == kernel && d.second == dev) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.emplace_back(kernel, dev);
   return e;
 }

@@ -1,0 +1,703 @@
+// zr_xent.cu — softmax cross entropy of a linear head: small kernels, plan and
+// C entry points.  The products are zr_gemm.cuh's.
+//
+// l[n, v] = x_n . w_v;  lse_n = log sum_v exp(l[n, v]);  the loss of row n with
+// label y is lse_n - l[n, y].  The logits are never kept: the forward's product
+// reduces each tile to a row's maximum and sum of exponentials in its epilogue
+// (8 bytes per row and 128 columns), and the backward computes the logits
+// again, a piece of the vocabulary at a time, straight into
+//   G[n, v] = c_n (exp(l[n, v] - lse_n) - [v = y]),
+// the operand of grad_x = G W and grad_w = G^T X.
+//
+// bfloat16 tensors are the tensor core's operands as they are.  A binary32
+// tensor is split into three bfloat16 parts, x = x0 + x1 + x2 to 2^-24, and a
+// product is the sum of the six products of parts whose size reaches 2^-24 of
+// the whole: x2 w0 + x1 w1 + x0 w2 + x1 w0 + x0 w1 + x0 w0, each exact in
+// binary32 before the accumulation.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "zr_checks.h"
+#include "zr_gemm.h"
+#include "zr_kernels.cuh"
+#include "zr_launch.h"
+
+namespace zr {
+
+// An operand copied into rows the tensor maps can read: [part][row][pitch],
+// zero past `cols`.  Rows whose label32 is -1 become zero.
+struct PackPlan {
+  const void* in;
+  uint16_t* out;
+  const int32_t* label32;    // or null
+  Decomp rows;               // slot 0
+  int64_t inner_stride;
+  int64_t part;              // elements between parts
+  uint32_t nrow, cols, pitch, vec;
+  FastDiv nvec_div;          // pitch / 8
+  uint64_t items;            // nrow * pitch / 8
+};
+
+struct XentRows {
+  const void* labels;
+  int64_t label_stride;
+  uint32_t label_i64;
+  int64_t ignore_index, vocab;
+  uint32_t n;
+  int reduction;
+  // forward
+  const float2* partial;     // [n][slots]
+  const float* at;
+  uint32_t slots;
+  float* lse;
+  float* row_loss;           // workspace, or the loss itself (no reduction)
+  float* loss;
+  // backward
+  const float* grad_loss;
+  float* scale;
+  int32_t* label32;
+};
+
+namespace {
+
+__device__ __forceinline__ int64_t row_label(const XentRows& p, uint32_t r) {
+  return p.label_i64 ? static_cast<const int64_t*>(p.labels)[int64_t(r) * p.label_stride]
+                     : int64_t(static_cast<const int32_t*>(p.labels)[int64_t(r) * p.label_stride]);
+}
+
+template <typename E, int PARTS>
+__global__ void __launch_bounds__(kThreads) k_xent_pack(const __grid_constant__ PackPlan p) {
+  pdl_trigger();
+  const uint64_t i = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
+  pdl_wait();
+  if (i >= p.items) return;
+  const uint32_t nvec = p.pitch / 8;
+  const uint32_t row = uint32_t(i / nvec);
+  const uint32_t c = uint32_t(i - uint64_t(row) * nvec) * 8;
+  float v[8];
+  if (p.label32 && p.label32[row] == -1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  } else {
+    int64_t off[kMaxOperands];
+    decomp_offsets(p.rows, row, off);
+    const E* src = static_cast<const E*>(p.in) + off[0] + int64_t(c) * p.inner_stride;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < p.cols ? ld1(src + j * p.inner_stride, false) : 0.f;
+  }
+  uint16_t* dst = p.out + int64_t(row) * p.pitch + c;
+#pragma unroll
+  for (int part = 0; part < PARTS; ++part, dst += p.part) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      v[2 * j] -= __uint_as_float(w[j] << 16);
+      v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+constexpr int kRowsThreads = 1024;
+
+__device__ __forceinline__ uint32_t block_count(uint32_t v, uint32_t* s) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kRowsThreads / 32; ++w) v += s[w];
+  return v;
+}
+
+// Backward: each row's factor c_n and label.  One block, since the mean needs
+// the count of the rows that take part.
+__global__ void __launch_bounds__(kRowsThreads) k_xent_scale(const __grid_constant__ XentRows p) {
+  pdl_trigger();
+  __shared__ uint32_t s_cnt[32];
+  pdl_wait();
+  uint32_t cnt = 0;
+  if (p.reduction == ZR_MEAN) {
+    for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) cnt += row_label(p, r) != p.ignore_index;
+    cnt = block_count(cnt, s_cnt);
+  }
+  for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) {
+    const int64_t y = row_label(p, r);
+    float g = p.grad_loss[p.reduction == ZR_NONE ? r : 0];
+    if (p.reduction == ZR_MEAN) g = __fdiv_rn(g, float(cnt));
+    if (y == p.ignore_index) {
+      p.scale[r] = 0.f;
+      p.label32[r] = -1;
+    } else if (y < 0 || y >= p.vocab) {
+      p.scale[r] = __uint_as_float(0x7FFFFFFFu);  // a label that is no class: NaN, not a guess
+      p.label32[r] = -2;
+    } else {
+      p.scale[r] = g;
+      p.label32[r] = int32_t(y);
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  return v;
+}
+
+// One warp joins a row's partial maxima and sums in a fixed order.
+__device__ __forceinline__ void xent_row(const XentRows& p, uint32_t r, uint32_t lane) {
+  const float2* q = p.partial + uint64_t(r) * p.slots;
+  float m = -INFINITY;
+  for (uint32_t i = lane; i < p.slots; i += 32) m = fmaxf(m, q[i].x);
+  m = warp_max(m);
+  const float base = m == -INFINITY ? 0.f : m;
+  float s = 0.f;
+  for (uint32_t i = lane; i < p.slots; i += 32) {
+    const float2 v = q[i];
+    // A part with no columns has s = 0 and the maximum -inf.
+    s = __fmaf_rn(v.y, expf(v.x - base), s);
+  }
+  s = warp_sum(s);
+  if (lane == 0) {
+    const float lse = m + logf(s);
+    p.lse[r] = lse;
+    const int64_t y = row_label(p, r);
+    float loss = 0.f;
+    if (y != p.ignore_index)
+      loss = y < 0 || y >= p.vocab ? __uint_as_float(0x7FFFFFFFu) : lse - p.at[r];
+    p.row_loss[r] = loss;
+  }
+}
+
+// Sum or mean of the rows' losses, by one block in a fixed order.
+__device__ __forceinline__ void xent_total(const XentRows& p, uint32_t* s_cnt, float* s_sum) {
+  uint32_t cnt = 0;
+  Kahan acc;
+  acc.init();
+  for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) {
+    cnt += row_label(p, r) != p.ignore_index;
+    acc.add(p.row_loss[r]);
+  }
+  cnt = block_count(cnt, s_cnt);
+  const float v = warp_sum(acc.s);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const float t = warp_sum(s_sum[threadIdx.x]);
+    if (threadIdx.x == 0)
+      *p.loss = p.reduction == ZR_MEAN ? (cnt ? __fdiv_rn(t, float(cnt)) : 0.f) : t;
+  }
+}
+
+constexpr uint32_t kRowsOneBlock = 256;  // rows that one block joins and totals in one launch
+
+template <bool ALL>
+__global__ void __launch_bounds__(kRowsThreads) k_xent_rows(const __grid_constant__ XentRows p) {
+  pdl_trigger();
+  __shared__ uint32_t s_cnt[32];
+  __shared__ float s_sum[32];
+  const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  pdl_wait();
+  if constexpr (ALL) {
+    for (uint32_t r = w; r < p.n; r += kRowsThreads / 32) xent_row(p, r, lane);
+    if (p.reduction == ZR_NONE) return;
+    __syncthreads();
+    xent_total(p, s_cnt, s_sum);
+  } else {
+    const uint32_t r = blockIdx.x * (kRowsThreads / 32) + w;
+    if (r < p.n) xent_row(p, r, lane);
+  }
+}
+
+__global__ void __launch_bounds__(kRowsThreads) k_xent_total(const __grid_constant__ XentRows p) {
+  pdl_trigger();
+  __shared__ uint32_t s_cnt[32];
+  __shared__ float s_sum[32];
+  pdl_wait();
+  xent_total(p, s_cnt, s_sum);
+}
+
+// ------------------------------------------------------------------ plan
+
+// Workspace regions start 256-byte aligned.
+size_t take(size_t* at, size_t bytes) {
+  const size_t o = *at;
+  *at = (o + bytes + 255) / 256 * 256;
+  return o;
+}
+
+// A matrix operand as the products read it.
+struct Operand {
+  TDesc t;
+  int64_t rows = 0, cols = 0;
+  bool pack = false;
+  int64_t pitch = 0;         // elements between rows, once packed or as given
+  size_t ws = 0;             // offset of the packed copy
+  PackPlan pp;
+};
+
+constexpr int kGemmCg = 1;
+constexpr uint64_t kPieceBytes = uint64_t(1) << 30;  // G of one piece of the vocabulary, about
+
+struct XentSet {
+  int es = 4;
+  uint32_t parts = 1, combos = 1;
+  bool empty = false;        // no rows
+  Operand x, w;
+  TDesc labels;
+  XentRows rows;
+  size_t ws = 0;
+  // forward
+  size_t ws_partial = 0, ws_at = 0, ws_row = 0;
+  // backward
+  size_t ws_scale = 0, ws_label = 0, ws_g = 0, ws_acc = 0;
+  int64_t piece = 0, n_piece = 0;
+};
+
+uint32_t tile_width(int64_t n) {
+  const int64_t t = (n + 255) / 256;
+  return uint32_t(((n + t - 1) / t + 63) / 64 * 64);
+}
+
+int plan_operand(Operand* o, int es, bool force) {
+  const int n = o->t.nd;
+  o->cols = o->t.size[n - 1];
+  o->rows = 1;
+  for (int d = 0; d < n - 1; ++d) o->rows *= o->t.size[d];
+  int64_t st[kProbSlots][kMaxDims] = {};
+  for (int d = 0; d < n - 1; ++d) st[0][d] = o->t.stride[d];
+  Prob P;
+  const int rc = coalesce(n - 1, o->t.size, st, 1u, -1, &P);
+  if (rc) return rc;
+  const int64_t inner = o->cols == 1 ? 1 : o->t.stride[n - 1];
+  const bool one = P.n == 1;
+  const int64_t pitch = P.st[0][P.n - 1];
+  o->pack = force || es == 4 || !one || inner != 1 || (o->rows > 1 && pitch < o->cols) ||
+            pitch % 8 != 0 || reinterpret_cast<uintptr_t>(o->t.ptr) % 16 != 0;
+  o->pitch = (o->cols + 7) / 8 * 8;
+  if (!o->pack) {
+    if (o->rows > 1) o->pitch = pitch;
+    return ZR_OK;
+  }
+  PackPlan& p = o->pp;
+  p = PackPlan{};
+  p.in = o->t.ptr;
+  p.rows.n = P.n;
+  for (int i = 0; i < P.n; ++i) {
+    const int d = P.n - 1 - i;
+    p.rows.div[i] = make_fastdiv(uint32_t(P.size[d]));
+    p.rows.stride[0][i] = P.st[0][d];
+  }
+  p.inner_stride = inner;
+  p.nrow = uint32_t(o->rows);
+  p.cols = uint32_t(o->cols);
+  p.pitch = uint32_t(o->pitch);
+  p.part = o->rows * o->pitch;
+  p.items = uint64_t(o->rows) * uint64_t(o->pitch / 8);
+  return ZR_OK;
+}
+
+int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index it,
+              const zr_tensor& labels, int64_t ignore, zr_reduction red, bool back, bool want_w,
+              XentSet* S) {
+  if (dtype != ZR_F32 && dtype != ZR_BF16) return ZR_ERR_DTYPE;
+  if (it != ZR_I32 && it != ZR_I64) return ZR_ERR_DTYPE;
+  if (red != ZR_NONE && red != ZR_MEAN && red != ZR_SUM) return ZR_ERR_NULL;
+  S->es = dtype == ZR_BF16 ? 2 : 4;
+  S->parts = S->es == 4 ? 3 : 1;
+  S->combos = S->es == 4 ? 6 : 1;
+  int rc = read_tensor(x, &S->x.t);
+  if (rc) return rc;
+  if ((rc = read_tensor(w, &S->w.t))) return rc;
+  if ((rc = read_tensor(labels, &S->labels))) return rc;
+  const int n = S->x.t.nd;
+  if (n < 1) return ZR_ERR_RANK;
+  if (S->w.t.nd != 2) return ZR_ERR_RANK;
+  const int64_t dim = S->x.t.size[n - 1], vocab = S->w.t.size[0];
+  if (dim < 1 || vocab < 1 || S->w.t.size[1] != dim) return ZR_ERR_SHAPE;
+  if (S->labels.nd != n - 1) return ZR_ERR_SHAPE;
+  for (int d = 0; d < n - 1; ++d)
+    if (S->labels.size[d] != S->x.t.size[d]) return ZR_ERR_SHAPE;
+  // Coordinates, labels and tile counts are 32-bit.
+  if (dim >= (int64_t(1) << 24) || vocab >= (int64_t(1) << 30)) return ZR_ERR_SIZE;
+  if (S->x.t.numel / dim >= (int64_t(1) << 30)) return ZR_ERR_SIZE;
+  if ((S->x.t.numel / dim / 128 + 1) * (vocab / 256 + 1) >= (int64_t(1) << 31)) return ZR_ERR_SIZE;
+  if (S->x.t.numel == 0) {
+    S->empty = true;
+    return ZR_OK;
+  }
+  if (!S->x.t.ptr || !S->w.t.ptr || !S->labels.ptr) return ZR_ERR_NULL;
+  // The backward reads x with the left-out rows zeroed (what they hold must
+  // not reach grad_w), so it always copies x: 1 / vocab of the products' work.
+  if ((rc = plan_operand(&S->x, S->es, back && want_w))) return rc;
+  if ((rc = plan_operand(&S->w, S->es, false))) return rc;
+  XentRows& r = S->rows;
+  r = XentRows{};
+  {
+    int64_t st[kProbSlots][kMaxDims] = {};
+    for (int d = 0; d < n - 1; ++d) st[0][d] = S->labels.stride[d];
+    Prob P;
+    if ((rc = coalesce(n - 1, S->labels.size, st, 1u, -1, &P))) return rc;
+    if (P.n != 1) return ZR_ERR_LAYOUT;
+    r.label_stride = P.st[0][0];
+  }
+  r.labels = S->labels.ptr;
+  r.label_i64 = it == ZR_I64;
+  r.ignore_index = ignore;
+  r.vocab = vocab;
+  r.n = uint32_t(S->x.rows);
+  r.reduction = red;
+
+  size_t at = 0;
+  const size_t N = size_t(S->x.rows);
+  for (Operand* o : {&S->x, &S->w})
+    if (o->pack) o->ws = take(&at, size_t(o->rows) * o->pitch * 2 * S->parts);
+  if (!back) {
+    r.slots = 2 * uint32_t((vocab + 255) / 256);
+    S->ws_partial = take(&at, N * r.slots * sizeof(float2));
+    S->ws_at = take(&at, N * 4);
+    S->ws_row = take(&at, N * 4);
+  } else {
+    S->ws_scale = take(&at, N * 4);
+    S->ws_label = take(&at, N * 4);
+    const int64_t most = std::max<int64_t>(2048, int64_t(kPieceBytes / (2 * S->parts * N)));
+    S->n_piece = (vocab + most - 1) / most;
+    S->piece = ((vocab + S->n_piece - 1) / S->n_piece + 255) / 256 * 256;
+    S->n_piece = (vocab + S->piece - 1) / S->piece;
+    const int64_t wide = std::min<int64_t>(S->piece, (vocab + 63) / 64 * 64);
+    S->ws_g = take(&at, N * size_t(wide) * 2 * S->parts);
+    if (S->n_piece > 1) S->ws_acc = take(&at, N * size_t((dim + 3) / 4 * 4) * 4);
+  }
+  S->ws = at;
+  return ZR_OK;
+}
+
+// ------------------------------------------------------------------ launches
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// Map over [parts][rows][cols] bfloat16 with the given row pitch and part
+// size in elements; boxes of 64 x box_rows, out-of-range elements read as zero.
+cudaError_t make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch,
+                     uint32_t parts, int64_t part, uint32_t box_rows) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), parts};
+  const int64_t plane = parts > 1 ? part : (rows * pitch + 7) / 8 * 8;
+  const cuuint64_t strides[2] = {cuuint64_t(pitch) * 2, cuuint64_t(plane) * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1}, step[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                        box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_pack(const Operand& o, int es, const int32_t* label32, char* ws, cudaStream_t s) {
+  PackPlan p = o.pp;
+  p.out = reinterpret_cast<uint16_t*>(ws + o.ws);
+  p.label32 = label32;
+  const uint64_t blocks = (p.items + kThreads - 1) / kThreads;
+  if (blocks >= (uint64_t(1) << 31)) return cudaErrorInvalidValue;
+  return es == 4 ? launch_k(k_xent_pack<float, 3>, unsigned(blocks), kThreads, 0, s, p)
+                 : launch_k(k_xent_pack<__nv_bfloat16, 1>, unsigned(blocks), kThreads, 0, s, p);
+}
+
+const char* operand_base(const Operand& o, const char* ws) {
+  return o.pack ? ws + o.ws : reinterpret_cast<const char*>(o.t.ptr);
+}
+
+// CTAs per cluster: pairs when there is more than one CTA's rows.
+int pick_cg(int64_t m) { return m > 128 ? kGemmCg : 1; }
+
+unsigned gemm_grid(const GemmPlan& g, int cg) {
+  return unsigned(std::min<uint32_t>(g.tiles, kSms / cg) * cg);
+}
+
+void set_tiles(GemmProblem* q, int cg) {
+  q->m_tiles = (q->m + 128 * cg - 1) / (128 * cg);
+  q->n_tiles = (q->n + q->tn - 1) / q->tn;
+  q->n_kb = (q->k + 63) / 64;
+}
+
+// Logits of rows of x against `n` rows of w from row v0.
+cudaError_t logits_problem(const XentSet& S, const char* ws, int64_t v0, int64_t n, int cg,
+                           GemmPlan* g) {
+  GemmProblem& q = g->pr[0];
+  q.m = uint32_t(S.x.rows);
+  q.n = uint32_t(n);
+  q.k = uint32_t(S.x.cols);
+  q.tn = n > 256 ? 256 : tile_width(n);
+  q.a_mn = q.b_mn = 0;
+  set_tiles(&q, cg);
+  cudaError_t e = make_map(&q.a, operand_base(S.x, ws), S.x.cols, S.x.rows, S.x.pitch, S.parts,
+                           S.x.rows * S.x.pitch, 128);
+  if (e != cudaSuccess) return e;
+  e = make_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, S.w.cols, n, S.w.pitch, S.parts,
+               S.w.rows * S.w.pitch, q.tn / cg);
+  g->n_prob = 1;
+  g->n_combo = S.combos;
+  g->tiles0 = g->tiles = q.m_tiles * q.n_tiles;
+  g->m_fast = 1;
+  return e;
+}
+
+int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s) {
+  cudaError_t e;
+  for (const Operand* o : {&S.x, &S.w})
+    if (o->pack && (e = launch_pack(*o, S.es, nullptr, ws, s)) != cudaSuccess) return cuda_status(e);
+  const int cg = pick_cg(S.x.rows);
+  GemmPlan g = {};
+  if ((e = logits_problem(S, ws, 0, S.w.rows, cg, &g)) != cudaSuccess) return cuda_status(e);
+  XentRows r = S.rows;
+  r.slots = 2 * g.pr[0].n_tiles;
+  r.partial = reinterpret_cast<const float2*>(ws + S.ws_partial);
+  r.at = reinterpret_cast<const float*>(ws + S.ws_at);
+  r.lse = lse;
+  r.row_loss = r.reduction == ZR_NONE ? loss : reinterpret_cast<float*>(ws + S.ws_row);
+  r.loss = loss;
+  g.labels = r.labels;
+  g.label_stride = r.label_stride;
+  g.label_i64 = r.label_i64;
+  g.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
+  g.at = reinterpret_cast<float*>(ws + S.ws_at);
+  if ((e = launch_gemm(kEpiLse, cg, g, gemm_grid(g, cg), s)) != cudaSuccess) return cuda_status(e);
+  if (r.n <= kRowsOneBlock)
+    return cuda_status(launch_k(k_xent_rows<true>, 1, kRowsThreads, 0, s, r));
+  const unsigned blocks = (r.n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
+  e = launch_k(k_xent_rows<false>, blocks, kRowsThreads, 0, s, r);
+  if (e != cudaSuccess || r.reduction == ZR_NONE) return cuda_status(e);
+  return cuda_status(launch_k(k_xent_total, 1, kRowsThreads, 0, s, r));
+}
+
+int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* grad_x, void* grad_w,
+            char* ws, cudaStream_t s) {
+  XentRows r = S.rows;
+  r.grad_loss = grad_loss;
+  r.scale = reinterpret_cast<float*>(ws + S.ws_scale);
+  r.label32 = reinterpret_cast<int32_t*>(ws + S.ws_label);
+  cudaError_t e = launch_k(k_xent_scale, 1, kRowsThreads, 0, s, r);
+  if (e != cudaSuccess) return cuda_status(e);
+  for (const Operand* o : {&S.x, &S.w})
+    if (o->pack &&
+        (e = launch_pack(*o, S.es, o == &S.x ? r.label32 : nullptr, ws, s)) != cudaSuccess)
+      return cuda_status(e);
+  const int64_t N = S.x.rows, D = S.x.cols, V = S.w.rows;
+  uint16_t* G = reinterpret_cast<uint16_t*>(ws + S.ws_g);
+  float* acc = reinterpret_cast<float*>(ws + S.ws_acc);
+  const int64_t lda = (D + 3) / 4 * 4;
+  const int per16 = 16 / S.es;
+  for (int64_t k = 0; k < S.n_piece; ++k) {
+    const int64_t v0 = k * S.piece, n = std::min(S.piece, V - v0);
+    const int64_t ldg = (n + 63) / 64 * 64;
+    int cg = pick_cg(N);
+    GemmPlan g = {};
+    if ((e = logits_problem(S, ws, v0, n, cg, &g)) != cudaSuccess) return cuda_status(e);
+    g.lse = lse;
+    g.scale = r.scale;
+    g.label32 = r.label32;
+    g.label_base = v0;
+    g.g = G;
+    g.ldg = ldg;
+    g.g_part = N * ldg;
+    g.n_part = S.parts;
+    if ((e = launch_gemm(kEpiGrad, cg, g, gemm_grid(g, cg), s)) != cudaSuccess) return cuda_status(e);
+
+    cg = pick_cg(std::min(N, n));
+    GemmPlan o = {};
+    o.n_combo = S.combos;
+    o.es = uint32_t(S.es);
+    // grad_x += G W: rows of x, k = this piece's vocabulary.
+    if (grad_x) {
+      GemmProblem& q = o.pr[o.n_prob++];
+      q.m = uint32_t(N);
+      q.n = uint32_t(D);
+      q.k = uint32_t(n);
+      q.tn = tile_width(D);
+      q.a_mn = 0;
+      q.b_mn = 1;
+      set_tiles(&q, cg);
+      q.out = grad_x;
+      q.ldo = D;
+      q.acc = acc;
+      q.lda = lda;
+      q.acc_in = k > 0;
+      q.acc_out = k + 1 < S.n_piece;
+      q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(grad_x) % 16 == 0;
+      if ((e = make_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 128)) != cudaSuccess)
+        return cuda_status(e);
+      if ((e = make_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, D, n, S.w.pitch, S.parts,
+                        S.w.rows * S.w.pitch, 64)) != cudaSuccess)
+        return cuda_status(e);
+    }
+    // This piece's rows of grad_w = G^T X: k = the rows of x.
+    if (grad_w) {
+      GemmProblem& q = o.pr[o.n_prob++];
+      q.m = uint32_t(n);
+      q.n = uint32_t(D);
+      q.k = uint32_t(N);
+      q.tn = tile_width(D);
+      q.a_mn = 1;
+      q.b_mn = 1;
+      set_tiles(&q, cg);
+      q.out = static_cast<char*>(grad_w) + v0 * D * S.es;
+      q.ldo = D;
+      q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0;
+      if ((e = make_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 64)) != cudaSuccess)
+        return cuda_status(e);
+      if ((e = make_map(&q.b, operand_base(S.x, ws), D, N, S.x.pitch, S.parts,
+                        S.x.rows * S.x.pitch, 64)) != cudaSuccess)
+        return cuda_status(e);
+    }
+    o.tiles0 = o.pr[0].m_tiles * o.pr[0].n_tiles;
+    o.tiles = o.tiles0 + (o.n_prob > 1 ? o.pr[1].m_tiles * o.pr[1].n_tiles : 0);
+    o.m_fast = 0;
+    if ((e = launch_gemm(kEpiOut, cg, o, gemm_grid(o, cg), s)) != cudaSuccess) return cuda_status(e);
+  }
+  return ZR_OK;
+}
+
+std::string xent_json(const XentSet& S) {
+  return "{\"kernel\":\"xent\",\"rows\":" + std::to_string(S.x.rows) + ",\"dim\":" +
+         std::to_string(S.x.cols) + ",\"vocab\":" + std::to_string(S.w.rows) + ",\"parts\":" +
+         std::to_string(S.parts) + ",\"pack_x\":" + std::to_string(S.x.pack) + ",\"pack_w\":" +
+         std::to_string(S.w.pack) + ",\"piece\":" + std::to_string(S.piece) + ",\"n_piece\":" +
+         std::to_string(S.n_piece) + ",\"ws\":" + std::to_string(S.ws) + "}";
+}
+
+int check_all(std::initializer_list<const void*> ps) {
+  for (const void* q : ps) {
+    if (!q) continue;
+    const int rc = check_device_ptr(q);
+    if (rc) return rc;
+  }
+  return ZR_OK;
+}
+
+int64_t loss_count(const XentSet& S, int red) {
+  return red == ZR_NONE ? S.x.t.numel / S.x.t.size[S.x.t.nd - 1] : 1;
+}
+
+// Outputs against inputs, one another and the workspace.
+int check_spans(const XentSet& S, std::initializer_list<Span> outs, std::initializer_list<Span> ins,
+                const Span& ws) {
+  const Span fixed[3] = {span_of(S.x.t.ptr, S.x.t.extent, S.es), span_of(S.w.t.ptr, S.w.t.extent, S.es),
+                         span_of(S.labels.ptr, S.labels.extent, S.rows.label_i64 ? 8 : 4)};
+  for (const Span& f : fixed)
+    if (overlaps(f, ws)) return ZR_ERR_LAYOUT;
+  for (const Span& i : ins)
+    if (overlaps(i, ws)) return ZR_ERR_LAYOUT;
+  for (const Span& o : outs) {
+    if (overlaps(o, ws)) return ZR_ERR_LAYOUT;
+    for (const Span& f : fixed)
+      if (overlaps(o, f)) return ZR_ERR_LAYOUT;
+    for (const Span& i : ins)
+      if (overlaps(o, i)) return ZR_ERR_LAYOUT;
+    for (const Span& q : outs)
+      if (&q != &o && overlaps(o, q)) return ZR_ERR_LAYOUT;
+  }
+  return ZR_OK;
+}
+
+}  // namespace
+}  // namespace zr
+
+using namespace zr;
+
+extern "C" {
+
+int zr_linear_xent_fwd(zr_dtype dtype, zr_tensor x, zr_tensor w, zr_index label_type,
+                       zr_tensor labels, int64_t ignore_index, zr_reduction reduction, float* loss,
+                       float* lse, void* workspace, size_t* workspace_bytes, zr_stream_t stream) {
+  if (!workspace_bytes) return ZR_ERR_NULL;
+  XentSet S;
+  int rc = plan_xent(dtype, x, w, label_type, labels, ignore_index, reduction, false, false, &S);
+  if (rc) return rc;
+  const int64_t nl = loss_count(S, reduction);
+  if ((nl > 0 && !loss) || (!S.empty && !lse)) return ZR_ERR_NULL;
+  const Span ws = span_of(workspace, int64_t(S.ws), 1);
+  if (!S.empty &&
+      (rc = check_spans(S, {span_of(loss, nl), span_of(lse, S.x.rows)}, {}, ws)))
+    return rc;
+  if (!workspace) {
+    *workspace_bytes = S.ws;
+    return ZR_OK;
+  }
+  if (*workspace_bytes < S.ws) return ZR_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return ZR_ERR_WORKSPACE;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (S.empty) {
+    if (nl == 0) return ZR_OK;
+    if ((rc = check_all({loss}))) return rc;
+    return cuda_status(cudaMemsetAsync(loss, 0, sizeof(float), st));
+  }
+  if (trace_on()) trace("zr_linear_xent_fwd", xent_json(S));
+  if ((rc = check_all({S.x.t.ptr, S.w.t.ptr, S.labels.ptr, loss, lse, workspace}))) return rc;
+  return run_fwd(S, loss, lse, static_cast<char*>(workspace), st);
+}
+
+int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_tensor w,
+                       zr_index label_type, zr_tensor labels, int64_t ignore_index,
+                       zr_reduction reduction, const float* lse, void* grad_x, void* grad_w,
+                       void* workspace, size_t* workspace_bytes, zr_stream_t stream) {
+  if (!workspace_bytes) return ZR_ERR_NULL;
+  XentSet S;
+  int rc = plan_xent(dtype, x, w, label_type, labels, ignore_index, reduction, true,
+                     grad_w != nullptr, &S);
+  if (rc) return rc;
+  const int64_t nl = loss_count(S, reduction);
+  const int64_t dim = S.w.t.size[1], vocab = S.w.t.size[0];
+  if (!S.empty && (!grad_loss || !lse)) return ZR_ERR_NULL;
+  const Span ws = span_of(workspace, int64_t(S.ws), 1);
+  if (!S.empty &&
+      (rc = check_spans(S, {span_of(grad_x, grad_x ? S.x.rows * dim : 0, S.es),
+                            span_of(grad_w, grad_w ? vocab * dim : 0, S.es)},
+                        {span_of(grad_loss, nl), span_of(lse, S.x.rows)}, ws)))
+    return rc;
+  if (!workspace) {
+    *workspace_bytes = S.ws;
+    return ZR_OK;
+  }
+  if (*workspace_bytes < S.ws) return ZR_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return ZR_ERR_WORKSPACE;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (S.empty) {
+    if (!grad_w) return ZR_OK;
+    if ((rc = check_all({grad_w}))) return rc;
+    return cuda_status(cudaMemsetAsync(grad_w, 0, size_t(vocab) * dim * S.es, st));
+  }
+  if (!grad_x && !grad_w) return ZR_OK;
+  if (trace_on()) trace("zr_linear_xent_bwd", xent_json(S));
+  if ((rc = check_all({grad_loss, S.x.t.ptr, S.w.t.ptr, S.labels.ptr, lse, grad_x, grad_w, workspace})))
+    return rc;
+  return run_bwd(S, grad_loss, lse, grad_x, grad_w, static_cast<char*>(workspace), st);
+}
+
+}  // extern "C"

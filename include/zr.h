@@ -455,6 +455,58 @@ int zr_dropout_fwd(zr_dtype dtype, zr_tensor x, zr_tensor residual, double p, zr
 int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, void* grad_x,
                    const int64_t* grad_x_strides, zr_stream_t stream);
 
+/*
+ * Softmax cross entropy of a linear head (the book's OpLinearCrossEntropy):
+ * logits l[n, v] = x_n . w_v over a vocabulary of V classes, which are never
+ * stored; lse_n = log(sum over v of exp(l[n, v])); row n's loss is
+ * lse_n - l[n, label_n].
+ *
+ * zr_linear_xent_fwd
+ *   x           [..., D], rank 1 to 8, any strides; N = the leading sizes'
+ *               product (rank 1: N = 1).
+ *   w           [V, D], any strides, x's element type (a weight-tied head is
+ *               the embedding itself).
+ *   labels      x's leading shape, int32 or int64 (label_type), with strides
+ *               that walk it row-major at one step (else ZR_ERR_LAYOUT).
+ *   ignore_index  rows with this label are left out: their loss is 0, their
+ *               gradients are 0 whatever x holds there (infinities and NaN
+ *               included), and a mean does not count them.  Any other label
+ *               outside [0, V) makes the row's loss and gradients NaN.
+ *   reduction   ZR_NONE: loss holds N floats; ZR_SUM, ZR_MEAN: one.  The mean
+ *               over no rows is 0.
+ *   lse         N floats (every row, the left-out ones too), which the backward
+ *               takes.
+ *   workspace   NULL queries the size; then at least that many bytes, 16-byte
+ *               aligned, contents irrelevant, used in stream order.
+ *
+ * zr_linear_xent_bwd — with c_n = grad_loss (one float; ZR_NONE: N of them;
+ * ZR_MEAN: divided by the count of rows that take part) and
+ * G[n, v] = c_n (exp(l[n, v] - lse_n) - [v = label_n]):
+ *   grad_x = G W and grad_w = G^T X, dense row-major, either may be NULL.
+ * The logits are computed again, a piece of the vocabulary at a time; the
+ * workspace holds one piece of G (about 1 GiB at most, or 2048 classes'
+ * worth for very many rows).
+ *
+ * Numerics.  Products accumulate in binary32 on the tensor cores; statistics
+ * and losses are binary32.  ZR_BF16: operands as stored, G rounded once to
+ * bfloat16 as an operand, gradients rounded once.  ZR_F32: each operand is
+ * split into three bfloat16 parts, whose products reach binary32 accuracy.
+ * A row with an infinite logit has a NaN loss.  Results are reproducible run
+ * to run (no atomics).
+ * Sizes: D < 2^24, V and N < 2^30 (else ZR_ERR_SIZE); D, V >= 1.  N = 0: loss
+ * (sum, mean) and grad_w become 0.  Errors as zr_binary_bwd, plus ZR_ERR_DTYPE.
+ */
+typedef enum { ZR_I32 = 0, ZR_I64 = 1 } zr_index;
+typedef enum { ZR_NONE = 0, ZR_MEAN = 1, ZR_SUM = 2 } zr_reduction;
+
+int zr_linear_xent_fwd(zr_dtype dtype, zr_tensor x, zr_tensor w, zr_index label_type,
+                       zr_tensor labels, int64_t ignore_index, zr_reduction reduction, float* loss,
+                       float* lse, void* workspace, size_t* workspace_bytes, zr_stream_t stream);
+int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_tensor w,
+                       zr_index label_type, zr_tensor labels, int64_t ignore_index,
+                       zr_reduction reduction, const float* lse, void* grad_x, void* grad_w,
+                       void* workspace, size_t* workspace_bytes, zr_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char* zr_status_string(int status);
 
