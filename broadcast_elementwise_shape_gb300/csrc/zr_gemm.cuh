@@ -305,9 +305,11 @@ __device__ __forceinline__ void epi_lse(const GemmPlan& p, const GemmProblem& q,
 
 // G = scale * (exp(l - lse) - [column is the label]).  G is the operand of
 // the two gradient products, so it is stored as their operand type: rounded
-// once to bfloat16 (2^-9 relative per element, the size of the rounding of
-// the bfloat16 results that average over it), or, for binary32 tensors, as
-// three bfloat16 parts that hold it to 2^-24.
+// once to bfloat16 (2^-8 relative per element at most, the size of the
+// rounding of the bfloat16 results that average over it), or, for binary32
+// tensors, as three bfloat16 parts that hold it to 2^-24.  A factor that all
+// rows share is left to the products' epilogue: then the label's element of a
+// row that is not yet learnt, the largest by far, is -1 and rounds to itself.
 __device__ __forceinline__ void epi_grad(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
   float scale = 0.f, lse2 = 0.f;
   int64_t at = -1;
@@ -358,6 +360,7 @@ __device__ __forceinline__ void epi_grad(const GemmPlan& p, const GemmProblem& q
 }
 
 __device__ __forceinline__ void epi_out(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
+  const float scale = p.out_scale && !q.acc_out ? *p.out_scale : 1.f;
   for (uint32_t c = e.c0; c < e.c1; c += 32) {
     const uint32_t n = e.n0 + c;
     if (n >= q.n) break;
@@ -384,6 +387,8 @@ __device__ __forceinline__ void epi_out(const GemmPlan& p, const GemmProblem& q,
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= scale;
     if (q.acc_out || p.es == 4) {
       float* o = q.acc_out ? acc : static_cast<float*>(q.out) + int64_t(e.row) * q.ldo + n;
 #pragma unroll

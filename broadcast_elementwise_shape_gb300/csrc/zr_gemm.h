@@ -39,6 +39,7 @@ struct GemmPlan {
   uint32_t tiles0, tiles;    // tiles of problem 0, of both
   uint32_t m_fast;           // consecutive tiles walk m first
   uint32_t es;               // kEpiOut: bytes per output element
+  const float* out_scale;    // kEpiOut: multiplies the finished product, or null (1)
   // kEpiLse
   const void* labels;        // label of row r: labels[r * label_stride]
   int64_t label_stride;

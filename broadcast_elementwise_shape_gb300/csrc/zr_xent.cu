@@ -59,6 +59,7 @@ struct XentRows {
   // backward
   const float* grad_loss;
   float* scale;
+  float* common;             // the factor all rows share (mean, sum)
   int32_t* label32;
 };
 
@@ -128,10 +129,12 @@ __global__ void __launch_bounds__(kRowsThreads) k_xent_scale(const __grid_consta
     for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) cnt += row_label(p, r) != p.ignore_index;
     cnt = block_count(cnt, s_cnt);
   }
+  if (threadIdx.x == 0 && p.reduction != ZR_NONE)
+    *p.common = p.reduction == ZR_MEAN ? (cnt ? __fdiv_rn(p.grad_loss[0], float(cnt)) : 0.f)
+                                       : p.grad_loss[0];
   for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) {
     const int64_t y = row_label(p, r);
-    float g = p.grad_loss[p.reduction == ZR_NONE ? r : 0];
-    if (p.reduction == ZR_MEAN) g = __fdiv_rn(g, float(cnt));
+    const float g = p.reduction == ZR_NONE ? p.grad_loss[r] : 1.f;
     if (y == p.ignore_index) {
       p.scale[r] = 0.f;
       p.label32[r] = -1;
@@ -248,7 +251,7 @@ struct Operand {
   PackPlan pp;
 };
 
-constexpr int kGemmCg = 1;
+constexpr int kGemmCg = 2;
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;  // G of one piece of the vocabulary, about
 
 struct XentSet {
@@ -262,7 +265,7 @@ struct XentSet {
   // forward
   size_t ws_partial = 0, ws_at = 0, ws_row = 0;
   // backward
-  size_t ws_scale = 0, ws_label = 0, ws_g = 0, ws_acc = 0;
+  size_t ws_scale = 0, ws_common = 0, ws_label = 0, ws_g = 0, ws_acc = 0;
   int64_t piece = 0, n_piece = 0;
 };
 
@@ -371,6 +374,7 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     S->ws_row = take(&at, N * 4);
   } else {
     S->ws_scale = take(&at, N * 4);
+    S->ws_common = take(&at, 4);
     S->ws_label = take(&at, N * 4);
     const int64_t most = std::max<int64_t>(2048, int64_t(kPieceBytes / (2 * S->parts * N)));
     S->n_piece = (vocab + most - 1) / most;
@@ -502,6 +506,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
   XentRows r = S.rows;
   r.grad_loss = grad_loss;
   r.scale = reinterpret_cast<float*>(ws + S.ws_scale);
+  r.common = reinterpret_cast<float*>(ws + S.ws_common);
   r.label32 = reinterpret_cast<int32_t*>(ws + S.ws_label);
   cudaError_t e = launch_k(k_xent_scale, 1, kRowsThreads, 0, s, r);
   if (e != cudaSuccess) return cuda_status(e);
@@ -534,6 +539,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     GemmPlan o = {};
     o.n_combo = S.combos;
     o.es = uint32_t(S.es);
+    o.out_scale = r.reduction == ZR_NONE ? nullptr : r.common;
     // grad_x += G W: rows of x, k = this piece's vocabulary.
     if (grad_x) {
       GemmProblem& q = o.pr[o.n_prob++];
