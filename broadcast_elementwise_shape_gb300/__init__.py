@@ -100,6 +100,10 @@ def lib() -> ctypes.CDLL:
                                          ctypes.c_int64, c_int, vp, vp, vp, vp, szp, vp]
         L.zr_status_string.argtypes = [c_int]
         L.zr_status_string.restype = ctypes.c_char_p
+        for f, n in (("layer_norm_fwd", 1), ("layer_norm_bwd", 2), ("dropout_fwd", 1),
+                     ("dropout_bwd", 1), ("linear_xent_fwd", 2), ("linear_xent_bwd", 2)):
+            getattr(L, "zr_packed_" + f).argtypes = [ctypes.c_char_p, vp][:n]
+            getattr(L, "zr_packed_" + f).restype = c_int
         for f in ("zr_broadcast_shape", "zr_binary_fwd", "zr_binary_bwd", "zr_sum_to_shape",
                   "zr_chain_fwd", "zr_chain_bwd", "zr_binary_bwd_ex", "zr_unary_fwd", "zr_unary_bwd",
                   "zr_binary_fwd_t", "zr_binary_bwd_t", "zr_sum_to_shape_t", "zr_unary_fwd_t",
@@ -376,209 +380,6 @@ def zr_unary_bwd(op, grad_out, x, alpha=1.0, grad_x=None):
     return grad_x
 
 
-def _none_desc():
-    return ZrTensor(None, 0, None, None)
 
-
-def _ptr(t):
-    return t.data_ptr() if t is not None and t.numel() else None
-
-
-def _shape_is(t, shape, what):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _dense(t, what):
-    if t is not None and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-
-
-def zr_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, out=None, keep_stats=True):
-    """(y, mean, rstd) of layer norm over x's last dim: y = (x - mean) * rstd *
-    gamma + beta.  mean and rstd are float32 of the leading shape, or None with
-    ``keep_stats`` false.  ``out`` may be a preallocated (strided) tensor of
-    x's shape, or x itself."""
-    import torch
-    dt = _dtype_of(x, gamma, beta, out)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _shape_is(out, x.shape, "out")
-    mean = rstd = None
-    if keep_stats:
-        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device).unbind(0)
-    dx, kx = _desc(x)
-    dg, kg = _desc(gamma) if gamma is not None else (_none_desc(), None)
-    db, kb = _desc(beta) if beta is not None else (_none_desc(), None)
-    rc = lib().zr_layer_norm_fwd(dt, dx, dg, db, float(eps), _ptr(out), _i64(out.stride()),
-                                 _ptr(mean), _ptr(rstd), _stream(x))
-    _check(rc, "zr_layer_norm_fwd")
-    return out, mean, rstd
-
-
-def zr_layer_norm_bwd(grad_out, x, gamma, mean, rstd, want=(True, True, True),
-                      grads=(None, None, None), workspace=None):
-    """(grad_x, grad_gamma, grad_beta) of layer norm given grad_out and the
-    forward's mean and rstd.  ``gamma`` may be None (1); ``grads`` may hold
-    preallocated outputs (grad_x of any strides, or grad_out or x itself)."""
-    import torch
-    dt = _dtype_of(grad_out, x, gamma, *grads)
-    dim = x.shape[-1] if x.dim() else 0
-    shapes = (x.shape, (dim,), (dim,))
-    gs = [g if g is not None else
-          (torch.empty(s, dtype=x.dtype, device=x.device) if w else None)
-          for g, s, w in zip(grads, shapes, want)]
-    for g, s, what in zip(gs, shapes, ("grad_x", "grad_gamma", "grad_beta")):
-        _shape_is(g, s, what)
-    for t, what in ((gs[1], "grad_gamma"), (gs[2], "grad_beta"), (mean, "mean"), (rstd, "rstd")):
-        _dense(t, what)
-    for t, what in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32:
-            raise TypeError(f"{what} must be float32")
-        _shape_is(t, x.shape[:-1], what)
-    dg, kg = _desc(grad_out)
-    dx, kx = _desc(x)
-    dga, kga = _desc(gamma) if gamma is not None else (_none_desc(), None)
-    args = (dt, dg, dx, dga, _ptr(mean), _ptr(rstd), _ptr(gs[0]),
-            _i64(gs[0].stride()) if gs[0] is not None else None, _ptr(gs[1]), _ptr(gs[2]))
-    L = lib()
-    nbytes = ctypes.c_size_t(0)
-    _check(L.zr_layer_norm_bwd(*args, None, ctypes.byref(nbytes), None),
-           "zr_layer_norm_bwd (workspace query)")
-    if workspace is None or workspace.numel() < nbytes.value:
-        workspace = _workspace(nbytes.value, x.device)
-    nbytes = ctypes.c_size_t(workspace.numel())
-    rc = L.zr_layer_norm_bwd(*args, workspace.data_ptr(), ctypes.byref(nbytes), _stream(x))
-    _check(rc, "zr_layer_norm_bwd")
-    return tuple(gs)
-
-
-def _rng(seed, offset, device_offset):
-    import torch
-    if device_offset is not None:
-        if device_offset.dtype != torch.int64 or device_offset.numel() != 1:
-            raise TypeError("device_offset must be one int64 element")
-        device_offset = device_offset.data_ptr()
-    m = (1 << 64) - 1
-    return ZrRng(int(seed) & m, int(offset) & m, device_offset)
-
-
-def zr_dropout_fwd(x, p, seed, offset=0, residual=None, out=None, device_offset=None):
-    """out = residual + (keep ? x / (1 - p) : 0).  The mask is a function of
-    (seed, offset, row-major element index) alone: a call uses the counters
-    offset .. offset + ceil(numel / 4) - 1.  ``device_offset`` (one int64 on
-    the device) is added to ``offset`` when the kernel runs.  ``out`` may be a
-    preallocated (strided) tensor, x, or the residual."""
-    import torch
-    dt = _dtype_of(x, residual, out)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _shape_is(out, x.shape, "out")
-    _shape_is(residual, x.shape, "residual")
-    rng = _rng(seed, offset, device_offset)
-    dx, kx = _desc(x)
-    dr, kr = _desc(residual) if residual is not None else (_none_desc(), None)
-    rc = lib().zr_dropout_fwd(dt, dx, dr, float(p), rng, _ptr(out),
-                              _i64(out.stride()), _stream(x))
-    _check(rc, "zr_dropout_fwd")
-    return out
-
-
-def zr_dropout_bwd(grad_out, p, seed, offset=0, grad_x=None, device_offset=None):
-    """grad_x = keep ? grad_out / (1 - p) : 0 with the forward's mask."""
-    import torch
-    dt = _dtype_of(grad_out, grad_x)
-    if grad_x is None:
-        grad_x = torch.empty(grad_out.shape, dtype=grad_out.dtype, device=grad_out.device)
-    _shape_is(grad_x, grad_out.shape, "grad_x")
-    dg, kg = _desc(grad_out)
-    rc = lib().zr_dropout_bwd(dt, dg, float(p), _rng(seed, offset, device_offset), _ptr(grad_x),
-                              _i64(grad_x.stride()), _stream(grad_out))
-    _check(rc, "zr_dropout_bwd")
-    return grad_x
-
-
-REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
-
-
-def _labels(labels, x):
-    """(index type, descriptor, what it keeps alive) of a label tensor."""
-    import torch
-    if labels.dtype not in (torch.int32, torch.int64):
-        raise TypeError("labels must be int32 or int64")
-    _shape_is(labels, x.shape[:-1], "labels")
-    if labels.numel() > 0 and not labels.is_cuda:
-        raise ValueError("zr operands must be CUDA tensors")
-    sizes, strides = _i64(labels.shape), _i64(labels.stride())
-    return (1 if labels.dtype == torch.int64 else 0,
-            ZrTensor(_ptr(labels), labels.dim(), sizes, strides), (sizes, strides, labels))
-
-
-def _reduction(reduction):
-    if reduction not in REDUCTIONS:
-        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}")
-    return REDUCTIONS[reduction]
-
-
-def zr_linear_xent_fwd(x, w, labels, reduction="mean", ignore_index=-100, workspace=None):
-    """(loss, lse) of the softmax cross entropy of logits x w^T, which are
-    never stored: x [..., D], w [V, D], labels x's leading shape.  loss is a
-    float32 scalar, or per row with reduction "none"; lse (float32 per row) is
-    what the backward takes."""
-    import torch
-    dt = _dtype_of(x, w)
-    red = _reduction(reduction)
-    it, dl, kl = _labels(labels, x)
-    lead = x.shape[:-1]
-    loss = torch.empty(lead if red == 0 else (), dtype=torch.float32, device=x.device)
-    lse = torch.empty(lead, dtype=torch.float32, device=x.device)
-    dx, kx = _desc(x)
-    dw, kw = _desc(w)
-    args = (dt, dx, dw, it, dl, int(ignore_index), red, _ptr(loss), _ptr(lse))
-    L = lib()
-    nbytes = ctypes.c_size_t(0)
-    _check(L.zr_linear_xent_fwd(*args, None, ctypes.byref(nbytes), None),
-           "zr_linear_xent_fwd (workspace query)")
-    if workspace is None or workspace.numel() < nbytes.value:
-        workspace = _workspace(nbytes.value, x.device)
-    nbytes = ctypes.c_size_t(workspace.numel())
-    rc = L.zr_linear_xent_fwd(*args, workspace.data_ptr(), ctypes.byref(nbytes), _stream(x))
-    _check(rc, "zr_linear_xent_fwd")
-    return loss, lse
-
-
-def zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction="mean", ignore_index=-100,
-                       want=(True, True), grads=(None, None), workspace=None):
-    """(grad_x, grad_w) of zr_linear_xent_fwd's loss given grad_loss (float32,
-    the loss's shape) and the forward's lse.  ``grads`` may hold preallocated
-    contiguous outputs."""
-    import torch
-    dt = _dtype_of(x, w, *grads)
-    red = _reduction(reduction)
-    it, dl, kl = _labels(labels, x)
-    for t, what, n in ((grad_loss, "grad_loss", labels.numel() if red == 0 else 1),
-                       (lse, "lse", labels.numel())):
-        if t.dtype != torch.float32:
-            raise TypeError(f"{what} must be float32")
-        if t.numel() != n:
-            raise ValueError(f"{what} has {t.numel()} elements, expected {n}")
-        _dense(t, what)
-    gs = [g if g is not None else (torch.empty(t.shape, dtype=t.dtype, device=t.device) if k else None)
-          for g, t, k in zip(grads, (x, w), want)]
-    for g, t, what in zip(gs, (x, w), ("grad_x", "grad_w")):
-        _shape_is(g, t.shape, what)
-        _dense(g, what)
-    dx, kx = _desc(x)
-    dw, kw = _desc(w)
-    args = (dt, _ptr(grad_loss), dx, dw, it, dl, int(ignore_index), red, _ptr(lse), _ptr(gs[0]),
-            _ptr(gs[1]))
-    L = lib()
-    nbytes = ctypes.c_size_t(0)
-    _check(L.zr_linear_xent_bwd(*args, None, ctypes.byref(nbytes), None),
-           "zr_linear_xent_bwd (workspace query)")
-    if workspace is None or workspace.numel() < nbytes.value:
-        workspace = _workspace(nbytes.value, x.device)
-    nbytes = ctypes.c_size_t(workspace.numel())
-    rc = L.zr_linear_xent_bwd(*args, workspace.data_ptr(), ctypes.byref(nbytes), _stream(x))
-    _check(rc, "zr_linear_xent_bwd")
-    return gs[0], gs[1]
+from .train import (zr_dropout_bwd, zr_dropout_fwd, zr_layer_norm_bwd,  # noqa: E402,F401
+                    zr_layer_norm_fwd, zr_linear_xent_bwd, zr_linear_xent_fwd)

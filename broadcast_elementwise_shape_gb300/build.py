@@ -21,7 +21,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["zr_api.cu", "zr_plan.cpp", "zr_launch_ew.cu", "zr_launch_red.cu", "zr_launch_sab.cu",
            "zr_launch_chain.cu", "zr_launch_bf16.cu", "zr_norm.cu", "zr_launch_norm_fwd.cu",
-           "zr_launch_norm_bwd.cu", "zr_dropout.cu", "zr_xent.cu", "zr_launch_gemm.cu"]
+           "zr_launch_norm_bwd.cu", "zr_dropout.cu", "zr_xent.cu", "zr_launch_gemm.cu",
+           "zr_packed.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-fmad=false", "-ftz=false",
          "-prec-div=true", "-prec-sqrt=true", "-I", INCLUDE]
