@@ -35,8 +35,11 @@ void norm_cases(F f) {
 #undef ZR_NORM_CASE
 }
 
-// Fewest lanes whose registers hold the row: 8 lanes only for rows that a
-// warp's single access would leave half empty.
+// Fewest lanes whose registers hold the row, 8 only for rows that a warp's
+// single access would leave half empty.  Element-wise access (odd sizes or
+// strides) goes to a block per row from 257 columns: a lane then has few
+// columns and many warps share the loads' latency ([4093, 1001] bf16 backward
+// with 32 columns per lane 41 us, with 4 per lane 15).
 void pick_group(NormPlan* p, int vec) {
   p->group = p->ni = 0;
   uint64_t best = ~uint64_t(0);
@@ -213,11 +216,16 @@ int plan_norm_bwd(zr_dtype dtype, const zr_tensor& g, const zr_tensor& x, const 
   if ((rc = plan_rows(S, 2, gx))) return rc;
   const bool sums = p.want_gamma || p.want_beta;
   if (p.group) {
-    // Persistent over rows: the column sums stay in registers.
-    const uint32_t rpb = p.group > 32 ? 1 : kNormBwdThreads / p.group;
+    // Persistent over rows: the column sums stay in registers.  The ring
+    // takes a third stage where that leaves every CTA its place on the SM.
+    const uint32_t rpb = kNormThreads / p.group;
     const uint32_t need = (p.nrow + rpb - 1) / rpb;
-    const uint32_t cols = p.ni * uint32_t(S->vec);
-    const uint32_t per_sm = p.group > 32 ? (cols > 16 ? 1 : 2) : (cols > 16 ? 3 : 4);
+    uint32_t per_sm = uint32_t(norm_bwd_occ(int(p.ni) * S->vec, S->vec));
+    const uint32_t ring = S->vec > 1 ? 2 * kNormThreads * p.ni * 16 : 0;  // one stage
+    p.stages = ring && 3 * ring * per_sm <= uint32_t(kNormSmemMax) ? 3 : 2;
+    while (per_sm > 1 && p.stages * ring * per_sm > uint32_t(kNormSmemMax)) --per_sm;
+    const uint32_t cols = p.group > 32 ? 0 : p.group * p.ni * uint32_t(S->vec) * 4;
+    p.smem = std::max(p.stages * ring, cols);
     p.n_cta = std::min<uint32_t>(need, kSms * per_sm);
   } else {
     // k_norm_sums: rows split so that the column blocks fill the GPU, at

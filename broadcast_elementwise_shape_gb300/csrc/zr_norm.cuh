@@ -229,19 +229,42 @@ k_norm_fwd_long(const __grid_constant__ NormPlan p) {
 
 // ------------------------------------------------------------------ backward
 
-template <int G>
-ZR_CX int norm_bwd_threads() { return G > 32 ? G : kNormBwdThreads; }
+// The 16 bytes of VEC elements at `raw` as floats.
+template <typename E, int VEC>
+__device__ __forceinline__ void norm_unpack(const uint4& q, float* v) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(E) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ void norm_cp16(uint4* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(src) : "memory");
+}
 
+// A row group's lanes keep the two column sums of their columns in registers
+// for all the rows the block meets.  What bounds the pass is the bytes in
+// flight: with 16-byte vectors each lane copies the vectors it will read
+// itself into its own slots of a shared-memory ring, p.stages - 1 rows ahead
+// (cp.async: no registers, and no barrier since no lane reads another's), and
+// reads them twice from there, once for the row's two means and the column
+// sums, once for grad_x.  Keeping the row in registers instead took 222 of
+// them and left 8 warps per SM: [65536, 1024] bf16 137 us against 78.
 template <typename E, int VEC, int G, int NI>
-__global__ void __launch_bounds__(norm_bwd_threads<G>())
+__global__ void __launch_bounds__(kNormThreads, norm_bwd_occ(NI * VEC, VEC))
 k_norm_bwd(const __grid_constant__ NormPlan p) {
   pdl_trigger();
-  constexpr int T = norm_bwd_threads<G>();
+  constexpr int T = kNormThreads;
   constexpr int RPB = T / G;           // rows per block per step
   constexpr int W = G * NI * VEC;      // columns the lanes cover
+  extern __shared__ uint4 s_ring[];    // [stage][row group][g, x][NI * G]; then column sums
   __shared__ float s_sum[2][2][32];
-  // Column sums of the block's row groups; one array at a time (G <= 32).
-  __shared__ float s_col[G > 32 ? 1 : W];
   const uint32_t lane = threadIdx.x % G, grp = threadIdx.x / G;
   const int64_t gs = VEC > 1 ? 1 : p.inner_stride[0];
   const int64_t xs = VEC > 1 ? 1 : p.inner_stride[1];
@@ -251,28 +274,81 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc_g[i][j] = acc_b[i][j] = 0.f;
+  const uint64_t step = uint64_t(gridDim.x) * RPB;
+  const uint64_t first = uint64_t(blockIdx.x) * RPB + grp;
+  const uint32_t S = p.stages;
+  auto slot = [&](uint32_t stage, int a) {
+    return s_ring + ((uint64_t(stage) * RPB + grp) * 2 + a) * (NI * G) + lane;
+  };
+  auto fetch = [&](uint32_t stage, uint64_t row) {
+    if constexpr (VEC > 1) {
+      if (row < p.nrow) {
+        int64_t off[kMaxOperands];
+        norm_row(p.rows, uint32_t(row), off);
+        const E* g = static_cast<const E*>(p.in[0]) + off[0];
+        const E* x = static_cast<const E*>(p.in[1]) + off[1];
+        uint4* sg = slot(stage, 0);
+        uint4* sx = slot(stage, 1);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const uint32_t c = (i * G + lane) * VEC;
+          if (c < p.dim) {
+            norm_cp16(sg + i * G, g + c);
+            norm_cp16(sx + i * G, x + c);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
+  };
   pdl_wait();
-  uint32_t flip = 0;
-  for (uint64_t r0 = uint64_t(blockIdx.x) * RPB; r0 < p.nrow; r0 += uint64_t(gridDim.x) * RPB) {
-    const uint32_t row = uint32_t(r0) + grp;
-    const bool live = r0 + grp < p.nrow;
+  if constexpr (VEC > 1)
+    for (uint32_t k = 0; k + 1 < S; ++k) fetch(k, first + k * step);
+  float mean = first < p.nrow ? p.mean_in[first] : 0.f;
+  float rstd = first < p.nrow ? p.rstd_in[first] : 0.f;
+  float gam[NI][VEC];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const uint32_t c = (i * G + lane) * VEC;
+    if (c < p.dim) {
+      norm_affine<E, VEC>(p.gamma, p.gamma_stride, p.affine_vec, c, 1.f, gam[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) gam[i][j] = 0.f;
+    }
+  }
+  uint32_t flip = 0, stage = 0, ahead = S - 1;
+  for (uint64_t r0 = uint64_t(blockIdx.x) * RPB; r0 < p.nrow; r0 += step) {
+    const uint64_t row = r0 + grp;
+    const bool live = row < p.nrow;
+    // The next row's statistics, and the vectors of the row S - 1 steps on.
+    const float mean_next = row + step < p.nrow ? p.mean_in[row + step] : 0.f;
+    const float rstd_next = row + step < p.nrow ? p.rstd_in[row + step] : 0.f;
     int64_t off[kMaxOperands];
-    norm_row(p.rows, live ? row : 0, off);
-    const E* g = static_cast<const E*>(p.in[0]) + off[0];
-    const E* x = static_cast<const E*>(p.in[1]) + off[1];
-    const float mean = live ? p.mean_in[row] : 0.f;
-    const float rstd = live ? p.rstd_in[row] : 0.f;
-    float gv[NI][VEC], xh[NI][VEC];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const uint32_t c = (i * G + lane) * VEC;
-      if (live && c < p.dim) {
-        norm_load<E, VEC>(g + int64_t(c) * gs, gv[i]);
-        norm_load<E, VEC>(x + int64_t(c) * xs, xh[i]);
+    norm_row(p.rows, live ? uint32_t(row) : 0, off);
+    if constexpr (VEC > 1) {
+      fetch(ahead, row + (S - 1) * step);
+      if (S == 3) asm volatile("cp.async.wait_group 2;\n" ::: "memory");
+      else asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    }
+    auto load = [&](int i, uint32_t c, float* gv, float* xv) {
+      if constexpr (VEC > 1) {
+        norm_unpack<E, VEC>(slot(stage, 0)[i * G], gv);
+        norm_unpack<E, VEC>(slot(stage, 1)[i * G], xv);
       } else {
-        // Dead lanes add nothing, whatever mean and rstd hold.
+        gv[0] = norm_ld(static_cast<const E*>(p.in[0]) + off[0] + int64_t(c) * gs);
+        xv[0] = norm_ld(static_cast<const E*>(p.in[1]) + off[1] + int64_t(c) * xs);
+      }
+    };
+    // One access's values stay in registers between the two walks.
+    float gk[VEC > 1 ? 1 : NI], xk[VEC > 1 ? 1 : NI];
+    if constexpr (VEC == 1) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) { gv[i][j] = 0.f; xh[i][j] = mean; }
+      for (int i = 0; i < NI; ++i) {
+        const uint32_t c = i * G + lane;
+        gk[i] = 0.f;
+        xk[i] = mean;
+        if (live && c < p.dim) load(i, c, &gk[i], &xk[i]);
       }
     }
     float sq = 0.f, sqx = 0.f;
@@ -280,16 +356,17 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
     for (int i = 0; i < NI; ++i) {
       const uint32_t c = (i * G + lane) * VEC;
       if (live && c < p.dim) {
-        float ga[VEC];
-        norm_affine<E, VEC>(p.gamma, p.gamma_stride, p.affine_vec, c, 1.f, ga);
+        float gv[VEC], xv[VEC];
+        if constexpr (VEC > 1) load(i, c, gv, xv);
+        else { gv[0] = gk[i]; xv[0] = xk[i]; }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          xh[i][j] = (xh[i][j] - mean) * rstd;
-          acc_b[i][j] += gv[i][j];
-          acc_g[i][j] = __fmaf_rn(gv[i][j], xh[i][j], acc_g[i][j]);
-          gv[i][j] *= ga[j];
-          sq += gv[i][j];
-          sqx = __fmaf_rn(gv[i][j], xh[i][j], sqx);
+          const float xh = (xv[j] - mean) * rstd;
+          acc_b[i][j] += gv[j];
+          acc_g[i][j] = __fmaf_rn(gv[j], xh, acc_g[i][j]);
+          const float q = gv[j] * gam[i][j];
+          sq += q;
+          sqx = __fmaf_rn(q, xh, sqx);
         }
       }
     }
@@ -302,18 +379,27 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
       for (int i = 0; i < NI; ++i) {
         const uint32_t c = (i * G + lane) * VEC;
         if (live && c < p.dim) {
-          float d[VEC];
+          float gv[VEC], xv[VEC];
+          if constexpr (VEC > 1) load(i, c, gv, xv);
+          else { gv[0] = gk[i]; xv[0] = xk[i]; }
 #pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            d[j] = rstd * __fmaf_rn(-xh[i][j], m2, gv[i][j] - m1);
-          norm_store<E, VEC>(o + int64_t(c) * os, d);
+          for (int j = 0; j < VEC; ++j) {
+            const float xh = (xv[j] - mean) * rstd;
+            xv[j] = rstd * __fmaf_rn(-xh, m2, gv[j] * gam[i][j] - m1);
+          }
+          norm_store<E, VEC>(o + int64_t(c) * os, xv);
         }
       }
     }
+    mean = mean_next;
+    rstd = rstd_next;
+    if (++stage == S) stage = 0;
+    if (++ahead == S) ahead = 0;
   }
   if (!p.partial) return;
   const uint32_t nw = p.want_gamma + p.want_beta;
   float* part = p.partial + uint64_t(blockIdx.x) * nw * p.dim;
+  float* s_col = reinterpret_cast<float*>(s_ring);  // [W]: the ring's copies are all in
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float(&acc)[NI][VEC] = k == 0 ? acc_g : acc_b;
@@ -328,6 +414,7 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
       }
     } else {
       // The row groups add into s_col one after another: a fixed order.
+      if constexpr (VEC > 1) asm volatile("cp.async.wait_all;\n" ::: "memory");
       for (int t = 0; t < RPB; ++t) {
         __syncthreads();
         if (int(grp) == t) {

@@ -30,10 +30,17 @@ struct NormPlan {
   // group == 0: rows longer than a block holds in registers.
   uint32_t group, ni;
   uint32_t n_cta;
+  uint32_t stages, smem;     // k_norm_bwd: ring stages (2 or 3), dynamic shared memory
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kNormBwdThreads = 128;     // row groups of 8 and 32 lanes
+// k_norm_bwd: CTAs per SM its registers allow without spills, by columns per
+// lane (element-wise access keeps the row in registers too).
+ZR_CX int norm_bwd_occ(int cols, int vec) {
+  return vec == 1 ? (cols > 16 ? 1 : (cols > 8 ? 2 : (cols > 4 ? 3 : 4)))
+                  : (cols > 16 ? 2 : (cols > 8 ? 3 : 4));
+}
+constexpr int kNormSmemMax = 224 * 1024; // k_norm_bwd's dynamic shared memory, all CTAs of an SM
 constexpr uint32_t kNormMaxCols = 32;    // columns per lane held in registers
 constexpr uint32_t kNormLongThreads = 1024;
 constexpr uint32_t kNormSumCols = 32;    // k_norm_sums: columns per CTA
@@ -43,9 +50,9 @@ constexpr uint32_t kNormSumCols = 32;    // k_norm_sums: columns per CTA
 // One list for the planner and the launchers (ZR_NORM_CASE(G, NI)).
 #define ZR_NORM_CASES(VEC_)                                                       \
   if constexpr (VEC_ == 1) {                                                      \
-    ZR_NORM_CASE(8, 4) ZR_NORM_CASE(8, 8)                                         \
-    ZR_NORM_CASE(32, 4) ZR_NORM_CASE(32, 8) ZR_NORM_CASE(32, 16) ZR_NORM_CASE(32, 32) \
-    ZR_NORM_CASE(256, 8) ZR_NORM_CASE(256, 16) ZR_NORM_CASE(256, 32)              \
+    ZR_NORM_CASE(8, 4) ZR_NORM_CASE(8, 8) ZR_NORM_CASE(32, 4) ZR_NORM_CASE(32, 8)  \
+    ZR_NORM_CASE(256, 2) ZR_NORM_CASE(256, 4) ZR_NORM_CASE(256, 8)                \
+    ZR_NORM_CASE(256, 16) ZR_NORM_CASE(256, 32)                                   \
   } else if constexpr (VEC_ == 4) {                                               \
     ZR_NORM_CASE(8, 1) ZR_NORM_CASE(8, 2)                                         \
     ZR_NORM_CASE(32, 1) ZR_NORM_CASE(32, 2) ZR_NORM_CASE(32, 4) ZR_NORM_CASE(32, 6) \
