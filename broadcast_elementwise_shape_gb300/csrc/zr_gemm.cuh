@@ -35,7 +35,9 @@ struct GemmCfg {
   static constexpr uint32_t kBBytes = 256 / CG * kGemmK * 2;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = CG == 1 ? 4 : 6;
-  static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;  // + alignment
+  // The ring, 4 KB of output staging per epilogue warp, alignment.
+  static constexpr uint32_t kOutAt = kStages * kStageBytes;
+  static constexpr uint32_t kSmem = kOutAt + 8 * 4096 + 1024;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -174,9 +176,8 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
         : "memory");
   }
 }
-// 32 columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tc_load32(uint32_t addr, float* v) {
-  uint32_t r[32];
+// 32 columns of this warp's 32 TMEM lanes; tc_wait_load() before their use.
+__device__ __forceinline__ void tc_load32_async(uint32_t addr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -187,9 +188,24 @@ __device__ __forceinline__ void tc_load32(uint32_t addr, float* v) {
         "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
+}
+__device__ __forceinline__ void tc_wait_load() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_load32(uint32_t addr, float* v) {
+  uint32_t r[32];
+  tc_load32_async(addr, r);
+  tc_wait_load();
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_load64(uint32_t addr, float* v) {
+  uint32_t r[64];
+  tc_load32_async(addr, r);
+  tc_load32_async(addr + 32, r + 32);
+  tc_wait_load();
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Shared-memory operand descriptor, 128-byte swizzle.  Both kinds of block
@@ -257,12 +273,46 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Where one epilogue warp's lane stands: row `row` (live: inside the product),
-// columns [c0, c1) of the tile, tile column 0 = column n0.
+// Where one epilogue warp's lane stands: row `row` (live: inside the product)
+// of the warp's 32 from row0, columns c0, c0 + 128, ... of the tile in chunks
+// of 64, tile column 0 = column n0.
 struct EpiPos {
-  uint32_t row, n0, c0, c1, tmem, nt, half;
+  uint32_t row, row0, n0, c0, tn, tmem, nt, half, lane;
+  uint32_t out;              // the warp's 4 KB of staging
   bool live, ok;
 };
+
+// 64 bfloat16 columns of the warp's 32 rows to global memory: each lane writes
+// its row into the staging (128-byte swizzle), one lane starts the TMA store.
+// 16-byte stores straight from the lanes touch 32 rows per instruction, half a
+// sector each; the gradient epilogue took 570 us with them on a [16384, 25088]
+// piece.
+__device__ __forceinline__ void epi_store(const CUtensorMap* map, const EpiPos& e, uint32_t c,
+                                          int part, float* v) {
+  // The staging's last store has been read.
+  if (e.lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+  const uint32_t base = e.out + e.lane * 128;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack_bf16(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + ((i ^ (e.lane & 7)) << 4)),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (e.lane == 0) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            map),
+        "r"(e.out), "r"(int(e.n0 + c)), "r"(int(e.row0)), "r"(part)
+        : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
 
 // Running maximum and sum of exponentials over the lane's columns, in one
 // walk: a chunk's maximum rescales the sum once.
@@ -271,7 +321,7 @@ __device__ __forceinline__ void epi_lse(const GemmPlan& p, const GemmProblem& q,
       e.live ? xent_label(p.labels, p.label_stride, p.label_i64, e.row) : int64_t(-1);
   const int64_t at = label - int64_t(e.n0);  // column of the label in this tile
   float m = -INFINITY, s = 0.f;
-  for (uint32_t c = e.c0; c < e.c1; c += 32) {
+  for (uint32_t c = e.c0; c < e.tn; c += c & 32 ? 96 : 32) {
     if (e.n0 + c >= q.n) break;
     float v[32];
     __syncwarp();
@@ -321,47 +371,55 @@ __device__ __forceinline__ void epi_grad(const GemmPlan& p, const GemmProblem& q
     lse2 = p.lse[e.row] * kLog2e;
     at = int64_t(lab) - p.label_base - int64_t(e.n0);
   }
-  for (uint32_t c = e.c0; c < e.c1; c += 32) {
+  for (uint32_t c = e.c0; c < e.tn; c += 128) {
     if (e.n0 + c >= q.n) break;
-    float v[32];
+    float v[64];
     __syncwarp();
-    tc_load32(e.tmem + c, v);
+    tc_load64(e.tmem + c, v);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = scale * ex2(__fmaf_rn(v[i], kLog2e, -lse2));
-    if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 32)) {
+    for (int i = 0; i < 64; ++i) v[i] = scale * ex2(__fmaf_rn(v[i], kLog2e, -lse2));
+    if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 64)) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < 64; ++i)
         if (at == int64_t(c) + i) v[i] -= scale;
     }
     if (out || !e.ok) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = e.ok ? 0.f : qnan();
+      for (int i = 0; i < 64; ++i) v[i] = e.ok ? 0.f : qnan();
     }
-    if (!e.live) continue;
-    // Rows of G are padded to a multiple of 64 columns: whole 16-byte stores.
-    uint16_t* g = p.g + int64_t(e.row) * p.ldg + e.n0 + c;
-    for (uint32_t part = 0; part < p.n_part; ++part, g += p.g_part) {
+    epi_store(&q.c, e, c, 0, v);
+    for (uint32_t part = 1; part < p.n_part; ++part) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (e.n0 + c + 8 * i >= q.n) break;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float& x = v[8 * i + 2 * j];
-          float& y = v[8 * i + 2 * j + 1];
-          w[j] = pack_bf16(x, y);
-          x -= __uint_as_float(w[j] << 16);
-          y -= __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-        *reinterpret_cast<uint4*>(g + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+      epi_store(&q.c, e, c, int(part), v);
     }
   }
 }
 
 __device__ __forceinline__ void epi_out(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
   const float scale = p.out_scale && !q.acc_out ? *p.out_scale : 1.f;
-  for (uint32_t c = e.c0; c < e.c1; c += 32) {
+  if (q.tma_out && !q.acc_out) {
+    for (uint32_t c = e.c0; c < e.tn; c += 128) {
+      if (e.n0 + c >= q.n) break;
+      float v[64];
+      __syncwarp();
+      tc_load64(e.tmem + c, v);
+      if (q.acc_in && e.live) {
+        const float* acc = q.acc + int64_t(e.row) * q.lda + e.n0 + c;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          if (e.n0 + c + i >= q.n) break;  // whole groups of 4: rows of acc are padded
+          const float4 o = *reinterpret_cast<const float4*>(acc + i);
+          v[i] += o.x; v[i + 1] += o.y; v[i + 2] += o.z; v[i + 3] += o.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = e.ok ? v[i] * scale : qnan();
+      epi_store(&q.c, e, c, 0, v);
+    }
+    return;
+  }
+  for (uint32_t c = e.c0; c < e.tn; c += c & 32 ? 96 : 32) {
     const uint32_t n = e.n0 + c;
     if (n >= q.n) break;
     float v[32];
@@ -452,14 +510,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;
+  GemmWalk walk = gemm_walk(p, blockIdx.x / CG);
   pdl_wait();
 
   if (warp == 8 && lane == 0) {
     // Producer: this CTA's rows of A and its share of B's columns.
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (uint32_t t = first; t < p.tiles && ok; t += step) {
+    for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
       const GemmTile g = gemm_tile(p, t);
       const GemmProblem& q = p.pr[g.prob];
       const uint32_t tnc = q.tn / CG;
@@ -501,7 +559,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     // Issuer.
     uint32_t stage = 0, phase = 0, it = 0;
     bool ok = true;
-    for (uint32_t t = first; t < p.tiles && ok; t += step, ++it) {
+    for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles; ++it) {
       const GemmTile g = gemm_tile(p, t);
       const GemmProblem& q = p.pr[g.prob];
       const uint32_t buf = it & 1;
@@ -530,7 +588,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     uint32_t it = 0;
     bool ok = true;
     const uint32_t quad = warp & 3, half = warp >> 2;
-    for (uint32_t t = first; t < p.tiles; t += step, ++it) {
+    for (uint32_t t; (t = gemm_next(p, &walk)) < p.tiles; ++it) {
       const GemmTile g = gemm_tile(p, t);
       const GemmProblem& q = p.pr[g.prob];
       const uint32_t buf = it & 1;
@@ -538,11 +596,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       ok = __all_sync(0xFFFFFFFFu, ok);
       tc_fence_after();
       EpiPos e;
-      e.row = (g.mt * CG + rank) * kGemmM + quad * 32 + lane;
+      e.row0 = (g.mt * CG + rank) * kGemmM + quad * 32;
+      e.row = e.row0 + lane;
+      e.lane = lane;
+      e.out = ring + Cfg::kOutAt + warp * 4096;
       e.live = e.row < q.m;
       e.n0 = g.nt * q.tn;
-      e.c0 = half * (q.tn / 2);
-      e.c1 = e.c0 + q.tn / 2;
+      e.c0 = half * 64;
+      e.tn = q.tn;
       e.tmem = tmem + (quad << 21) + buf * 256;
       e.nt = g.nt;
       e.half = half;
@@ -557,6 +618,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
         mbar_arrive_cluster(CG == 1 ? bar : cluster_addr(bar, 0));
       }
     }
+    // This warp's stores are complete.
+    if (EPI != kEpiLse && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncthreads();
   if (*abort) {

@@ -19,6 +19,10 @@ struct GemmProblem {
   uint32_t a_mn, b_mn;       // 1: MN-major
   uint32_t tn;               // tile width, a multiple of 64, <= 256
   uint32_t m_tiles, n_tiles, n_kb;  // n_kb: 64-wide k blocks
+  // Epilogues kEpiGrad and kEpiOut with tma_out: bfloat16 results leave through
+  // this map, in boxes of 64 columns by 32 rows.
+  CUtensorMap c;
+  uint32_t tma_out;
   // Epilogue kEpiOut: out = [acc_in +] product, in `es` bytes per element
   // with row stride ldo; or to the binary32 array acc when acc_out.
   void* out;
@@ -38,6 +42,8 @@ struct GemmPlan {
   uint32_t n_prob, n_combo;
   uint32_t tiles0, tiles;    // tiles of problem 0, of both
   uint32_t m_fast;           // consecutive tiles walk m first
+  // Two problems' tiles over `workers` clusters (GemmWalk).
+  uint32_t workers, head, extra, late_first;
   uint32_t es;               // kEpiOut: bytes per output element
   const float* out_scale;    // kEpiOut: multiplies the finished product, or null (1)
   // kEpiLse
@@ -51,10 +57,48 @@ struct GemmPlan {
   const float* scale;        // [m]
   const int32_t* label32;    // [m], -1: the row is left out
   int64_t label_base;        // column 0 of this product is this label
-  uint16_t* g;               // [n_part][m][ldg]
-  int64_t ldg, g_part;
-  uint32_t n_part;
+  uint32_t n_part;           // parts of G, stored through pr[0].c
 };
+
+// The tiles of worker w, in order: its share of problem 0 round-robin, then of
+// problem 1.  Problem 0's tiles may not divide evenly: the first `head`
+// workers then have one more than the rest, which take `extra` tiles of
+// problem 1 meanwhile (about as long as one of problem 0), before all walk the
+// remaining ones round-robin, those that are ahead first.  Tiles that run at
+// the same time are neighbours throughout, so they share operands in L2.
+struct GemmWalk {
+  uint32_t w, n0, j;
+};
+#if defined(__CUDACC__)
+#define ZR_GEMM_HD __host__ __device__ __forceinline__
+#else
+#define ZR_GEMM_HD inline
+#endif
+ZR_GEMM_HD GemmWalk gemm_walk(const GemmPlan& p, uint32_t w) {
+  GemmWalk g;
+  g.w = w;
+  g.n0 = w < p.tiles0 ? (p.tiles0 - w - 1) / p.workers + 1 : 0;
+  g.j = 0;
+  return g;
+}
+// The next tile, or p.tiles when there is none.
+ZR_GEMM_HD uint32_t gemm_next(const GemmPlan& p, GemmWalk* g) {
+  const uint32_t j = g->j++;
+  if (j < g->n0) return g->w + j * p.workers;
+  uint32_t k = j - g->n0;                     // k-th tile of problem 1
+  const uint32_t rest = p.workers - p.head;   // workers with one tile fewer
+  uint32_t l;
+  if (g->w >= p.head && k < p.extra) {
+    l = k * rest + (g->w - p.head);
+  } else {
+    if (g->w >= p.head) k -= p.extra;
+    uint32_t at = g->w;
+    if (p.late_first) at = at >= p.head ? at - p.head : at + rest;
+    l = p.extra * rest + k * p.workers + at;
+  }
+  const uint32_t t = p.tiles0 + l;
+  return t < p.tiles ? t : p.tiles;
+}
 
 // grid: CTAs (a multiple of cg); cg: CTAs per cluster, 1 or 2.
 cudaError_t launch_gemm(int epi, int cg, const GemmPlan& p, unsigned grid, cudaStream_t s);

@@ -441,8 +441,18 @@ const char* operand_base(const Operand& o, const char* ws) {
 // CTAs per cluster: pairs when there is more than one CTA's rows.
 int pick_cg(int64_t m) { return m > 128 ? kGemmCg : 1; }
 
-unsigned gemm_grid(const GemmPlan& g, int cg) {
-  return unsigned(std::min<uint32_t>(g.tiles, kSms / cg) * cg);
+// The grid, and how two problems' tiles are dealt out (GemmWalk).
+unsigned gemm_grid(GemmPlan* g, int cg) {
+  const uint32_t W = std::min<uint32_t>(g->tiles, kSms / cg);
+  g->workers = W;
+  g->head = g->n_prob > 1 ? g->tiles0 % W : 0;
+  g->extra = g->late_first = 0;
+  if (g->head) {
+    const uint32_t k0 = g->pr[0].n_kb * g->pr[0].tn, k1 = g->pr[1].n_kb * g->pr[1].tn;
+    g->extra = (k0 + k1 / 2) / k1;
+    g->late_first = uint64_t(g->extra) * k1 < k0;
+  }
+  return unsigned(W * cg);
 }
 
 void set_tiles(GemmProblem* q, int cg) {
@@ -492,7 +502,7 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
   g.label_i64 = r.label_i64;
   g.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
   g.at = reinterpret_cast<float*>(ws + S.ws_at);
-  if ((e = launch_gemm(kEpiLse, cg, g, gemm_grid(g, cg), s)) != cudaSuccess) return cuda_status(e);
+  if ((e = launch_gemm(kEpiLse, cg, g, gemm_grid(&g, cg), s)) != cudaSuccess) return cuda_status(e);
   if (r.n <= kRowsOneBlock)
     return cuda_status(launch_k(k_xent_rows<true>, 1, kRowsThreads, 0, s, r));
   const unsigned blocks = (r.n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
@@ -529,11 +539,10 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     g.scale = r.scale;
     g.label32 = r.label32;
     g.label_base = v0;
-    g.g = G;
-    g.ldg = ldg;
-    g.g_part = N * ldg;
     g.n_part = S.parts;
-    if ((e = launch_gemm(kEpiGrad, cg, g, gemm_grid(g, cg), s)) != cudaSuccess) return cuda_status(e);
+    if ((e = make_map(&g.pr[0].c, G, n, N, ldg, S.parts, N * ldg, 32)) != cudaSuccess)
+      return cuda_status(e);
+    if ((e = launch_gemm(kEpiGrad, cg, g, gemm_grid(&g, cg), s)) != cudaSuccess) return cuda_status(e);
 
     cg = pick_cg(std::min(N, n));
     GemmPlan o = {};
@@ -557,6 +566,9 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.acc_in = k > 0;
       q.acc_out = k + 1 < S.n_piece;
       q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(grad_x) % 16 == 0;
+      q.tma_out = q.vec && S.es == 2;
+      if (q.tma_out && (e = make_map(&q.c, grad_x, D, N, D, 1, 0, 32)) != cudaSuccess)
+        return cuda_status(e);
       if ((e = make_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 128)) != cudaSuccess)
         return cuda_status(e);
       if ((e = make_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, D, n, S.w.pitch, S.parts,
@@ -576,6 +588,9 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.out = static_cast<char*>(grad_w) + v0 * D * S.es;
       q.ldo = D;
       q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0;
+      q.tma_out = q.vec && S.es == 2;
+      if (q.tma_out && (e = make_map(&q.c, q.out, D, n, D, 1, 0, 32)) != cudaSuccess)
+        return cuda_status(e);
       if ((e = make_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 64)) != cudaSuccess)
         return cuda_status(e);
       if ((e = make_map(&q.b, operand_base(S.x, ws), D, N, S.x.pitch, S.parts,
@@ -585,7 +600,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     o.tiles0 = o.pr[0].m_tiles * o.pr[0].n_tiles;
     o.tiles = o.tiles0 + (o.n_prob > 1 ? o.pr[1].m_tiles * o.pr[1].n_tiles : 0);
     o.m_fast = 0;
-    if ((e = launch_gemm(kEpiOut, cg, o, gemm_grid(o, cg), s)) != cudaSuccess) return cuda_status(e);
+    if ((e = launch_gemm(kEpiOut, cg, o, gemm_grid(&o, cg), s)) != cudaSuccess) return cuda_status(e);
   }
   return ZR_OK;
 }
