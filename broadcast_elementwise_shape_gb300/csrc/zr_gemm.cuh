@@ -260,6 +260,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The same with subnormal results kept: the gradient of a class that is all
+// but impossible is as exact as any other.
+__device__ __forceinline__ float ex2_full(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float qnan() { return __uint_as_float(0x7FFFFFFFu); }
 
 __device__ __forceinline__ int64_t xent_label(const void* labels, int64_t stride, uint32_t i64,
@@ -277,7 +284,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // of the warp's 32 from row0, columns c0, c0 + 128, ... of the tile in chunks
 // of 64, tile column 0 = column n0.
 struct EpiPos {
-  uint32_t row, row0, n0, c0, tn, tmem, nt, half, lane;
+  uint32_t row, row0, n0, c0, tn, nt, half, lane;
   uint32_t out;              // the warp's 4 KB of staging
   bool live, ok;
 };
@@ -316,42 +323,47 @@ __device__ __forceinline__ void epi_store(const CUtensorMap* map, const EpiPos& 
 
 // Running maximum and sum of exponentials over the lane's columns, in one
 // walk: a chunk's maximum rescales the sum once.
-__device__ __forceinline__ void epi_lse(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
-  const int64_t label =
-      e.live ? xent_label(p.labels, p.label_stride, p.label_i64, e.row) : int64_t(-1);
-  const int64_t at = label - int64_t(e.n0);  // column of the label in this tile
-  float m = -INFINITY, s = 0.f;
-  for (uint32_t c = e.c0; c < e.tn; c += c & 32 ? 96 : 32) {
-    if (e.n0 + c >= q.n) break;
-    float v[32];
-    __syncwarp();
-    tc_load32(e.tmem + c, v);
-    if (e.n0 + c + 32 > q.n) {
+struct EpiLse {
+  int64_t at;                // column of the label in this tile
+  float m, s;
+
+  __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem&, const EpiPos& e) {
+    const int64_t label =
+        e.live ? xent_label(p.labels, p.label_stride, p.label_i64, e.row) : int64_t(-1);
+    at = e.live ? label - int64_t(e.n0) : int64_t(-1);
+    m = -INFINITY;
+    s = 0.f;
+  }
+  __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
+                                        uint32_t c, float* v) {
+    if (e.n0 + c + 64 > q.n) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < 64; ++i)
         if (e.n0 + c + i >= q.n) v[i] = -INFINITY;
     }
-    if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 32 && e.live)) {
+    if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 64)) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (e.live && at == int64_t(c) + i) p.at[e.row] = e.ok ? v[i] : qnan();
+      for (int i = 0; i < 64; ++i)
+        if (at == int64_t(c) + i) p.at[e.row] = e.ok ? v[i] : qnan();
     }
-    float top = v[0];
+    float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-    const float mn = fmaxf(m, top);
+    for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+    const float mn = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
     const float ms = mn == -INFINITY ? 0.f : mn * kLog2e;
     s *= ex2(__fmaf_rn(m, kLog2e, -ms));
     float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) add[i & 3] += ex2(__fmaf_rn(v[i], kLog2e, -ms));
+    for (int i = 0; i < 64; ++i) add[i & 3] += ex2(__fmaf_rn(v[i], kLog2e, -ms));
     s += (add[0] + add[1]) + (add[2] + add[3]);
     m = mn;
   }
-  if (e.live)
-    p.partial[uint64_t(e.row) * (2 * q.n_tiles) + 2 * e.nt + e.half] =
-        e.ok ? make_float2(m, s) : make_float2(0.f, qnan());
-}
+  __device__ __forceinline__ void end(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
+    if (e.live)
+      p.partial[uint64_t(e.row) * (2 * q.n_tiles) + 2 * e.nt + e.half] =
+          e.ok ? make_float2(m, s) : make_float2(0.f, qnan());
+  }
+};
 
 // G = scale * (exp(l - lse) - [column is the label]).  G is the operand of
 // the two gradient products, so it is stored as their operand type: rounded
@@ -360,24 +372,27 @@ __device__ __forceinline__ void epi_lse(const GemmPlan& p, const GemmProblem& q,
 // tensors, as three bfloat16 parts that hold it to 2^-24.  A factor that all
 // rows share is left to the products' epilogue: then the label's element of a
 // row that is not yet learnt, the largest by far, is -1 and rounds to itself.
-__device__ __forceinline__ void epi_grad(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
-  float scale = 0.f, lse2 = 0.f;
-  int64_t at = -1;
-  bool out = true;  // the row is left out: zeros, whatever its products are
-  if (e.live) {
-    const int32_t lab = p.label32[e.row];
-    out = lab == -1;
-    scale = p.scale[e.row];
-    lse2 = p.lse[e.row] * kLog2e;
-    at = int64_t(lab) - p.label_base - int64_t(e.n0);
+struct EpiGrad {
+  float scale, lse2;
+  int64_t at;
+  bool out;                  // the row is left out: zeros, whatever its products are
+
+  __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem&, const EpiPos& e) {
+    scale = lse2 = 0.f;
+    at = -1;
+    out = true;
+    if (e.live) {
+      const int32_t lab = p.label32[e.row];
+      out = lab == -1;
+      scale = p.scale[e.row];
+      lse2 = p.lse[e.row] * kLog2e;
+      at = int64_t(lab) - p.label_base - int64_t(e.n0);
+    }
   }
-  for (uint32_t c = e.c0; c < e.tn; c += 128) {
-    if (e.n0 + c >= q.n) break;
-    float v[64];
-    __syncwarp();
-    tc_load64(e.tmem + c, v);
+  __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
+                                        uint32_t c, float* v) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = scale * ex2(__fmaf_rn(v[i], kLog2e, -lse2));
+    for (int i = 0; i < 64; ++i) v[i] = scale * ex2_full(__fmaf_rn(v[i], kLog2e, -lse2));
     if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 64)) {
 #pragma unroll
       for (int i = 0; i < 64; ++i)
@@ -394,65 +409,51 @@ __device__ __forceinline__ void epi_grad(const GemmPlan& p, const GemmProblem& q
       epi_store(&q.c, e, c, int(part), v);
     }
   }
-}
+  __device__ __forceinline__ void end(const GemmPlan&, const GemmProblem&, const EpiPos&) {}
+};
 
-__device__ __forceinline__ void epi_out(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
-  const float scale = p.out_scale && !q.acc_out ? *p.out_scale : 1.f;
-  if (q.tma_out && !q.acc_out) {
-    for (uint32_t c = e.c0; c < e.tn; c += 128) {
-      if (e.n0 + c >= q.n) break;
-      float v[64];
-      __syncwarp();
-      tc_load64(e.tmem + c, v);
-      if (q.acc_in && e.live) {
-        const float* acc = q.acc + int64_t(e.row) * q.lda + e.n0 + c;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          if (e.n0 + c + i >= q.n) break;  // whole groups of 4: rows of acc are padded
-          const float4 o = *reinterpret_cast<const float4*>(acc + i);
-          v[i] += o.x; v[i + 1] += o.y; v[i + 2] += o.z; v[i + 3] += o.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = e.ok ? v[i] * scale : qnan();
-      epi_store(&q.c, e, c, 0, v);
-    }
-    return;
+struct EpiOut {
+  float scale;
+
+  __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem& q, const EpiPos&) {
+    scale = p.out_scale && !q.acc_out ? *p.out_scale : 1.f;
   }
-  for (uint32_t c = e.c0; c < e.tn; c += c & 32 ? 96 : 32) {
+  __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
+                                        uint32_t c, float* v) {
     const uint32_t n = e.n0 + c;
-    if (n >= q.n) break;
-    float v[32];
-    __syncwarp();
-    tc_load32(e.tmem + c, v);
-    if (!e.ok) {
+    float* acc = q.acc + int64_t(e.row) * q.lda + n;  // rows of acc are padded to groups of 4
+    if (q.acc_in && e.live) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = qnan();
-    }
-    if (!e.live) continue;
-    const bool whole = q.vec && n + 32 <= q.n;
-    float* acc = q.acc + int64_t(e.row) * q.lda + n;
-    if (q.acc_in) {
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        if (whole) {
+      for (int i = 0; i < 64; i += 4) {
+        if (n + i < q.n) {
           const float4 o = *reinterpret_cast<const float4*>(acc + i);
           v[i] += o.x; v[i + 1] += o.y; v[i + 2] += o.z; v[i + 3] += o.w;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (n + i + j < q.n) v[i + j] += acc[i + j];
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= scale;
-    if (q.acc_out || p.es == 4) {
-      float* o = q.acc_out ? acc : static_cast<float*>(q.out) + int64_t(e.row) * q.ldo + n;
+    for (int i = 0; i < 64; ++i) v[i] = e.ok ? v[i] * scale : qnan();
+    if (q.acc_out) {
+      if (e.live) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        if (whole) {
-          *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        for (int i = 0; i < 64; i += 4)
+          if (n + i < q.n)
+            *reinterpret_cast<float4*>(acc + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+      return;
+    }
+    if (q.tma_out) {
+      epi_store(&q.c, e, c, 0, v);
+      return;
+    }
+    if (!e.live) return;
+    if (p.es == 4) {
+      float* o = static_cast<float*>(q.out) + int64_t(e.row) * q.ldo + n;
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        if (q.vec) {
+          if (n + i < q.n)
+            *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -462,24 +463,29 @@ __device__ __forceinline__ void epi_out(const GemmPlan& p, const GemmProblem& q,
     } else {
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(q.out) + int64_t(e.row) * q.ldo + n;
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        if (whole) {
-          *reinterpret_cast<uint4*>(o + i) =
-              make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
-                         pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (n + i + j < q.n) o[i + j] = __float2bfloat16_rn(v[i + j]);
-        }
-      }
+      for (int i = 0; i < 64; ++i)
+        if (n + i < q.n) o[i] = __float2bfloat16_rn(v[i]);
     }
   }
-}
+  __device__ __forceinline__ void end(const GemmPlan&, const GemmProblem&, const EpiPos&) {}
+};
+
+template <int EPI>
+struct EpiOf { using type = EpiLse; };
+template <>
+struct EpiOf<kEpiGrad> { using type = EpiGrad; };
+template <>
+struct EpiOf<kEpiOut> { using type = EpiOut; };
 
 // ------------------------------------------------------------------ kernel
 
-template <int EPI, int CG>
+// SUM: the accumulator covers only q.chunk blocks of k, and the epilogue warps
+// add the chunks in registers, rounding to nearest.  The tensor core's own
+// accumulation truncates: sums of positive terms fell short by 1.2 to 1.4 times
+// 2^-24 of their size per 16 terms (7.1e-5 at k = 16384), always towards zero.
+// Results of 24 bits need the chunks; those of 8 bits do without until k is
+// some hundred thousand.
+template <int EPI, int CG, bool SUM>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant__ GemmPlan p) {
   using Cfg = GemmCfg<CG>;
   constexpr int S = Cfg::kStages;
@@ -524,10 +530,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       const int m0 = int((g.mt * CG + rank) * kGemmM);
       const int n0 = int(g.nt * q.tn + rank * tnc);
       const uint32_t nb = q.b_mn ? (tnc + 63) / 64 * 8192 : tnc * 128;
+      for (uint32_t k1 = 0; k1 < q.n_kb && ok; k1 += q.chunk)
       for (uint32_t c = 0; c < p.n_combo && ok; ++c) {
         int pa, pb;
         gemm_combo(p.n_combo, c, &pa, &pb);
-        for (uint32_t kb = 0; kb < q.n_kb; ++kb) {
+        const uint32_t k2 = k1 + q.chunk < q.n_kb ? k1 + q.chunk : q.n_kb;
+        for (uint32_t kb = k1; kb < k2; ++kb) {
           if (!mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort)) { ok = false; break; }
           const uint32_t local = smem_u32(&s_full[stage]);
           if (rank == 0) mbar_expect(local, (kABytes + nb) * CG);
@@ -559,42 +567,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     // Issuer.
     uint32_t stage = 0, phase = 0, it = 0;
     bool ok = true;
-    for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles; ++it) {
+    for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
       const GemmTile g = gemm_tile(p, t);
       const GemmProblem& q = p.pr[g.prob];
-      const uint32_t buf = it & 1;
       // D binary32, A and B bfloat16, their majors, N / 8, M / 16.
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (q.a_mn << 15) | (q.b_mn << 16) |
                              ((q.tn >> 3) << 17) | (uint32_t(kGemmM * CG / 16) << 24);
       const uint32_t ka = q.a_mn ? 2048 >> 4 : 32 >> 4, kb16 = q.b_mn ? 2048 >> 4 : 32 >> 4;
-      if (!mbar_wait(smem_u32(&s_tempty[buf]), ((it >> 1) & 1) ^ 1, abort)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * 256;
-      const uint32_t nk = q.n_kb * p.n_combo;
-      for (uint32_t kb = 0; kb < nk; ++kb) {
-        if (!mbar_wait(smem_u32(&s_full[stage]), phase, abort)) { ok = false; break; }
+      for (uint32_t k1 = 0; k1 < q.n_kb && ok; k1 += q.chunk, ++it) {
+        const uint32_t buf = it & 1;
+        if (!mbar_wait(smem_u32(&s_tempty[buf]), ((it >> 1) & 1) ^ 1, abort)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t sa = ring + stage * Cfg::kStageBytes;
-        const uint64_t da = operand_desc(sa, q.a_mn), db = operand_desc(sa + kABytes, q.b_mn);
+        const uint32_t d = tmem + buf * 256;
+        const uint32_t nk = (q.n_kb - k1 < q.chunk ? q.n_kb - k1 : q.chunk) * p.n_combo;
+        for (uint32_t kb = 0; kb < nk; ++kb) {
+          if (!mbar_wait(smem_u32(&s_full[stage]), phase, abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = ring + stage * Cfg::kStageBytes;
+          const uint64_t da = operand_desc(sa, q.a_mn), db = operand_desc(sa + kABytes, q.b_mn);
 #pragma unroll
-        for (uint32_t j = 0; j < kGemmK / 16; ++j)
-          tc_mma<CG>(d, da + j * ka, db + j * kb16, idesc, (kb | j) != 0);
-        tc_commit<CG>(smem_u32(&s_empty[stage]));
-        if (++stage == S) { stage = 0; phase ^= 1; }
+          for (uint32_t j = 0; j < kGemmK / 16; ++j)
+            tc_mma<CG>(d, da + j * ka, db + j * kb16, idesc, (kb | j) != 0);
+          tc_commit<CG>(smem_u32(&s_empty[stage]));
+          if (++stage == S) { stage = 0; phase ^= 1; }
+        }
+        if (ok) tc_commit<CG>(smem_u32(&s_tfull[buf]));
       }
-      if (ok) tc_commit<CG>(smem_u32(&s_tfull[buf]));
     }
   } else if (warp < 8) {
     uint32_t it = 0;
     bool ok = true;
     const uint32_t quad = warp & 3, half = warp >> 2;
-    for (uint32_t t; (t = gemm_next(p, &walk)) < p.tiles; ++it) {
+    for (uint32_t t; (t = gemm_next(p, &walk)) < p.tiles;) {
       const GemmTile g = gemm_tile(p, t);
       const GemmProblem& q = p.pr[g.prob];
-      const uint32_t buf = it & 1;
-      ok = ok && mbar_wait(smem_u32(&s_tfull[buf]), (it >> 1) & 1, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tc_fence_after();
       EpiPos e;
       e.row0 = (g.mt * CG + rank) * kGemmM + quad * 32;
       e.row = e.row0 + lane;
@@ -604,19 +610,64 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       e.n0 = g.nt * q.tn;
       e.c0 = half * 64;
       e.tn = q.tn;
-      e.tmem = tmem + (quad << 21) + buf * 256;
       e.nt = g.nt;
       e.half = half;
-      e.ok = ok;
-      if constexpr (EPI == kEpiLse) epi_lse(p, q, e);
-      else if constexpr (EPI == kEpiGrad) epi_grad(p, q, e);
-      else epi_out(p, q, e);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&s_tempty[buf]);
-        mbar_arrive_cluster(CG == 1 ? bar : cluster_addr(bar, 0));
+      typename EpiOf<EPI>::type epi;
+      epi.begin(p, q, e);
+      auto acquire = [&]() {
+        const uint32_t buf = it & 1;
+        ok = ok && mbar_wait(smem_u32(&s_tfull[buf]), (it >> 1) & 1, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+        e.ok = ok;
+        return tmem + (quad << 21) + buf * 256;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&s_tempty[it & 1]);
+          mbar_arrive_cluster(CG == 1 ? bar : cluster_addr(bar, 0));
+        }
+        ++it;
+      };
+      if constexpr (!SUM) {
+        const uint32_t d = acquire();
+        for (uint32_t c = e.c0; c < e.tn; c += 128) {
+          if (e.n0 + c >= q.n) break;
+          float v[64];
+          __syncwarp();
+          tc_load64(d + c, v);
+          epi.chunk(p, q, e, c, v);
+        }
+        release();
+      } else {
+        float v[2][64];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i / 64][i % 64] = 0.f;
+        for (uint32_t k1 = 0; k1 < q.n_kb; k1 += q.chunk) {
+          const uint32_t d = acquire();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t c = e.c0 + (j / 2) * 128 + (j & 1) * 32;
+            if (c < e.tn) {
+              float w[32];
+              __syncwarp();
+              tc_load32(d + c, w);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[j / 2][(j & 1) * 32 + i] += w[i];
+            }
+          }
+          release();
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t c = e.c0 + j * 128;
+          __syncwarp();
+          if (c < e.tn && e.n0 + c < q.n) epi.chunk(p, q, e, c, v[j]);
+        }
       }
+      epi.end(p, q, e);
     }
     // This warp's stores are complete.
     if (EPI != kEpiLse && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

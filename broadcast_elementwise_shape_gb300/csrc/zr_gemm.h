@@ -19,6 +19,7 @@ struct GemmProblem {
   uint32_t a_mn, b_mn;       // 1: MN-major
   uint32_t tn;               // tile width, a multiple of 64, <= 256
   uint32_t m_tiles, n_tiles, n_kb;  // n_kb: 64-wide k blocks
+  uint32_t chunk;            // k blocks per accumulation in TMEM
   // Epilogues kEpiGrad and kEpiOut with tma_out: bfloat16 results leave through
   // this map, in boxes of 64 columns by 32 rows.
   CUtensorMap c;
@@ -100,7 +101,8 @@ ZR_GEMM_HD uint32_t gemm_next(const GemmPlan& p, GemmWalk* g) {
   return t < p.tiles ? t : p.tiles;
 }
 
-// grid: CTAs (a multiple of cg); cg: CTAs per cluster, 1 or 2.
-cudaError_t launch_gemm(int epi, int cg, const GemmPlan& p, unsigned grid, cudaStream_t s);
+// grid: CTAs (a multiple of cg); cg: CTAs per cluster, 1 or 2.  sum: chunks of
+// k are added in registers (else every problem's chunk is its whole k).
+cudaError_t launch_gemm(int epi, int cg, bool sum, const GemmPlan& p, unsigned grid, cudaStream_t s);
 
 }  // namespace zr

@@ -5,26 +5,32 @@
 namespace zr {
 namespace {
 
-template <int EPI, int CG>
+template <int EPI, int CG, bool SUM>
 cudaError_t go(const GemmPlan& p, unsigned grid, cudaStream_t s) {
-  auto* k = k_gemm<EPI, CG>;
+  auto* k = k_gemm<EPI, CG, SUM>;
   const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), int(GemmCfg<CG>::kSmem));
   if (e != cudaSuccess) return e;
   if (CG == 1) return launch_k(k, grid, kGemmThreads, GemmCfg<CG>::kSmem, s, p);
   return launch_k_cluster(k, grid, kGemmThreads, GemmCfg<CG>::kSmem, s, CG, p);
 }
 
+template <int EPI>
+cudaError_t pick(int cg, bool sum, const GemmPlan& p, unsigned grid, cudaStream_t s) {
+  if (cg == 1) return sum ? go<EPI, 1, true>(p, grid, s) : go<EPI, 1, false>(p, grid, s);
+  return sum ? go<EPI, 2, true>(p, grid, s) : go<EPI, 2, false>(p, grid, s);
+}
+
 }  // namespace
 
-cudaError_t launch_gemm(int epi, int cg, const GemmPlan& p, unsigned grid, cudaStream_t s) {
+cudaError_t launch_gemm(int epi, int cg, bool sum, const GemmPlan& p, unsigned grid,
+                        cudaStream_t s) {
   if (grid == 0 || (cg != 1 && cg != 2) || grid % unsigned(cg) != 0) return cudaErrorInvalidValue;
-  switch (epi * 2 + cg - 1) {
-    case kEpiLse * 2: return go<kEpiLse, 1>(p, grid, s);
-    case kEpiLse * 2 + 1: return go<kEpiLse, 2>(p, grid, s);
-    case kEpiGrad * 2: return go<kEpiGrad, 1>(p, grid, s);
-    case kEpiGrad * 2 + 1: return go<kEpiGrad, 2>(p, grid, s);
-    case kEpiOut * 2: return go<kEpiOut, 1>(p, grid, s);
-    case kEpiOut * 2 + 1: return go<kEpiOut, 2>(p, grid, s);
+  for (uint32_t i = 0; i < p.n_prob; ++i)
+    if (p.pr[i].chunk == 0 || (!sum && p.pr[i].chunk < p.pr[i].n_kb)) return cudaErrorInvalidValue;
+  switch (epi) {
+    case kEpiLse: return pick<kEpiLse>(cg, sum, p, grid, s);
+    case kEpiGrad: return pick<kEpiGrad>(cg, sum, p, grid, s);
+    case kEpiOut: return pick<kEpiOut>(cg, sum, p, grid, s);
   }
   return cudaErrorInvalidValue;
 }

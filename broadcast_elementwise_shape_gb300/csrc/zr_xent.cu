@@ -232,6 +232,158 @@ __global__ void __launch_bounds__(kRowsThreads) k_xent_total(const __grid_consta
   xent_total(p, s_cnt, s_sum);
 }
 
+// ------------------------------------------------------------------ few rows
+
+// Forward for at most kFewRows rows of x (generation, scoring): bound by
+// reading w once.  A warp takes four rows of w at a time, its lanes 16 bytes
+// each, all of them in flight before the first is used; x waits in shared
+// memory as binary32, and so does the arithmetic run on either storage.  A
+// warp keeps a running maximum and sum per row of x, a block joins its warps'
+// in order.  The tensor-core path reads w in tiles of 256 rows, too few to
+// fill the GPU evenly, and every one of its 128-row blocks of x is padding but
+// for a few rows.
+struct FewPlan {
+  const void* x;             // packed or as given: rows of pitch xp
+  const void* w;
+  int64_t xp, wp;
+  uint32_t n, vocab, dim;
+  const void* labels;
+  int64_t label_stride;
+  uint32_t label_i64;
+  float2* partial;           // [n][gridDim.x]
+  float* at;
+};
+constexpr uint32_t kFewRows = 4;
+constexpr uint32_t kFewMaxDim = 12288;  // x in shared memory: 4 rows of it as binary32
+constexpr int kFewBlocks = 2;           // CTAs per SM
+
+template <typename E, int NT>
+__global__ void __launch_bounds__(kThreads, kFewBlocks) k_xent_few(const __grid_constant__ FewPlan p) {
+  pdl_trigger();
+  constexpr int V = 16 / sizeof(E);    // elements per access
+  constexpr int R = 4;                 // rows of w at a time
+  constexpr int U = 3;                 // accesses per row in flight
+  extern __shared__ float s_x[];       // [NT][dim padded to 32 V]
+  __shared__ float2 s_part[kThreads / 32][NT];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t padded = (p.dim + 32 * V - 1) / (32 * V) * (32 * V);
+  pdl_wait();
+  for (uint32_t i = threadIdx.x; i < NT * padded; i += kThreads) {
+    const uint32_t t = i / padded, c = i - t * padded;
+    s_x[i] = t < p.n && c < p.dim
+                 ? ld1(static_cast<const E*>(p.x) + int64_t(t) * p.xp + c, false) : 0.f;
+  }
+  __syncthreads();
+  int64_t label[NT];
+  float m[NT], s[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = -INFINITY;
+    s[t] = 0.f;
+    label[t] = -1;
+    if (t < int(p.n))
+      label[t] = p.label_i64
+                     ? static_cast<const int64_t*>(p.labels)[int64_t(t) * p.label_stride]
+                     : int64_t(static_cast<const int32_t*>(p.labels)[int64_t(t) * p.label_stride]);
+  }
+  const uint32_t steps = padded / (32 * V);
+  const uint32_t groups = (p.vocab + R - 1) / R;
+  for (uint32_t g = blockIdx.x * (kThreads / 32) + warp; g < groups; g += gridDim.x * (kThreads / 32)) {
+    const uint32_t v0 = g * R;
+    const E* row[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)  // past the end: the last row again, left out below
+      row[r] = static_cast<const E*>(p.w) + int64_t(v0 + r < p.vocab ? v0 + r : p.vocab - 1) * p.wp;
+    float acc[R][NT];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[r][t] = 0.f;
+    for (uint32_t k = 0; k < steps; k += U) {
+      uint4 q[U][R];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t c = ((k + u) * 32 + lane) * V;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          q[u][r] = make_uint4(0, 0, 0, 0);
+          if (c + V <= p.dim) {
+            q[u][r] = __ldg(reinterpret_cast<const uint4*>(row[r] + c));
+          } else if (c < p.dim) {
+            E tail[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) tail[j] = c + j < p.dim ? row[r][c + j] : E(0.f);
+            q[u][r] = *reinterpret_cast<const uint4*>(tail);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k + u >= steps) break;
+        const uint32_t c = ((k + u) * 32 + lane) * V;
+        float xv[NT][V];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < V; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&s_x[t * padded + c + j]);
+            xv[t][j] = f.x; xv[t][j + 1] = f.y; xv[t][j + 2] = f.z; xv[t][j + 3] = f.w;
+          }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t w[4] = {q[u][r].x, q[u][r].y, q[u][r].z, q[u][r].w};
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            float f;
+            if constexpr (sizeof(E) == 4) f = __uint_as_float(w[j]);
+            else f = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[r][t] = __fmaf_rn(f, xv[t][j], acc[r][t]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float l[R];
+      float top = m[t];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        l[r] = warp_sum(acc[r][t]);
+        if (v0 + r < p.vocab) {
+          if (lane == 0 && int64_t(v0 + r) == label[t]) p.at[t] = l[r];
+        } else {
+          l[r] = -INFINITY;
+        }
+        top = fmaxf(top, l[r]);
+      }
+      // Every lane keeps the same running pair.
+      const float base = top == -INFINITY ? 0.f : top;
+      float add = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) add += __expf(l[r] - base);
+      s[t] = __fmaf_rn(s[t], __expf(m[t] - base), add);
+      m[t] = top;
+    }
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s_part[warp][t] = make_float2(m[t], s[t]);
+  __syncthreads();
+  if (threadIdx.x < NT && threadIdx.x < p.n) {
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, s_part[w][threadIdx.x].x);
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const float2 v = s_part[w][threadIdx.x];
+      sum = __fmaf_rn(v.y, expf(v.x - base), sum);
+    }
+    p.partial[uint64_t(threadIdx.x) * gridDim.x + blockIdx.x] = make_float2(top, sum);
+  }
+}
+
 // ------------------------------------------------------------------ plan
 
 // Workspace regions start 256-byte aligned.
@@ -245,6 +397,8 @@ size_t take(size_t* at, size_t bytes) {
 struct Operand {
   TDesc t;
   int64_t rows = 0, cols = 0;
+  bool one_step = false;     // unit stride along a row, one stride between rows
+  int64_t row_step = 0;
   bool pack = false;
   int64_t pitch = 0;         // elements between rows, once packed or as given
   size_t ws = 0;             // offset of the packed copy
@@ -258,6 +412,7 @@ struct XentSet {
   int es = 4;
   uint32_t parts = 1, combos = 1;
   bool empty = false;        // no rows
+  bool few = false;          // forward by k_xent_few
   Operand x, w;
   TDesc labels;
   XentRows rows;
@@ -268,6 +423,10 @@ struct XentSet {
   size_t ws_scale = 0, ws_common = 0, ws_label = 0, ws_g = 0, ws_acc = 0;
   int64_t piece = 0, n_piece = 0;
 };
+
+uint32_t few_grid(int64_t vocab) {
+  return uint32_t(std::min<int64_t>(kSms * kFewBlocks, (vocab + 31) / 32));
+}
 
 uint32_t tile_width(int64_t n) {
   const int64_t t = (n + 255) / 256;
@@ -287,6 +446,8 @@ int plan_operand(Operand* o, int es, bool force) {
   const int64_t inner = o->cols == 1 ? 1 : o->t.stride[n - 1];
   const bool one = P.n == 1;
   const int64_t pitch = P.st[0][P.n - 1];
+  o->one_step = one && inner == 1;
+  o->row_step = pitch;
   o->pack = force || es == 4 || !one || inner != 1 || (o->rows > 1 && pitch < o->cols) ||
             pitch % 8 != 0 || reinterpret_cast<uintptr_t>(o->t.ptr) % 16 != 0;
   o->pitch = (o->cols + 7) / 8 * 8;
@@ -346,6 +507,14 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
   // not reach grad_w), so it always copies x: 1 / vocab of the products' work.
   if ((rc = plan_operand(&S->x, S->es, back && want_w))) return rc;
   if ((rc = plan_operand(&S->w, S->es, false))) return rc;
+  if (!back && S->x.rows <= kFewRows && dim <= kFewMaxDim) {
+    // Rows of elements side by side, w's starting at 16-byte boundaries.
+    const int V = 16 / S->es;
+    const TDesc& wt = S->w.t;
+    S->few = S->x.one_step && (dim == 1 || wt.stride[1] == 1) &&
+             (vocab == 1 || wt.stride[0] % V == 0) && reinterpret_cast<uintptr_t>(wt.ptr) % 16 == 0;
+    if (S->few) S->x.pack = S->w.pack = false;
+  }
   XentRows& r = S->rows;
   r = XentRows{};
   {
@@ -368,7 +537,7 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
   for (Operand* o : {&S->x, &S->w})
     if (o->pack) o->ws = take(&at, size_t(o->rows) * o->pitch * 2 * S->parts);
   if (!back) {
-    r.slots = 2 * uint32_t((vocab + 255) / 256);
+    r.slots = S->few ? few_grid(vocab) : 2 * uint32_t((vocab + 255) / 256);
     S->ws_partial = take(&at, N * r.slots * sizeof(float2));
     S->ws_at = take(&at, N * 4);
     S->ws_row = take(&at, N * 4);
@@ -455,6 +624,34 @@ unsigned gemm_grid(GemmPlan* g, int cg) {
   return unsigned(W * cg);
 }
 
+// k blocks per accumulation where chunks are added in registers: 256 terms
+// for binary32 results (a chunk's truncation is then 16 steps of 2^-24, beside
+// the roundings of the plain sums: [4080, 384] x [5003, 384], gradients'
+// relative error 5.3e-7; 6.0e-6 in one go), 4096 for bfloat16 ones.
+constexpr uint32_t kChunkF32 = 4, kChunkBf16 = 64;
+// Longest k (in blocks) that bfloat16 results accumulate in one go: its
+// truncation stays below 2^-10 of the sum.
+constexpr uint32_t kLongK = 2048;
+
+// The forward's logits of bfloat16 rows give binary32 results: chunks of 2048
+// terms, so that only rows longer than that pay for them ([16384, 768] x
+// [50001, 768]: 0.79 ms in one go, 0.84 through the registers).
+constexpr uint32_t kChunkLse = 32;
+
+bool sum_chunks(const XentSet& S, int epi, GemmPlan* g) {
+  const uint32_t most = S.es == 4 ? 0 : (epi == kEpiLse ? kChunkLse : kLongK);
+  const uint32_t chunk = S.es == 4 ? kChunkF32 : (epi == kEpiLse ? kChunkLse : kChunkBf16);
+  bool sum = false;
+  for (uint32_t i = 0; i < g->n_prob; ++i) sum |= g->pr[i].n_kb > most;
+  for (uint32_t i = 0; i < g->n_prob; ++i) g->pr[i].chunk = sum ? chunk : g->pr[i].n_kb;
+  return sum;
+}
+cudaError_t launch_product(const XentSet& S, int epi, int cg, GemmPlan* g, cudaStream_t s) {
+  const bool sum = sum_chunks(S, epi, g);
+  const unsigned grid = gemm_grid(g, cg);
+  return launch_gemm(epi, cg, sum, *g, grid, s);
+}
+
 void set_tiles(GemmProblem* q, int cg) {
   q->m_tiles = (q->m + 128 * cg - 1) / (128 * cg);
   q->n_tiles = (q->n + q->tn - 1) / q->tn;
@@ -483,8 +680,49 @@ cudaError_t logits_problem(const XentSet& S, const char* ws, int64_t v0, int64_t
   return e;
 }
 
+template <typename E>
+cudaError_t launch_few(const FewPlan& p, unsigned grid, cudaStream_t s) {
+  const int nt = p.n == 1 ? 1 : (p.n == 2 ? 2 : 4);
+  constexpr uint32_t step = 32 * 16 / sizeof(E);
+  const size_t smem = size_t(nt) * ((p.dim + step - 1) / step * step) * 4;
+  auto go = [&](auto* k) {
+    if (smem > 40 * 1024) {
+      const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), 200 * 1024);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_k(k, grid, kThreads, smem, s, p);
+  };
+  if (nt == 1) return go(k_xent_few<E, 1>);
+  if (nt == 2) return go(k_xent_few<E, 2>);
+  return go(k_xent_few<E, 4>);
+}
+
 int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s) {
   cudaError_t e;
+  if (S.few) {
+    XentRows r = S.rows;
+    FewPlan p = {};
+    p.x = S.x.t.ptr;
+    p.w = S.w.t.ptr;
+    p.xp = S.x.row_step;
+    p.wp = S.w.row_step;
+    p.n = r.n;
+    p.vocab = uint32_t(S.w.rows);
+    p.dim = uint32_t(S.x.cols);
+    p.labels = r.labels;
+    p.label_stride = r.label_stride;
+    p.label_i64 = r.label_i64;
+    p.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
+    p.at = reinterpret_cast<float*>(ws + S.ws_at);
+    e = S.es == 4 ? launch_few<float>(p, r.slots, s) : launch_few<__nv_bfloat16>(p, r.slots, s);
+    if (e != cudaSuccess) return cuda_status(e);
+    r.partial = p.partial;
+    r.at = p.at;
+    r.lse = lse;
+    r.row_loss = r.reduction == ZR_NONE ? loss : reinterpret_cast<float*>(ws + S.ws_row);
+    r.loss = loss;
+    return cuda_status(launch_k(k_xent_rows<true>, 1, kRowsThreads, 0, s, r));
+  }
   for (const Operand* o : {&S.x, &S.w})
     if (o->pack && (e = launch_pack(*o, S.es, nullptr, ws, s)) != cudaSuccess) return cuda_status(e);
   const int cg = pick_cg(S.x.rows);
@@ -502,7 +740,7 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
   g.label_i64 = r.label_i64;
   g.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
   g.at = reinterpret_cast<float*>(ws + S.ws_at);
-  if ((e = launch_gemm(kEpiLse, cg, g, gemm_grid(&g, cg), s)) != cudaSuccess) return cuda_status(e);
+  if ((e = launch_product(S, kEpiLse, cg, &g, s)) != cudaSuccess) return cuda_status(e);
   if (r.n <= kRowsOneBlock)
     return cuda_status(launch_k(k_xent_rows<true>, 1, kRowsThreads, 0, s, r));
   const unsigned blocks = (r.n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
@@ -542,7 +780,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     g.n_part = S.parts;
     if ((e = make_map(&g.pr[0].c, G, n, N, ldg, S.parts, N * ldg, 32)) != cudaSuccess)
       return cuda_status(e);
-    if ((e = launch_gemm(kEpiGrad, cg, g, gemm_grid(&g, cg), s)) != cudaSuccess) return cuda_status(e);
+    if ((e = launch_product(S, kEpiGrad, cg, &g, s)) != cudaSuccess) return cuda_status(e);
 
     cg = pick_cg(std::min(N, n));
     GemmPlan o = {};
@@ -600,7 +838,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     o.tiles0 = o.pr[0].m_tiles * o.pr[0].n_tiles;
     o.tiles = o.tiles0 + (o.n_prob > 1 ? o.pr[1].m_tiles * o.pr[1].n_tiles : 0);
     o.m_fast = 0;
-    if ((e = launch_gemm(kEpiOut, cg, o, gemm_grid(&o, cg), s)) != cudaSuccess) return cuda_status(e);
+    if ((e = launch_product(S, kEpiOut, cg, &o, s)) != cudaSuccess) return cuda_status(e);
   }
   return ZR_OK;
 }

@@ -294,3 +294,34 @@ def test_pieces_of_the_vocabulary(dtype, N, V, D):
     us = 2.0 ** -8 if dtype == torch.bfloat16 else U
     close(gw, gw_ref, gw_err + us * (gw_ref.abs() + gw_err), "grad_w")
     assert abs(float(loss) - total / count) <= 1e-4 * total / count
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5])
+def test_few_rows(N, dtype):
+    """The forward's own path for a handful of rows, and around it."""
+    for V, D in ((1, 1), (3, 7), (31, 8), (33, 264), (2500, 768), (1501, 1000), (700, 5000), (40, 12288),
+                 (40, 12289)):
+        x, w, y = make(V + D, N, V, D, dtype, ignored=0)
+        check(x, w, y)
+        wide = torch.randn(V, D + 8, device="cuda").to(dtype)
+        check(x, wide[:, :D], y, "none")
+        check(x, wide[:, 1:D + 1], y, "sum")
+        tall = torch.randn(N, 3, D, device="cuda").to(dtype)
+        check(tall[:, 1], w, y)
+        check(torch.randn(D, N, device="cuda").to(dtype).t(), w, y)
+    y[:] = IGN
+    assert float(zr.zr_linear_xent_fwd(x, w, y)[0]) == 0
+
+
+def test_one_row_sums_to_binary32():
+    """Long rows of positive terms: the worst case for sums that truncate."""
+    for N in (1, 200):
+        for D in (64, 2048, 4096, 16384):
+            g = torch.Generator("cuda").manual_seed(D)
+            x = torch.rand(N, D, generator=g, device="cuda").bfloat16()
+            w = torch.rand(3, D, generator=g, device="cuda").bfloat16()
+            lse = zr.zr_linear_xent_fwd(x, w, torch.zeros(N, dtype=torch.int64, device="cuda"))[1]
+            want = torch.logsumexp(x.double() @ w.double().t(), 1)
+            # 128 truncating steps of at most 2u, then a few roundings.
+            assert ((lse.double() - want).abs() <= (128 * 2 + D / 2048 + 8) * U * want).all(), (N, D)
