@@ -382,11 +382,12 @@ struct EpiGrad {
     at = -1;
     out = true;
     if (e.live) {
-      const int32_t lab = p.label32[e.row];
-      out = lab == -1;
-      scale = p.scale[e.row];
+      const int64_t label = xent_label(p.labels, p.label_stride, p.label_i64, e.row);
+      out = label == p.ignore_index;
+      scale = p.row_scale ? p.row_scale[e.row] : 1.f;
+      if (label < 0 || label >= p.vocab) scale = qnan();  // no class: NaN, not a guess
       lse2 = p.lse[e.row] * kLog2e;
-      at = int64_t(lab) - p.label_base - int64_t(e.n0);
+      at = label - p.label_base - int64_t(e.n0);
     }
   }
   __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
@@ -518,6 +519,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   const uint32_t tmem = s_tmem;
   GemmWalk walk = gemm_walk(p, blockIdx.x / CG);
   pdl_wait();
+  if (EPI == kEpiLse && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
 
   if (warp == 8 && lane == 0) {
     // Producer: this CTA's rows of A and its share of B's columns.

@@ -47,16 +47,18 @@ struct GemmPlan {
   uint32_t workers, head, extra, late_first;
   uint32_t es;               // kEpiOut: bytes per output element
   const float* out_scale;    // kEpiOut: multiplies the finished product, or null (1)
-  // kEpiLse
+  // kEpiLse, kEpiGrad
   const void* labels;        // label of row r: labels[r * label_stride]
   int64_t label_stride;
   uint32_t label_i64;
+  // kEpiLse
+  uint32_t* ticket;          // set to 0
   float2* partial;           // [m][2 * n_tiles] (maximum, sum)
   float* at;                 // [m] product at the label
   // kEpiGrad
   const float* lse;          // [m]
-  const float* scale;        // [m]
-  const int32_t* label32;    // [m], -1: the row is left out
+  const float* row_scale;    // [m], or null (1)
+  int64_t ignore_index, vocab;
   int64_t label_base;        // column 0 of this product is this label
   uint32_t n_part;           // parts of G, stored through pr[0].c
 };

@@ -37,6 +37,20 @@ struct Reader {
   }
 };
 
+// Runs call(workspace, &bytes); where the workspace given is too small, *need
+// becomes the size it should have.
+template <typename F>
+int with_need(void* ws, int64_t given, int64_t* need, F call) {
+  size_t bytes = size_t(given);
+  int rc = call(ws, &bytes);
+  if (rc == ZR_ERR_WORKSPACE && ws) {
+    bytes = 0;
+    if (call(nullptr, &bytes) == ZR_OK && bytes <= size_t(given)) return rc;  // misaligned
+  }
+  *need = int64_t(bytes);
+  return rc;
+}
+
 }  // namespace
 
 extern "C" {
@@ -67,14 +81,14 @@ int zr_packed_layer_norm_bwd(const int64_t* words, int64_t* need) {
   void* gg = r.ptr<void>();
   void* gb = r.ptr<void>();
   void* ws = r.ptr<void>();
-  size_t bytes = size_t(r.i64());
+  const int64_t given = r.i64();
   const zr_tensor g = r.tensor(), x = r.tensor(), gamma = r.tensor(), gx = r.tensor();
   if (!r.ok) return ZR_ERR_RANK;
   if (gx.data && gx.ndim != x.ndim) return ZR_ERR_SHAPE;
-  const int rc = zr_layer_norm_bwd(dt, g, x, gamma, mean, rstd, const_cast<void*>(gx.data),
-                                   gx.data ? gx.strides : nullptr, gg, gb, ws, &bytes, stream);
-  *need = int64_t(bytes);
-  return rc;
+  return with_need(ws, given, need, [&](void* w, size_t* n) {
+    return zr_layer_norm_bwd(dt, g, x, gamma, mean, rstd, const_cast<void*>(gx.data),
+                             gx.data ? gx.strides : nullptr, gg, gb, w, n, stream);
+  });
 }
 
 int zr_packed_dropout_fwd(const int64_t* words) {
@@ -117,12 +131,12 @@ int zr_packed_linear_xent_fwd(const int64_t* words, int64_t* need) {
   float* loss = r.ptr<float>();
   float* lse = r.ptr<float>();
   void* ws = r.ptr<void>();
-  size_t bytes = size_t(r.i64());
+  const int64_t given = r.i64();
   const zr_tensor x = r.tensor(), w = r.tensor(), labels = r.tensor();
   if (!r.ok) return ZR_ERR_RANK;
-  const int rc = zr_linear_xent_fwd(dt, x, w, it, labels, ignore, red, loss, lse, ws, &bytes, stream);
-  *need = int64_t(bytes);
-  return rc;
+  return with_need(ws, given, need, [&](void* wp, size_t* n) {
+    return zr_linear_xent_fwd(dt, x, w, it, labels, ignore, red, loss, lse, wp, n, stream);
+  });
 }
 
 int zr_packed_linear_xent_bwd(const int64_t* words, int64_t* need) {
@@ -139,13 +153,12 @@ int zr_packed_linear_xent_bwd(const int64_t* words, int64_t* need) {
   void* gx = r.ptr<void>();
   void* gw = r.ptr<void>();
   void* ws = r.ptr<void>();
-  size_t bytes = size_t(r.i64());
+  const int64_t given = r.i64();
   const zr_tensor x = r.tensor(), w = r.tensor(), labels = r.tensor();
   if (!r.ok) return ZR_ERR_RANK;
-  const int rc = zr_linear_xent_bwd(dt, grad_loss, x, w, it, labels, ignore, red, lse, gx, gw, ws,
-                                    &bytes, stream);
-  *need = int64_t(bytes);
-  return rc;
+  return with_need(ws, given, need, [&](void* wp, size_t* n) {
+    return zr_linear_xent_bwd(dt, grad_loss, x, w, it, labels, ignore, red, lse, gx, gw, wp, n, stream);
+  });
 }
 
 }  // extern "C"

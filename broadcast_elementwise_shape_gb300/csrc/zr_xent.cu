@@ -29,17 +29,16 @@
 namespace zr {
 
 // An operand copied into rows the tensor maps can read: [part][row][pitch],
-// zero past `cols`.  Rows whose label32 is -1 become zero.
+// zero past `cols`.
 struct PackPlan {
   const void* in;
   uint16_t* out;
-  const int32_t* label32;    // or null
   Decomp rows;               // slot 0
   int64_t inner_stride;
   int64_t part;              // elements between parts
-  uint32_t nrow, cols, pitch, vec;
-  FastDiv nvec_div;          // pitch / 8
-  uint64_t items;            // nrow * pitch / 8
+  uint32_t nrow, cols, pitch;
+  uint32_t wide;             // 16-byte loads of unit-stride rows
+  uint64_t items;            // nrow * pitch / 8; 0: not packed
 };
 
 struct XentRows {
@@ -56,11 +55,18 @@ struct XentRows {
   float* lse;
   float* row_loss;           // workspace, or the loss itself (no reduction)
   float* loss;
+  uint32_t* ticket;          // blocks done (zeroed by the product before)
   // backward
   const float* grad_loss;
-  float* scale;
   float* common;             // the factor all rows share (mean, sum)
-  int32_t* label32;
+};
+
+// The backward's first launch: blocks [0, blocks_x) pack x with its left-out
+// rows zeroed, the next blocks_w pack w, one more finds the shared factor.
+struct PrepPlan {
+  PackPlan x, w;
+  XentRows rows;
+  uint32_t blocks_x, blocks_w, zero_rows;
 };
 
 namespace {
@@ -71,24 +77,38 @@ __device__ __forceinline__ int64_t row_label(const XentRows& p, uint32_t r) {
 }
 
 template <typename E, int PARTS>
-__global__ void __launch_bounds__(kThreads) k_xent_pack(const __grid_constant__ PackPlan p) {
-  pdl_trigger();
-  const uint64_t i = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
-  pdl_wait();
+__device__ __forceinline__ void xent_pack(const PackPlan& p, const XentRows* zero, uint64_t i) {
   if (i >= p.items) return;
   const uint32_t nvec = p.pitch / 8;
   const uint32_t row = uint32_t(i / nvec);
   const uint32_t c = uint32_t(i - uint64_t(row) * nvec) * 8;
   float v[8];
-  if (p.label32 && p.label32[row] == -1) {
+  if (zero && row_label(*zero, row) == zero->ignore_index) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
   } else {
     int64_t off[kMaxOperands];
     decomp_offsets(p.rows, row, off);
     const E* src = static_cast<const E*>(p.in) + off[0] + int64_t(c) * p.inner_stride;
+    if (p.wide && c + 8 <= p.cols) {
+      if constexpr (sizeof(E) == 4) {
+        const float4 lo = reinterpret_cast<const float4*>(src)[0];
+        const float4 hi = reinterpret_cast<const float4*>(src)[1];
+        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+      } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(src);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < p.cols ? ld1(src + j * p.inner_stride, false) : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          v[2 * j] = __uint_as_float(w[j] << 16);
+          v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < p.cols ? ld1(src + j * p.inner_stride, false) : 0.f;
+    }
   }
   uint16_t* dst = p.out + int64_t(row) * p.pitch + c;
 #pragma unroll
@@ -105,8 +125,7 @@ __global__ void __launch_bounds__(kThreads) k_xent_pack(const __grid_constant__ 
   }
 }
 
-constexpr int kRowsThreads = 1024;
-
+template <int T>
 __device__ __forceinline__ uint32_t block_count(uint32_t v, uint32_t* s) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
@@ -114,39 +133,39 @@ __device__ __forceinline__ uint32_t block_count(uint32_t v, uint32_t* s) {
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int w = 0; w < kRowsThreads / 32; ++w) v += s[w];
+  for (int w = 0; w < T / 32; ++w) v += s[w];
   return v;
 }
 
-// Backward: each row's factor c_n and label.  One block, since the mean needs
-// the count of the rows that take part.
-__global__ void __launch_bounds__(kRowsThreads) k_xent_scale(const __grid_constant__ XentRows p) {
+template <typename E, int PARTS>
+__global__ void __launch_bounds__(kThreads) k_xent_prep(const __grid_constant__ PrepPlan p) {
   pdl_trigger();
-  __shared__ uint32_t s_cnt[32];
+  __shared__ uint32_t s_cnt[kThreads / 32];
+  uint32_t b = blockIdx.x;
   pdl_wait();
+  if (b < p.blocks_x) {
+    xent_pack<E, PARTS>(p.x, p.zero_rows ? &p.rows : nullptr, uint64_t(b) * kThreads + threadIdx.x);
+    return;
+  }
+  b -= p.blocks_x;
+  if (b < p.blocks_w) {
+    xent_pack<E, PARTS>(p.w, nullptr, uint64_t(b) * kThreads + threadIdx.x);
+    return;
+  }
+  const XentRows& r = p.rows;
+  if (r.common == nullptr) return;
   uint32_t cnt = 0;
-  if (p.reduction == ZR_MEAN) {
-    for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) cnt += row_label(p, r) != p.ignore_index;
-    cnt = block_count(cnt, s_cnt);
+  if (r.reduction == ZR_MEAN) {
+#pragma unroll 8
+    for (uint32_t i = threadIdx.x; i < r.n; i += kThreads) cnt += row_label(r, i) != r.ignore_index;
+    cnt = block_count<kThreads>(cnt, s_cnt);
   }
-  if (threadIdx.x == 0 && p.reduction != ZR_NONE)
-    *p.common = p.reduction == ZR_MEAN ? (cnt ? __fdiv_rn(p.grad_loss[0], float(cnt)) : 0.f)
-                                       : p.grad_loss[0];
-  for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) {
-    const int64_t y = row_label(p, r);
-    const float g = p.reduction == ZR_NONE ? p.grad_loss[r] : 1.f;
-    if (y == p.ignore_index) {
-      p.scale[r] = 0.f;
-      p.label32[r] = -1;
-    } else if (y < 0 || y >= p.vocab) {
-      p.scale[r] = __uint_as_float(0x7FFFFFFFu);  // a label that is no class: NaN, not a guess
-      p.label32[r] = -2;
-    } else {
-      p.scale[r] = g;
-      p.label32[r] = int32_t(y);
-    }
-  }
+  if (threadIdx.x == 0)
+    *r.common = r.reduction == ZR_MEAN ? (cnt ? __fdiv_rn(r.grad_loss[0], float(cnt)) : 0.f)
+                                       : r.grad_loss[0];
 }
+
+constexpr int kRowsThreads = 1024;
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -162,15 +181,24 @@ __device__ __forceinline__ float warp_sum(float v) {
 // One warp joins a row's partial maxima and sums in a fixed order.
 __device__ __forceinline__ void xent_row(const XentRows& p, uint32_t r, uint32_t lane) {
   const float2* q = p.partial + uint64_t(r) * p.slots;
+  // 512 slots' worth stays in registers between the two walks.
+  float2 v[16];
   float m = -INFINITY;
-  for (uint32_t i = lane; i < p.slots; i += 32) m = fmaxf(m, q[i].x);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = lane + 32 * i < p.slots ? q[lane + 32 * i] : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, v[i].x);
+  }
+  for (uint32_t i = lane + 512; i < p.slots; i += 32) m = fmaxf(m, q[i].x);
   m = warp_max(m);
   const float base = m == -INFINITY ? 0.f : m;
   float s = 0.f;
-  for (uint32_t i = lane; i < p.slots; i += 32) {
-    const float2 v = q[i];
-    // A part with no columns has s = 0 and the maximum -inf.
-    s = __fmaf_rn(v.y, expf(v.x - base), s);
+  // A slot with no columns has s = 0 and the maximum -inf.
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s = __fmaf_rn(v[i].y, expf(v[i].x - base), s);
+  for (uint32_t i = lane + 512; i < p.slots; i += 32) {
+    const float2 w = q[i];
+    s = __fmaf_rn(w.y, expf(w.x - base), s);
   }
   s = warp_sum(s);
   if (lane == 0) {
@@ -191,9 +219,9 @@ __device__ __forceinline__ void xent_total(const XentRows& p, uint32_t* s_cnt, f
   acc.init();
   for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) {
     cnt += row_label(p, r) != p.ignore_index;
-    acc.add(p.row_loss[r]);
+    acc.add(__ldcg(p.row_loss + r));
   }
-  cnt = block_count(cnt, s_cnt);
+  cnt = block_count<kRowsThreads>(cnt, s_cnt);
   const float v = warp_sum(acc.s);
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
   __syncthreads();
@@ -206,29 +234,31 @@ __device__ __forceinline__ void xent_total(const XentRows& p, uint32_t* s_cnt, f
 
 constexpr uint32_t kRowsOneBlock = 256;  // rows that one block joins and totals in one launch
 
+// ALL: one block joins every row.  Else a warp per row; the block that
+// finishes last totals the rows (which one that is changes nothing in the sum).
 template <bool ALL>
 __global__ void __launch_bounds__(kRowsThreads) k_xent_rows(const __grid_constant__ XentRows p) {
   pdl_trigger();
   __shared__ uint32_t s_cnt[32];
   __shared__ float s_sum[32];
+  __shared__ bool s_last;
   const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_wait();
   if constexpr (ALL) {
     for (uint32_t r = w; r < p.n; r += kRowsThreads / 32) xent_row(p, r, lane);
     if (p.reduction == ZR_NONE) return;
     __syncthreads();
-    xent_total(p, s_cnt, s_sum);
   } else {
     const uint32_t r = blockIdx.x * (kRowsThreads / 32) + w;
     if (r < p.n) xent_row(p, r, lane);
+    if (p.reduction == ZR_NONE) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = atomicAdd(p.ticket, 1u) + 1 == gridDim.x;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
   }
-}
-
-__global__ void __launch_bounds__(kRowsThreads) k_xent_total(const __grid_constant__ XentRows p) {
-  pdl_trigger();
-  __shared__ uint32_t s_cnt[32];
-  __shared__ float s_sum[32];
-  pdl_wait();
   xent_total(p, s_cnt, s_sum);
 }
 
@@ -418,9 +448,9 @@ struct XentSet {
   XentRows rows;
   size_t ws = 0;
   // forward
-  size_t ws_partial = 0, ws_at = 0, ws_row = 0;
+  size_t ws_partial = 0, ws_at = 0, ws_row = 0, ws_ticket = 0;
   // backward
-  size_t ws_scale = 0, ws_common = 0, ws_label = 0, ws_g = 0, ws_acc = 0;
+  size_t ws_common = 0, ws_g = 0, ws_acc = 0;
   int64_t piece = 0, n_piece = 0;
 };
 
@@ -468,6 +498,9 @@ int plan_operand(Operand* o, int es, bool force) {
   p.nrow = uint32_t(o->rows);
   p.cols = uint32_t(o->cols);
   p.pitch = uint32_t(o->pitch);
+  p.wide = inner == 1 && reinterpret_cast<uintptr_t>(o->t.ptr) % 16 == 0;
+  for (int i = 0; i < P.n; ++i)
+    if (p.rows.stride[0][i] * es % 16 != 0) p.wide = 0;
   p.part = o->rows * o->pitch;
   p.items = uint64_t(o->rows) * uint64_t(o->pitch / 8);
   return ZR_OK;
@@ -541,10 +574,9 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     S->ws_partial = take(&at, N * r.slots * sizeof(float2));
     S->ws_at = take(&at, N * 4);
     S->ws_row = take(&at, N * 4);
+    S->ws_ticket = take(&at, 4);
   } else {
-    S->ws_scale = take(&at, N * 4);
     S->ws_common = take(&at, 4);
-    S->ws_label = take(&at, N * 4);
     const int64_t most = std::max<int64_t>(2048, int64_t(kPieceBytes / (2 * S->parts * N)));
     S->n_piece = (vocab + most - 1) / most;
     S->piece = ((vocab + S->n_piece - 1) / S->n_piece + 255) / 256 * 256;
@@ -593,14 +625,28 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t row
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_pack(const Operand& o, int es, const int32_t* label32, char* ws, cudaStream_t s) {
-  PackPlan p = o.pp;
-  p.out = reinterpret_cast<uint16_t*>(ws + o.ws);
-  p.label32 = label32;
-  const uint64_t blocks = (p.items + kThreads - 1) / kThreads;
-  if (blocks >= (uint64_t(1) << 31)) return cudaErrorInvalidValue;
-  return es == 4 ? launch_k(k_xent_pack<float, 3>, unsigned(blocks), kThreads, 0, s, p)
-                 : launch_k(k_xent_pack<__nv_bfloat16, 1>, unsigned(blocks), kThreads, 0, s, p);
+// Packs the operands that need it; r: the backward's row data, or null.
+cudaError_t launch_prep(const XentSet& S, const XentRows* r, char* ws, cudaStream_t s) {
+  PrepPlan p = {};
+  uint64_t blocks[2] = {0, 0};
+  const Operand* ops[2] = {&S.x, &S.w};
+  PackPlan* packs[2] = {&p.x, &p.w};
+  for (int i = 0; i < 2; ++i) {
+    if (!ops[i]->pack) continue;
+    *packs[i] = ops[i]->pp;
+    packs[i]->out = reinterpret_cast<uint16_t*>(ws + ops[i]->ws);
+    blocks[i] = (packs[i]->items + kThreads - 1) / kThreads;
+  }
+  p.blocks_x = uint32_t(blocks[0]);
+  p.blocks_w = uint32_t(blocks[1]);
+  const bool shared = r && r->common;
+  if (r) p.rows = *r;
+  p.zero_rows = r != nullptr;
+  const uint64_t n = blocks[0] + blocks[1] + (shared ? 1 : 0);
+  if (n == 0) return cudaSuccess;
+  if (n >= (uint64_t(1) << 31)) return cudaErrorInvalidValue;
+  return S.es == 4 ? launch_k(k_xent_prep<float, 3>, unsigned(n), kThreads, 0, s, p)
+                   : launch_k(k_xent_prep<__nv_bfloat16, 1>, unsigned(n), kThreads, 0, s, p);
 }
 
 const char* operand_base(const Operand& o, const char* ws) {
@@ -723,8 +769,7 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
     r.loss = loss;
     return cuda_status(launch_k(k_xent_rows<true>, 1, kRowsThreads, 0, s, r));
   }
-  for (const Operand* o : {&S.x, &S.w})
-    if (o->pack && (e = launch_pack(*o, S.es, nullptr, ws, s)) != cudaSuccess) return cuda_status(e);
+  if ((e = launch_prep(S, nullptr, ws, s)) != cudaSuccess) return cuda_status(e);
   const int cg = pick_cg(S.x.rows);
   GemmPlan g = {};
   if ((e = logits_problem(S, ws, 0, S.w.rows, cg, &g)) != cudaSuccess) return cuda_status(e);
@@ -740,28 +785,21 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
   g.label_i64 = r.label_i64;
   g.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
   g.at = reinterpret_cast<float*>(ws + S.ws_at);
+  r.ticket = g.ticket = reinterpret_cast<uint32_t*>(ws + S.ws_ticket);
   if ((e = launch_product(S, kEpiLse, cg, &g, s)) != cudaSuccess) return cuda_status(e);
   if (r.n <= kRowsOneBlock)
     return cuda_status(launch_k(k_xent_rows<true>, 1, kRowsThreads, 0, s, r));
   const unsigned blocks = (r.n + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
-  e = launch_k(k_xent_rows<false>, blocks, kRowsThreads, 0, s, r);
-  if (e != cudaSuccess || r.reduction == ZR_NONE) return cuda_status(e);
-  return cuda_status(launch_k(k_xent_total, 1, kRowsThreads, 0, s, r));
+  return cuda_status(launch_k(k_xent_rows<false>, blocks, kRowsThreads, 0, s, r));
 }
 
 int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* grad_x, void* grad_w,
             char* ws, cudaStream_t s) {
   XentRows r = S.rows;
   r.grad_loss = grad_loss;
-  r.scale = reinterpret_cast<float*>(ws + S.ws_scale);
-  r.common = reinterpret_cast<float*>(ws + S.ws_common);
-  r.label32 = reinterpret_cast<int32_t*>(ws + S.ws_label);
-  cudaError_t e = launch_k(k_xent_scale, 1, kRowsThreads, 0, s, r);
+  if (r.reduction != ZR_NONE) r.common = reinterpret_cast<float*>(ws + S.ws_common);
+  cudaError_t e = launch_prep(S, &r, ws, s);
   if (e != cudaSuccess) return cuda_status(e);
-  for (const Operand* o : {&S.x, &S.w})
-    if (o->pack &&
-        (e = launch_pack(*o, S.es, o == &S.x ? r.label32 : nullptr, ws, s)) != cudaSuccess)
-      return cuda_status(e);
   const int64_t N = S.x.rows, D = S.x.cols, V = S.w.rows;
   uint16_t* G = reinterpret_cast<uint16_t*>(ws + S.ws_g);
   float* acc = reinterpret_cast<float*>(ws + S.ws_acc);
@@ -774,8 +812,12 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     GemmPlan g = {};
     if ((e = logits_problem(S, ws, v0, n, cg, &g)) != cudaSuccess) return cuda_status(e);
     g.lse = lse;
-    g.scale = r.scale;
-    g.label32 = r.label32;
+    g.labels = r.labels;
+    g.label_stride = r.label_stride;
+    g.label_i64 = r.label_i64;
+    g.ignore_index = r.ignore_index;
+    g.vocab = V;
+    g.row_scale = r.reduction == ZR_NONE ? grad_loss : nullptr;
     g.label_base = v0;
     g.n_part = S.parts;
     if ((e = make_map(&g.pr[0].c, G, n, N, ldg, S.parts, N * ldg, 32)) != cudaSuccess)
@@ -786,7 +828,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     GemmPlan o = {};
     o.n_combo = S.combos;
     o.es = uint32_t(S.es);
-    o.out_scale = r.reduction == ZR_NONE ? nullptr : r.common;
+    o.out_scale = r.common;
     // grad_x += G W: rows of x, k = this piece's vocabulary.
     if (grad_x) {
       GemmProblem& q = o.pr[o.n_prob++];
@@ -901,6 +943,8 @@ int zr_linear_xent_fwd(zr_dtype dtype, zr_tensor x, zr_tensor w, zr_index label_
   if (rc) return rc;
   const int64_t nl = loss_count(S, reduction);
   if ((nl > 0 && !loss) || (!S.empty && !lse)) return ZR_ERR_NULL;
+  if (workspace && (*workspace_bytes < S.ws || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+    return ZR_ERR_WORKSPACE;
   const Span ws = span_of(workspace, int64_t(S.ws), 1);
   if (!S.empty &&
       (rc = check_spans(S, {span_of(loss, nl), span_of(lse, S.x.rows)}, {}, ws)))
@@ -909,8 +953,6 @@ int zr_linear_xent_fwd(zr_dtype dtype, zr_tensor x, zr_tensor w, zr_index label_
     *workspace_bytes = S.ws;
     return ZR_OK;
   }
-  if (*workspace_bytes < S.ws) return ZR_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return ZR_ERR_WORKSPACE;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (S.empty) {
     if (nl == 0) return ZR_OK;
@@ -934,6 +976,8 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
   const int64_t nl = loss_count(S, reduction);
   const int64_t dim = S.w.t.size[1], vocab = S.w.t.size[0];
   if (!S.empty && (!grad_loss || !lse)) return ZR_ERR_NULL;
+  if (workspace && (*workspace_bytes < S.ws || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+    return ZR_ERR_WORKSPACE;
   const Span ws = span_of(workspace, int64_t(S.ws), 1);
   if (!S.empty &&
       (rc = check_spans(S, {span_of(grad_x, grad_x ? S.x.rows * dim : 0, S.es),
@@ -944,8 +988,6 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
     *workspace_bytes = S.ws;
     return ZR_OK;
   }
-  if (*workspace_bytes < S.ws) return ZR_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return ZR_ERR_WORKSPACE;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (S.empty) {
     if (!grad_w) return ZR_OK;

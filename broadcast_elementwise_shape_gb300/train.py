@@ -18,6 +18,7 @@ import broadcast_elementwise_shape_gb300 as _zr
 _F32, _BF16 = torch.float32, torch.bfloat16
 _CODE = {_F32: 0, _BF16: 1}  # zr_dtype
 _NONE = (0, 0)               # a tensor that is not given
+_ERR_WORKSPACE = -7
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _empty = torch.empty
 
@@ -68,19 +69,25 @@ def _pack(scalar, words):
     return struct.pack(f"d{len(words)}q", scalar, *words)
 
 
+_TRY = 1 << 16  # bytes: enough for short calls, which then take one call instead of two
+
+
 def _with_workspace(fn, name, words, at, workspace, device):
-    """Query, allocate where the caller gave too little, call.  words[at] and
+    """Call with the caller's workspace or a small one; where that is too
+    little, once more with what the call asked for.  words[at] and
     words[at + 1] are the workspace's address and size."""
+    if workspace is None or workspace.numel() < 16:
+        workspace = _empty(_TRY, dtype=torch.uint8, device=device)
+    n = workspace.numel()
+    words[at] = workspace.data_ptr()
+    words[at + 1] = n
     need = ctypes.c_int64(0)
     rc = fn(_pack(0.0, words), ctypes.byref(need))
-    if rc:
-        _fail(rc, name + " (workspace query)")
-    n = need.value
-    if workspace is None or workspace.numel() < n:
-        workspace = _empty(n if n > 16 else 16, dtype=torch.uint8, device=device)
-    words[at] = workspace.data_ptr()
-    words[at + 1] = workspace.numel()
-    rc = fn(_pack(0.0, words), ctypes.byref(need))
+    if rc == _ERR_WORKSPACE and need.value > n:
+        workspace = _empty(need.value, dtype=torch.uint8, device=device)
+        words[at] = workspace.data_ptr()
+        words[at + 1] = need.value
+        rc = fn(_pack(0.0, words), ctypes.byref(need))
     if rc:
         _fail(rc, name)
 

@@ -8,6 +8,9 @@
  * double's bit pattern; pointers and integers are one word each.  Every check,
  * result and status is that of the zr.h function of the same name; ndim
  * outside 0..8 in any tensor is ZR_ERR_RANK and nothing after it is read.
+ * Entry points with `need`: with workspace 0 the call stores the workspace's
+ * size in *need and launches nothing; with one that is too small it returns
+ * ZR_ERR_WORKSPACE and stores the size too (not if it is merely misaligned).
  */
 #ifndef ZR_PACKED_H_
 #define ZR_PACKED_H_
@@ -21,8 +24,7 @@ extern "C" {
 /* S eps, dtype, stream, mean, rstd, x, gamma, beta, y (data and strides count; its sizes are x's). */
 int zr_packed_layer_norm_fwd(const int64_t* words);
 /* S unused, dtype, stream, mean, rstd, grad_gamma, grad_beta, workspace, workspace bytes,
- * grad_out, x, gamma, grad_x.  With workspace 0: returns the status and stores the size
- * in *need. */
+ * grad_out, x, gamma, grad_x. */
 int zr_packed_layer_norm_bwd(const int64_t* words, int64_t* need);
 /* S p, dtype, stream, seed, offset, device_offset, x, residual, out. */
 int zr_packed_dropout_fwd(const int64_t* words);
