@@ -100,10 +100,6 @@ def lib() -> ctypes.CDLL:
                                          ctypes.c_int64, c_int, vp, vp, vp, vp, szp, vp]
         L.zr_status_string.argtypes = [c_int]
         L.zr_status_string.restype = ctypes.c_char_p
-        for f, n in (("layer_norm_fwd", 1), ("layer_norm_bwd", 2), ("dropout_fwd", 1),
-                     ("dropout_bwd", 1), ("linear_xent_fwd", 2), ("linear_xent_bwd", 2)):
-            getattr(L, "zr_packed_" + f).argtypes = [ctypes.c_char_p, vp][:n]
-            getattr(L, "zr_packed_" + f).restype = c_int
         for f in ("zr_broadcast_shape", "zr_binary_fwd", "zr_binary_bwd", "zr_sum_to_shape",
                   "zr_chain_fwd", "zr_chain_bwd", "zr_binary_bwd_ex", "zr_unary_fwd", "zr_unary_bwd",
                   "zr_binary_fwd_t", "zr_binary_bwd_t", "zr_sum_to_shape_t", "zr_unary_fwd_t",
