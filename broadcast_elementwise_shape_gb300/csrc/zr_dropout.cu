@@ -26,7 +26,8 @@ struct DropPlan {
   const void* residual;      // or null
   void* out;
   const uint64_t* device_offset;  // added to offset, or null
-  uint64_t seed, offset;
+  uint64_t offset;
+  uint32_t key[20];          // the seed's ten round keys
   Decomp rows;
   int64_t inner_stride[kMaxOperands];
   uint64_t numel;
@@ -41,19 +42,17 @@ struct DropPlan {
 namespace {
 
 // The four words of one counter: ten rounds of two 32 x 32 -> 64
-// multiplications, the key raised by the paper's Weyl constants in between.
-__device__ __forceinline__ void philox(uint64_t counter, uint64_t seed, uint32_t* w) {
+// multiplications.  The key's schedule (the paper's Weyl constants added from
+// round to round) is the same for every element, so the host computes it.
+__device__ __forceinline__ void philox(uint64_t counter, const uint32_t* key, uint32_t* w) {
   uint32_t c0 = uint32_t(counter), c1 = uint32_t(counter >> 32), c2 = 0, c3 = 0;
-  uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;
-    c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+    c0 = uint32_t(b >> 32) ^ c1 ^ key[2 * r];
     c1 = uint32_t(b);
-    c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+    c2 = uint32_t(a >> 32) ^ c3 ^ key[2 * r + 1];
     c3 = uint32_t(a);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   w[0] = c0; w[1] = c1; w[2] = c2; w[3] = c3;
 }
@@ -104,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout_vec(const __grid_constant_
     if ((i + 1) * VEC > p.numel) {
       for (uint64_t e = i * VEC; e < p.numel; ++e) {
         uint32_t w[4];
-        philox(base + e / 4, p.seed, w);
+        philox(base + e / 4, p.key, w);
         const uint32_t word = e % 4 == 0 ? w[0] : e % 4 == 1 ? w[1] : e % 4 == 2 ? w[2] : w[3];
         dropout_one<E, RES>(p, word, int64_t(e), int64_t(e), int64_t(e));
       }
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout_vec(const __grid_constant_
 #pragma unroll
     for (int b = 0; b < VEC / 4; ++b) {
       uint32_t w[4];
-      philox(base + i * (VEC / 4) + b, p.seed, w);
+      philox(base + i * (VEC / 4) + b, p.key, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = 4 * b + j;
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout_any(const __grid_constant_
   if (i >= p.nitems) return;
   const uint64_t base = p.offset + (p.device_offset ? *p.device_offset : 0);
   uint32_t w[4];
-  philox(base + i, p.seed, w);
+  philox(base + i, p.key, w);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint64_t e = 4 * i + j;
@@ -235,7 +234,11 @@ int plan_dropout(zr_dtype dtype, const zr_tensor& x, const zr_tensor* residual, 
   p.residual = res ? S->r.ptr : nullptr;
   p.out = out;
   p.device_offset = rng.device_offset;
-  p.seed = rng.seed;
+  uint32_t k0 = uint32_t(rng.seed), k1 = uint32_t(rng.seed >> 32);
+  for (int r = 0; r < 10; ++r, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
+    p.key[2 * r] = k0;
+    p.key[2 * r + 1] = k1;
+  }
   p.offset = rng.offset;
   p.numel = uint64_t(S->x.numel);
   const double thr = std::nearbyint(prob * 4294967296.0);

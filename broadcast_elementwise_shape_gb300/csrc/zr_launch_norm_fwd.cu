@@ -6,7 +6,12 @@ namespace {
 
 template <typename E, int VEC, int G, int NI>
 cudaError_t go(const NormPlan& p, cudaStream_t s) {
-  return launch_k(k_norm_fwd<E, VEC, G, NI>, p.n_cta, kNormThreads, 0, s, p);
+  auto* k = k_norm_fwd<E, VEC, G, NI>;
+  if (p.smem > 40 * 1024) {  // with the static shared memory, under 48 KB otherwise
+    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), kNormSmemMax);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_k(k, p.n_cta, kNormThreads, p.smem, s, p);
 }
 
 template <typename E, int VEC>

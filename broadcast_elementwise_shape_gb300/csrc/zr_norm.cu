@@ -54,6 +54,17 @@ void pick_group(NormPlan* p, int vec) {
   else norm_cases<8>(see);
 }
 
+// A persistent grid of at most per_sm blocks per SM over rings of `streams`
+// inputs.  A third stage where that leaves every block its place on the SM.
+void pick_ring(NormPlan* p, uint32_t streams, uint32_t per_sm, uint32_t at_least) {
+  const uint32_t ring = streams * kNormThreads * p->ni * 16;  // one stage
+  const uint32_t most = uint32_t(kNormSmemMax);
+  p->stages = 3 * ring * per_sm <= most ? 3 : 2;
+  p->smem = std::max(p->stages * ring, at_least);
+  while (per_sm > 1 && p->smem * per_sm > most) --per_sm;
+  p->n_cta = std::min(p->n_cta, kSms * per_sm);
+}
+
 // Rows and access width over the input slots 0 .. nin-1 and the output.
 int plan_rows(NormSet* S, int nin, const void* out) {
   NormPlan& p = S->p;
@@ -168,6 +179,7 @@ int plan_norm_fwd(zr_dtype dtype, const zr_tensor& x, const zr_tensor& gamma, co
   if ((rc = plan_rows(S, 1, y))) return rc;
   const uint32_t rpb = p.group ? kNormThreads / p.group : 1;
   p.n_cta = (p.nrow + rpb - 1) / rpb;
+  if (p.group && S->vec > 1) pick_ring(&p, 1, uint32_t(norm_fwd_occ(int(p.ni) * S->vec, S->vec)), 0);
   return ZR_OK;
 }
 
@@ -214,19 +226,12 @@ int plan_norm_bwd(zr_dtype dtype, const zr_tensor& g, const zr_tensor& x, const 
   p.mean_in = mean;
   p.rstd_in = rstd;
   if ((rc = plan_rows(S, 2, gx))) return rc;
-  const bool sums = p.want_gamma || p.want_beta;
   if (p.group) {
-    // Persistent over rows: the column sums stay in registers.  The ring
-    // takes a third stage where that leaves every CTA its place on the SM.
     const uint32_t rpb = kNormThreads / p.group;
-    const uint32_t need = (p.nrow + rpb - 1) / rpb;
-    uint32_t per_sm = uint32_t(norm_bwd_occ(int(p.ni) * S->vec, S->vec));
-    const uint32_t ring = S->vec > 1 ? 2 * kNormThreads * p.ni * 16 : 0;  // one stage
-    p.stages = ring && 3 * ring * per_sm <= uint32_t(kNormSmemMax) ? 3 : 2;
-    while (per_sm > 1 && p.stages * ring * per_sm > uint32_t(kNormSmemMax)) --per_sm;
-    const uint32_t cols = p.group > 32 ? 0 : p.group * p.ni * uint32_t(S->vec) * 4;
-    p.smem = std::max(p.stages * ring, cols);
-    p.n_cta = std::min<uint32_t>(need, kSms * per_sm);
+    p.n_cta = (p.nrow + rpb - 1) / rpb;
+    // After the rows the ring holds every row group's column sums.
+    const uint32_t sums = p.group > 32 ? 0 : kNormThreads * p.ni * uint32_t(S->vec) * 4;
+    pick_ring(&p, S->vec > 1 ? 2 : 0, uint32_t(norm_bwd_occ(int(p.ni) * S->vec, S->vec)), sums);
   } else {
     // k_norm_sums: rows split so that the column blocks fill the GPU, at
     // least 64 rows to a split.
@@ -234,7 +239,7 @@ int plan_norm_bwd(zr_dtype dtype, const zr_tensor& g, const zr_tensor& x, const 
     const uint32_t want = (kSms * 8 + cb - 1) / cb;
     p.n_cta = std::max<uint32_t>(1, std::min<uint32_t>(want, p.nrow / 64));
   }
-  if (sums) S->ws = size_t(p.n_cta) * (p.want_gamma + p.want_beta) * size_t(dim) * sizeof(float);
+  if (p.want_gamma || p.want_beta) S->ws = size_t(p.n_cta) * (p.want_gamma + p.want_beta) * size_t(dim) * sizeof(float);
   return ZR_OK;
 }
 

@@ -8,17 +8,25 @@
 // All arithmetic and every sum is binary32; outputs are rounded once.
 //
 // Both passes are bound by HBM: the forward must read x and write y, the
-// backward read g and x and write grad_x.  So a row is read once and stays in
-// registers (the variance is the two-pass one, from the differences, at no
-// cost in traffic): G lanes hold a row of up to 32 columns each.  G = 8 for
-// very short rows, a warp up to 1024 columns, a block of 256 up to 8192.
-// Longer rows loop over the row, whose re-reads come from L1 and L2.
+// backward read g and x and write grad_x.  So a row is read once (the variance
+// is the two-pass one, from the differences, at no cost in traffic): G lanes
+// hold a row of up to 32 columns each.  G = 8 for very short rows, a warp up to
+// 1024 columns, a block of 256 up to 8192.  Longer rows loop over the row,
+// whose re-reads come from L1 and L2.
 //
-// In the backward a lane's columns are the same for every row it meets, so
-// the two column sums build up in its registers over a persistent grid's
-// rows; each block adds its row groups in a fixed order and writes one
-// partial row, and the library's second pass adds the partials in order.  No
-// atomics: the order is a function of the shape.
+// The grid is persistent and what it needs is bytes in flight: with 16-byte
+// vectors each lane copies the vectors it will read itself into its own slots
+// of a shared-memory ring, p.stages - 1 rows ahead (cp.async: no registers, and
+// no barrier since no lane reads another's).  A lane's columns are the same for
+// every row it meets, so gamma and beta stay in its registers, and in the
+// backward the two column sums build up there; each block adds its row groups
+// in a fixed order and writes one partial row, and the library's second pass
+// adds the partials in order.  No atomics: the order is a function of the
+// shape.  Arithmetic goes in pairs through the packed binary32 instructions,
+// each lane of which rounds as the scalar one does.
+//
+// Element-wise access (VEC = 1: odd sizes, strides or bases) loads straight
+// into registers.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -113,64 +121,189 @@ __device__ __forceinline__ float norm_sum(float v, float* s) {
   return v;
 }
 
+// ------------------------------------------------------------------ the ring
+
+__device__ __forceinline__ void norm_cp16(uint4* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void norm_commit() {
+  asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
+// All copies but those of the last `stages - 1` commits have landed.
+__device__ __forceinline__ void norm_wait(uint32_t stages) {
+  if (stages == 3) asm volatile("cp.async.wait_group 2;\n" ::: "memory");
+  else asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+}
+// The VEC elements of a 16-byte slot as pairs.
+template <typename E>
+__device__ __forceinline__ void norm_pairs(const uint4* slot, F2* v) {
+  if constexpr (sizeof(E) == 4) {
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(slot);
+    v[0].v = q.x;
+    v[1].v = q.y;
+  } else {
+    const uint4 q = *slot;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+}
+template <typename E, int VEC>
+__device__ __forceinline__ void norm_store_pairs(E* p, const F2* v) {
+  float f[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) f2_unpack(v[i], f[2 * i], f[2 * i + 1]);
+  norm_store<E, VEC>(p, f);
+}
+template <typename E, int VEC>
+__device__ __forceinline__ void norm_affine_pairs(const void* base, int64_t stride, uint32_t vec_ok,
+                                                  uint32_t c, bool in, float none, F2* v) {
+  float f[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) f[j] = 0.f;
+  if (in) norm_affine<E, VEC>(base, stride, vec_ok, c, none, f);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) v[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+  float lo, hi;
+  f2_unpack(a, lo, hi);
+  return lo + hi;
+}
+
 template <typename E, int VEC, int G, int NI>
-__global__ void __launch_bounds__(kNormThreads) k_norm_fwd(const __grid_constant__ NormPlan p) {
+__global__ void __launch_bounds__(kNormThreads, norm_fwd_occ(NI * VEC, VEC))
+k_norm_fwd(const __grid_constant__ NormPlan p) {
   pdl_trigger();
-  __shared__ float s_sum[2][32];
-  const uint32_t lane = threadIdx.x % G;
-  const uint32_t row = blockIdx.x * (kNormThreads / G) + threadIdx.x / G;
-  const bool live = row < p.nrow;  // whole row groups; a block's rows all live when G is a block
-  int64_t off[kMaxOperands];
-  norm_row(p.rows, live ? row : 0, off);
-  const E* x = static_cast<const E*>(p.in[0]) + off[0];
-  const int64_t xs = VEC > 1 ? 1 : p.inner_stride[0];
-  pdl_wait();
-  float v[NI][VEC];
-  float sum = 0.f;
+  constexpr int RPB = kNormThreads / G;
+  __shared__ float s_sum[2][2][32];
+  const uint32_t lane = threadIdx.x % G, grp = threadIdx.x / G;
+  if constexpr (VEC == 1) {
+    const uint32_t row = blockIdx.x * RPB + grp;
+    const bool live = row < p.nrow;  // whole row groups; a block's rows all live when G is a block
+    int64_t off[kMaxOperands];
+    norm_row(p.rows, live ? row : 0, off);
+    const E* x = static_cast<const E*>(p.in[0]) + off[0];
+    pdl_wait();
+    float v[NI];
+    float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const uint32_t c = (i * G + lane) * VEC;
-    if (live && c < p.dim) {
-      norm_load<E, VEC>(x + int64_t(c) * xs, v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t c = i * G + lane;
+      v[i] = live && c < p.dim ? norm_ld(x + int64_t(c) * p.inner_stride[0]) : 0.f;
     }
-  }
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i) sum += v[i];
+    const float mean = __fmul_rn(norm_sum<G>(sum, s_sum[0][0]), p.inv_dim);
+    float sq = 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) sum += v[i][j];
-  const float mean = __fmul_rn(norm_sum<G>(sum, s_sum[0]), p.inv_dim);
-  float sq = 0.f;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const uint32_t c = (i * G + lane) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      v[i][j] -= mean;
-      if (c < p.dim) sq = __fmaf_rn(v[i][j], v[i][j], sq);
+    for (int i = 0; i < NI; ++i) {
+      v[i] -= mean;
+      if (i * G + lane < p.dim) sq = __fmaf_rn(v[i], v[i], sq);
     }
-  }
-  const float var = __fmul_rn(norm_sum<G>(sq, s_sum[1]), p.inv_dim);
-  const float rstd = __frcp_rn(__fsqrt_rn(var + p.eps));
-  if (!live) return;
-  if (lane == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
-  E* y = static_cast<E*>(p.out) + off[kSlotOut];
-  const int64_t ys = VEC > 1 ? 1 : p.inner_stride[kSlotOut];
+    const float var = __fmul_rn(norm_sum<G>(sq, s_sum[0][1]), p.inv_dim);
+    const float rstd = __frcp_rn(__fsqrt_rn(var + p.eps));
+    if (!live) return;
+    if (lane == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    E* y = static_cast<E*>(p.out) + off[kSlotOut];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const uint32_t c = (i * G + lane) * VEC;
-    if (c < p.dim) {
-      float ga[VEC], be[VEC], o[VEC];
-      norm_affine<E, VEC>(p.gamma, p.gamma_stride, p.affine_vec, c, 1.f, ga);
-      norm_affine<E, VEC>(p.beta, p.beta_stride, p.affine_vec, c, 0.f, be);
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t c = i * G + lane;
+      if (c < p.dim) {
+        float ga, be;
+        norm_affine<E, 1>(p.gamma, p.gamma_stride, 0, c, 1.f, &ga);
+        norm_affine<E, 1>(p.beta, p.beta_stride, 0, c, 0.f, &be);
+        st1(y + int64_t(c) * p.inner_stride[kSlotOut], __fmaf_rn(v[i] * rstd, ga, be));
+      }
+    }
+  } else {
+    constexpr int H = VEC / 2;
+    extern __shared__ uint4 s_ring[];  // [stage][row group][NI * G]
+    const uint64_t step = uint64_t(gridDim.x) * RPB;
+    const uint64_t first = uint64_t(blockIdx.x) * RPB + grp;
+    const uint32_t S = p.stages;
+    auto slot = [&](uint32_t stage) { return s_ring + (uint64_t(stage) * RPB + grp) * (NI * G) + lane; };
+    auto fetch = [&](uint32_t stage, uint64_t row) {
+      if (row < p.nrow) {
+        int64_t off[kMaxOperands];
+        norm_row(p.rows, uint32_t(row), off);
+        const E* x = static_cast<const E*>(p.in[0]) + off[0] + lane * VEC;
+        uint4* q = slot(stage);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = __fmaf_rn(v[i][j] * rstd, ga[j], be[j]);
-      norm_store<E, VEC>(y + int64_t(c) * ys, o);
+        for (int i = 0; i < NI; ++i)
+          if ((i * G + lane) * VEC < p.dim) norm_cp16(q + i * G, x + i * G * VEC);
+      }
+      norm_commit();
+    };
+    pdl_wait();
+    for (uint32_t k = 0; k + 1 < S; ++k) fetch(k, first + k * step);
+    F2 ga[NI][H], be[NI][H];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t c = (i * G + lane) * VEC;
+      norm_affine_pairs<E, VEC>(p.gamma, p.gamma_stride, p.affine_vec, c, c < p.dim, 1.f, ga[i]);
+      norm_affine_pairs<E, VEC>(p.beta, p.beta_stride, p.affine_vec, c, c < p.dim, 0.f, be[i]);
+    }
+    uint32_t stage = 0, ahead = S - 1, flip = 0;
+    for (uint64_t r0 = uint64_t(blockIdx.x) * RPB; r0 < p.nrow; r0 += step) {
+      const uint64_t row = r0 + grp;
+      const bool live = row < p.nrow;
+      fetch(ahead, row + (S - 1) * step);
+      norm_wait(S);
+      F2 v[NI][H];
+      F2 acc = f2_splat(0.f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (live && (i * G + lane) * VEC < p.dim) {
+          norm_pairs<E>(slot(stage) + i * G, v[i]);
+#pragma unroll
+          for (int j = 0; j < H; ++j) acc = f2_add(acc, v[i][j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < H; ++j) v[i][j] = f2_splat(0.f);
+        }
+      }
+      const float mean = __fmul_rn(norm_sum<G>(f2_sum(acc), s_sum[flip][0]), p.inv_dim);
+      const F2 minus = f2_splat(-mean);
+      acc = f2_splat(0.f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if ((i * G + lane) * VEC < p.dim) {
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            v[i][j] = f2_add(v[i][j], minus);
+            acc = f2_fma(v[i][j], v[i][j], acc);
+          }
+        }
+      }
+      const float var = __fmul_rn(norm_sum<G>(f2_sum(acc), s_sum[flip][1]), p.inv_dim);
+      flip ^= 1;  // a block's next row writes the other pair: one barrier lies between
+      const float rstd = __frcp_rn(__fsqrt_rn(var + p.eps));
+      if (live) {
+        int64_t off[kMaxOperands];
+        norm_row(p.rows, uint32_t(row), off);
+        if (lane == 0) {
+          if (p.mean) p.mean[row] = mean;
+          if (p.rstd) p.rstd[row] = rstd;
+        }
+        E* y = static_cast<E*>(p.out) + off[kSlotOut] + lane * VEC;
+        const F2 r2 = f2_splat(rstd);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if ((i * G + lane) * VEC < p.dim) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) v[i][j] = f2_fma(f2_mul(v[i][j], r2), ga[i][j], be[i][j]);
+            norm_store_pairs<E, VEC>(y + i * G * VEC, v[i]);
+          }
+        }
+      }
+      if (++stage == S) stage = 0;
+      if (++ahead == S) ahead = 0;
     }
   }
 }
@@ -229,33 +362,10 @@ k_norm_fwd_long(const __grid_constant__ NormPlan p) {
 
 // ------------------------------------------------------------------ backward
 
-// The 16 bytes of VEC elements at `raw` as floats.
-template <typename E, int VEC>
-__device__ __forceinline__ void norm_unpack(const uint4& q, float* v) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(E) == 4) {
-      v[i] = __uint_as_float(w[i]);
-    } else {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
-__device__ __forceinline__ void norm_cp16(uint4* dst, const void* src) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(src) : "memory");
-}
-
-// A row group's lanes keep the two column sums of their columns in registers
-// for all the rows the block meets.  What bounds the pass is the bytes in
-// flight: with 16-byte vectors each lane copies the vectors it will read
-// itself into its own slots of a shared-memory ring, p.stages - 1 rows ahead
-// (cp.async: no registers, and no barrier since no lane reads another's), and
-// reads them twice from there, once for the row's two means and the column
-// sums, once for grad_x.  Keeping the row in registers instead took 222 of
-// them and left 8 warps per SM: [65536, 1024] bf16 137 us against 78.
+// With 16-byte vectors a row waits in the ring and is read twice from there,
+// once for its two means and the column sums, once for grad_x: kept in
+// registers instead it took 222 of them, 8 warps per SM, and [65536, 1024] bf16
+// 137 us.
 template <typename E, int VEC, int G, int NI>
 __global__ void __launch_bounds__(kNormThreads, norm_bwd_occ(NI * VEC, VEC))
 k_norm_bwd(const __grid_constant__ NormPlan p) {
@@ -263,17 +373,17 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
   constexpr int T = kNormThreads;
   constexpr int RPB = T / G;           // rows per block per step
   constexpr int W = G * NI * VEC;      // columns the lanes cover
+  // Pairs: of a vector's neighbours, or (VEC = 1) of columns G apart.
+  constexpr int H = VEC > 1 ? VEC / 2 : 1;
+  constexpr int NP = VEC > 1 ? NI : NI / 2;
   extern __shared__ uint4 s_ring[];    // [stage][row group][g, x][NI * G]; then column sums
   __shared__ float s_sum[2][2][32];
   const uint32_t lane = threadIdx.x % G, grp = threadIdx.x / G;
-  const int64_t gs = VEC > 1 ? 1 : p.inner_stride[0];
-  const int64_t xs = VEC > 1 ? 1 : p.inner_stride[1];
-  const int64_t os = VEC > 1 ? 1 : p.inner_stride[kSlotOut];
-  float acc_g[NI][VEC], acc_b[NI][VEC];
+  F2 acc_g[NP][H], acc_b[NP][H], gam[NP][H];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NP; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc_g[i][j] = acc_b[i][j] = 0.f;
+    for (int j = 0; j < H; ++j) acc_g[i][j] = acc_b[i][j] = f2_splat(0.f);
   const uint64_t step = uint64_t(gridDim.x) * RPB;
   const uint64_t first = uint64_t(blockIdx.x) * RPB + grp;
   const uint32_t S = p.stages;
@@ -281,40 +391,41 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
     return s_ring + ((uint64_t(stage) * RPB + grp) * 2 + a) * (NI * G) + lane;
   };
   auto fetch = [&](uint32_t stage, uint64_t row) {
-    if constexpr (VEC > 1) {
-      if (row < p.nrow) {
-        int64_t off[kMaxOperands];
-        norm_row(p.rows, uint32_t(row), off);
-        const E* g = static_cast<const E*>(p.in[0]) + off[0];
-        const E* x = static_cast<const E*>(p.in[1]) + off[1];
-        uint4* sg = slot(stage, 0);
-        uint4* sx = slot(stage, 1);
+    if (row < p.nrow) {
+      int64_t off[kMaxOperands];
+      norm_row(p.rows, uint32_t(row), off);
+      const E* g = static_cast<const E*>(p.in[0]) + off[0] + lane * VEC;
+      const E* x = static_cast<const E*>(p.in[1]) + off[1] + lane * VEC;
+      uint4* sg = slot(stage, 0);
+      uint4* sx = slot(stage, 1);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const uint32_t c = (i * G + lane) * VEC;
-          if (c < p.dim) {
-            norm_cp16(sg + i * G, g + c);
-            norm_cp16(sx + i * G, x + c);
-          }
+      for (int i = 0; i < NI; ++i) {
+        if ((i * G + lane) * VEC < p.dim) {
+          norm_cp16(sg + i * G, g + i * G * VEC);
+          norm_cp16(sx + i * G, x + i * G * VEC);
         }
       }
-      asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
+    norm_commit();
   };
   pdl_wait();
   if constexpr (VEC > 1)
     for (uint32_t k = 0; k + 1 < S; ++k) fetch(k, first + k * step);
   float mean = first < p.nrow ? p.mean_in[first] : 0.f;
   float rstd = first < p.nrow ? p.rstd_in[first] : 0.f;
-  float gam[NI][VEC];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const uint32_t c = (i * G + lane) * VEC;
-    if (c < p.dim) {
-      norm_affine<E, VEC>(p.gamma, p.gamma_stride, p.affine_vec, c, 1.f, gam[i]);
+  for (int i = 0; i < NP; ++i) {
+    if constexpr (VEC > 1) {
+      const uint32_t c = (i * G + lane) * VEC;
+      norm_affine_pairs<E, VEC>(p.gamma, p.gamma_stride, p.affine_vec, c, c < p.dim, 1.f, gam[i]);
     } else {
+      float f[2] = {0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) gam[i][j] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c = (2 * i + h) * G + lane;
+        if (c < p.dim) norm_affine<E, 1>(p.gamma, p.gamma_stride, 0, c, 1.f, &f[h]);
+      }
+      gam[i][0] = f2_pack(f[0], f[1]);
     }
   }
   uint32_t flip = 0, stage = 0, ahead = S - 1;
@@ -328,66 +439,83 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
     norm_row(p.rows, live ? uint32_t(row) : 0, off);
     if constexpr (VEC > 1) {
       fetch(ahead, row + (S - 1) * step);
-      if (S == 3) asm volatile("cp.async.wait_group 2;\n" ::: "memory");
-      else asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+      norm_wait(S);
     }
-    auto load = [&](int i, uint32_t c, float* gv, float* xv) {
-      if constexpr (VEC > 1) {
-        norm_unpack<E, VEC>(slot(stage, 0)[i * G], gv);
-        norm_unpack<E, VEC>(slot(stage, 1)[i * G], xv);
-      } else {
-        gv[0] = norm_ld(static_cast<const E*>(p.in[0]) + off[0] + int64_t(c) * gs);
-        xv[0] = norm_ld(static_cast<const E*>(p.in[1]) + off[1] + int64_t(c) * xs);
-      }
-    };
-    // One access's values stay in registers between the two walks.
-    float gk[VEC > 1 ? 1 : NI], xk[VEC > 1 ? 1 : NI];
+    const F2 minus = f2_splat(-mean), r2 = f2_splat(rstd);
+    F2 sq = f2_splat(0.f), sqx = f2_splat(0.f);
+    F2 gk[VEC > 1 ? 1 : NP], xk[VEC > 1 ? 1 : NP];  // VEC = 1: the row
     if constexpr (VEC == 1) {
+      float gv[NI], xv[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const uint32_t c = i * G + lane;
-        gk[i] = 0.f;
-        xk[i] = mean;
-        if (live && c < p.dim) load(i, c, &gk[i], &xk[i]);
+        gv[i] = 0.f;
+        xv[i] = mean;
+        if (live && c < p.dim) {
+          gv[i] = norm_ld(static_cast<const E*>(p.in[0]) + off[0] + int64_t(c) * p.inner_stride[0]);
+          xv[i] = norm_ld(static_cast<const E*>(p.in[1]) + off[1] + int64_t(c) * p.inner_stride[1]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        gk[i] = f2_pack(gv[2 * i], gv[2 * i + 1]);
+        xk[i] = f2_pack(xv[2 * i], xv[2 * i + 1]);
       }
     }
-    float sq = 0.f, sqx = 0.f;
+    auto load = [&](int i, F2* gv, F2* xv) {
+      if constexpr (VEC > 1) {
+        norm_pairs<E>(slot(stage, 0) + i * G, gv);
+        norm_pairs<E>(slot(stage, 1) + i * G, xv);
+      } else {
+        gv[0] = gk[i];
+        xv[0] = xk[i];
+      }
+    };
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const uint32_t c = (i * G + lane) * VEC;
-      if (live && c < p.dim) {
-        float gv[VEC], xv[VEC];
-        if constexpr (VEC > 1) load(i, c, gv, xv);
-        else { gv[0] = gk[i]; xv[0] = xk[i]; }
+    for (int i = 0; i < NP; ++i) {
+      if (live && (VEC == 1 || (i * G + lane) * VEC < p.dim)) {
+        F2 gv[H], xv[H];
+        load(i, gv, xv);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (xv[j] - mean) * rstd;
-          acc_b[i][j] += gv[j];
-          acc_g[i][j] = __fmaf_rn(gv[j], xh, acc_g[i][j]);
-          const float q = gv[j] * gam[i][j];
-          sq += q;
-          sqx = __fmaf_rn(q, xh, sqx);
+        for (int j = 0; j < H; ++j) {
+          const F2 xh = f2_mul(f2_add(xv[j], minus), r2);
+          acc_b[i][j] = f2_add(acc_b[i][j], gv[j]);
+          acc_g[i][j] = f2_fma(gv[j], xh, acc_g[i][j]);
+          const F2 q = f2_mul(gv[j], gam[i][j]);
+          sq = f2_add(sq, q);
+          sqx = f2_fma(q, xh, sqx);
         }
       }
     }
     if (p.out) {
-      const float m1 = __fmul_rn(norm_sum<G>(sq, s_sum[flip][0]), p.inv_dim);
-      const float m2 = __fmul_rn(norm_sum<G>(sqx, s_sum[flip][1]), p.inv_dim);
+      const float m1 = __fmul_rn(norm_sum<G>(f2_sum(sq), s_sum[flip][0]), p.inv_dim);
+      const float m2 = __fmul_rn(norm_sum<G>(f2_sum(sqx), s_sum[flip][1]), p.inv_dim);
       flip ^= 1;  // a block's next row writes the other pair: one barrier lies between
+      // grad_x = g (gamma rstd) - (xh (m2 rstd) + m1 rstd)
+      const F2 a = f2_splat(-__fmul_rn(m2, rstd)), b = f2_splat(-__fmul_rn(m1, rstd));
       E* o = static_cast<E*>(p.out) + off[kSlotOut];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
+      for (int i = 0; i < NP; ++i) {
         const uint32_t c = (i * G + lane) * VEC;
-        if (live && c < p.dim) {
-          float gv[VEC], xv[VEC];
-          if constexpr (VEC > 1) load(i, c, gv, xv);
-          else { gv[0] = gk[i]; xv[0] = xk[i]; }
+        if (live && (VEC == 1 || c < p.dim)) {
+          F2 gv[H], xv[H];
+          load(i, gv, xv);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float xh = (xv[j] - mean) * rstd;
-            xv[j] = rstd * __fmaf_rn(-xh, m2, gv[j] * gam[i][j] - m1);
+          for (int j = 0; j < H; ++j) {
+            const F2 xh = f2_mul(f2_add(xv[j], minus), r2);
+            xv[j] = f2_fma(gv[j], f2_mul(gam[i][j], r2), f2_fma(xh, a, b));
           }
-          norm_store<E, VEC>(o + int64_t(c) * os, xv);
+          if constexpr (VEC > 1) {
+            norm_store_pairs<E, VEC>(o + c, xv);
+          } else {
+            float f[2];
+            f2_unpack(xv[0], f[0], f[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t ch = (2 * i + h) * G + lane;
+              if (ch < p.dim) st1(o + int64_t(ch) * p.inner_stride[kSlotOut], f[h]);
+            }
+          }
         }
       }
     }
@@ -399,35 +527,39 @@ k_norm_bwd(const __grid_constant__ NormPlan p) {
   if (!p.partial) return;
   const uint32_t nw = p.want_gamma + p.want_beta;
   float* part = p.partial + uint64_t(blockIdx.x) * nw * p.dim;
-  float* s_col = reinterpret_cast<float*>(s_ring);  // [W]: the ring's copies are all in
+  // Every row group's sums side by side (the ring's copies are all in), then
+  // each column's in the groups' order.
+  float* s_col = reinterpret_cast<float*>(s_ring);  // [row group][W]
+  if constexpr (G <= 32) {
+    if constexpr (VEC > 1) asm volatile("cp.async.wait_all;\n" ::: "memory");
+    __syncthreads();
+  }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    float(&acc)[NI][VEC] = k == 0 ? acc_g : acc_b;
+    F2(&acc)[NP][H] = k == 0 ? acc_g : acc_b;
     if (!(k == 0 ? p.want_gamma : p.want_beta)) continue;
-    if constexpr (G > 32) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const uint32_t c = (i * G + lane) * VEC;
+    for (int i = 0; i < NP; ++i) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (c + j < p.dim) part[c + j] = acc[i][j];
-      }
-    } else {
-      // The row groups add into s_col one after another: a fixed order.
-      if constexpr (VEC > 1) asm volatile("cp.async.wait_all;\n" ::: "memory");
-      for (int t = 0; t < RPB; ++t) {
-        __syncthreads();
-        if (int(grp) == t) {
+      for (int j = 0; j < H; ++j) {
+        float v[2];
+        f2_unpack(acc[i][j], v[0], v[1]);
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const uint32_t c = (i * G + lane) * VEC;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) s_col[c + j] = (t ? s_col[c + j] : 0.f) + acc[i][j];
-          }
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t c = VEC > 1 ? (i * G + lane) * VEC + 2 * j + h : (2 * i + h) * G + lane;
+          if constexpr (G <= 32) s_col[grp * W + c] = v[h];
+          else if (c < p.dim) part[c] = v[h];
         }
       }
+    }
+    if constexpr (G <= 32) {
       __syncthreads();
-      for (uint32_t c = threadIdx.x; c < p.dim; c += T) part[c] = s_col[c];
+      for (uint32_t c = threadIdx.x; c < p.dim; c += T) {
+        float t = s_col[c];
+#pragma unroll
+        for (int r = 1; r < RPB; ++r) t += s_col[r * W + c];
+        part[c] = t;
+      }
       __syncthreads();
     }
     part += p.dim;

@@ -30,17 +30,21 @@ struct NormPlan {
   // group == 0: rows longer than a block holds in registers.
   uint32_t group, ni;
   uint32_t n_cta;
-  uint32_t stages, smem;     // k_norm_bwd: ring stages (2 or 3), dynamic shared memory
+  uint32_t stages, smem;     // ring stages (2 or 3), dynamic shared memory
 };
 
 constexpr int kNormThreads = 256;
+// k_norm_fwd likewise.
+ZR_CX int norm_fwd_occ(int cols, int vec) {
+  return vec == 1 ? (cols > 16 ? 3 : 4) : (cols > 16 ? 2 : (cols > 8 ? 3 : 4));
+}
 // k_norm_bwd: CTAs per SM its registers allow without spills, by columns per
 // lane (element-wise access keeps the row in registers too).
 ZR_CX int norm_bwd_occ(int cols, int vec) {
   return vec == 1 ? (cols > 16 ? 1 : (cols > 8 ? 2 : (cols > 4 ? 3 : 4)))
                   : (cols > 16 ? 2 : (cols > 8 ? 3 : 4));
 }
-constexpr int kNormSmemMax = 224 * 1024; // k_norm_bwd's dynamic shared memory, all CTAs of an SM
+constexpr int kNormSmemMax = 224 * 1024; // dynamic shared memory of all CTAs of an SM
 constexpr uint32_t kNormMaxCols = 32;    // columns per lane held in registers
 constexpr uint32_t kNormLongThreads = 1024;
 constexpr uint32_t kNormSumCols = 32;    // k_norm_sums: columns per CTA
