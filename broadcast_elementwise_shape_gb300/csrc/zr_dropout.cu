@@ -67,9 +67,8 @@ __device__ __forceinline__ void dropout_one(const DropPlan& p, uint32_t word, in
   st1(static_cast<E*>(p.out) + o_off, y);
 }
 
-// 16-byte vectors: VEC consecutive elements of one row, VEC / 4 counters.
-// Bound by HBM in principle (read x and the residual, write out); see the
-// launch rule below for the split.
+// 16-byte vectors: VEC consecutive elements of one row, VEC / 4 counters.  Must
+// read x and the residual and write out; what bounds it is at drop_unroll.
 template <typename E, int VEC, bool RES, int U>
 __global__ void __launch_bounds__(kThreads) k_dropout_vec(const __grid_constant__ DropPlan p) {
   pdl_trigger();
@@ -175,7 +174,12 @@ __global__ void __launch_bounds__(kThreads) k_dropout_any(const __grid_constant_
   }
 }
 
-constexpr int kDropUnroll = 4;
+// Vectors per thread, loaded before the first is used.  binary32 is bound by
+// HBM (without a residual [65536, 1536] 120 us with 3 and 127 with 1, with one
+// [16384, 768] 21.7 us with 2 and 22.8 with 4); bfloat16 by the generator's
+// integer multiplications (25 M counters in 95 us), where more warps help
+// ([16384, 768] with a residual 14.3 us with 2 and 16.1 with 4).
+ZR_CX int drop_unroll(int es, bool residual) { return es == 4 && !residual ? 3 : 2; }
 
 struct DropSet {
   int es = 4, vec = 1;
@@ -192,9 +196,10 @@ cudaError_t launch(const DropSet& S, cudaStream_t s) {
   if (S.vec == 1)
     return p.residual ? launch_k(k_dropout_any<E, true>, n, kThreads, 0, s, p)
                       : launch_k(k_dropout_any<E, false>, n, kThreads, 0, s, p);
-  constexpr int U = kDropUnroll;
-  return p.residual ? launch_k(k_dropout_vec<E, VEC, true, U>, n, kThreads, 0, s, p)
-                    : launch_k(k_dropout_vec<E, VEC, false, U>, n, kThreads, 0, s, p);
+  constexpr int es = sizeof(E);
+  return p.residual
+             ? launch_k(k_dropout_vec<E, VEC, true, drop_unroll(es, true)>, n, kThreads, 0, s, p)
+             : launch_k(k_dropout_vec<E, VEC, false, drop_unroll(es, false)>, n, kThreads, 0, s, p);
 }
 
 int plan_dropout(zr_dtype dtype, const zr_tensor& x, const zr_tensor* residual, double prob,
@@ -296,7 +301,7 @@ int plan_dropout(zr_dtype dtype, const zr_tensor& x, const zr_tensor* residual, 
   }
   S->vec = wide ? V : 1;
   if (!wide) p.nitems = (p.numel + 3) / 4;
-  const uint64_t per = uint64_t(kThreads) * (wide ? kDropUnroll : 1);
+  const uint64_t per = uint64_t(kThreads) * (wide ? drop_unroll(S->es, res) : 1);
   S->n_cta = (p.nitems + per - 1) / per;
   return S->n_cta < (uint64_t(1) << 31) ? ZR_OK : ZR_ERR_SIZE;
 }
