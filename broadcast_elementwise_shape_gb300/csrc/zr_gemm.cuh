@@ -30,11 +30,14 @@ constexpr uint32_t kGemmK = 64;        // k per block (128 bytes)
 constexpr uint32_t kABytes = kGemmM * kGemmK * 2;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-template <int CG>
+// PARTS = 3: a stage holds all three parts of both operands, which its six
+// products share; half the traffic of loading a pair of parts for each.  Tiles
+// of a single CTA are then at most 128 columns wide.
+template <int CG, int PARTS>
 struct GemmCfg {
-  static constexpr uint32_t kBBytes = 256 / CG * kGemmK * 2;
-  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = CG == 1 ? 4 : 6;
+  static constexpr uint32_t kBBytes = (PARTS == 3 ? 128 : 256 / CG) * kGemmK * 2;
+  static constexpr uint32_t kStageBytes = PARTS * (kABytes + kBBytes);
+  static constexpr int kStages = PARTS == 3 ? 2 : (CG == 1 ? 4 : 6);
   // The ring, 4 KB of output staging per epilogue warp, alignment.
   static constexpr uint32_t kOutAt = kStages * kStageBytes;
   static constexpr uint32_t kSmem = kOutAt + 8 * 4096 + 1024;
@@ -240,16 +243,14 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmPlan& p, uint32_t t) {
   return g;
 }
 
-// Pairs of parts (a, b) in the order they are added: smallest products first,
-// so that the sum is small until the last, largest pair (parts 0, 0).
-__device__ __forceinline__ void gemm_combo(uint32_t n_combo, uint32_t i, int* a, int* b) {
-  if (n_combo == 1) {
-    *a = *b = 0;
-    return;
-  }
-  const uint32_t pa = 0x001012u, pb = 0x010210u;  // hex digit i, lowest first
-  *a = int((pa >> (4 * i)) & 3u);
-  *b = int((pb >> (4 * i)) & 3u);
+// The pairs of parts (a, b) of a block of k in the order they are added:
+// smallest products first, so that the sum is small until the last, largest
+// pair (parts 0, 0).
+template <int PARTS>
+__device__ __forceinline__ constexpr uint32_t gemm_pair(int i, int operand) {
+  if (PARTS == 1) return 0;
+  constexpr uint32_t pairs[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
+  return pairs[i][operand];
 }
 
 // ------------------------------------------------------------------ epilogues
@@ -404,7 +405,7 @@ struct EpiGrad {
       for (int i = 0; i < 64; ++i) v[i] = e.ok ? 0.f : qnan();
     }
     epi_store(&q.c, e, c, 0, v);
-    for (uint32_t part = 1; part < p.n_part; ++part) {
+    for (uint32_t part = 1; part < p.parts; ++part) {
 #pragma unroll
       for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
       epi_store(&q.c, e, c, int(part), v);
@@ -486,9 +487,9 @@ struct EpiOf<kEpiOut> { using type = EpiOut; };
 // 2^-24 of their size per 16 terms (7.1e-5 at k = 16384), always towards zero.
 // Results of 24 bits need the chunks; those of 8 bits do without until k is
 // some hundred thousand.
-template <int EPI, int CG, bool SUM>
+template <int EPI, int CG, bool SUM, int PARTS>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant__ GemmPlan p) {
-  using Cfg = GemmCfg<CG>;
+  using Cfg = GemmCfg<CG, PARTS>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint64_t s_full[S], s_empty[S], s_tfull[2], s_tempty[2];
@@ -532,32 +533,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       const int m0 = int((g.mt * CG + rank) * kGemmM);
       const int n0 = int(g.nt * q.tn + rank * tnc);
       const uint32_t nb = q.b_mn ? (tnc + 63) / 64 * 8192 : tnc * 128;
-      for (uint32_t k1 = 0; k1 < q.n_kb && ok; k1 += q.chunk)
-      for (uint32_t c = 0; c < p.n_combo && ok; ++c) {
-        int pa, pb;
-        gemm_combo(p.n_combo, c, &pa, &pb);
-        const uint32_t k2 = k1 + q.chunk < q.n_kb ? k1 + q.chunk : q.n_kb;
-        for (uint32_t kb = k1; kb < k2; ++kb) {
-          if (!mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort)) { ok = false; break; }
-          const uint32_t local = smem_u32(&s_full[stage]);
-          if (rank == 0) mbar_expect(local, (kABytes + nb) * CG);
-          const uint32_t bar = CG == 1 ? local : cluster_addr(local, 0);
-          const uint32_t sa = ring + stage * Cfg::kStageBytes, sb = sa + kABytes;
-          const int k0 = int(kb * kGemmK);
+      for (uint32_t kb = 0; kb < q.n_kb; ++kb) {
+        if (!mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort)) { ok = false; break; }
+        const uint32_t local = smem_u32(&s_full[stage]);
+        if (rank == 0) mbar_expect(local, (kABytes + nb) * PARTS * CG);
+        const uint32_t bar = CG == 1 ? local : cluster_addr(local, 0);
+        const int k0 = int(kb * kGemmK);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          const uint32_t sa = ring + stage * Cfg::kStageBytes + part * kABytes;
+          const uint32_t sb = ring + stage * Cfg::kStageBytes + PARTS * kABytes + part * Cfg::kBBytes;
           if (q.a_mn) {
-            tma_load<CG>(sa, &q.a, bar, m0, k0, pa);
-            tma_load<CG>(sa + 8192, &q.a, bar, m0 + 64, k0, pa);
+            tma_load<CG>(sa, &q.a, bar, m0, k0, part);
+            tma_load<CG>(sa + 8192, &q.a, bar, m0 + 64, k0, part);
           } else {
-            tma_load<CG>(sa, &q.a, bar, k0, m0, pa);
+            tma_load<CG>(sa, &q.a, bar, k0, m0, part);
           }
           if (q.b_mn) {
             for (uint32_t j = 0; j < tnc; j += 64)
-              tma_load<CG>(sb + j * 128, &q.b, bar, n0 + int(j), k0, pb);
+              tma_load<CG>(sb + j * 128, &q.b, bar, n0 + int(j), k0, part);
           } else {
-            tma_load<CG>(sb, &q.b, bar, k0, n0, pb);
+            tma_load<CG>(sb, &q.b, bar, k0, n0, part);
           }
-          if (++stage == S) { stage = 0; phase ^= 1; }
         }
+        if (++stage == S) { stage = 0; phase ^= 1; }
       }
     }
     // Every slot is read before the CTA may end (and its peer's signals are in).
@@ -581,15 +580,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
         if (!mbar_wait(smem_u32(&s_tempty[buf]), ((it >> 1) & 1) ^ 1, abort)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
-        const uint32_t nk = (q.n_kb - k1 < q.chunk ? q.n_kb - k1 : q.chunk) * p.n_combo;
+        const uint32_t nk = q.n_kb - k1 < q.chunk ? q.n_kb - k1 : q.chunk;
         for (uint32_t kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(smem_u32(&s_full[stage]), phase, abort)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = ring + stage * Cfg::kStageBytes;
-          const uint64_t da = operand_desc(sa, q.a_mn), db = operand_desc(sa + kABytes, q.b_mn);
+          const uint64_t da = operand_desc(sa, q.a_mn);
+          const uint64_t db = operand_desc(sa + PARTS * kABytes, q.b_mn);
 #pragma unroll
-          for (uint32_t j = 0; j < kGemmK / 16; ++j)
-            tc_mma<CG>(d, da + j * ka, db + j * kb16, idesc, (kb | j) != 0);
+          for (int i = 0; i < (PARTS == 3 ? 6 : 1); ++i) {
+            const uint64_t pa = da + gemm_pair<PARTS>(i, 0) * (kABytes >> 4);
+            const uint64_t pb = db + gemm_pair<PARTS>(i, 1) * (Cfg::kBBytes >> 4);
+#pragma unroll
+            for (uint32_t j = 0; j < kGemmK / 16; ++j)
+              tc_mma<CG>(d, pa + j * ka, pb + j * kb16, idesc, (kb | i | j) != 0);
+          }
           tc_commit<CG>(smem_u32(&s_empty[stage]));
           if (++stage == S) { stage = 0; phase ^= 1; }
         }

@@ -11,8 +11,8 @@ namespace zr {
 // One product out[m, n] = sum_k A[m, k] B[n, k] of bfloat16 operands, binary32
 // accumulation.  Each operand is a 3-d tensor map over (inner, outer, part):
 // K-major operands have k as the inner (contiguous) dim, MN-major ones m or n.
-// Parts are the pieces of a binary32 operand (zr_xent.cu): the product runs
-// over n_combo pairs of parts.
+// Parts: one, or the three that a binary32 operand is split into (zr_xent.cu),
+// whose product is the sum of six.
 struct GemmProblem {
   CUtensorMap a, b;
   uint32_t m, n, k;
@@ -40,7 +40,7 @@ enum GemmEpilogue : int {
 
 struct GemmPlan {
   GemmProblem pr[2];
-  uint32_t n_prob, n_combo;
+  uint32_t n_prob, parts;
   uint32_t tiles0, tiles;    // tiles of problem 0, of both
   uint32_t m_fast;           // consecutive tiles walk m first
   // Two problems' tiles over `workers` clusters (GemmWalk).
@@ -60,7 +60,6 @@ struct GemmPlan {
   const float* row_scale;    // [m], or null (1)
   int64_t ignore_index, vocab;
   int64_t label_base;        // column 0 of this product is this label
-  uint32_t n_part;           // parts of G, stored through pr[0].c
 };
 
 // The tiles of worker w, in order: its share of problem 0 round-robin, then of
@@ -104,7 +103,8 @@ ZR_GEMM_HD uint32_t gemm_next(const GemmPlan& p, GemmWalk* g) {
 }
 
 // grid: CTAs (a multiple of cg); cg: CTAs per cluster, 1 or 2.  sum: chunks of
-// k are added in registers (else every problem's chunk is its whole k).
+// k are added in registers (else every problem's chunk is its whole k); always
+// with three parts.
 cudaError_t launch_gemm(int epi, int cg, bool sum, const GemmPlan& p, unsigned grid, cudaStream_t s);
 
 }  // namespace zr

@@ -5,19 +5,19 @@
 namespace zr {
 namespace {
 
-template <int EPI, int CG, bool SUM>
+template <int EPI, int CG, bool SUM, int PARTS>
 cudaError_t go(const GemmPlan& p, unsigned grid, cudaStream_t s) {
-  auto* k = k_gemm<EPI, CG, SUM>;
-  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), int(GemmCfg<CG>::kSmem));
+  auto* k = k_gemm<EPI, CG, SUM, PARTS>;
+  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), int(GemmCfg<CG, PARTS>::kSmem));
   if (e != cudaSuccess) return e;
-  if (CG == 1) return launch_k(k, grid, kGemmThreads, GemmCfg<CG>::kSmem, s, p);
-  return launch_k_cluster(k, grid, kGemmThreads, GemmCfg<CG>::kSmem, s, CG, p);
+  if (CG == 1) return launch_k(k, grid, kGemmThreads, GemmCfg<CG, PARTS>::kSmem, s, p);
+  return launch_k_cluster(k, grid, kGemmThreads, GemmCfg<CG, PARTS>::kSmem, s, CG, p);
 }
 
-template <int EPI>
-cudaError_t pick(int cg, bool sum, const GemmPlan& p, unsigned grid, cudaStream_t s) {
-  if (cg == 1) return sum ? go<EPI, 1, true>(p, grid, s) : go<EPI, 1, false>(p, grid, s);
-  return sum ? go<EPI, 2, true>(p, grid, s) : go<EPI, 2, false>(p, grid, s);
+template <int EPI, int CG>
+cudaError_t pick(bool sum, const GemmPlan& p, unsigned grid, cudaStream_t s) {
+  if (p.parts == 3) return go<EPI, CG, true, 3>(p, grid, s);
+  return sum ? go<EPI, CG, true, 1>(p, grid, s) : go<EPI, CG, false, 1>(p, grid, s);
 }
 
 }  // namespace
@@ -27,10 +27,15 @@ cudaError_t launch_gemm(int epi, int cg, bool sum, const GemmPlan& p, unsigned g
   if (grid == 0 || (cg != 1 && cg != 2) || grid % unsigned(cg) != 0) return cudaErrorInvalidValue;
   for (uint32_t i = 0; i < p.n_prob; ++i)
     if (p.pr[i].chunk == 0 || (!sum && p.pr[i].chunk < p.pr[i].n_kb)) return cudaErrorInvalidValue;
+  if ((p.parts != 1 && p.parts != 3) || (p.parts == 3 && !sum)) return cudaErrorInvalidValue;
+  const uint32_t widest = p.parts == 3 && cg == 1 ? 128 : 256;
+  for (uint32_t i = 0; i < p.n_prob; ++i)
+    if (p.pr[i].tn > widest) return cudaErrorInvalidValue;
+  const bool two = cg == 2;
   switch (epi) {
-    case kEpiLse: return pick<kEpiLse>(cg, sum, p, grid, s);
-    case kEpiGrad: return pick<kEpiGrad>(cg, sum, p, grid, s);
-    case kEpiOut: return pick<kEpiOut>(cg, sum, p, grid, s);
+    case kEpiLse: return two ? pick<kEpiLse, 2>(sum, p, grid, s) : pick<kEpiLse, 1>(sum, p, grid, s);
+    case kEpiGrad: return two ? pick<kEpiGrad, 2>(sum, p, grid, s) : pick<kEpiGrad, 1>(sum, p, grid, s);
+    case kEpiOut: return two ? pick<kEpiOut, 2>(sum, p, grid, s) : pick<kEpiOut, 1>(sum, p, grid, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) k_xent_prep(const __grid_constant__ 
                                        : r.grad_loss[0];
 }
 
-constexpr int kRowsThreads = 1024;
+constexpr int kRowsThreads = 256;
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -178,8 +178,13 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// One warp joins a row's partial maxima and sums in a fixed order.
-__device__ __forceinline__ void xent_row(const XentRows& p, uint32_t r, uint32_t lane) {
+// One warp joins a row's partial maxima and sums in a fixed order.  Returns the
+// row's loss (0 when it is left out), *used: whether it takes part.
+__device__ __forceinline__ float xent_row(const XentRows& p, uint32_t r, uint32_t lane, bool* used) {
+  const int64_t y = row_label(p, r);
+  const bool known = y >= 0 && y < p.vocab;
+  *used = y != p.ignore_index;
+  const float at = known ? p.at[r] : __uint_as_float(0x7FFFFFFFu);  // no class: NaN
   const float2* q = p.partial + uint64_t(r) * p.slots;
   // 512 slots' worth stays in registers between the two walks.
   float2 v[16];
@@ -200,78 +205,86 @@ __device__ __forceinline__ void xent_row(const XentRows& p, uint32_t r, uint32_t
     const float2 w = q[i];
     s = __fmaf_rn(w.y, expf(w.x - base), s);
   }
-  s = warp_sum(s);
-  if (lane == 0) {
-    const float lse = m + logf(s);
-    p.lse[r] = lse;
-    const int64_t y = row_label(p, r);
-    float loss = 0.f;
-    if (y != p.ignore_index)
-      loss = y < 0 || y >= p.vocab ? __uint_as_float(0x7FFFFFFFu) : lse - p.at[r];
-    p.row_loss[r] = loss;
-  }
+  const float lse = m + logf(warp_sum(s));
+  if (lane == 0) p.lse[r] = lse;
+  return *used ? lse - at : 0.f;
 }
 
-// Sum or mean of the rows' losses, by one block in a fixed order.
-__device__ __forceinline__ void xent_total(const XentRows& p, uint32_t* s_cnt, float* s_sum) {
-  uint32_t cnt = 0;
-  Kahan acc;
-  acc.init();
-  for (uint32_t r = threadIdx.x; r < p.n; r += kRowsThreads) {
-    cnt += row_label(p, r) != p.ignore_index;
-    acc.add(__ldcg(p.row_loss + r));
-  }
-  cnt = block_count<kRowsThreads>(cnt, s_cnt);
-  const float v = warp_sum(acc.s);
+constexpr uint32_t kRowsOneBlock = 32;  // rows that one block joins and totals
+
+// Sum or mean of this thread's share of the losses and counts over the block.
+__device__ __forceinline__ void xent_total(const XentRows& p, float v, uint32_t cnt, uint32_t* s_cnt,
+                                           float* s_sum) {
+  v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
-  __syncthreads();
+  cnt = block_count<kRowsThreads>(cnt, s_cnt);
   if (threadIdx.x < 32) {
-    const float t = warp_sum(s_sum[threadIdx.x]);
+    const float t = warp_sum(threadIdx.x < kRowsThreads / 32 ? s_sum[threadIdx.x] : 0.f);
     if (threadIdx.x == 0)
       *p.loss = p.reduction == ZR_MEAN ? (cnt ? __fdiv_rn(t, float(cnt)) : 0.f) : t;
   }
 }
-
-constexpr uint32_t kRowsOneBlock = 256;  // rows that one block joins and totals in one launch
 
 // ALL: one block joins every row.  Else a warp per row; the block that
 // finishes last totals the rows (which one that is changes nothing in the sum).
 template <bool ALL>
 __global__ void __launch_bounds__(kRowsThreads) k_xent_rows(const __grid_constant__ XentRows p) {
   pdl_trigger();
-  __shared__ uint32_t s_cnt[32];
-  __shared__ float s_sum[32];
+  __shared__ uint32_t s_cnt[kRowsThreads / 32];
+  __shared__ float s_sum[kRowsThreads / 32];
   __shared__ bool s_last;
   const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  bool used = false;
   pdl_wait();
   if constexpr (ALL) {
-    for (uint32_t r = w; r < p.n; r += kRowsThreads / 32) xent_row(p, r, lane);
-    if (p.reduction == ZR_NONE) return;
-    __syncthreads();
-  } else {
-    const uint32_t r = blockIdx.x * (kRowsThreads / 32) + w;
-    if (r < p.n) xent_row(p, r, lane);
-    if (p.reduction == ZR_NONE) return;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(p.ticket, 1u) + 1 == gridDim.x;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
+    Kahan acc;
+    acc.init();
+    uint32_t cnt = 0;
+    for (uint32_t r = w; r < p.n; r += kRowsThreads / 32) {
+      const float loss = xent_row(p, r, lane, &used);
+      if (lane == 0) {
+        if (p.reduction == ZR_NONE) p.row_loss[r] = loss;
+        acc.add(loss);
+        cnt += used;
+      }
+    }
+    if (p.reduction != ZR_NONE) xent_total(p, acc.s, cnt, s_cnt, s_sum);
+    return;
   }
-  xent_total(p, s_cnt, s_sum);
+  const uint32_t r = blockIdx.x * (kRowsThreads / 32) + w;
+  if (r < p.n) {
+    const float loss = xent_row(p, r, lane, &used);
+    if (lane == 0) p.row_loss[r] = loss;
+  }
+  if (p.reduction == ZR_NONE) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(p.ticket, 1u) + 1 == gridDim.x;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  uint32_t cnt = 0;
+  Kahan acc;
+  acc.init();
+#pragma unroll 8
+  for (uint32_t i = threadIdx.x; i < p.n; i += kRowsThreads) {
+    cnt += row_label(p, i) != p.ignore_index;
+    acc.add(__ldcg(p.row_loss + i));
+  }
+  xent_total(p, acc.s, cnt, s_cnt, s_sum);
 }
 
 // ------------------------------------------------------------------ few rows
 
 // Forward for at most kFewRows rows of x (generation, scoring): bound by
-// reading w once.  A warp takes four rows of w at a time, its lanes 16 bytes
-// each, all of them in flight before the first is used; x waits in shared
-// memory as binary32, and so does the arithmetic run on either storage.  A
-// warp keeps a running maximum and sum per row of x, a block joins its warps'
-// in order.  The tensor-core path reads w in tiles of 256 rows, too few to
-// fill the GPU evenly, and every one of its 128-row blocks of x is padding but
-// for a few rows.
+// reading w once.  Each warp takes an equal run of w's rows, two at a time, its
+// lanes 16 bytes each, with the next loads in flight while the last are used;
+// x waits in shared memory as binary32, and so does the arithmetic run on
+// either storage.  A warp keeps a running maximum and sum per row of x, a
+// block joins its warps' in order.  The tensor-core path reads w in tiles of
+// 256 rows, too few to fill the GPU evenly, and every one of its 128-row blocks
+// of x is padding but for a few rows.  One row against [50001, 768] bf16:
+// 19 us a call (slope 6.9 TB/s); the tensor-core path 23.
 struct FewPlan {
   const void* x;             // packed or as given: rows of pitch xp
   const void* w;
@@ -285,25 +298,55 @@ struct FewPlan {
 };
 constexpr uint32_t kFewRows = 4;
 constexpr uint32_t kFewMaxDim = 12288;  // x in shared memory: 4 rows of it as binary32
-constexpr int kFewBlocks = 2;           // CTAs per SM
+constexpr int kFewBlocks = 3;           // CTAs per SM (2 for four rows of x)
 
 template <typename E, int NT>
-__global__ void __launch_bounds__(kThreads, kFewBlocks) k_xent_few(const __grid_constant__ FewPlan p) {
+__global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : kFewBlocks)
+k_xent_few(const __grid_constant__ FewPlan p) {
   pdl_trigger();
   constexpr int V = 16 / sizeof(E);    // elements per access
-  constexpr int R = 4;                 // rows of w at a time
+  constexpr int R = 2;                 // rows of w at a time
   constexpr int U = 3;                 // accesses per row in flight
   extern __shared__ float s_x[];       // [NT][dim padded to 32 V]
   __shared__ float2 s_part[kThreads / 32][NT];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t padded = (p.dim + 32 * V - 1) / (32 * V) * (32 * V);
+  const uint32_t steps = (p.dim + 32 * V - 1) / (32 * V);
+  const uint32_t padded = steps * 32 * V;
+  const uint32_t nw = gridDim.x * (kThreads / 32), me = blockIdx.x * (kThreads / 32) + warp;
+  const uint32_t lo = uint32_t(uint64_t(p.vocab) * me / nw);
+  const uint32_t hi = uint32_t(uint64_t(p.vocab) * (me + 1) / nw);
   pdl_wait();
+  // The position of the next loads: rows v, v + 1, accesses k .. k + U - 1.
+  uint32_t lv = lo, lk = 0;
+  auto load = [&](uint4 (&q)[U][R]) {
+    if (lv >= hi) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const E* row = static_cast<const E*>(p.w) + int64_t(lv + r < hi ? lv + r : lv) * p.wp;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t c = ((lk + u) * 32 + lane) * V;
+        q[u][r] = make_uint4(0, 0, 0, 0);
+        if (c + V <= p.dim) {
+          q[u][r] = __ldg(reinterpret_cast<const uint4*>(row + c));
+        } else if (c < p.dim) {
+          E tail[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) tail[j] = c + j < p.dim ? row[c + j] : E(0.f);
+          q[u][r] = *reinterpret_cast<const uint4*>(tail);
+        }
+      }
+    }
+    lk += U;
+    if (lk >= steps) { lk = 0; lv += R; }
+  };
+  uint4 qa[U][R], qb[U][R];
+  load(qa);
   for (uint32_t i = threadIdx.x; i < NT * padded; i += kThreads) {
     const uint32_t t = i / padded, c = i - t * padded;
     s_x[i] = t < p.n && c < p.dim
                  ? ld1(static_cast<const E*>(p.x) + int64_t(t) * p.xp + c, false) : 0.f;
   }
-  __syncthreads();
   int64_t label[NT];
   float m[NT], s[NT];
 #pragma unroll
@@ -316,63 +359,42 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_xent_few(const __grid_
                      ? static_cast<const int64_t*>(p.labels)[int64_t(t) * p.label_stride]
                      : int64_t(static_cast<const int32_t*>(p.labels)[int64_t(t) * p.label_stride]);
   }
-  const uint32_t steps = padded / (32 * V);
-  const uint32_t groups = (p.vocab + R - 1) / R;
-  for (uint32_t g = blockIdx.x * (kThreads / 32) + warp; g < groups; g += gridDim.x * (kThreads / 32)) {
-    const uint32_t v0 = g * R;
-    const E* row[R];
+  __syncthreads();
+  float acc[R][NT];
 #pragma unroll
-    for (int r = 0; r < R; ++r)  // past the end: the last row again, left out below
-      row[r] = static_cast<const E*>(p.w) + int64_t(v0 + r < p.vocab ? v0 + r : p.vocab - 1) * p.wp;
-    float acc[R][NT];
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int t = 0; t < NT; ++t) acc[r][t] = 0.f;
+  uint32_t v = lo, k = 0;
+  auto use = [&](const uint4 (&q)[U][R]) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[r][t] = 0.f;
-    for (uint32_t k = 0; k < steps; k += U) {
-      uint4 q[U][R];
+    for (int u = 0; u < U; ++u) {
+      if (k + u >= steps) break;
+      const uint32_t c = ((k + u) * 32 + lane) * V;
+      float xv[NT][V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t c = ((k + u) * 32 + lane) * V;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          q[u][r] = make_uint4(0, 0, 0, 0);
-          if (c + V <= p.dim) {
-            q[u][r] = __ldg(reinterpret_cast<const uint4*>(row[r] + c));
-          } else if (c < p.dim) {
-            E tail[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) tail[j] = c + j < p.dim ? row[r][c + j] : E(0.f);
-            q[u][r] = *reinterpret_cast<const uint4*>(tail);
-          }
+        for (int j = 0; j < V; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&s_x[t * padded + c + j]);
+          xv[t][j] = f.x; xv[t][j + 1] = f.y; xv[t][j + 2] = f.z; xv[t][j + 3] = f.w;
         }
-      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (k + u >= steps) break;
-        const uint32_t c = ((k + u) * 32 + lane) * V;
-        float xv[NT][V];
+      for (int r = 0; r < R; ++r) {
+        const uint32_t w[4] = {q[u][r].x, q[u][r].y, q[u][r].z, q[u][r].w};
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int j = 0; j < V; ++j) {
+          float f;
+          if constexpr (sizeof(E) == 4) f = __uint_as_float(w[j]);
+          else f = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
 #pragma unroll
-          for (int j = 0; j < V; j += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&s_x[t * padded + c + j]);
-            xv[t][j] = f.x; xv[t][j + 1] = f.y; xv[t][j + 2] = f.z; xv[t][j + 3] = f.w;
-          }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint32_t w[4] = {q[u][r].x, q[u][r].y, q[u][r].z, q[u][r].w};
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            float f;
-            if constexpr (sizeof(E) == 4) f = __uint_as_float(w[j]);
-            else f = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[r][t] = __fmaf_rn(f, xv[t][j], acc[r][t]);
-          }
+          for (int t = 0; t < NT; ++t) acc[r][t] = __fmaf_rn(f, xv[t][j], acc[r][t]);
         }
       }
     }
+    k += U;
+    if (k < steps) return;
+    // The rows are complete.  Every lane keeps the same running pairs.
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float l[R];
@@ -380,14 +402,14 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_xent_few(const __grid_
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         l[r] = warp_sum(acc[r][t]);
-        if (v0 + r < p.vocab) {
-          if (lane == 0 && int64_t(v0 + r) == label[t]) p.at[t] = l[r];
+        acc[r][t] = 0.f;
+        if (v + r < hi) {
+          if (lane == 0 && int64_t(v + r) == label[t]) p.at[t] = l[r];
         } else {
           l[r] = -INFINITY;
         }
         top = fmaxf(top, l[r]);
       }
-      // Every lane keeps the same running pair.
       const float base = top == -INFINITY ? 0.f : top;
       float add = 0.f;
 #pragma unroll
@@ -395,6 +417,15 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_xent_few(const __grid_
       s[t] = __fmaf_rn(s[t], __expf(m[t] - base), add);
       m[t] = top;
     }
+    k = 0;
+    v += R;
+  };
+  while (v < hi) {
+    load(qb);
+    use(qa);
+    if (v >= hi) break;
+    load(qa);
+    use(qb);
   }
   if (lane == 0)
 #pragma unroll
@@ -435,12 +466,11 @@ struct Operand {
   PackPlan pp;
 };
 
-constexpr int kGemmCg = 2;
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;  // G of one piece of the vocabulary, about
 
 struct XentSet {
   int es = 4;
-  uint32_t parts = 1, combos = 1;
+  uint32_t parts = 1;
   bool empty = false;        // no rows
   bool few = false;          // forward by k_xent_few
   Operand x, w;
@@ -454,12 +484,18 @@ struct XentSet {
   int64_t piece = 0, n_piece = 0;
 };
 
-uint32_t few_grid(int64_t vocab) {
-  return uint32_t(std::min<int64_t>(kSms * kFewBlocks, (vocab + 31) / 32));
+// CTAs per cluster: pairs when there is more than one CTA's rows.
+int pick_cg(int64_t m) { return m > 128 ? 2 : 1; }
+// Widest tile (zr_gemm.cuh: a single CTA's stage of three parts).
+int64_t widest(const XentSet& S, int cg) { return S.parts == 3 && cg == 1 ? 128 : 256; }
+
+uint32_t few_grid(int64_t rows, int64_t vocab) {
+  return uint32_t(std::min<int64_t>(kSms * (rows > 2 ? 2 : kFewBlocks), (vocab + 15) / 16));
 }
 
-uint32_t tile_width(int64_t n) {
-  const int64_t t = (n + 255) / 256;
+// Tile columns: the fewest tiles of at most `most`, as narrow as they may be.
+uint32_t tile_width(int64_t n, int64_t most) {
+  const int64_t t = (n + most - 1) / most;
   return uint32_t(((n + t - 1) / t + 63) / 64 * 64);
 }
 
@@ -514,7 +550,6 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
   if (red != ZR_NONE && red != ZR_MEAN && red != ZR_SUM) return ZR_ERR_NULL;
   S->es = dtype == ZR_BF16 ? 2 : 4;
   S->parts = S->es == 4 ? 3 : 1;
-  S->combos = S->es == 4 ? 6 : 1;
   int rc = read_tensor(x, &S->x.t);
   if (rc) return rc;
   if ((rc = read_tensor(w, &S->w.t))) return rc;
@@ -570,7 +605,8 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
   for (Operand* o : {&S->x, &S->w})
     if (o->pack) o->ws = take(&at, size_t(o->rows) * o->pitch * 2 * S->parts);
   if (!back) {
-    r.slots = S->few ? few_grid(vocab) : 2 * uint32_t((vocab + 255) / 256);
+    const int64_t tn = widest(*S, pick_cg(S->x.rows));
+    r.slots = S->few ? few_grid(S->x.rows, vocab) : 2 * uint32_t((vocab + tn - 1) / tn);
     S->ws_partial = take(&at, N * r.slots * sizeof(float2));
     S->ws_at = take(&at, N * 4);
     S->ws_row = take(&at, N * 4);
@@ -653,9 +689,6 @@ const char* operand_base(const Operand& o, const char* ws) {
   return o.pack ? ws + o.ws : reinterpret_cast<const char*>(o.t.ptr);
 }
 
-// CTAs per cluster: pairs when there is more than one CTA's rows.
-int pick_cg(int64_t m) { return m > 128 ? kGemmCg : 1; }
-
 // The grid, and how two problems' tiles are dealt out (GemmWalk).
 unsigned gemm_grid(GemmPlan* g, int cg) {
   const uint32_t W = std::min<uint32_t>(g->tiles, kSms / cg);
@@ -670,11 +703,10 @@ unsigned gemm_grid(GemmPlan* g, int cg) {
   return unsigned(W * cg);
 }
 
-// k blocks per accumulation where chunks are added in registers: 256 terms
-// for binary32 results (a chunk's truncation is then 16 steps of 2^-24, beside
-// the roundings of the plain sums: [4080, 384] x [5003, 384], gradients'
-// relative error 5.3e-7; 6.0e-6 in one go), 4096 for bfloat16 ones.
-constexpr uint32_t kChunkF32 = 4, kChunkBf16 = 64;
+// k blocks per accumulation where chunks are added in registers: one for
+// binary32 operands (24 instructions; the truncation is that of the last four,
+// beside the roundings of the plain sums), 4096 terms for bfloat16 ones.
+constexpr uint32_t kChunkF32 = 1, kChunkBf16 = 64;
 // Longest k (in blocks) that bfloat16 results accumulate in one go: its
 // truncation stays below 2^-10 of the sum.
 constexpr uint32_t kLongK = 2048;
@@ -711,7 +743,7 @@ cudaError_t logits_problem(const XentSet& S, const char* ws, int64_t v0, int64_t
   q.m = uint32_t(S.x.rows);
   q.n = uint32_t(n);
   q.k = uint32_t(S.x.cols);
-  q.tn = n > 256 ? 256 : tile_width(n);
+  q.tn = n > widest(S, cg) ? uint32_t(widest(S, cg)) : tile_width(n, widest(S, cg));
   q.a_mn = q.b_mn = 0;
   set_tiles(&q, cg);
   cudaError_t e = make_map(&q.a, operand_base(S.x, ws), S.x.cols, S.x.rows, S.x.pitch, S.parts,
@@ -720,7 +752,7 @@ cudaError_t logits_problem(const XentSet& S, const char* ws, int64_t v0, int64_t
   e = make_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, S.w.cols, n, S.w.pitch, S.parts,
                S.w.rows * S.w.pitch, q.tn / cg);
   g->n_prob = 1;
-  g->n_combo = S.combos;
+  g->parts = S.parts;
   g->tiles0 = g->tiles = q.m_tiles * q.n_tiles;
   g->m_fast = 1;
   return e;
@@ -819,14 +851,13 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     g.vocab = V;
     g.row_scale = r.reduction == ZR_NONE ? grad_loss : nullptr;
     g.label_base = v0;
-    g.n_part = S.parts;
     if ((e = make_map(&g.pr[0].c, G, n, N, ldg, S.parts, N * ldg, 32)) != cudaSuccess)
       return cuda_status(e);
     if ((e = launch_product(S, kEpiGrad, cg, &g, s)) != cudaSuccess) return cuda_status(e);
 
     cg = pick_cg(std::min(N, n));
     GemmPlan o = {};
-    o.n_combo = S.combos;
+    o.parts = S.parts;
     o.es = uint32_t(S.es);
     o.out_scale = r.common;
     // grad_x += G W: rows of x, k = this piece's vocabulary.
@@ -835,7 +866,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.m = uint32_t(N);
       q.n = uint32_t(D);
       q.k = uint32_t(n);
-      q.tn = tile_width(D);
+      q.tn = tile_width(D, widest(S, cg));
       q.a_mn = 0;
       q.b_mn = 1;
       set_tiles(&q, cg);
@@ -861,7 +892,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.m = uint32_t(n);
       q.n = uint32_t(D);
       q.k = uint32_t(N);
-      q.tn = tile_width(D);
+      q.tn = tile_width(D, widest(S, cg));
       q.a_mn = 1;
       q.b_mn = 1;
       set_tiles(&q, cg);
