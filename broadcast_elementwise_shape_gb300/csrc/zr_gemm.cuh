@@ -100,19 +100,19 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 
 // ------------------------------------------------------------------ TMA, tcgen05
 template <int CG>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
-                                         int y, int z) {
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t row,
+                                         uint32_t block, uint32_t part) {
   if constexpr (CG == 1) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(0), "r"(row), "r"(block), "r"(part)
         : "memory");
   } else {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(0), "r"(row), "r"(block), "r"(part)
         : "memory");
   }
 }
@@ -226,8 +226,9 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t mn_majo
 }
 
 struct GemmTile {
-  uint32_t prob, mt, nt;
+  uint32_t prob, mt, nt, n0, tn;
 };
+template <int CG>
 __device__ __forceinline__ GemmTile gemm_tile(const GemmPlan& p, uint32_t t) {
   GemmTile g;
   g.prob = t >= p.tiles0 ? 1u : 0u;
@@ -239,6 +240,12 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmPlan& p, uint32_t t) {
   } else {
     g.mt = l / q.n_tiles;
     g.nt = l - g.mt * q.n_tiles;
+  }
+  g.n0 = g.nt * q.tn;
+  g.tn = q.tn;
+  if (q.b_mn) {  // each CTA's share is whole blocks of 64
+    const uint32_t left = (q.n - g.n0 + 64 * CG - 1) / (64 * CG) * (64 * CG);
+    if (left < g.tn) g.tn = left;
   }
   return g;
 }
@@ -404,6 +411,11 @@ struct EpiGrad {
 #pragma unroll
       for (int i = 0; i < 64; ++i) v[i] = e.ok ? 0.f : qnan();
     }
+    if (e.n0 + c + 64 > q.n) {  // G's rows are padded with zeros to whole blocks of 64
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (e.n0 + c + i >= q.n) v[i] = 0.f;
+    }
     epi_store(&q.c, e, c, 0, v);
     for (uint32_t part = 1; part < p.parts; ++part) {
 #pragma unroll
@@ -527,34 +539,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
-      const GemmTile g = gemm_tile(p, t);
+      const GemmTile g = gemm_tile<CG>(p, t);
       const GemmProblem& q = p.pr[g.prob];
-      const uint32_t tnc = q.tn / CG;
-      const int m0 = int((g.mt * CG + rank) * kGemmM);
-      const int n0 = int(g.nt * q.tn + rank * tnc);
-      const uint32_t nb = q.b_mn ? (tnc + 63) / 64 * 8192 : tnc * 128;
+      const uint32_t m0 = (g.mt * CG + rank) * kGemmM;
+      const uint32_t n0 = g.n0 + rank * (g.tn / CG);
+      // Whole boxes, whatever part of them is inside the operand.
+      const uint32_t bytes = (kABytes + q.tn / CG * kGemmK * 2) * PARTS * CG;
       for (uint32_t kb = 0; kb < q.n_kb; ++kb) {
         if (!mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort)) { ok = false; break; }
         const uint32_t local = smem_u32(&s_full[stage]);
-        if (rank == 0) mbar_expect(local, (kABytes + nb) * PARTS * CG);
+        if (rank == 0) mbar_expect(local, bytes);
         const uint32_t bar = CG == 1 ? local : cluster_addr(local, 0);
-        const int k0 = int(kb * kGemmK);
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
           const uint32_t sa = ring + stage * Cfg::kStageBytes + part * kABytes;
           const uint32_t sb = ring + stage * Cfg::kStageBytes + PARTS * kABytes + part * Cfg::kBBytes;
-          if (q.a_mn) {
-            tma_load<CG>(sa, &q.a, bar, m0, k0, part);
-            tma_load<CG>(sa + 8192, &q.a, bar, m0 + 64, k0, part);
-          } else {
-            tma_load<CG>(sa, &q.a, bar, k0, m0, part);
-          }
-          if (q.b_mn) {
-            for (uint32_t j = 0; j < tnc; j += 64)
-              tma_load<CG>(sb + j * 128, &q.b, bar, n0 + int(j), k0, part);
-          } else {
-            tma_load<CG>(sb, &q.b, bar, k0, n0, part);
-          }
+          if (q.a_mn) tma_load<CG>(sa, &q.a, bar, kb * kGemmK, m0 / 64, part);
+          else tma_load<CG>(sa, &q.a, bar, m0, kb, part);
+          if (q.b_mn) tma_load<CG>(sb, &q.b, bar, kb * kGemmK, n0 / 64, part);
+          else tma_load<CG>(sb, &q.b, bar, n0, kb, part);
         }
         if (++stage == S) { stage = 0; phase ^= 1; }
       }
@@ -569,11 +572,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     uint32_t stage = 0, phase = 0, it = 0;
     bool ok = true;
     for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
-      const GemmTile g = gemm_tile(p, t);
+      const GemmTile g = gemm_tile<CG>(p, t);
       const GemmProblem& q = p.pr[g.prob];
       // D binary32, A and B bfloat16, their majors, N / 8, M / 16.
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (q.a_mn << 15) | (q.b_mn << 16) |
-                             ((q.tn >> 3) << 17) | (uint32_t(kGemmM * CG / 16) << 24);
+                             ((g.tn >> 3) << 17) | (uint32_t(kGemmM * CG / 16) << 24);
       const uint32_t ka = q.a_mn ? 2048 >> 4 : 32 >> 4, kb16 = q.b_mn ? 2048 >> 4 : 32 >> 4;
       for (uint32_t k1 = 0; k1 < q.n_kb && ok; k1 += q.chunk, ++it) {
         const uint32_t buf = it & 1;
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     bool ok = true;
     const uint32_t quad = warp & 3, half = warp >> 2;
     for (uint32_t t; (t = gemm_next(p, &walk)) < p.tiles;) {
-      const GemmTile g = gemm_tile(p, t);
+      const GemmTile g = gemm_tile<CG>(p, t);
       const GemmProblem& q = p.pr[g.prob];
       EpiPos e;
       e.row0 = (g.mt * CG + rank) * kGemmM + quad * 32;
@@ -614,9 +617,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       e.lane = lane;
       e.out = ring + Cfg::kOutAt + warp * 4096;
       e.live = e.row < q.m;
-      e.n0 = g.nt * q.tn;
+      e.n0 = g.n0;
       e.c0 = half * 64;
-      e.tn = q.tn;
+      e.tn = g.tn;
       e.nt = g.nt;
       e.half = half;
       typename EpiOf<EPI>::type epi;

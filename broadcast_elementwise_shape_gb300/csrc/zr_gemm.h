@@ -9,15 +9,20 @@
 namespace zr {
 
 // One product out[m, n] = sum_k A[m, k] B[n, k] of bfloat16 operands, binary32
-// accumulation.  Each operand is a 3-d tensor map over (inner, outer, part):
-// K-major operands have k as the inner (contiguous) dim, MN-major ones m or n.
+// accumulation.  K-major operands have k as their contiguous dim, MN-major ones
+// m or n.  Each is a 4-d tensor map over (64 columns, rows, blocks of 64
+// columns, parts), whose box is one stage's share: 64 columns of 128 rows
+// (K-major), or 64 rows of two or four column blocks (MN-major).  One box per
+// operand and stage: two of 8 KB instead of one of 16 KB cost MN-major products
+// 12 % ([4096, 32000] x [32000, 1024]: 193 against 172 us).
 // Parts: one, or the three that a binary32 operand is split into (zr_xent.cu),
 // whose product is the sum of six.
 struct GemmProblem {
   CUtensorMap a, b;
   uint32_t m, n, k;
   uint32_t a_mn, b_mn;       // 1: MN-major
-  uint32_t tn;               // tile width, a multiple of 64, <= 256
+  uint32_t tn;               // tile width; the last tile of an MN-major B is
+                             // as narrow as its boxes allow
   uint32_t m_tiles, n_tiles, n_kb;  // n_kb: 64-wide k blocks
   uint32_t chunk;            // k blocks per accumulation in TMEM
   // Epilogues kEpiGrad and kEpiOut with tma_out: bfloat16 results leave through

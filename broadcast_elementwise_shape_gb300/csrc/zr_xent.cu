@@ -487,16 +487,10 @@ struct XentSet {
 // CTAs per cluster: pairs when there is more than one CTA's rows.
 int pick_cg(int64_t m) { return m > 128 ? 2 : 1; }
 // Widest tile (zr_gemm.cuh: a single CTA's stage of three parts).
-int64_t widest(const XentSet& S, int cg) { return S.parts == 3 && cg == 1 ? 128 : 256; }
+uint32_t widest(const XentSet& S, int cg) { return S.parts == 3 && cg == 1 ? 128 : 256; }
 
 uint32_t few_grid(int64_t rows, int64_t vocab) {
   return uint32_t(std::min<int64_t>(kSms * (rows > 2 ? 2 : kFewBlocks), (vocab + 15) / 16));
-}
-
-// Tile columns: the fewest tiles of at most `most`, as narrow as they may be.
-uint32_t tile_width(int64_t n, int64_t most) {
-  const int64_t t = (n + most - 1) / most;
-  return uint32_t(((n + t - 1) / t + 63) / 64 * 64);
 }
 
 int plan_operand(Operand* o, int es, bool force) {
@@ -515,8 +509,9 @@ int plan_operand(Operand* o, int es, bool force) {
   o->one_step = one && inner == 1;
   o->row_step = pitch;
   o->pack = force || es == 4 || !one || inner != 1 || (o->rows > 1 && pitch < o->cols) ||
-            pitch % 8 != 0 || reinterpret_cast<uintptr_t>(o->t.ptr) % 16 != 0;
-  o->pitch = (o->cols + 7) / 8 * 8;
+            pitch % 8 != 0 || o->cols % 64 != 0 ||
+            reinterpret_cast<uintptr_t>(o->t.ptr) % 16 != 0;
+  o->pitch = (o->cols + 63) / 64 * 64;
   if (!o->pack) {
     if (o->rows > 1) o->pitch = pitch;
     return ZR_OK;
@@ -645,19 +640,34 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Map over [parts][rows][cols] bfloat16 with the given row pitch and part
-// size in elements; boxes of 64 x box_rows, out-of-range elements read as zero.
-cudaError_t make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch,
-                     uint32_t parts, int64_t part, uint32_t box_rows) {
+// Map of an operand [parts][rows][cols] of bfloat16 (zr_gemm.h): rows `pitch`
+// elements apart that hold whole blocks of 64 columns, parts `part` apart;
+// rows, blocks and parts out of range read as zero.
+cudaError_t operand_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch,
+                        uint32_t parts, int64_t part, uint32_t box_rows, uint32_t box_blocks) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(cols + 63) / 64, parts};
+  const int64_t plane = parts > 1 ? part : (rows * pitch + 7) / 8 * 8;
+  const cuuint64_t strides[3] = {cuuint64_t(pitch) * 2, 128, cuuint64_t(plane) * 2};
+  const cuuint32_t box[4] = {64, box_rows, box_blocks, 1}, step[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                        box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// Map of an output [parts][rows][cols] that tiles of 64 x 32 are stored to.
+cudaError_t output_map(CUtensorMap* m, void* base, int64_t cols, int64_t rows, int64_t pitch,
+                       uint32_t parts, int64_t part) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), parts};
   const int64_t plane = parts > 1 ? part : (rows * pitch + 7) / 8 * 8;
   const cuuint64_t strides[2] = {cuuint64_t(pitch) * 2, cuuint64_t(plane) * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1}, step[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                        box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t box[3] = {64, 32, 1}, step[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -696,7 +706,7 @@ unsigned gemm_grid(GemmPlan* g, int cg) {
   g->head = g->n_prob > 1 ? g->tiles0 % W : 0;
   g->extra = g->late_first = 0;
   if (g->head) {
-    const uint32_t k0 = g->pr[0].n_kb * g->pr[0].tn, k1 = g->pr[1].n_kb * g->pr[1].tn;
+    const uint32_t k0 = g->pr[0].n_kb, k1 = g->pr[1].n_kb;
     g->extra = (k0 + k1 / 2) / k1;
     g->late_first = uint64_t(g->extra) * k1 < k0;
   }
@@ -743,14 +753,14 @@ cudaError_t logits_problem(const XentSet& S, const char* ws, int64_t v0, int64_t
   q.m = uint32_t(S.x.rows);
   q.n = uint32_t(n);
   q.k = uint32_t(S.x.cols);
-  q.tn = n > widest(S, cg) ? uint32_t(widest(S, cg)) : tile_width(n, widest(S, cg));
+  q.tn = widest(S, cg);
   q.a_mn = q.b_mn = 0;
   set_tiles(&q, cg);
-  cudaError_t e = make_map(&q.a, operand_base(S.x, ws), S.x.cols, S.x.rows, S.x.pitch, S.parts,
-                           S.x.rows * S.x.pitch, 128);
+  cudaError_t e = operand_map(&q.a, operand_base(S.x, ws), S.x.cols, S.x.rows, S.x.pitch, S.parts,
+                              S.x.rows * S.x.pitch, 128, 1);
   if (e != cudaSuccess) return e;
-  e = make_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, S.w.cols, n, S.w.pitch, S.parts,
-               S.w.rows * S.w.pitch, q.tn / cg);
+  e = operand_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, S.w.cols, n, S.w.pitch, S.parts,
+                  S.w.rows * S.w.pitch, q.tn / cg, 1);
   g->n_prob = 1;
   g->parts = S.parts;
   g->tiles0 = g->tiles = q.m_tiles * q.n_tiles;
@@ -851,7 +861,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     g.vocab = V;
     g.row_scale = r.reduction == ZR_NONE ? grad_loss : nullptr;
     g.label_base = v0;
-    if ((e = make_map(&g.pr[0].c, G, n, N, ldg, S.parts, N * ldg, 32)) != cudaSuccess)
+    if ((e = output_map(&g.pr[0].c, G, ldg, N, ldg, S.parts, N * ldg)) != cudaSuccess)
       return cuda_status(e);
     if ((e = launch_product(S, kEpiGrad, cg, &g, s)) != cudaSuccess) return cuda_status(e);
 
@@ -866,7 +876,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.m = uint32_t(N);
       q.n = uint32_t(D);
       q.k = uint32_t(n);
-      q.tn = tile_width(D, widest(S, cg));
+      q.tn = widest(S, cg);
       q.a_mn = 0;
       q.b_mn = 1;
       set_tiles(&q, cg);
@@ -878,12 +888,12 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.acc_out = k + 1 < S.n_piece;
       q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(grad_x) % 16 == 0;
       q.tma_out = q.vec && S.es == 2;
-      if (q.tma_out && (e = make_map(&q.c, grad_x, D, N, D, 1, 0, 32)) != cudaSuccess)
+      if (q.tma_out && (e = output_map(&q.c, grad_x, D, N, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
-      if ((e = make_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 128)) != cudaSuccess)
+      if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 128, 1)) != cudaSuccess)
         return cuda_status(e);
-      if ((e = make_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, D, n, S.w.pitch, S.parts,
-                        S.w.rows * S.w.pitch, 64)) != cudaSuccess)
+      if ((e = operand_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, D, n, S.w.pitch, S.parts,
+                           S.w.rows * S.w.pitch, 64, q.tn / cg / 64)) != cudaSuccess)
         return cuda_status(e);
     }
     // This piece's rows of grad_w = G^T X: k = the rows of x.
@@ -892,7 +902,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.m = uint32_t(n);
       q.n = uint32_t(D);
       q.k = uint32_t(N);
-      q.tn = tile_width(D, widest(S, cg));
+      q.tn = widest(S, cg);
       q.a_mn = 1;
       q.b_mn = 1;
       set_tiles(&q, cg);
@@ -900,12 +910,12 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.ldo = D;
       q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0;
       q.tma_out = q.vec && S.es == 2;
-      if (q.tma_out && (e = make_map(&q.c, q.out, D, n, D, 1, 0, 32)) != cudaSuccess)
+      if (q.tma_out && (e = output_map(&q.c, q.out, D, n, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
-      if ((e = make_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 64)) != cudaSuccess)
+      if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 64, 2)) != cudaSuccess)
         return cuda_status(e);
-      if ((e = make_map(&q.b, operand_base(S.x, ws), D, N, S.x.pitch, S.parts,
-                        S.x.rows * S.x.pitch, 64)) != cudaSuccess)
+      if ((e = operand_map(&q.b, operand_base(S.x, ws), D, N, S.x.pitch, S.parts,
+                           S.x.rows * S.x.pitch, 64, q.tn / cg / 64)) != cudaSuccess)
         return cuda_status(e);
     }
     o.tiles0 = o.pr[0].m_tiles * o.pr[0].n_tiles;
