@@ -268,8 +268,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The same with subnormal results kept: the gradient of a class that is all
-// but impossible is as exact as any other.
+// The same with subnormal results kept, at some more instructions.
 __device__ __forceinline__ float ex2_full(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -354,16 +353,29 @@ struct EpiLse {
       for (int i = 0; i < 64; ++i)
         if (at == int64_t(c) + i) p.at[e.row] = e.ok ? v[i] : qnan();
     }
-    float top[4] = {v[0], v[1], v[2], v[3]};
+    float top[4] = {m, v[1], v[2], v[3]};
+    top[0] = fmaxf(top[0], v[0]);
 #pragma unroll
-    for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
-    const float mn = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
+    for (int i = 4; i < 64; i += 8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        top[j] = i + 4 + j < 64 ? fmaxf(fmaxf(top[j], v[i + j]), v[i + 4 + j]) : fmaxf(top[j], v[i + j]);
+    }
+    const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     const float ms = mn == -INFINITY ? 0.f : mn * kLog2e;
-    s *= ex2(__fmaf_rn(m, kLog2e, -ms));
-    float add[4] = {0.f, 0.f, 0.f, 0.f};
+    const F2 k = f2_splat(kLog2e), off = f2_splat(-ms);
+    F2 add[4];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) add[i & 3] += ex2(__fmaf_rn(v[i], kLog2e, -ms));
-    s += (add[0] + add[1]) + (add[2] + add[3]);
+    for (int i = 0; i < 4; ++i) add[i] = f2_splat(0.f);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float lo, hi;
+      f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), k, off), lo, hi);
+      add[i & 3] = f2_add(add[i & 3], f2_pack(ex2(lo), ex2(hi)));
+    }
+    float lo, hi;
+    f2_unpack(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
+    s = __fmaf_rn(s, ex2(__fmaf_rn(m, kLog2e, -ms)), lo + hi);
     m = mn;
   }
   __device__ __forceinline__ void end(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
@@ -386,22 +398,43 @@ struct EpiGrad {
   bool out;                  // the row is left out: zeros, whatever its products are
 
   __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem&, const EpiPos& e) {
-    scale = lse2 = 0.f;
+    scale = 1.f;
+    lse2 = 0.f;
     at = -1;
     out = true;
     if (e.live) {
       const int64_t label = xent_label(p.labels, p.label_stride, p.label_i64, e.row);
       out = label == p.ignore_index;
-      scale = p.row_scale ? p.row_scale[e.row] : 1.f;
-      if (label < 0 || label >= p.vocab) scale = qnan();  // no class: NaN, not a guess
-      lse2 = p.lse[e.row] * kLog2e;
-      at = label - p.label_base - int64_t(e.n0);
+      if (!out) {
+        if (p.row_scale) scale = p.row_scale[e.row];
+        if (label < 0 || label >= p.vocab) scale = qnan();  // no class: NaN, not a guess
+        lse2 = p.lse[e.row] * kLog2e;
+        at = label - p.label_base - int64_t(e.n0);
+      }
     }
   }
   __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
                                         uint32_t c, float* v) {
+    const F2 k = f2_splat(kLog2e), off = f2_splat(-lse2);
+    float low = 0.f;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = scale * ex2_full(__fmaf_rn(v[i], kLog2e, -lse2));
+    for (int i = 0; i < 32; ++i) {
+      f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), k, off), v[2 * i], v[2 * i + 1]);
+      low = fminf(fminf(low, v[2 * i]), v[2 * i + 1]);
+    }
+    // The short exponential flushes subnormal results; the gradient of a class
+    // that is all but impossible is as exact as any other.
+    if (__any_sync(0xFFFFFFFFu, low < -126.f)) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = ex2_full(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = ex2(v[i]);
+    }
+    if (__any_sync(0xFFFFFFFFu, scale != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] *= scale;
+    }
     if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 64)) {
 #pragma unroll
       for (int i = 0; i < 64; ++i)
@@ -642,15 +675,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
         ++it;
       };
       if constexpr (!SUM) {
+        // The tile's values move to registers at once, so that the tensor core
+        // gets its accumulator back before they are worked on.
         const uint32_t d = acquire();
-        for (uint32_t c = e.c0; c < e.tn; c += 128) {
-          if (e.n0 + c >= q.n) break;
-          float v[64];
-          __syncwarp();
-          tc_load64(d + c, v);
-          epi.chunk(p, q, e, c, v);
-        }
+        float v[2][64];
+        __syncwarp();
+        if (e.c0 < e.tn) tc_load64(d + e.c0, v[0]);
+        if (e.c0 + 128 < e.tn) tc_load64(d + e.c0 + 128, v[1]);
         release();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t c = e.c0 + j * 128;
+          __syncwarp();
+          if (c < e.tn && e.n0 + c < q.n) epi.chunk(p, q, e, c, v[j]);
+        }
       } else {
         float v[2][64];
 #pragma unroll

@@ -53,7 +53,7 @@ struct XentRows {
   const float* at;
   uint32_t slots;
   float* lse;
-  float* row_loss;           // workspace, or the loss itself (no reduction)
+  float* row_loss;           // the losses (no reduction), or workspace: each block's sums
   float* loss;
   uint32_t* ticket;          // blocks done (zeroed by the product before)
   // backward
@@ -186,13 +186,24 @@ __device__ __forceinline__ float xent_row(const XentRows& p, uint32_t r, uint32_
   *used = y != p.ignore_index;
   const float at = known ? p.at[r] : __uint_as_float(0x7FFFFFFFu);  // no class: NaN
   const float2* q = p.partial + uint64_t(r) * p.slots;
-  // 512 slots' worth stays in registers between the two walks.
-  float2 v[16];
+  // Up to 512 slots stay in registers between the two walks, all loads of a
+  // group of 128 in flight together.
+  float2 v[4][4];
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = lane + 32 * i < p.slots ? q[lane + 32 * i] : make_float2(-INFINITY, 0.f);
-    m = fmaxf(m, v[i].x);
+  for (int g = 0; g < 4; ++g) {
+    if (128 * g >= p.slots) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t k = lane + 128 * g + 32 * i;
+      v[g][i] = k < p.slots ? q[k] : make_float2(-INFINITY, 0.f);
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (128 * g >= p.slots) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, v[g][i].x);
   }
   for (uint32_t i = lane + 512; i < p.slots; i += 32) m = fmaxf(m, q[i].x);
   m = warp_max(m);
@@ -200,7 +211,11 @@ __device__ __forceinline__ float xent_row(const XentRows& p, uint32_t r, uint32_
   float s = 0.f;
   // A slot with no columns has s = 0 and the maximum -inf.
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s = __fmaf_rn(v[i].y, expf(v[i].x - base), s);
+  for (int g = 0; g < 4; ++g) {
+    if (128 * g >= p.slots) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __fmaf_rn(v[g][i].y, expf(v[g][i].x - base), s);
+  }
   for (uint32_t i = lane + 512; i < p.slots; i += 32) {
     const float2 w = q[i];
     s = __fmaf_rn(w.y, expf(w.x - base), s);
@@ -212,21 +227,20 @@ __device__ __forceinline__ float xent_row(const XentRows& p, uint32_t r, uint32_
 
 constexpr uint32_t kRowsOneBlock = 32;  // rows that one block joins and totals
 
-// Sum or mean of this thread's share of the losses and counts over the block.
-__device__ __forceinline__ void xent_total(const XentRows& p, float v, uint32_t cnt, uint32_t* s_cnt,
-                                           float* s_sum) {
+// The block's sum of its threads' losses and counts, in thread 0.
+__device__ __forceinline__ float block_total(float v, uint32_t* cnt, uint32_t* s_cnt, float* s_sum) {
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
-  cnt = block_count<kRowsThreads>(cnt, s_cnt);
-  if (threadIdx.x < 32) {
-    const float t = warp_sum(threadIdx.x < kRowsThreads / 32 ? s_sum[threadIdx.x] : 0.f);
-    if (threadIdx.x == 0)
-      *p.loss = p.reduction == ZR_MEAN ? (cnt ? __fdiv_rn(t, float(cnt)) : 0.f) : t;
-  }
+  *cnt = block_count<kRowsThreads>(*cnt, s_cnt);
+  return threadIdx.x < 32 ? warp_sum(threadIdx.x < kRowsThreads / 32 ? s_sum[threadIdx.x] : 0.f) : 0.f;
+}
+__device__ __forceinline__ void write_loss(const XentRows& p, float t, uint32_t cnt) {
+  *p.loss = p.reduction == ZR_MEAN ? (cnt ? __fdiv_rn(t, float(cnt)) : 0.f) : t;
 }
 
-// ALL: one block joins every row.  Else a warp per row; the block that
-// finishes last totals the rows (which one that is changes nothing in the sum).
+// ALL: one block joins every row.  Else a warp per row and one sum per block,
+// in row_loss as (loss, count); the block that finishes last adds those (which
+// one that is changes nothing in the sum).
 template <bool ALL>
 __global__ void __launch_bounds__(kRowsThreads) k_xent_rows(const __grid_constant__ XentRows p) {
   pdl_trigger();
@@ -234,44 +248,45 @@ __global__ void __launch_bounds__(kRowsThreads) k_xent_rows(const __grid_constan
   __shared__ float s_sum[kRowsThreads / 32];
   __shared__ bool s_last;
   const uint32_t lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  bool used = false;
   pdl_wait();
-  if constexpr (ALL) {
-    Kahan acc;
-    acc.init();
-    uint32_t cnt = 0;
-    for (uint32_t r = w; r < p.n; r += kRowsThreads / 32) {
-      const float loss = xent_row(p, r, lane, &used);
-      if (lane == 0) {
-        if (p.reduction == ZR_NONE) p.row_loss[r] = loss;
-        acc.add(loss);
-        cnt += used;
-      }
-    }
-    if (p.reduction != ZR_NONE) xent_total(p, acc.s, cnt, s_cnt, s_sum);
-    return;
-  }
-  const uint32_t r = blockIdx.x * (kRowsThreads / 32) + w;
-  if (r < p.n) {
-    const float loss = xent_row(p, r, lane, &used);
-    if (lane == 0) p.row_loss[r] = loss;
-  }
-  if (p.reduction == ZR_NONE) return;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(p.ticket, 1u) + 1 == gridDim.x;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  uint32_t cnt = 0;
   Kahan acc;
   acc.init();
-#pragma unroll 8
-  for (uint32_t i = threadIdx.x; i < p.n; i += kRowsThreads) {
-    cnt += row_label(p, i) != p.ignore_index;
-    acc.add(__ldcg(p.row_loss + i));
+  uint32_t cnt = 0;
+  const uint32_t step = ALL ? kRowsThreads / 32 : p.n;
+  for (uint32_t r = blockIdx.x * (kRowsThreads / 32) + w; r < p.n; r += step) {
+    bool used;
+    const float loss = xent_row(p, r, lane, &used);
+    if (lane == 0) {
+      if (p.reduction == ZR_NONE) p.row_loss[r] = loss;
+      acc.add(loss);
+      cnt += used;
+    }
   }
-  xent_total(p, acc.s, cnt, s_cnt, s_sum);
+  if (p.reduction == ZR_NONE) return;
+  const float t = block_total(acc.s, &cnt, s_cnt, s_sum);
+  if constexpr (ALL) {
+    if (threadIdx.x == 0) write_loss(p, t, cnt);
+  } else {
+    float2* sums = reinterpret_cast<float2*>(p.row_loss);
+    if (threadIdx.x == 0) {
+      sums[blockIdx.x] = make_float2(t, __uint_as_float(cnt));
+      __threadfence();
+      s_last = atomicAdd(p.ticket, 1u) + 1 == gridDim.x;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    acc.init();
+    cnt = 0;
+#pragma unroll 8
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kRowsThreads) {
+      const float2 v = __ldcg(sums + i);
+      acc.add(v.x);
+      cnt += __float_as_uint(v.y);
+    }
+    const float all = block_total(acc.s, &cnt, s_cnt, s_sum);
+    if (threadIdx.x == 0) write_loss(p, all, cnt);
+  }
 }
 
 // ------------------------------------------------------------------ few rows
@@ -604,7 +619,7 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     r.slots = S->few ? few_grid(S->x.rows, vocab) : 2 * uint32_t((vocab + tn - 1) / tn);
     S->ws_partial = take(&at, N * r.slots * sizeof(float2));
     S->ws_at = take(&at, N * 4);
-    S->ws_row = take(&at, N * 4);
+    S->ws_row = take(&at, (N + 7) / 8 * 8);  // (float, count) per block of eight rows
     S->ws_ticket = take(&at, 4);
   } else {
     S->ws_common = take(&at, 4);
