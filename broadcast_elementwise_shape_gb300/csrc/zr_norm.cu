@@ -35,29 +35,44 @@ void norm_cases(F f) {
 #undef ZR_NORM_CASE
 }
 
-// Fewest lanes whose registers hold the row, 8 only for rows that a warp's
-// single access would leave half empty.  Element-wise access (odd sizes or
-// strides) goes to a block per row from 257 columns: a lane then has few
-// columns and many warps share the loads' latency ([4093, 1001] bf16 backward
-// with 32 columns per lane 41 us, with 4 per lane 15).
+uint32_t ring_slot(const NormPlan& p, int es, int vec) {
+  return vec > 1 ? p.group * p.ni : (p.dim * uint32_t(es) + 16 - uint32_t(es) + 15) / 16;
+}
+
+// The fewest lanes per row.  Vectors: up to 32 columns each, but a block where
+// the rows are too few to give every SM two blocks and lanes have over 8 columns.
+// Element-wise: up to 16 each as far as that goes; a row takes longer there, and
+// 24 warps per SM do better than 16 ([4093, 1001] bf16, forward and backward:
+// 15.4 and 21.0 us at 32 columns, 11.9 and 19.1 at 16, 15.6 and 20.1 at 4; [12000,
+// 1001] 25 and 39, 23 and 35, 32 and 45).  8 lanes only for rows that a warp's
+// single access would leave half empty.
 void pick_group(NormPlan* p, int vec) {
-  p->group = p->ni = 0;
-  uint64_t best = ~uint64_t(0);
-  auto see = [&](uint32_t g, uint32_t ni) {
-    const uint64_t cols = uint64_t(g) * ni * vec;
-    if (cols < p->dim || (g == 8 && p->dim > 16u * uint32_t(vec > 1 ? vec : 4))) return;
-    const uint64_t cost = uint64_t(g) * 1000 + ni;
-    if (cost < best) { best = cost; p->group = g; p->ni = ni; }
+  uint32_t group = 0, best = 0;
+  auto see = [&](uint32_t g, uint32_t ni) {  // groups come in ascending order
+    const uint32_t cols = ni * uint32_t(vec), had = best * uint32_t(vec);
+    if (uint64_t(g) * cols < p->dim || (g == 8 && p->dim > 16u * uint32_t(vec > 1 ? vec : 4))) return;
+    if (group) {
+      if (cols >= had) return;
+      const bool idle = uint64_t(p->nrow) * group < 2 * uint64_t(kSms) * kNormThreads && had > 8;
+      if (g != group && !(vec == 1 ? had > 16 : idle)) return;
+    }
+    group = g;
+    best = ni;
   };
   if (vec == 1) norm_cases<1>(see);
   else if (vec == 4) norm_cases<4>(see);
   else norm_cases<8>(see);
+  p->group = group;
+  p->ni = best;
 }
 
 // A persistent grid of at most per_sm blocks per SM over rings of `streams`
 // inputs.  A third stage where that leaves every block its place on the SM.
-void pick_ring(NormPlan* p, uint32_t streams, uint32_t per_sm, uint32_t at_least) {
-  const uint32_t ring = streams * kNormThreads * p->ni * 16;  // one stage
+void pick_ring(NormPlan* p, int es, int vec, uint32_t streams, uint32_t per_sm, uint32_t at_least) {
+  const uint32_t rpb = kNormThreads / p->group;
+  p->n_cta = (p->nrow + rpb - 1) / rpb;
+  p->slot = vec > 1 ? p->group * p->ni : (p->dim * uint32_t(es) + 16 - uint32_t(es) + 15) / 16;
+  const uint32_t ring = streams * rpb * p->slot * 16;  // one stage
   const uint32_t most = uint32_t(kNormSmemMax);
   p->stages = 3 * ring * per_sm <= most ? 3 : 2;
   p->smem = std::max(p->stages * ring, at_least);
@@ -105,6 +120,12 @@ int plan_rows(NormSet* S, int nin, const void* out) {
   for (int k = 0; k < nin; ++k) look(S->in[k], k, S->in[k].ptr);
   if (out) look(S->out, kSlotOut, out);
   S->vec = wide ? V : 1;
+  p.raw = !wide;
+  for (int k = 0; k < nin; ++k)
+    if (dim > 1 && p.inner_stride[k] != 1) p.raw = 0;
+  p.out_pairs = out && p.inner_stride[kSlotOut] == 1 && aligned(out, 4);
+  for (int i = 0; i < P.n; ++i)
+    if (p.rows.stride[kSlotOut][i] % 2 != 0) p.out_pairs = 0;
   p.gamma = S->gamma.ptr;
   p.beta = S->beta.ptr;
   p.gamma_stride = S->gamma.nd ? S->gamma.stride[0] : 0;
@@ -177,9 +198,8 @@ int plan_norm_fwd(zr_dtype dtype, const zr_tensor& x, const zr_tensor& gamma, co
   p.rstd = rstd;
   p.eps = eps;
   if ((rc = plan_rows(S, 1, y))) return rc;
-  const uint32_t rpb = p.group ? kNormThreads / p.group : 1;
-  p.n_cta = (p.nrow + rpb - 1) / rpb;
-  if (p.group && S->vec > 1) pick_ring(&p, 1, uint32_t(norm_fwd_occ(int(p.ni) * S->vec, S->vec)), 0);
+  if (p.group) pick_ring(&p, S->es, S->vec, 1, uint32_t(norm_fwd_occ(int(p.ni) * S->vec)), 0);
+  else p.n_cta = p.nrow;
   return ZR_OK;
 }
 
@@ -227,11 +247,9 @@ int plan_norm_bwd(zr_dtype dtype, const zr_tensor& g, const zr_tensor& x, const 
   p.rstd_in = rstd;
   if ((rc = plan_rows(S, 2, gx))) return rc;
   if (p.group) {
-    const uint32_t rpb = kNormThreads / p.group;
-    p.n_cta = (p.nrow + rpb - 1) / rpb;
     // After the rows the ring holds every row group's column sums.
-    const uint32_t sums = p.group > 32 ? 0 : kNormThreads * p.ni * uint32_t(S->vec) * 4;
-    pick_ring(&p, S->vec > 1 ? 2 : 0, uint32_t(norm_bwd_occ(int(p.ni) * S->vec, S->vec)), sums);
+    const uint32_t sums = p.group == kNormThreads ? 0 : kNormThreads * p.ni * uint32_t(S->vec) * 4;
+    pick_ring(&p, S->es, S->vec, 2, uint32_t(norm_bwd_occ(int(p.ni) * S->vec)), sums);
   } else {
     // k_norm_sums: rows split so that the column blocks fill the GPU, at
     // least 64 rows to a split.

@@ -30,41 +30,43 @@ struct NormPlan {
   // group == 0: rows longer than a block holds in registers.
   uint32_t group, ni;
   uint32_t n_cta;
-  uint32_t stages, smem;     // ring stages (2 or 3), dynamic shared memory
+  // The ring: stages (2 or 3), 16-byte units per row and input, dynamic shared
+  // memory in all.  raw: element-wise rows of neighbouring elements; out_pairs: rows of a
+  // 2-byte output start at 4-byte boundaries.
+  uint32_t stages, slot, smem, raw, out_pairs;
 };
 
 constexpr int kNormThreads = 256;
-// k_norm_fwd likewise.
-ZR_CX int norm_fwd_occ(int cols, int vec) {
-  return vec == 1 ? (cols > 16 ? 3 : 4) : (cols > 16 ? 2 : (cols > 8 ? 3 : 4));
-}
-// k_norm_bwd: CTAs per SM its registers allow without spills, by columns per
-// lane (element-wise access keeps the row in registers too).
-ZR_CX int norm_bwd_occ(int cols, int vec) {
-  return vec == 1 ? (cols > 16 ? 1 : (cols > 8 ? 2 : (cols > 4 ? 3 : 4)))
-                  : (cols > 16 ? 2 : (cols > 8 ? 3 : 4));
-}
+// CTAs per SM that the kernels' registers allow without spills, by columns per
+// lane.
+ZR_CX int norm_fwd_occ(int cols) { return cols > 16 ? 2 : (cols > 8 ? 3 : 4); }
+ZR_CX int norm_bwd_occ(int cols) { return cols > 16 ? 2 : (cols > 8 ? 3 : 4); }
 constexpr int kNormSmemMax = 224 * 1024; // dynamic shared memory of all CTAs of an SM
-constexpr uint32_t kNormMaxCols = 32;    // columns per lane held in registers
 constexpr uint32_t kNormLongThreads = 1024;
 constexpr uint32_t kNormSumCols = 32;    // k_norm_sums: columns per CTA
 
-// Vectors per lane that a plan may use, per access width: enough steps that no
-// lane of a full row group holds more than 1.5 times the columns it needs.
+// Vectors (elements) per lane that a plan may use, per access width, close
+// enough that lanes of the larger groups idle for a quarter of a row at most.
 // One list for the planner and the launchers (ZR_NORM_CASE(G, NI)).
-#define ZR_NORM_CASES(VEC_)                                                       \
-  if constexpr (VEC_ == 1) {                                                      \
-    ZR_NORM_CASE(8, 4) ZR_NORM_CASE(8, 8) ZR_NORM_CASE(32, 4) ZR_NORM_CASE(32, 8)  \
-    ZR_NORM_CASE(256, 2) ZR_NORM_CASE(256, 4) ZR_NORM_CASE(256, 8)                \
-    ZR_NORM_CASE(256, 16) ZR_NORM_CASE(256, 32)                                   \
-  } else if constexpr (VEC_ == 4) {                                               \
-    ZR_NORM_CASE(8, 1) ZR_NORM_CASE(8, 2)                                         \
+#define ZR_NORM_CASES(VEC_)                                                        \
+  if constexpr (VEC_ == 1) {                                                       \
+    ZR_NORM_CASE(8, 4) ZR_NORM_CASE(8, 8) ZR_NORM_CASE(32, 4) ZR_NORM_CASE(32, 8)   \
+    ZR_NORM_CASE(32, 12) ZR_NORM_CASE(32, 16) ZR_NORM_CASE(64, 12)                 \
+    ZR_NORM_CASE(64, 16) ZR_NORM_CASE(128, 12) ZR_NORM_CASE(128, 16)               \
+    ZR_NORM_CASE(256, 12) ZR_NORM_CASE(256, 16) ZR_NORM_CASE(256, 24) ZR_NORM_CASE(256, 32) \
+  } else if constexpr (VEC_ == 4) {                                                \
+    ZR_NORM_CASE(8, 1) ZR_NORM_CASE(8, 2)                                          \
     ZR_NORM_CASE(32, 1) ZR_NORM_CASE(32, 2) ZR_NORM_CASE(32, 4) ZR_NORM_CASE(32, 6) \
-    ZR_NORM_CASE(32, 8) ZR_NORM_CASE(256, 2) ZR_NORM_CASE(256, 4) ZR_NORM_CASE(256, 8) \
-  } else {                                                                        \
-    ZR_NORM_CASE(8, 1) ZR_NORM_CASE(8, 2)                                         \
+    ZR_NORM_CASE(32, 8) ZR_NORM_CASE(64, 4) ZR_NORM_CASE(64, 6) ZR_NORM_CASE(64, 8) \
+    ZR_NORM_CASE(128, 4) ZR_NORM_CASE(128, 6) ZR_NORM_CASE(128, 8)                 \
+    ZR_NORM_CASE(256, 1) ZR_NORM_CASE(256, 2) ZR_NORM_CASE(256, 4)                 \
+    ZR_NORM_CASE(256, 6) ZR_NORM_CASE(256, 8)                                      \
+  } else {                                                                         \
+    ZR_NORM_CASE(8, 1) ZR_NORM_CASE(8, 2)                                          \
     ZR_NORM_CASE(32, 1) ZR_NORM_CASE(32, 2) ZR_NORM_CASE(32, 3) ZR_NORM_CASE(32, 4) \
-    ZR_NORM_CASE(256, 1) ZR_NORM_CASE(256, 2) ZR_NORM_CASE(256, 4)                \
+    ZR_NORM_CASE(64, 2) ZR_NORM_CASE(64, 3) ZR_NORM_CASE(64, 4)                    \
+    ZR_NORM_CASE(128, 2) ZR_NORM_CASE(128, 3) ZR_NORM_CASE(128, 4)                 \
+    ZR_NORM_CASE(256, 1) ZR_NORM_CASE(256, 2) ZR_NORM_CASE(256, 3) ZR_NORM_CASE(256, 4) \
   }
 
 // vec: elements per access, 16 bytes' worth or 1.
