@@ -942,7 +942,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
 }
 
 std::string xent_json(const XentSet& S) {
-  return "{\"kernel\":\"xent\",\"rows\":" + std::to_string(S.x.rows) + ",\"dim\":" +
+  return std::string("{\"kernel\":\"") + (S.few ? "xent_few" : "xent") + "\",\"rows\":" + std::to_string(S.x.rows) + ",\"dim\":" +
          std::to_string(S.x.cols) + ",\"vocab\":" + std::to_string(S.w.rows) + ",\"parts\":" +
          std::to_string(S.parts) + ",\"pack_x\":" + std::to_string(S.x.pack) + ",\"pack_w\":" +
          std::to_string(S.w.pack) + ",\"piece\":" + std::to_string(S.piece) + ",\"n_piece\":" +
@@ -1055,6 +1055,37 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
   if ((rc = check_all({grad_loss, S.x.t.ptr, S.w.t.ptr, S.labels.ptr, lse, grad_x, grad_w, workspace})))
     return rc;
   return run_bwd(S, grad_loss, lse, grad_x, grad_w, static_cast<char*>(workspace), st);
+}
+
+int zr_test_describe_linear_xent(zr_dtype dtype, zr_tensor x, zr_tensor w, zr_index label_type,
+                                 zr_tensor labels, int backward, char* buf, size_t len) {
+  XentSet S;
+  const int rc = plan_xent(dtype, x, w, label_type, labels, -100, ZR_MEAN, backward != 0, backward != 0, &S);
+  if (rc) return rc;
+  return copy_json(S.empty ? std::string("{\"kernel\":\"none\"}") : xent_json(S), buf, len);
+}
+
+int zr_test_gemm_walk(uint32_t tiles0, uint32_t tiles1, uint32_t kb0, uint32_t kb1, int cg,
+                      uint32_t* visits, uint64_t* load, uint32_t* workers) {
+  if (!visits || !load || !workers || tiles0 == 0 || kb0 == 0 || kb1 == 0 || (cg != 1 && cg != 2))
+    return ZR_ERR_NULL;
+  GemmPlan g = {};
+  g.n_prob = tiles1 ? 2 : 1;
+  g.pr[0].n_kb = kb0;
+  g.pr[1].n_kb = kb1;
+  g.tiles0 = tiles0;
+  g.tiles = tiles0 + tiles1;
+  *workers = gemm_grid(&g, cg) / unsigned(cg);
+  for (uint32_t t = 0; t < g.tiles; ++t) visits[t] = 0;
+  for (uint32_t w = 0; w < *workers; ++w) {
+    GemmWalk k = gemm_walk(g, w);
+    load[w] = 0;
+    for (uint32_t t; (t = gemm_next(g, &k)) < g.tiles;) {
+      ++visits[t];
+      load[w] += t < tiles0 ? kb0 : kb1;
+    }
+  }
+  return ZR_OK;
 }
 
 }  // extern "C"

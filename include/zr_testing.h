@@ -55,6 +55,18 @@ int zr_test_dry_run_chain_bwd(zr_op op1, zr_op op2, zr_tensor grad_out, zr_tenso
 int zr_test_describe_layer_norm(zr_dtype dtype, zr_tensor grad_out, zr_tensor x, char* buf,
                                 size_t len);
 
+/* The plan of zr_linear_xent_fwd (backward == 0) or zr_linear_xent_bwd (both
+ * gradients) with ignore_index -100 and the mean. */
+int zr_test_describe_linear_xent(zr_dtype dtype, zr_tensor x, zr_tensor w, zr_index label_type,
+                                 zr_tensor labels, int backward, char* buf, size_t len);
+
+/* How the tensor-core kernel deals out the tiles of one product (tiles1 == 0)
+ * or two: tiles0 tiles of kb0 blocks of k and tiles1 of kb1, over clusters of
+ * cg CTAs.  visits[tile] counts the workers that take it, load[worker] adds up
+ * its blocks of k (load holds 152 values), *workers is their number. */
+int zr_test_gemm_walk(uint32_t tiles0, uint32_t tiles1, uint32_t kb0, uint32_t kb1, int cg,
+                      uint32_t* visits, uint64_t* load, uint32_t* workers);
+
 /* Plan a call and run the launch-time operand checks without launching:
  * ZR_OK, an argument error, or ZR_ERR_CUDA if a kernel would read an operand
  * the plan does not provide. */

@@ -149,3 +149,104 @@ def test_binding_refusals():
         zr.zr_dropout_fwd(x, 0.1, 1, device_offset=torch.zeros(1))
     with pytest.raises(ValueError):
         zr.zr_layer_norm_bwd(x, x, None, torch.zeros(5), torch.zeros(4))
+
+
+def test_linear_xent_refusals(L):
+    x, w, y = TT(T, (6, 64)), TT(2 * T, (50, 64)), TT(3 * T, (6,))
+    nb = ctypes.c_size_t(0)
+    MEAN, NONE_, SUM = 1, 0, 2
+
+    def fwd(x=x.desc, w=w.desc, it=1, y=y.desc, red=MEAN, loss=4 * T, lse=5 * T, ws=None, n=0, dt=BF16):
+        nb.value = n
+        return L.zr_linear_xent_fwd(dt, x, w, it, y, -100, red, loss, lse, ws, ctypes.byref(nb), None)
+
+    assert fwd() == 0 and nb.value > 0
+    need = nb.value
+    assert fwd(dt=2) == DTYPE and fwd(it=2) == DTYPE and fwd(red=3) == NULL
+    assert fwd(x=TT(T, ()).desc) == RANK and fwd(w=TT(2 * T, (64,)).desc) == RANK
+    assert fwd(w=TT(2 * T, (50, 63)).desc) == SHAPE and fwd(w=TT(2 * T, (0, 64)).desc) == SHAPE
+    assert fwd(x=TT(T, (6, 0)).desc, w=TT(2 * T, (50, 0)).desc) == SHAPE
+    assert fwd(y=TT(3 * T, (7,)).desc) == SHAPE and fwd(y=TT(3 * T, (6, 1)).desc) == SHAPE
+    assert fwd(w=TT(2 * T, (1 << 30, 64)).desc) == SIZE
+    assert fwd(x=TT(T, (1 << 30, 64)).desc, y=TT(3 * T, (1 << 30,)).desc) == SIZE
+    assert fwd(x=TT(T, (6, 64), (-64, 1)).desc) == SIZE
+    assert fwd(x=TT(T, (2, 3, 64)).desc, y=TT(3 * T, (2, 3), (1, 2)).desc) == LAYOUT  # labels out of order
+    assert fwd(x=TT(None, (6, 64)).desc) == NULL and fwd(y=TT(None, (6,)).desc) == NULL
+    assert fwd(loss=None) == NULL and fwd(lse=None) == NULL
+    assert fwd(loss=5 * T) == LAYOUT and fwd(lse=T) == LAYOUT and fwd(loss=3 * T) == LAYOUT
+    assert fwd(ws=6 * T, n=need - 1) == WORKSPACE and fwd(ws=6 * T + 8, n=need) == WORKSPACE
+    assert fwd(ws=T, n=need) == LAYOUT and fwd(ws=5 * T, n=need) == LAYOUT
+    assert fwd(red=NONE_, loss=None) == NULL
+    assert L.zr_linear_xent_fwd(BF16, x.desc, w.desc, 1, y.desc, -100, MEAN, 4 * T, 5 * T, None, None, None) == NULL
+
+    def bwd(gl=4 * T, x=x.desc, w=w.desc, y=y.desc, lse=5 * T, gx=7 * T, gw=8 * T, ws=None, n=0, red=MEAN, dt=BF16):
+        nb.value = n
+        return L.zr_linear_xent_bwd(dt, gl, x, w, 0, y, -100, red, lse, gx, gw, ws, ctypes.byref(nb), None)
+
+    assert bwd() == 0 and nb.value > 6 * 64 * 2
+    need = nb.value
+    assert bwd(dt=9) == DTYPE and bwd(gl=None) == NULL and bwd(lse=None) == NULL
+    assert bwd(gx=8 * T) == LAYOUT and bwd(gx=T) == LAYOUT and bwd(gw=2 * T + 16) == LAYOUT
+    assert bwd(gx=5 * T) == LAYOUT and bwd(gw=4 * T) == LAYOUT
+    assert bwd(ws=9 * T, n=need - 1) == WORKSPACE and bwd(ws=7 * T, n=need) == LAYOUT
+    assert bwd(gx=None, gw=None, ws=9 * T, n=need) == 0          # nothing asked for
+    assert bwd(x=TT(None, (0, 64)).desc, y=TT(None, (0,)).desc, gl=None, lse=None, gx=None, gw=None, ws=9 * T,
+               n=0) == 0
+
+
+def _xent_plan(L, dt, N, V, D, back, strides=None, base=T):
+    L.zr_test_describe_linear_xent.argtypes = [ctypes.c_int, ZrTensor, ZrTensor, ctypes.c_int, ZrTensor,
+                                               ctypes.c_int, ctypes.c_char_p, ctypes.c_size_t]
+    buf = ctypes.create_string_buffer(1024)
+    x, w, y = TT(base, (N, D), strides), TT(1 << 50, (V, D)), TT(1 << 55, (N,))
+    assert L.zr_test_describe_linear_xent(dt, x.desc, w.desc, 1, y.desc, back, buf, 1024) == 0
+    return json.loads(buf.value)
+
+
+def test_linear_xent_plans(L):
+    """Operands go as they are only where the tensor maps can take them; the
+    backward's pieces cover the vocabulary within the workspace's bound."""
+    d = _xent_plan(L, BF16, 100, 1000, 128, 0)
+    assert (d["parts"], d["pack_x"], d["pack_w"], d["kernel"]) == (1, 0, 0, "xent")
+    assert _xent_plan(L, BF16, 100, 1000, 72, 0)["pack_w"] == 1           # whole blocks of 64
+    assert _xent_plan(L, BF16, 100, 1000, 128, 0, strides=(132, 1))["pack_x"] == 1
+    assert _xent_plan(L, BF16, 100, 1000, 128, 0, strides=(136, 1))["pack_x"] == 0
+    assert _xent_plan(L, BF16, 100, 1000, 128, 0, base=T + 2)["pack_x"] == 1
+    assert _xent_plan(L, BF16, 100, 1000, 128, 0, strides=(0, 1))["pack_x"] == 1
+    assert _xent_plan(L, BF16, 100, 1000, 128, 1)["pack_x"] == 1          # rows left out become zero
+    f = _xent_plan(L, F32, 100, 1000, 128, 0)
+    assert (f["parts"], f["pack_x"], f["pack_w"]) == (3, 1, 1)
+    for n in (1, 4):
+        assert _xent_plan(L, BF16, n, 1000, 128, 0)["kernel"] == "xent_few"
+    assert _xent_plan(L, BF16, 5, 1000, 128, 0)["kernel"] == "xent"
+    for dt, parts in ((BF16, 1), (F32, 3)):
+        for N in (1, 7, 4096, 100000, 1000003):
+            for V in (1, 255, 50001, 262144):
+                d = _xent_plan(L, dt, N, V, 64, 1)
+                assert d["piece"] % 256 == 0 and (d["n_piece"] - 1) * d["piece"] < V <= d["n_piece"] * d["piece"]
+                g = N * min(d["piece"], (V + 63) // 64 * 64) * 2 * parts
+                assert d["ws"] >= g and g <= max((1 << 30) + N * 512 * parts, N * 2304 * 2 * parts)
+
+
+@pytest.mark.parametrize("cg", [1, 2])
+def test_every_tile_is_dealt_out_once(L, cg):
+    """All tiles of one and of two products, each to one worker, and no worker
+    with more than a tile over the mean."""
+    import random
+    L.zr_test_gemm_walk.argtypes = [ctypes.c_uint32] * 4 + [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                                           ctypes.c_void_p]
+    rng = random.Random(5)
+    cases = [(1, 0, 1, 1), (76, 0, 3, 1), (1000, 0, 5, 1), (1, 1, 9, 2), (192, 588, 782, 256), (32, 40, 79, 64),
+             (75, 1, 100, 1), (77, 400, 4, 300), (5, 1000, 900, 1)]
+    cases += [(rng.randrange(1, 500), rng.randrange(0, 3000), rng.randrange(1, 800), rng.randrange(1, 800))
+              for _ in range(300)]
+    for t0, t1, k0, k1 in cases:
+        visits = (ctypes.c_uint32 * (t0 + t1))()
+        load = (ctypes.c_uint64 * 152)()
+        workers = ctypes.c_uint32(0)
+        assert L.zr_test_gemm_walk(t0, t1, k0, k1, cg, visits, load, ctypes.byref(workers)) == 0
+        n = workers.value
+        assert n == min(t0 + t1, 152 // cg)
+        assert all(v == 1 for v in visits), (t0, t1, k0, k1)
+        mean = (t0 * k0 + t1 * k1) / n
+        assert max(load[:n]) <= mean + k0 + 2 * k1, (t0, t1, k0, k1)
