@@ -64,7 +64,7 @@ def _build_binding(obj: str) -> None:
     root = _torch_root()
     tmp = f"{TORCH_LIB}.{os.getpid()}.tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(root, "lib"), "-ltorch_python",
-           "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libzr.so",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libzr.so",
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

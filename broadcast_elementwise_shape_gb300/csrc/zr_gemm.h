@@ -11,8 +11,9 @@ namespace zr {
 // One product out[m, n] = sum_k A[m, k] B[n, k] of bfloat16 operands, binary32
 // accumulation.  K-major operands have k as their contiguous dim, MN-major ones
 // m or n.  Each is a 4-d tensor map over (64 columns, rows, blocks of 64
-// columns, parts), whose box is one stage's share: 64 columns of 128 rows
-// (K-major), or 64 rows of two or four column blocks (MN-major).  One box per
+// columns, parts), whose box is one stage's share, all parts of it: 64 columns
+// of 128 or 256 rows (K-major), or 64 rows of two or four column blocks
+// (MN-major).  One box per
 // operand and stage: two of 8 KB instead of one of 16 KB cost MN-major products
 // 12 % ([4096, 32000] x [32000, 1024]: 193 against 172 us).
 // Parts: one, or the three that a binary32 operand is split into (zr_xent.cu),

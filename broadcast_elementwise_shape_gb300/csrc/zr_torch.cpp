@@ -8,6 +8,7 @@
 // Each function returns its tensors, or the zr_status of a failed call as an
 // int (train.py raises it).  Wrong argument types raise here.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -71,7 +72,7 @@ zr_tensor desc(const Tensor* t) { return t ? desc(*t) : zr_tensor{nullptr, 0, nu
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 Tensor empty(at::IntArrayRef shape, const Tensor& like, at::ScalarType dt) {
-  return at::empty(shape, like.options().dtype(dt));
+  return at::detail::empty_cuda(shape, dt, like.device(), c10::nullopt);
 }
 // The caller's output tensor, or a new contiguous one.
 Tensor output(const Tensor* given, at::IntArrayRef shape, const Tensor& like, const char* what) {

@@ -665,7 +665,7 @@ cudaError_t operand_map(CUtensorMap* m, const void* base, int64_t cols, int64_t 
   const cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(cols + 63) / 64, parts};
   const int64_t plane = parts > 1 ? part : (rows * pitch + 7) / 8 * 8;
   const cuuint64_t strides[3] = {cuuint64_t(pitch) * 2, 128, cuuint64_t(plane) * 2};
-  const cuuint32_t box[4] = {64, box_rows, box_blocks, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, box_rows, box_blocks, parts}, step[4] = {1, 1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
                         box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
