@@ -90,8 +90,8 @@ inline int copy_json(const std::string& s, char* buf, size_t len) {
   return ZR_OK;
 }
 
-// ZR_TRACE set (and not "0"): every forward, backward, sum-to-shape and
-// unary call that is about to launch writes one line "zr_trace <entry> <plan JSON>" to
+// ZR_TRACE set (and not "0"): every forward, backward, sum-to-shape, unary and
+// training-operator call about to launch writes one line "zr_trace <entry> <plan JSON>" to
 // stderr.  Read once per process.
 inline bool trace_on() {
   static const bool on = [] {

@@ -1,7 +1,8 @@
 /*
  * zr.h — C ABI of a GB300 (sm_103a) library of broadcasting elementwise
  * binary operators on strided fp32 tensors: forward, fused backward and
- * deterministic sum-to-shape.
+ * deterministic sum-to-shape; and of the training operators next to them:
+ * layer norm, dropout with its residual, cross entropy of a linear head.
  *
  * Semantics follow the "Zero" book (ismantic.github.io/zero):
  *   - Tensor page, section 形状与步长 (shape and strides): a tensor is a base
@@ -48,7 +49,8 @@
  * Tracing.  With the environment variable ZR_TRACE set (and not "0") when
  * the library is first used, every zr_binary_fwd, zr_binary_bwd,
  * zr_binary_bwd_noalloc, zr_sum_to_shape, zr_unary_fwd and zr_unary_bwd call
- * (and their _t forms) that passes planning writes one
+ * (and their _t forms), and every layer norm, dropout and linear cross entropy
+ * call, that passes planning writes one
  * line "zr_trace <entry point> <plan as JSON>" to stderr before its device
  * checks and launches: the kernels, vector width, tiling, grid and
  * workspace it chose.
