@@ -89,6 +89,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
   }
 }
+// The same by a whole warp: true when all its lanes saw the phase.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  const bool ok = mbar_wait(bar, parity, abort);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
@@ -229,6 +234,19 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t mn_majo
   d |= uint64_t(1) << 46;
   d |= uint64_t(2) << 61;
   return d;
+}
+
+// A value that every lane of the warp holds, in a form the compiler knows to be
+// the same: operands of the copy engine and the tensor core are then kept in
+// uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+// True in one lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 struct GemmTile {
@@ -546,8 +564,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   __shared__ uint64_t s_full[S], s_empty[S], s_tfull[2], s_tempty[2];
   __shared__ uint32_t s_tmem, s_abort;
   pdl_trigger();
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 1 ? 0 : cluster_rank();
+  const uint32_t warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0 : uniform(cluster_rank());
   const uint32_t ring = (smem_u32(s_raw) + 1023u) & ~1023u;
   volatile uint32_t* abort = &s_abort;
 
@@ -568,13 +586,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = uniform(s_tmem);
   GemmWalk walk = gemm_walk(p, blockIdx.x / CG);
   pdl_wait();
   if (EPI == kEpiLse && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
 
-  if (warp == 8 && lane == 0) {
-    // Producer: this CTA's rows of A and its share of B's columns.
+  if (warp == 8) {
+    // Producer: this CTA's rows of A and its share of B's columns.  The whole
+    // warp walks and waits, one lane starts the copies (see the issuer).
+    const bool leader = elect_one();
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
@@ -584,26 +604,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       const uint32_t n0 = g.n0 + rank * (g.tn / CG);
       // Whole boxes, whatever part of them is inside the operand.
       const uint32_t bytes = (kABytes + q.tn / CG * kGemmK * 2) * PARTS * CG;
-      for (uint32_t kb = 0; kb < q.n_kb; ++kb) {
-        if (!mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort)) { ok = false; break; }
-        const uint32_t local = smem_u32(&s_full[stage]);
-        if (rank == 0) mbar_expect(local, bytes);
-        const uint32_t bar = CG == 1 ? local : cluster_addr(local, 0);
-        const uint32_t sa = ring + stage * Cfg::kStageBytes, sb = sa + PARTS * kABytes;
-        if (q.a_mn) tma_load<CG>(sa, &q.a, bar, kb * kGemmK, m0 / 64);
-        else tma_load<CG>(sa, &q.a, bar, m0, kb);
-        if (q.b_mn) tma_load<CG>(sb, &q.b, bar, kb * kGemmK, n0 / 64);
-        else tma_load<CG>(sb, &q.b, bar, n0, kb);
+      const uint32_t n_kb = q.n_kb, a_mn = q.a_mn, b_mn = q.b_mn;
+      for (uint32_t kb = 0; kb < n_kb; ++kb) {
+        ok = warp_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort);
+        if (!ok) break;
+        if (leader) {
+          const uint32_t local = smem_u32(&s_full[stage]);
+          if (rank == 0) mbar_expect(local, bytes);
+          const uint32_t bar = CG == 1 ? local : cluster_addr(local, 0);
+          const uint32_t sa = ring + stage * Cfg::kStageBytes, sb = sa + PARTS * kABytes;
+          tma_load<CG>(sa, &q.a, bar, a_mn ? kb * kGemmK : m0, a_mn ? m0 / 64 : kb);
+          tma_load<CG>(sb, &q.b, bar, b_mn ? kb * kGemmK : n0, b_mn ? n0 / 64 : kb);
+        }
+        __syncwarp();
         if (++stage == S) { stage = 0; phase ^= 1; }
       }
     }
     // Every slot is read before the CTA may end (and its peer's signals are in).
     for (int i = 0; i < S && ok; ++i) {
-      ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort);
+      ok = warp_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort);
       if (++stage == S) { stage = 0; phase ^= 1; }
     }
-  } else if (warp == 9 && lane == 0 && rank == 0) {
-    // Issuer.
+  } else if (warp == 9 && rank == 0) {
+    // Issuer.  The whole warp walks and waits, one lane issues: control flow and
+    // operands are then the same for the warp, and a block of k is a few
+    // instructions to the tensor core with little to work out between them.
+    // With one lane in the loop the tensor core waited for its instructions:
+    // [16384, 768] x [50001, 768], 755 us against 624 us now.
+    const bool leader = elect_one();
     uint32_t stage = 0, phase = 0, it = 0;
     bool ok = true;
     for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
@@ -613,30 +641,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (q.a_mn << 15) | (q.b_mn << 16) |
                              ((g.tn >> 3) << 17) | (uint32_t(kGemmM * CG / 16) << 24);
       const uint32_t ka = q.a_mn ? 2048 >> 4 : 32 >> 4, kb16 = q.b_mn ? 2048 >> 4 : 32 >> 4;
-      for (uint32_t k1 = 0; k1 < q.n_kb && ok; k1 += q.chunk, ++it) {
+      const uint64_t da = operand_desc(ring, q.a_mn);
+      const uint64_t db = operand_desc(ring + PARTS * kABytes, q.b_mn);
+      const uint32_t n_kb = q.n_kb, chunk = q.chunk;
+      for (uint32_t k1 = 0; k1 < n_kb && ok; k1 += chunk, ++it) {
         const uint32_t buf = it & 1;
-        if (!mbar_wait(smem_u32(&s_tempty[buf]), ((it >> 1) & 1) ^ 1, abort)) { ok = false; break; }
+        ok = warp_wait(smem_u32(&s_tempty[buf]), ((it >> 1) & 1) ^ 1, abort);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
-        const uint32_t nk = q.n_kb - k1 < q.chunk ? q.n_kb - k1 : q.chunk;
+        const uint32_t nk = n_kb - k1 < chunk ? n_kb - k1 : chunk;
         for (uint32_t kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(smem_u32(&s_full[stage]), phase, abort)) { ok = false; break; }
+          ok = warp_wait(smem_u32(&s_full[stage]), phase, abort);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = ring + stage * Cfg::kStageBytes;
-          const uint64_t da = operand_desc(sa, q.a_mn);
-          const uint64_t db = operand_desc(sa + PARTS * kABytes, q.b_mn);
+          if (leader) {
+            const uint64_t at = stage * (Cfg::kStageBytes >> 4);
 #pragma unroll
-          for (int i = 0; i < (PARTS == 3 ? 6 : 1); ++i) {
-            const uint64_t pa = da + gemm_pair<PARTS>(i, 0) * (kABytes >> 4);
-            const uint64_t pb = db + gemm_pair<PARTS>(i, 1) * (Cfg::kBBytes >> 4);
+            for (int i = 0; i < (PARTS == 3 ? 6 : 1); ++i) {
+              const uint64_t pa = da + at + gemm_pair<PARTS>(i, 0) * (kABytes >> 4);
+              const uint64_t pb = db + at + gemm_pair<PARTS>(i, 1) * (Cfg::kBBytes >> 4);
 #pragma unroll
-            for (uint32_t j = 0; j < kGemmK / 16; ++j)
-              tc_mma<CG>(d, pa + j * ka, pb + j * kb16, idesc, (kb | i | j) != 0);
+              for (uint32_t j = 0; j < kGemmK / 16; ++j)
+                tc_mma<CG>(d, pa + j * ka, pb + j * kb16, idesc, (kb | i | j) != 0);
+            }
+            tc_commit<CG>(smem_u32(&s_empty[stage]));
           }
-          tc_commit<CG>(smem_u32(&s_empty[stage]));
+          __syncwarp();
           if (++stage == S) { stage = 0; phase ^= 1; }
         }
-        if (ok) tc_commit<CG>(smem_u32(&s_tfull[buf]));
+        if (ok && leader) tc_commit<CG>(smem_u32(&s_tfull[buf]));
+        __syncwarp();
       }
     }
   } else if (warp < 8) {
@@ -661,8 +696,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       epi.begin(p, q, e);
       auto acquire = [&]() {
         const uint32_t buf = it & 1;
-        ok = ok && mbar_wait(smem_u32(&s_tfull[buf]), (it >> 1) & 1, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = ok && warp_wait(smem_u32(&s_tfull[buf]), (it >> 1) & 1, abort);
         tc_fence_after();
         e.ok = ok;
         return tmem + (quad << 21) + buf * 256;
