@@ -251,13 +251,24 @@ __device__ __forceinline__ bool elect_one() {
 
 struct GemmTile {
   uint32_t prob, mt, nt, n0, tn;
+  uint32_t slice, kb0, n_kb; // its blocks of k
 };
-template <int CG>
+template <int EPI, int CG>
 __device__ __forceinline__ GemmTile gemm_tile(const GemmPlan& p, uint32_t t) {
   GemmTile g;
   g.prob = t >= p.tiles0 ? 1u : 0u;
-  const uint32_t l = t - (g.prob ? p.tiles0 : 0u);
+  uint32_t l = t - (g.prob ? p.tiles0 : 0u);
   const GemmProblem& q = p.pr[g.prob];
+  g.slice = g.kb0 = 0;
+  g.n_kb = q.n_kb;
+  if (EPI == kEpiOut && q.slices > 1) {
+    const uint32_t per = q.m_tiles * q.n_tiles;
+    g.slice = l / per;
+    l -= g.slice * per;
+    g.kb0 = g.slice * q.kb_slice;
+    const uint32_t left = q.n_kb - g.kb0;
+    g.n_kb = left < q.kb_slice ? left : q.kb_slice;
+  }
   if (p.m_fast) {
     g.nt = l / q.m_tiles;
     g.mt = l - g.nt * q.m_tiles;
@@ -315,7 +326,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // of the warp's 32 from row0, columns c0, c0 + 128, ... of the tile in chunks
 // of 64, tile column 0 = column n0.
 struct EpiPos {
-  uint32_t row, row0, n0, c0, tn, nt, half, lane;
+  uint32_t row, row0, n0, c0, tn, nt, half, slice, lane;
   uint32_t out;              // the warp's 4 KB of staging
   bool live, ok;
 };
@@ -492,7 +503,7 @@ struct EpiOut {
   __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
                                         uint32_t c, float* v) {
     const uint32_t n = e.n0 + c;
-    float* acc = q.acc + int64_t(e.row) * q.lda + n;  // rows of acc are padded to groups of 4
+    float* acc = q.acc + int64_t(e.slice) * q.plane + int64_t(e.row) * q.lda + n;  // rows of acc are padded to groups of 4
     if (q.acc_in && e.live) {
 #pragma unroll
       for (int i = 0; i < 64; i += 4) {
@@ -598,14 +609,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
-      const GemmTile g = gemm_tile<CG>(p, t);
+      const GemmTile g = gemm_tile<EPI, CG>(p, t);
       const GemmProblem& q = p.pr[g.prob];
       const uint32_t m0 = (g.mt * CG + rank) * kGemmM;
       const uint32_t n0 = g.n0 + rank * (g.tn / CG);
       // Whole boxes, whatever part of them is inside the operand.
       const uint32_t bytes = (kABytes + q.tn / CG * kGemmK * 2) * PARTS * CG;
-      const uint32_t n_kb = q.n_kb, a_mn = q.a_mn, b_mn = q.b_mn;
-      for (uint32_t kb = 0; kb < n_kb; ++kb) {
+      const uint32_t end = g.kb0 + g.n_kb, a_mn = q.a_mn, b_mn = q.b_mn;
+      for (uint32_t kb = g.kb0; kb < end; ++kb) {
         ok = warp_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort);
         if (!ok) break;
         if (leader) {
@@ -635,7 +646,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     uint32_t stage = 0, phase = 0, it = 0;
     bool ok = true;
     for (uint32_t t; ok && (t = gemm_next(p, &walk)) < p.tiles;) {
-      const GemmTile g = gemm_tile<CG>(p, t);
+      const GemmTile g = gemm_tile<EPI, CG>(p, t);
       const GemmProblem& q = p.pr[g.prob];
       // D binary32, A and B bfloat16, their majors, N / 8, M / 16.
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (q.a_mn << 15) | (q.b_mn << 16) |
@@ -643,7 +654,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       const uint32_t ka = q.a_mn ? 2048 >> 4 : 32 >> 4, kb16 = q.b_mn ? 2048 >> 4 : 32 >> 4;
       const uint64_t da = operand_desc(ring, q.a_mn);
       const uint64_t db = operand_desc(ring + PARTS * kABytes, q.b_mn);
-      const uint32_t n_kb = q.n_kb, chunk = q.chunk;
+      const uint32_t n_kb = g.n_kb, chunk = q.chunk;
       for (uint32_t k1 = 0; k1 < n_kb && ok; k1 += chunk, ++it) {
         const uint32_t buf = it & 1;
         ok = warp_wait(smem_u32(&s_tempty[buf]), ((it >> 1) & 1) ^ 1, abort);
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
     bool ok = true;
     const uint32_t quad = warp & 3, half = warp >> 2;
     for (uint32_t t; (t = gemm_next(p, &walk)) < p.tiles;) {
-      const GemmTile g = gemm_tile<CG>(p, t);
+      const GemmTile g = gemm_tile<EPI, CG>(p, t);
       const GemmProblem& q = p.pr[g.prob];
       EpiPos e;
       e.row0 = (g.mt * CG + rank) * kGemmM + quad * 32;
@@ -692,6 +703,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       e.tn = g.tn;
       e.nt = g.nt;
       e.half = half;
+      e.slice = g.slice;
       typename EpiOf<EPI>::type epi;
       epi.begin(p, q, e);
       auto acquire = [&]() {
@@ -729,7 +741,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
         float v[2][64];
 #pragma unroll
         for (int i = 0; i < 128; ++i) v[i / 64][i % 64] = 0.f;
-        for (uint32_t k1 = 0; k1 < q.n_kb; k1 += q.chunk) {
+        for (uint32_t k1 = 0; k1 < g.n_kb; k1 += q.chunk) {
           const uint32_t d = acquire();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {

@@ -25,6 +25,11 @@ struct GemmProblem {
   uint32_t tn;               // tile width; the last tile of an MN-major B is
                              // as narrow as its boxes allow
   uint32_t m_tiles, n_tiles, n_kb;  // n_kb: 64-wide k blocks
+  // Epilogue kEpiOut: k in `slices` parts of kb_slice blocks (the last one
+  // shorter), each with tiles of its own whose results go to plane `slice` of
+  // acc, `plane` elements apart; elsewhere one of all blocks.
+  uint32_t slices, kb_slice;
+  int64_t plane;
   uint32_t chunk;            // k blocks per accumulation in TMEM
   // Epilogues kEpiGrad and kEpiOut with tma_out: bfloat16 results leave through
   // this map, in boxes of 64 columns by 32 rows.

@@ -26,7 +26,7 @@ cudaError_t launch_gemm(int epi, int cg, bool sum, const GemmPlan& p, unsigned g
                         cudaStream_t s) {
   if (grid == 0 || (cg != 1 && cg != 2) || grid % unsigned(cg) != 0) return cudaErrorInvalidValue;
   for (uint32_t i = 0; i < p.n_prob; ++i)
-    if (p.pr[i].chunk == 0 || (!sum && p.pr[i].chunk < p.pr[i].n_kb)) return cudaErrorInvalidValue;
+    if (p.pr[i].chunk == 0 || (!sum && p.pr[i].chunk < p.pr[i].kb_slice)) return cudaErrorInvalidValue;
   if ((p.parts != 1 && p.parts != 3) || (p.parts == 3 && !sum)) return cudaErrorInvalidValue;
   const uint32_t widest = p.parts == 3 && cg == 1 ? 128 : 256;
   for (uint32_t i = 0; i < p.n_prob; ++i)

@@ -481,6 +481,59 @@ struct Operand {
   PackPlan pp;
 };
 
+// out = scale * the sum of its planes, in their order: results whose k was cut
+// into slices (plan_slices).  One pass over planes that are still in L2; four
+// columns per thread.
+struct JoinPart {
+  const float* acc;          // [slices][rows][lda]
+  int64_t plane;
+  uint32_t slices, rows, cols, vec;
+  FastDiv quads;             // lda / 4
+  void* out;                 // [rows][cols]
+  uint32_t blocks;
+};
+struct JoinPlan {
+  JoinPart p[2];
+  const float* scale;        // or null (1)
+};
+
+__device__ __forceinline__ uint32_t join_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads) k_xent_join(const __grid_constant__ JoinPlan p) {
+  pdl_trigger();
+  const bool second = blockIdx.x >= p.p[0].blocks;
+  const JoinPart& q = second ? p.p[1] : p.p[0];
+  const uint32_t i = (blockIdx.x - (second ? p.p[0].blocks : 0u)) * kThreads + threadIdx.x;
+  const uint32_t row = fd_div(q.quads, i), c = (i - row * q.quads.d) * 4;
+  if (row >= q.rows) return;
+  const float* a = q.acc + uint64_t(i) * 4;
+  pdl_wait();
+  const float scale = p.scale ? *p.scale : 1.f;
+  float4 v = *reinterpret_cast<const float4*>(a);
+#pragma unroll 4
+  for (uint32_t k = 1; k < q.slices; ++k) {
+    const float4 o = *reinterpret_cast<const float4*>(a + k * q.plane);
+    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+  }
+  const float r[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+  E* out = static_cast<E*>(q.out) + uint64_t(row) * q.cols + c;
+  if (q.vec) {
+    if constexpr (sizeof(E) == 4) {
+      *reinterpret_cast<float4*>(out) = make_float4(r[0], r[1], r[2], r[3]);
+    } else {
+      *reinterpret_cast<uint2*>(out) = make_uint2(join_bf16(r[0], r[1]), join_bf16(r[2], r[3]));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < q.cols) st1(out + j, r[j]);
+  }
+}
+
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;  // G of one piece of the vocabulary, about
 
 struct XentSet {
@@ -495,8 +548,9 @@ struct XentSet {
   // forward
   size_t ws_partial = 0, ws_at = 0, ws_row = 0, ws_ticket = 0;
   // backward
-  size_t ws_common = 0, ws_g = 0, ws_acc = 0;
+  size_t ws_common = 0, ws_g = 0, ws_acc[2] = {0, 0};
   int64_t piece = 0, n_piece = 0;
+  uint32_t slices[2] = {1, 1};  // of grad_x's and grad_w's k (plan_slices)
 };
 
 // CTAs per cluster: pairs when there is more than one CTA's rows.
@@ -550,6 +604,45 @@ int plan_operand(Operand* o, int es, bool force) {
   p.part = o->rows * o->pitch;
   p.items = uint64_t(o->rows) * uint64_t(o->pitch / 8);
   return ZR_OK;
+}
+
+// Few rows or a small vocabulary leave one gradient with few tiles of long k,
+// each longer than an even share of all the work, and the other workers wait
+// for them.  Such a gradient's k is cut into slices of about a share (half a
+// share for grad_w, whose tiles come last), summed by k_xent_join, where that
+// saves more than the join costs.  The last slices end half a slice apart.
+//   [40, 384] x [100000, 384] f32, backward: 2258 us whole, 293 in 16 slices;
+//   [300, 1024] x [32000, 1024] bf16: 171 us whole, 81 in 4;
+//   [16384, 1024] x [500, 1024] bf16, grad_w: 117 us whole, 71 in 7;
+//   but [4080, 384] x [5003, 384] f32: 237 us whole, 291 in 2, and
+//   [2048, 2048] x [8192, 2048] bf16: 122 us whole, 144 in 2.
+// From the sizes alone, whichever gradients a call asks for: a workspace that
+// serves both serves one.
+void plan_slices(XentSet* S, int64_t dim) {
+  const int64_t rows = S->x.rows, n = std::min(S->piece, S->w.rows);
+  const int cg = pick_cg(std::min(rows, n));
+  const int64_t m[2] = {rows, n}, k[2] = {n, rows};
+  const double W = kSms / cg;
+  const double us = S->es == 4 ? 2.0 : 0.33;        // a block of k takes
+  const double tile_cost = S->es == 4 ? 4 : 6;      // what a tile takes besides, in blocks
+  const int64_t least = S->es == 4 ? 2 : 16;        // blocks of a slice
+  const int64_t nt = (dim + widest(*S, cg) - 1) / widest(*S, cg);
+  double share = 0;
+  for (int i = 0; i < 2; ++i)
+    share += double((m[i] + 128 * cg - 1) / (128 * cg) * nt) * (double(k[i] + 63) / 64 + tile_cost) / W;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t kb = (k[i] + 63) / 64;
+    const double plane = double(m[i]) * double((dim + 3) / 4 * 4) * 4;
+    int64_t len = std::max<int64_t>(int64_t(i ? share / 2 : share), least);
+    // All planes together stay within the bound of a piece.
+    len = std::max<int64_t>(len, int64_t(double(kb) * plane / double(kPieceBytes)) + 1);
+    if (len >= kb) continue;
+    const int64_t s = (kb + len - 1) / len, even = (kb + s - 1) / s;
+    // A launch, and the planes out and in at 3 TB/s.
+    const double join = 8 + 2 * plane * double(s) / 3e6;
+    if ((double(kb) - share - double(len) / 2) * us > join)
+      S->slices[i] = uint32_t((kb + even - 1) / even);
+  }
 }
 
 int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index it,
@@ -629,7 +722,11 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     S->n_piece = (vocab + S->piece - 1) / S->piece;
     const int64_t wide = std::min<int64_t>(S->piece, (vocab + 63) / 64 * 64);
     S->ws_g = take(&at, N * size_t(wide) * 2 * S->parts);
-    if (S->n_piece > 1) S->ws_acc = take(&at, N * size_t((dim + 3) / 4 * 4) * 4);
+    plan_slices(S, dim);
+    const size_t lda = size_t(dim + 3) / 4 * 4;
+    if (S->n_piece > 1 || S->slices[0] > 1) S->ws_acc[0] = take(&at, S->slices[0] * N * lda * 4);
+    if (S->slices[1] > 1)
+      S->ws_acc[1] = take(&at, S->slices[1] * size_t(std::min(S->piece, vocab)) * lda * 4);
   }
   S->ws = at;
   return ZR_OK;
@@ -721,7 +818,7 @@ unsigned gemm_grid(GemmPlan* g, int cg) {
   g->head = g->n_prob > 1 ? g->tiles0 % W : 0;
   g->extra = g->late_first = 0;
   if (g->head) {
-    const uint32_t k0 = g->pr[0].n_kb, k1 = g->pr[1].n_kb;
+    const uint32_t k0 = g->pr[0].kb_slice, k1 = g->pr[1].kb_slice;
     g->extra = (k0 + k1 / 2) / k1;
     g->late_first = uint64_t(g->extra) * k1 < k0;
   }
@@ -745,8 +842,8 @@ bool sum_chunks(const XentSet& S, int epi, GemmPlan* g) {
   const uint32_t most = S.es == 4 ? 0 : (epi == kEpiLse ? kChunkLse : kLongK);
   const uint32_t chunk = S.es == 4 ? kChunkF32 : (epi == kEpiLse ? kChunkLse : kChunkBf16);
   bool sum = false;
-  for (uint32_t i = 0; i < g->n_prob; ++i) sum |= g->pr[i].n_kb > most;
-  for (uint32_t i = 0; i < g->n_prob; ++i) g->pr[i].chunk = sum ? chunk : g->pr[i].n_kb;
+  for (uint32_t i = 0; i < g->n_prob; ++i) sum |= g->pr[i].kb_slice > most;
+  for (uint32_t i = 0; i < g->n_prob; ++i) g->pr[i].chunk = sum ? chunk : g->pr[i].kb_slice;
   return sum;
 }
 cudaError_t launch_product(const XentSet& S, int epi, int cg, GemmPlan* g, cudaStream_t s) {
@@ -755,10 +852,13 @@ cudaError_t launch_product(const XentSet& S, int epi, int cg, GemmPlan* g, cudaS
   return launch_gemm(epi, cg, sum, *g, grid, s);
 }
 
-void set_tiles(GemmProblem* q, int cg) {
+// k in at most `slices` parts.
+void set_tiles(GemmProblem* q, int cg, uint32_t slices) {
   q->m_tiles = (q->m + 128 * cg - 1) / (128 * cg);
   q->n_tiles = (q->n + q->tn - 1) / q->tn;
   q->n_kb = (q->k + 63) / 64;
+  q->kb_slice = (q->n_kb + slices - 1) / slices;
+  q->slices = (q->n_kb + q->kb_slice - 1) / q->kb_slice;
 }
 
 // Logits of rows of x against `n` rows of w from row v0.
@@ -770,7 +870,7 @@ cudaError_t logits_problem(const XentSet& S, const char* ws, int64_t v0, int64_t
   q.k = uint32_t(S.x.cols);
   q.tn = widest(S, cg);
   q.a_mn = q.b_mn = 0;
-  set_tiles(&q, cg);
+  set_tiles(&q, cg, 1);
   cudaError_t e = operand_map(&q.a, operand_base(S.x, ws), S.x.cols, S.x.rows, S.x.pitch, S.parts,
                               S.x.rows * S.x.pitch, 128, 1);
   if (e != cudaSuccess) return e;
@@ -859,7 +959,21 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
   if (e != cudaSuccess) return cuda_status(e);
   const int64_t N = S.x.rows, D = S.x.cols, V = S.w.rows;
   uint16_t* G = reinterpret_cast<uint16_t*>(ws + S.ws_g);
-  float* acc = reinterpret_cast<float*>(ws + S.ws_acc);
+  float* acc[2] = {reinterpret_cast<float*>(ws + S.ws_acc[0]),
+                   reinterpret_cast<float*>(ws + S.ws_acc[1])};
+  JoinPlan join = {};
+  join.scale = r.common;
+  auto join_part = [&](JoinPart* j, const GemmProblem& q, uint32_t slices) {
+    j->acc = q.acc;
+    j->plane = q.plane;
+    j->slices = slices;
+    j->rows = q.m;
+    j->cols = q.n;
+    j->vec = q.vec;
+    j->quads = make_fastdiv(uint32_t(q.lda / 4));
+    j->out = q.out;
+    j->blocks = uint32_t((uint64_t(q.m) * (q.lda / 4) + kThreads - 1) / kThreads);
+  };
   const int64_t lda = (D + 3) / 4 * 4;
   const int per16 = 16 / S.es;
   for (int64_t k = 0; k < S.n_piece; ++k) {
@@ -894,15 +1008,17 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.tn = widest(S, cg);
       q.a_mn = 0;
       q.b_mn = 1;
-      set_tiles(&q, cg);
+      set_tiles(&q, cg, S.slices[0]);
       q.out = grad_x;
       q.ldo = D;
-      q.acc = acc;
+      q.acc = acc[0];
       q.lda = lda;
+      q.plane = N * lda;
       q.acc_in = k > 0;
-      q.acc_out = k + 1 < S.n_piece;
+      q.acc_out = k + 1 < S.n_piece || S.slices[0] > 1;
       q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(grad_x) % 16 == 0;
-      q.tma_out = q.vec && S.es == 2;
+      q.tma_out = q.vec && S.es == 2 && !q.acc_out;
+      if (S.slices[0] > 1 && k + 1 == S.n_piece) join_part(&join.p[0], q, S.slices[0]);
       if (q.tma_out && (e = output_map(&q.c, grad_x, D, N, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
       if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 128, 1)) != cudaSuccess)
@@ -920,11 +1036,16 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.tn = widest(S, cg);
       q.a_mn = 1;
       q.b_mn = 1;
-      set_tiles(&q, cg);
+      set_tiles(&q, cg, S.slices[1]);
       q.out = static_cast<char*>(grad_w) + v0 * D * S.es;
       q.ldo = D;
+      q.acc = acc[1];
+      q.lda = lda;
+      q.plane = int64_t(n) * lda;
+      q.acc_out = S.slices[1] > 1;
       q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0;
-      q.tma_out = q.vec && S.es == 2;
+      q.tma_out = q.vec && S.es == 2 && !q.acc_out;
+      if (q.acc_out) join_part(&join.p[1], q, q.slices);
       if (q.tma_out && (e = output_map(&q.c, q.out, D, n, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
       if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 64, 2)) != cudaSuccess)
@@ -933,10 +1054,15 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
                            S.x.rows * S.x.pitch, 64, q.tn / cg / 64)) != cudaSuccess)
         return cuda_status(e);
     }
-    o.tiles0 = o.pr[0].m_tiles * o.pr[0].n_tiles;
-    o.tiles = o.tiles0 + (o.n_prob > 1 ? o.pr[1].m_tiles * o.pr[1].n_tiles : 0);
+    o.tiles0 = o.pr[0].m_tiles * o.pr[0].n_tiles * o.pr[0].slices;
+    o.tiles = o.tiles0 + (o.n_prob > 1 ? o.pr[1].m_tiles * o.pr[1].n_tiles * o.pr[1].slices : 0);
     o.m_fast = 0;
     if ((e = launch_product(S, kEpiOut, cg, &o, s)) != cudaSuccess) return cuda_status(e);
+    if (const unsigned blocks = join.p[0].blocks + join.p[1].blocks) {
+      e = S.es == 4 ? launch_k(k_xent_join<float>, blocks, kThreads, 0, s, join)
+                    : launch_k(k_xent_join<__nv_bfloat16>, blocks, kThreads, 0, s, join);
+      if (e != cudaSuccess) return cuda_status(e);
+    }
   }
   return ZR_OK;
 }
@@ -946,7 +1072,8 @@ std::string xent_json(const XentSet& S) {
          std::to_string(S.x.cols) + ",\"vocab\":" + std::to_string(S.w.rows) + ",\"parts\":" +
          std::to_string(S.parts) + ",\"pack_x\":" + std::to_string(S.x.pack) + ",\"pack_w\":" +
          std::to_string(S.w.pack) + ",\"piece\":" + std::to_string(S.piece) + ",\"n_piece\":" +
-         std::to_string(S.n_piece) + ",\"ws\":" + std::to_string(S.ws) + "}";
+         std::to_string(S.n_piece) + ",\"slices_x\":" + std::to_string(S.slices[0]) +
+         ",\"slices_w\":" + std::to_string(S.slices[1]) + ",\"ws\":" + std::to_string(S.ws) + "}";
 }
 
 int check_all(std::initializer_list<const void*> ps) {
@@ -1071,8 +1198,8 @@ int zr_test_gemm_walk(uint32_t tiles0, uint32_t tiles1, uint32_t kb0, uint32_t k
     return ZR_ERR_NULL;
   GemmPlan g = {};
   g.n_prob = tiles1 ? 2 : 1;
-  g.pr[0].n_kb = kb0;
-  g.pr[1].n_kb = kb1;
+  g.pr[0].kb_slice = kb0;
+  g.pr[1].kb_slice = kb1;
   g.tiles0 = tiles0;
   g.tiles = tiles0 + tiles1;
   *workers = gemm_grid(&g, cg) / unsigned(cg);

@@ -297,6 +297,33 @@ def test_pieces_of_the_vocabulary(dtype, N, V, D):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,V,D", [(1, 40000, 72), (40, 20000, 65), (300, 9001, 200), (129, 33000, 64), (2500, 130, 384),
+                                   (9000, 65, 130)])
+def test_long_sums_in_slices(N, V, D, dtype):
+    """Few rows, or few classes: one gradient's sum is cut into slices."""
+    x, w, y = make(N + V, N, V, D, dtype)
+    for want in ((True, True), (True, False), (False, True)):
+        check(x, w, y, "mean", want=want)
+    check(x, w, y, "none")
+    loss, lse = zr.zr_linear_xent_fwd(x, w, y, "sum", IGN)
+    g = torch.tensor(0.5, device="cuda")
+    want = zr.zr_linear_xent_bwd(g, x, w, y, lse, "sum", IGN)
+    bufs = [torch.full((t.numel() + 17,), -7.25, dtype=dtype, device="cuda") for t in (x, w)]
+    outs = [b[1:1 + t.numel()].view(t.shape) for b, t in zip(bufs, (x, w))]
+    zr.zr_linear_xent_bwd(g, x, w, y, lse, "sum", IGN, grads=outs)
+    for b, o, v in zip(bufs, outs, want):
+        assert torch.equal(o, v) and bool((b[:1] == -7.25).all()) and bool((b[1 + o.numel():] == -7.25).all())
+
+
+def test_slices_over_pieces():
+    """Few rows against more classes than one piece of the workspace holds."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40e9:
+        pytest.skip("needs 40 GB")
+    check(*make(11, 280, 650000, 24, torch.float32))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N", [1, 2, 3, 4, 5])
 def test_few_rows(N, dtype):
     """The forward's own path for a handful of rows, and around it."""

@@ -228,6 +228,30 @@ def test_linear_xent_plans(L):
                 assert d["ws"] >= g and g <= max((1 << 30) + N * 512 * parts, N * 2304 * 2 * parts)
 
 
+def test_linear_xent_slices(L):
+    """A long sum over few tiles is cut into slices, none of them empty, whose
+    planes the workspace holds; sums that fill the GPU stay whole."""
+    for dt, N, V, D, cut in ((F32, 40, 100000, 384, 0), (BF16, 300, 32000, 1024, 0), (BF16, 1, 50001, 768, 0),
+                             (BF16, 16384, 500, 1024, 1), (F32, 280, 650000, 24, 0)):
+        d = _xent_plan(L, dt, N, V, D, 1)
+        s = (d["slices_x"], d["slices_w"])
+        assert s[cut] > 1 and s[1 - cut] == 1, (N, V, D, s)
+        assert d["ws"] >= s[cut] * (N, V)[cut] * D * 4
+    for dt, N, V, D in ((F32, 4080, 5003, 384), (BF16, 2048, 8192, 2048), (BF16, 4096, 32000, 1024), (F32, 1, 1, 1),
+                        (BF16, 16384, 50001, 768), (F32, 64, 64, 64)):
+        d = _xent_plan(L, dt, N, V, D, 1)
+        assert (d["slices_x"], d["slices_w"]) == (1, 1), (N, V, D)
+    for dt in (F32, BF16):
+        for N in (1, 65, 129, 1000, 16384, 1000003):
+            for V in (1, 64, 500, 50001, 1000000):
+                for D in (1, 65, 2048):
+                    d = _xent_plan(L, dt, N, V, D, 1)
+                    for s, k, m in ((d["slices_x"], min(d["piece"], V), N), (d["slices_w"], N, min(d["piece"], V))):
+                        kb = (k + 63) // 64
+                        assert 1 <= s <= kb and -(-kb // -(-kb // s)) == s
+                        assert s == 1 or s * m * D * 4 <= (1 << 30)
+
+
 @pytest.mark.parametrize("cg", [1, 2])
 def test_every_tile_is_dealt_out_once(L, cg):
     """All tiles of one and of two products, each to one worker, and no worker
