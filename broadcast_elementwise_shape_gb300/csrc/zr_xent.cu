@@ -833,17 +833,22 @@ constexpr uint32_t kChunkF32 = 1, kChunkBf16 = 64;
 // truncation stays below 2^-10 of the sum.
 constexpr uint32_t kLongK = 2048;
 
-// The forward's logits of bfloat16 rows give binary32 results: chunks of 2048
-// terms, so that only rows longer than that pay for them ([16384, 768] x
-// [50001, 768]: 0.79 ms in one go, 0.84 through the registers).
-constexpr uint32_t kChunkLse = 32;
+// The forward's logits of bfloat16 rows give binary32 results: at most 1024
+// terms in one go, so that only longer rows pay for the registers.  Longer or
+// shorter: [4096, 2048] x [20000, 2048], 171 us and a loss off by 1.6e-6 in one
+// go, 174 us and 0.8e-6 in two; [4096, 1024], 88 us and 0.9e-6 in one, 106 us
+// and 0.5e-6 in two.
+constexpr uint32_t kChunkLse = 16;
 
 bool sum_chunks(const XentSet& S, int epi, GemmPlan* g) {
   const uint32_t most = S.es == 4 ? 0 : (epi == kEpiLse ? kChunkLse : kLongK);
   const uint32_t chunk = S.es == 4 ? kChunkF32 : (epi == kEpiLse ? kChunkLse : kChunkBf16);
   bool sum = false;
   for (uint32_t i = 0; i < g->n_prob; ++i) sum |= g->pr[i].kb_slice > most;
-  for (uint32_t i = 0; i < g->n_prob; ++i) g->pr[i].chunk = sum ? chunk : g->pr[i].kb_slice;
+  for (uint32_t i = 0; i < g->n_prob; ++i) {
+    const uint32_t kb = g->pr[i].kb_slice, n = sum ? (kb + chunk - 1) / chunk : 1;
+    g->pr[i].chunk = (kb + n - 1) / n;  // of even length
+  }
   return sum;
 }
 cudaError_t launch_product(const XentSet& S, int epi, int cg, GemmPlan* g, cudaStream_t s) {
