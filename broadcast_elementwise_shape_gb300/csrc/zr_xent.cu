@@ -291,43 +291,56 @@ __global__ void __launch_bounds__(kRowsThreads) k_xent_rows(const __grid_constan
 
 // ------------------------------------------------------------------ few rows
 
-// Forward for at most kFewRows rows of x (generation, scoring): bound by
-// reading w once.  Each warp takes an equal run of w's rows, two at a time, its
-// lanes 16 bytes each, with the next loads in flight while the last are used;
-// x waits in shared memory as binary32, and so does the arithmetic run on
-// either storage.  A warp keeps a running maximum and sum per row of x, a
-// block joins its warps' in order.  The tensor-core path reads w in tiles of
-// 256 rows, too few to fill the GPU evenly, and every one of its 128-row blocks
-// of x is padding but for a few rows.  One row against [50001, 768] bf16:
-// 19 us a call (slope 6.9 TB/s); the tensor-core path 23.
+// Forward for a few rows of x (generation, scoring): bound by reading w once.
+// Each warp takes an equal run of w's rows, two at a time, its lanes 16 bytes
+// each, with the next loads in flight while the last are used; x waits in
+// shared memory as binary32, and so does the arithmetic run on either storage,
+// two columns to an instruction.  The 2 NT sums of two rows of w and NT of x
+// are added across the warp by halving: each step exchanges half of what is
+// left, until every lane holds one sum (9 exchanges for 8 sums; 40 one by one),
+// of which it keeps the running maximum and sum of exponentials.  A block joins
+// its warps' in order.  More rows than NT: groups of them, in neighbouring
+// blocks, so that L2 serves w to all but one.
+//   [50001, 768] bf16: one row 18.5 us with w from DRAM, two 20; the tensor-core
+//   path, whose 128-row blocks of x are padding but for the rows, 22.
+//   [50001, 768] f32: one row 30 us, 8 rows 42, 16 rows 69; the tensor-core path,
+//   which writes w's three parts first, 141.  [32000, 4096] f32: 16 rows 353 us
+//   against 434, 24 rows (in three groups) 491.
 struct FewPlan {
   const void* x;             // packed or as given: rows of pitch xp
   const void* w;
   int64_t xp, wp;
   uint32_t n, vocab, dim;
+  uint32_t groups, slots;    // of NT rows; blocks of each
   const void* labels;
   int64_t label_stride;
   uint32_t label_i64;
-  float2* partial;           // [n][gridDim.x]
+  float2* partial;           // [n][slots]
   float* at;
 };
-constexpr uint32_t kFewRows = 4;
-constexpr uint32_t kFewMaxDim = 12288;  // x in shared memory: 4 rows of it as binary32
-constexpr int kFewBlocks = 3;           // CTAs per SM (2 for four rows of x)
+constexpr uint32_t kFewElems = 49152;   // rows of x times columns in shared memory, as binary32
+constexpr int few_blocks(int rows) { return rows > 1 ? 2 : 3; }  // CTAs per SM
+// Rows of x that take this path, and how many of them a block does.
+uint32_t few_rows(int es) { return es == 4 ? 16 : 4; }
+uint32_t few_nt(uint32_t n) { return n <= 2 ? n : (n <= 4 ? 4 : 8); }
 
 template <typename E, int NT>
-__global__ void __launch_bounds__(kThreads, NT > 2 ? 2 : kFewBlocks)
+__global__ void __launch_bounds__(kThreads, few_blocks(NT))
 k_xent_few(const __grid_constant__ FewPlan p) {
   pdl_trigger();
   constexpr int V = 16 / sizeof(E);    // elements per access
   constexpr int R = 2;                 // rows of w at a time
   constexpr int U = 3;                 // accesses per row in flight
   extern __shared__ float s_x[];       // [NT][dim padded to 32 V]
-  __shared__ float2 s_part[kThreads / 32][NT];
+  constexpr int N = R * NT;            // sums: of row i / NT of w and i % NT of x
+  constexpr uint32_t kLanes = 32 / N;  // lanes that end up with the same one
+  __shared__ float2 s_part[kThreads / 32][N];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t group = blockIdx.x % p.groups, block = blockIdx.x / p.groups;
+  const uint32_t t0 = group * NT;
   const uint32_t steps = (p.dim + 32 * V - 1) / (32 * V);
   const uint32_t padded = steps * 32 * V;
-  const uint32_t nw = gridDim.x * (kThreads / 32), me = blockIdx.x * (kThreads / 32) + warp;
+  const uint32_t nw = p.slots * (kThreads / 32), me = block * (kThreads / 32) + warp;
   const uint32_t lo = uint32_t(uint64_t(p.vocab) * me / nw);
   const uint32_t hi = uint32_t(uint64_t(p.vocab) * (me + 1) / nw);
   pdl_wait();
@@ -359,78 +372,79 @@ k_xent_few(const __grid_constant__ FewPlan p) {
   load(qa);
   for (uint32_t i = threadIdx.x; i < NT * padded; i += kThreads) {
     const uint32_t t = i / padded, c = i - t * padded;
-    s_x[i] = t < p.n && c < p.dim
-                 ? ld1(static_cast<const E*>(p.x) + int64_t(t) * p.xp + c, false) : 0.f;
+    s_x[i] = t0 + t < p.n && c < p.dim
+                 ? ld1(static_cast<const E*>(p.x) + int64_t(t0 + t) * p.xp + c, false) : 0.f;
   }
-  int64_t label[NT];
-  float m[NT], s[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t] = -INFINITY;
-    s[t] = 0.f;
-    label[t] = -1;
-    if (t < int(p.n))
-      label[t] = p.label_i64
-                     ? static_cast<const int64_t*>(p.labels)[int64_t(t) * p.label_stride]
-                     : int64_t(static_cast<const int32_t*>(p.labels)[int64_t(t) * p.label_stride]);
-  }
+  const uint32_t mine = lane / kLanes, my_r = mine / NT, my_t = t0 + mine % NT;
+  int64_t label = -1;
+  if (my_t < p.n)
+    label = p.label_i64
+                ? static_cast<const int64_t*>(p.labels)[int64_t(my_t) * p.label_stride]
+                : int64_t(static_cast<const int32_t*>(p.labels)[int64_t(my_t) * p.label_stride]);
+  float m = -INFINITY, s = 0.f;
   __syncthreads();
-  float acc[R][NT];
+  F2 acc[N];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[r][t] = 0.f;
+  for (int i = 0; i < N; ++i) acc[i] = f2_splat(0.f);
   uint32_t v = lo, k = 0;
   auto use = [&](const uint4 (&q)[U][R]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (k + u >= steps) break;
       const uint32_t c = ((k + u) * 32 + lane) * V;
-      float xv[NT][V];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < V; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&s_x[t * padded + c + j]);
-          xv[t][j] = f.x; xv[t][j + 1] = f.y; xv[t][j + 2] = f.z; xv[t][j + 3] = f.w;
-        }
+      F2 w[R][V / 2];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const uint32_t w[4] = {q[u][r].x, q[u][r].y, q[u][r].z, q[u][r].w};
+        const uint32_t e[4] = {q[u][r].x, q[u][r].y, q[u][r].z, q[u][r].w};
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float f;
-          if constexpr (sizeof(E) == 4) f = __uint_as_float(w[j]);
-          else f = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+        for (int j = 0; j < V / 2; ++j) {
+          if constexpr (sizeof(E) == 4)
+            w[r][j] = f2_pack(__uint_as_float(e[2 * j]), __uint_as_float(e[2 * j + 1]));
+          else
+            w[r][j] = f2_pack(__uint_as_float(e[j] << 16), __uint_as_float(e[j] & 0xFFFF0000u));
+        }
+      }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[r][t] = __fmaf_rn(f, xv[t][j], acc[r][t]);
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < V / 2; j += 2) {
+          const float4 f = *reinterpret_cast<const float4*>(&s_x[t * padded + c + 2 * j]);
+          const F2 x0 = f2_pack(f.x, f.y), x1 = f2_pack(f.z, f.w);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            acc[r * NT + t] = f2_fma(w[r][j], x0, acc[r * NT + t]);
+            acc[r * NT + t] = f2_fma(w[r][j + 1], x1, acc[r * NT + t]);
+          }
         }
       }
     }
     k += U;
     if (k < steps) return;
-    // The rows are complete.  Every lane keeps the same running pairs.
+    // The rows are complete.
+    float a[N];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float l[R];
-      float top = m[t];
+    for (int i = 0; i < N; ++i) {
+      float hi2;
+      f2_unpack(acc[i], a[i], hi2);
+      a[i] += hi2;
+      acc[i] = f2_splat(0.f);
+    }
+    uint32_t bit = 16;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        l[r] = warp_sum(acc[r][t]);
-        acc[r][t] = 0.f;
-        if (v + r < hi) {
-          if (lane == 0 && int64_t(v + r) == label[t]) p.at[t] = l[r];
-        } else {
-          l[r] = -INFINITY;
-        }
-        top = fmaxf(top, l[r]);
-      }
+    for (int h = N / 2; h > 0; h /= 2, bit /= 2) {
+      const bool up = lane & bit;
+#pragma unroll
+      for (int i = 0; i < h; ++i)
+        a[i] = (up ? a[i + h] : a[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? a[i] : a[i + h], bit);
+    }
+#pragma unroll
+    for (uint32_t o = kLanes / 2; o > 0; o /= 2) a[0] += __shfl_xor_sync(0xFFFFFFFFu, a[0], o);
+    if (v + my_r < hi) {
+      const float l = a[0], top = fmaxf(m, l);
+      if (lane % kLanes == 0 && int64_t(v + my_r) == label) p.at[my_t] = l;
       const float base = top == -INFINITY ? 0.f : top;
-      float add = 0.f;
-#pragma unroll
-      for (int r = 0; r < R; ++r) add += __expf(l[r] - base);
-      s[t] = __fmaf_rn(s[t], __expf(m[t] - base), add);
-      m[t] = top;
+      s = __fmaf_rn(s, __expf(m - base), __expf(l - base));
+      m = top;
     }
     k = 0;
     v += R;
@@ -442,21 +456,23 @@ k_xent_few(const __grid_constant__ FewPlan p) {
     load(qa);
     use(qb);
   }
-  if (lane == 0)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) s_part[warp][t] = make_float2(m[t], s[t]);
+  if (lane % kLanes == 0) s_part[warp][mine] = make_float2(m, s);
   __syncthreads();
-  if (threadIdx.x < NT && threadIdx.x < p.n) {
+  if (threadIdx.x < NT && t0 + threadIdx.x < p.n) {
     float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, s_part[w][threadIdx.x].x);
+    for (int w = 0; w < kThreads / 32; ++w)
+#pragma unroll
+      for (int r = 0; r < R; ++r) top = fmaxf(top, s_part[w][r * NT + threadIdx.x].x);
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const float2 v = s_part[w][threadIdx.x];
-      sum = __fmaf_rn(v.y, expf(v.x - base), sum);
-    }
-    p.partial[uint64_t(threadIdx.x) * gridDim.x + blockIdx.x] = make_float2(top, sum);
+    for (int w = 0; w < kThreads / 32; ++w)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 e = s_part[w][r * NT + threadIdx.x];
+        sum = __fmaf_rn(e.y, expf(e.x - base), sum);
+      }
+    p.partial[uint64_t(t0 + threadIdx.x) * p.slots + block] = make_float2(top, sum);
   }
 }
 
@@ -558,8 +574,10 @@ int pick_cg(int64_t m) { return m > 128 ? 2 : 1; }
 // Widest tile (zr_gemm.cuh: a single CTA's stage of three parts).
 uint32_t widest(const XentSet& S, int cg) { return S.parts == 3 && cg == 1 ? 128 : 256; }
 
-uint32_t few_grid(int64_t rows, int64_t vocab) {
-  return uint32_t(std::min<int64_t>(kSms * (rows > 2 ? 2 : kFewBlocks), (vocab + 15) / 16));
+// Blocks of each group of rows: those of all groups run at the same time.
+uint32_t few_slots(int64_t rows, int64_t vocab) {
+  const int64_t nt = few_nt(uint32_t(rows)), groups = (rows + nt - 1) / nt;
+  return uint32_t(std::min<int64_t>(kSms * few_blocks(int(rows)) / groups, (vocab + 15) / 16));
 }
 
 int plan_operand(Operand* o, int es, bool force) {
@@ -678,12 +696,16 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
   // not reach grad_w), so it always copies x: 1 / vocab of the products' work.
   if ((rc = plan_operand(&S->x, S->es, back && want_w))) return rc;
   if ((rc = plan_operand(&S->w, S->es, false))) return rc;
-  if (!back && S->x.rows <= kFewRows && dim <= kFewMaxDim) {
+  if (!back && S->x.rows <= few_rows(S->es) &&
+      dim * few_nt(uint32_t(S->x.rows)) <= kFewElems) {
     // Rows of elements side by side, w's starting at 16-byte boundaries.
     const int V = 16 / S->es;
     const TDesc& wt = S->w.t;
     S->few = S->x.one_step && (dim == 1 || wt.stride[1] == 1) &&
              (vocab == 1 || wt.stride[0] % V == 0) && reinterpret_cast<uintptr_t>(wt.ptr) % 16 == 0;
+    // Three or four bfloat16 rows against much of w that the tensor cores can
+    // read as it is: [50001, 768], 29 us here and 22 there; [8000, 512], 8 and 10.
+    if (S->es == 2 && S->x.rows > 2 && !S->w.pack && vocab * dim > (int64_t(1) << 24)) S->few = false;
     if (S->few) S->x.pack = S->w.pack = false;
   }
   XentRows& r = S->rows;
@@ -709,7 +731,7 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     if (o->pack) o->ws = take(&at, size_t(o->rows) * o->pitch * 2 * S->parts);
   if (!back) {
     const int64_t tn = widest(*S, pick_cg(S->x.rows));
-    r.slots = S->few ? few_grid(S->x.rows, vocab) : 2 * uint32_t((vocab + tn - 1) / tn);
+    r.slots = S->few ? few_slots(S->x.rows, vocab) : 2 * uint32_t((vocab + tn - 1) / tn);
     S->ws_partial = take(&at, N * r.slots * sizeof(float2));
     S->ws_at = take(&at, N * 4);
     S->ws_row = take(&at, (N + 7) / 8 * 8);  // (float, count) per block of eight rows
@@ -889,8 +911,8 @@ cudaError_t logits_problem(const XentSet& S, const char* ws, int64_t v0, int64_t
 }
 
 template <typename E>
-cudaError_t launch_few(const FewPlan& p, unsigned grid, cudaStream_t s) {
-  const int nt = p.n == 1 ? 1 : (p.n == 2 ? 2 : 4);
+cudaError_t launch_few(const FewPlan& p, cudaStream_t s) {
+  const uint32_t nt = few_nt(p.n);
   constexpr uint32_t step = 32 * 16 / sizeof(E);
   const size_t smem = size_t(nt) * ((p.dim + step - 1) / step * step) * 4;
   auto go = [&](auto* k) {
@@ -898,10 +920,12 @@ cudaError_t launch_few(const FewPlan& p, unsigned grid, cudaStream_t s) {
       const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), 200 * 1024);
       if (e != cudaSuccess) return e;
     }
-    return launch_k(k, grid, kThreads, smem, s, p);
+    return launch_k(k, p.groups * p.slots, kThreads, smem, s, p);
   };
   if (nt == 1) return go(k_xent_few<E, 1>);
   if (nt == 2) return go(k_xent_few<E, 2>);
+  if constexpr (sizeof(E) == 4)
+    if (nt == 8) return go(k_xent_few<E, 8>);
   return go(k_xent_few<E, 4>);
 }
 
@@ -915,6 +939,8 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
     p.xp = S.x.row_step;
     p.wp = S.w.row_step;
     p.n = r.n;
+    p.slots = r.slots;
+    p.groups = (r.n + few_nt(r.n) - 1) / few_nt(r.n);
     p.vocab = uint32_t(S.w.rows);
     p.dim = uint32_t(S.x.cols);
     p.labels = r.labels;
@@ -922,7 +948,7 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
     p.label_i64 = r.label_i64;
     p.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
     p.at = reinterpret_cast<float*>(ws + S.ws_at);
-    e = S.es == 4 ? launch_few<float>(p, r.slots, s) : launch_few<__nv_bfloat16>(p, r.slots, s);
+    e = S.es == 4 ? launch_few<float>(p, s) : launch_few<__nv_bfloat16>(p, s);
     if (e != cudaSuccess) return cuda_status(e);
     r.partial = p.partial;
     r.at = p.at;

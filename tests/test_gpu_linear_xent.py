@@ -341,6 +341,21 @@ def test_few_rows(N, dtype):
     assert float(zr.zr_linear_xent_fwd(x, w, y)[0]) == 0
 
 
+@pytest.mark.parametrize("N", [5, 8, 9, 16, 17])
+def test_several_rows(N):
+    """binary32 rows in groups of eight, and the first count past them."""
+    for V, D in ((1, 1), (33, 264), (2501, 769), (1500, 1000), (40, 6144), (40, 6145)):
+        x, w, y = make(V + D + N, N, V, D, torch.float32)
+        for reduction in ("mean", "none"):
+            check(x, w, y, reduction)
+    bad = x.clone()
+    bad[4] = float("nan")
+    y = y.clamp(min=0)
+    rows, _ = zr.zr_linear_xent_fwd(bad, w, y, "none", IGN)
+    want, _ = zr.zr_linear_xent_fwd(x, w, y, "none", IGN)
+    assert torch.isnan(rows[4]) and torch.equal(rows[:4], want[:4]) and torch.equal(rows[5:], want[5:])
+
+
 def test_one_row_sums_to_binary32():
     """Long rows of positive terms: the worst case for sums that truncate."""
     for N in (1, 200):

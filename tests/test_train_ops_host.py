@@ -219,6 +219,11 @@ def test_linear_xent_plans(L):
     for n in (1, 4):
         assert _xent_plan(L, BF16, n, 1000, 128, 0)["kernel"] == "xent_few"
     assert _xent_plan(L, BF16, 5, 1000, 128, 0)["kernel"] == "xent"
+    assert _xent_plan(L, BF16, 4, 50001, 768, 0)["kernel"] == "xent"      # w as it is, and much of it
+    assert _xent_plan(L, BF16, 4, 50001, 776, 0)["kernel"] == "xent_few"  # w would have to be copied
+    for n, D, kernel in ((16, 1000, "xent_few"), (17, 1000, "xent"), (16, 6144, "xent_few"), (16, 6145, "xent"),
+                         (4, 12288, "xent_few"), (4, 12289, "xent")):
+        assert _xent_plan(L, F32, n, 1000, D, 0)["kernel"] == ("xent" if D % 4 else kernel)
     for dt, parts in ((BF16, 1), (F32, 3)):
         for N in (1, 7, 4096, 100000, 1000003):
             for V in (1, 255, 50001, 262144):
