@@ -487,7 +487,8 @@ int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, voi
  *   grad_x = G W and grad_w = G^T X, dense row-major, either may be NULL.
  * The logits are computed again, a piece of the vocabulary at a time; the
  * workspace holds one piece of G (about 1 GiB at most, or 2048 classes'
- * worth for very many rows).
+ * worth for very many rows) and, where a gradient's long sum over few outputs
+ * is cut into slices, their results (1 GiB at most per gradient).
  *
  * Numerics.  Products accumulate in binary32 on the tensor cores; statistics
  * and losses are binary32.  ZR_BF16: operands as stored, G rounded once to
