@@ -31,16 +31,16 @@ struct GemmProblem {
   uint32_t slices, kb_slice;
   int64_t plane;
   uint32_t chunk;            // k blocks per accumulation in TMEM
-  // Epilogues kEpiGrad and kEpiOut with tma_out: bfloat16 results leave through
-  // this map, in boxes of 64 columns by 32 rows.
+  // Epilogues kEpiGrad and kEpiOut with tma_out: results leave through this map,
+  // in boxes of 128 bytes by 32 rows.
   CUtensorMap c;
   uint32_t tma_out;
-  // Epilogue kEpiOut: out = [acc_in +] product, in `es` bytes per element
-  // with row stride ldo; or to the binary32 array acc when acc_out.
+  // Epilogue kEpiOut: out = [acc_in +] product, in the operands' type with row
+  // stride ldo; or to the binary32 array acc when acc_out.
   void* out;
   float* acc;
   int64_t ldo, lda;
-  uint32_t acc_in, acc_out, vec;
+  uint32_t acc_in, acc_out;
 };
 
 enum GemmEpilogue : int {
@@ -56,7 +56,6 @@ struct GemmPlan {
   uint32_t m_fast;           // consecutive tiles walk m first
   // Two problems' tiles over `workers` clusters (GemmWalk).
   uint32_t workers, head, extra, late_first;
-  uint32_t es;               // kEpiOut: bytes per output element
   const float* out_scale;    // kEpiOut: multiplies the finished product, or null (1)
   // kEpiLse, kEpiGrad
   const void* labels;        // label of row r: labels[r * label_stride]

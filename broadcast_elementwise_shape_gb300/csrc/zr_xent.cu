@@ -790,18 +790,20 @@ cudaError_t operand_map(CUtensorMap* m, const void* base, int64_t cols, int64_t 
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-// Map of an output [parts][rows][cols] that tiles of 64 x 32 are stored to.
-cudaError_t output_map(CUtensorMap* m, void* base, int64_t cols, int64_t rows, int64_t pitch,
+// Map of an output [parts][rows][cols] of `es` bytes per element that tiles of
+// 128 bytes x 32 rows are stored to.
+cudaError_t output_map(CUtensorMap* m, void* base, int es, int64_t cols, int64_t rows, int64_t pitch,
                        uint32_t parts, int64_t part) {
   const EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), parts};
-  const int64_t plane = parts > 1 ? part : (rows * pitch + 7) / 8 * 8;
-  const cuuint64_t strides[2] = {cuuint64_t(pitch) * 2, cuuint64_t(plane) * 2};
-  const cuuint32_t box[3] = {64, 32, 1}, step[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, step,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const int64_t plane = (parts > 1 ? part : rows * pitch) * es;
+  const cuuint64_t strides[2] = {cuuint64_t(pitch) * es, cuuint64_t(plane + 15) / 16 * 16};
+  const cuuint32_t box[3] = {cuuint32_t(128 / es), 32, 1}, step[3] = {1, 1, 1};
+  const CUresult r = fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                        base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -994,13 +996,13 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
                    reinterpret_cast<float*>(ws + S.ws_acc[1])};
   JoinPlan join = {};
   join.scale = r.common;
-  auto join_part = [&](JoinPart* j, const GemmProblem& q, uint32_t slices) {
+  auto join_part = [&](JoinPart* j, const GemmProblem& q, uint32_t slices, bool vec) {
     j->acc = q.acc;
     j->plane = q.plane;
     j->slices = slices;
     j->rows = q.m;
     j->cols = q.n;
-    j->vec = q.vec;
+    j->vec = vec;
     j->quads = make_fastdiv(uint32_t(q.lda / 4));
     j->out = q.out;
     j->blocks = uint32_t((uint64_t(q.m) * (q.lda / 4) + kThreads - 1) / kThreads);
@@ -1021,14 +1023,13 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     g.vocab = V;
     g.row_scale = r.reduction == ZR_NONE ? grad_loss : nullptr;
     g.label_base = v0;
-    if ((e = output_map(&g.pr[0].c, G, ldg, N, ldg, S.parts, N * ldg)) != cudaSuccess)
+    if ((e = output_map(&g.pr[0].c, G, 2, ldg, N, ldg, S.parts, N * ldg)) != cudaSuccess)
       return cuda_status(e);
     if ((e = launch_product(S, kEpiGrad, cg, &g, s)) != cudaSuccess) return cuda_status(e);
 
     cg = pick_cg(std::min(N, n));
     GemmPlan o = {};
     o.parts = S.parts;
-    o.es = uint32_t(S.es);
     o.out_scale = r.common;
     // grad_x += G W: rows of x, k = this piece's vocabulary.
     if (grad_x) {
@@ -1047,10 +1048,10 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.plane = N * lda;
       q.acc_in = k > 0;
       q.acc_out = k + 1 < S.n_piece || S.slices[0] > 1;
-      q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(grad_x) % 16 == 0;
-      q.tma_out = q.vec && S.es == 2 && !q.acc_out;
-      if (S.slices[0] > 1 && k + 1 == S.n_piece) join_part(&join.p[0], q, S.slices[0]);
-      if (q.tma_out && (e = output_map(&q.c, grad_x, D, N, D, 1, 0)) != cudaSuccess)
+      const bool vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(grad_x) % 16 == 0;
+      q.tma_out = vec && !q.acc_out;
+      if (S.slices[0] > 1 && k + 1 == S.n_piece) join_part(&join.p[0], q, S.slices[0], vec);
+      if (q.tma_out && (e = output_map(&q.c, grad_x, S.es, D, N, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
       if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 128, 1)) != cudaSuccess)
         return cuda_status(e);
@@ -1074,10 +1075,10 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       q.lda = lda;
       q.plane = int64_t(n) * lda;
       q.acc_out = S.slices[1] > 1;
-      q.vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0;
-      q.tma_out = q.vec && S.es == 2 && !q.acc_out;
-      if (q.acc_out) join_part(&join.p[1], q, q.slices);
-      if (q.tma_out && (e = output_map(&q.c, q.out, D, n, D, 1, 0)) != cudaSuccess)
+      const bool vec = D % per16 == 0 && reinterpret_cast<uintptr_t>(q.out) % 16 == 0;
+      q.tma_out = vec && !q.acc_out;
+      if (q.acc_out) join_part(&join.p[1], q, q.slices, vec);
+      if (q.tma_out && (e = output_map(&q.c, q.out, S.es, D, n, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
       if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 64, 2)) != cudaSuccess)
         return cuda_status(e);
