@@ -857,16 +857,21 @@ constexpr uint32_t kChunkF32 = 1, kChunkBf16 = 64;
 // truncation stays below 2^-10 of the sum.
 constexpr uint32_t kLongK = 2048;
 
-// The forward's logits of bfloat16 rows give binary32 results: at most 1024
-// terms in one go, so that only longer rows pay for the registers.  Longer or
-// shorter: [4096, 2048] x [20000, 2048], 171 us and a loss off by 1.6e-6 in one
+// The logits of bfloat16 rows give binary32 results: at most 1024 terms in one
+// go, so that only longer rows pay for the registers.  Longer or shorter, the
+// forward: [4096, 2048] x [20000, 2048], 171 us and a loss off by 1.6e-6 in one
 // go, 174 us and 0.8e-6 in two; [4096, 1024], 88 us and 0.9e-6 in one, 106 us
-// and 0.5e-6 in two.
+// and 0.5e-6 in two.  The backward's logits go the same way, for
+// exp(l - lse) - 1 of a row that is learnt shows every difference between them
+// and those that lse was summed from: rows of 4096 positive terms, l = 20, had
+// the label's gradient off by 1.2 times its size at 1 - p = 1.5e-4 when the
+// backward added them in one go.
 constexpr uint32_t kChunkLse = 16;
 
 bool sum_chunks(const XentSet& S, int epi, GemmPlan* g) {
-  const uint32_t most = S.es == 4 ? 0 : (epi == kEpiLse ? kChunkLse : kLongK);
-  const uint32_t chunk = S.es == 4 ? kChunkF32 : (epi == kEpiLse ? kChunkLse : kChunkBf16);
+  const bool logits = epi != kEpiOut;
+  const uint32_t most = S.es == 4 ? 0 : (logits ? kChunkLse : kLongK);
+  const uint32_t chunk = S.es == 4 ? kChunkF32 : (logits ? kChunkLse : kChunkBf16);
   bool sum = false;
   for (uint32_t i = 0; i < g->n_prob; ++i) sum |= g->pr[i].kb_slice > most;
   for (uint32_t i = 0; i < g->n_prob; ++i) {
