@@ -446,15 +446,21 @@ struct EpiLse {
 // tensors, as three bfloat16 parts that hold it to 2^-24.  A factor that all
 // rows share is left to the products' epilogue: then the label's element of a
 // row that is not yet learnt, the largest by far, is -1 and rounds to itself.
+//
+// The label's element, p - 1, is a small difference where the row is learnt:
+// lse's rounding alone (2^-25 of it) was 1.7e-5 of a whole binary32 gradient of
+// one row.  So it is taken as what the other elements sum to, which is as exact
+// as they are: with p.sums every half tile leaves its sum of exp(l - lse) but
+// for the label's, and k_xent_label puts -sum / (sum + the label's) in its place.
 template <int PARTS>
 struct EpiGrad {
-  float scale, lse2;
+  float scale, lse2, sum;
   int64_t at;
   bool out;                  // the row is left out: zeros, whatever its products are
 
   __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem&, const EpiPos& e) {
     scale = 1.f;
-    lse2 = 0.f;
+    lse2 = sum = 0.f;
     at = -1;
     out = true;
     if (e.live) {
@@ -462,9 +468,9 @@ struct EpiGrad {
       out = label == p.ignore_index;
       if (!out) {
         if (p.row_scale) scale = p.row_scale[e.row];
-        if (label < 0 || label >= p.vocab) scale = qnan();  // no class: NaN, not a guess
         lse2 = p.lse[e.row] * kLog2e;
-        at = label - p.label_base - int64_t(e.n0);
+        if (label < 0 || label >= p.vocab) scale = qnan();  // no class: NaN, not a guess
+        else at = label - p.label_base - int64_t(e.n0);
       }
     }
   }
@@ -486,23 +492,52 @@ struct EpiGrad {
 #pragma unroll
       for (int i = 0; i < 64; ++i) v[i] = ex2(v[i]);
     }
-    if (__any_sync(0xFFFFFFFFu, scale != 1.f)) {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] *= scale;
-    }
-    if (__any_sync(0xFFFFFFFFu, at >= int64_t(c) && at < int64_t(c) + 64)) {
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (at == int64_t(c) + i) v[i] -= scale;
-    }
-    if (out || !e.ok) {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = e.ok ? 0.f : qnan();
-    }
     if (e.n0 + c + 64 > q.n) {  // G's rows are padded with zeros to whole blocks of 64
 #pragma unroll
       for (int i = 0; i < 64; ++i)
         if (e.n0 + c + i >= q.n) v[i] = 0.f;
+    }
+    const bool mine = at >= int64_t(c) && at < int64_t(c) + 64;
+    if (__any_sync(0xFFFFFFFFu, mine)) {
+      if (p.sums) {          // what is stored in its place is overwritten
+        float own = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          if (at == int64_t(c) + i) {
+            own = v[i];
+            v[i] = 0.f;
+          }
+        }
+        if (mine) p.at[e.row] = e.ok ? own : qnan();
+      } else if (p.label_g) {
+        const float g = mine ? p.label_g[e.row] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (at == int64_t(c) + i) v[i] = g;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (at == int64_t(c) + i) v[i] -= 1.f;
+      }
+    }
+    if (p.sums) {
+      F2 add[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+      for (int i = 4; i < 32; ++i) add[i & 3] = f2_add(add[i & 3], f2_pack(v[2 * i], v[2 * i + 1]));
+      float lo, hi;
+      f2_unpack(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
+      sum += lo + hi;
+      if (!q.tma_out) return;
+    }
+    if (__any_sync(0xFFFFFFFFu, scale != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] *= scale;
+    }
+    if (out || !e.ok) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = e.ok ? 0.f : qnan();
     }
     epi_store(&q.c, e, c, 0, v);
     #pragma unroll 1
@@ -512,7 +547,10 @@ struct EpiGrad {
       epi_store(&q.c, e, c, part, v);
     }
   }
-  __device__ __forceinline__ void end(const GemmPlan&, const GemmProblem&, const EpiPos&) {}
+  __device__ __forceinline__ void end(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
+    if (p.sums && e.live)
+      p.sums[uint64_t(e.row) * (2 * q.n_tiles) + 2 * e.nt + e.half] = e.ok ? sum : qnan();
+  }
 };
 
 // Results in the operands' type: binary32 where they come in three parts.

@@ -32,7 +32,7 @@ struct GemmProblem {
   int64_t plane;
   uint32_t chunk;            // k blocks per accumulation in TMEM
   // Epilogues kEpiGrad and kEpiOut with tma_out: results leave through this map,
-  // in boxes of 128 bytes by 32 rows.
+  // in boxes of 128 bytes by 32 rows.  kEpiGrad without it: not stored.
   CUtensorMap c;
   uint32_t tma_out;
   // Epilogue kEpiOut: out = [acc_in +] product, in the operands' type with row
@@ -45,7 +45,8 @@ struct GemmProblem {
 
 enum GemmEpilogue : int {
   kEpiLse = 0,   // per row and half tile: maximum and sum of exponentials
-  kEpiGrad = 1,  // scale * (exp(product - lse) - [column == label]) as bfloat16 parts
+  kEpiGrad = 1,  // scale * (exp(product - lse) - [column == label]) as bfloat16 parts,
+                 // and the sums that the label's element is worked out from
   kEpiOut = 2    // the product itself
 };
 
@@ -64,10 +65,12 @@ struct GemmPlan {
   // kEpiLse
   uint32_t* ticket;          // set to 0
   float2* partial;           // [m][2 * n_tiles] (maximum, sum)
-  float* at;                 // [m] product at the label
+  float* at;                 // [m] product at the label; kEpiGrad: exp(product - lse) there
   // kEpiGrad
   const float* lse;          // [m]
   const float* row_scale;    // [m], or null (1)
+  float* sums;               // [m][2 * n_tiles] sum of exp(product - lse) but for the label, or null
+  const float* label_g;      // [m] the label's element less its factor, or null (exp(...) - 1)
   int64_t ignore_index, vocab;
   int64_t label_base;        // column 0 of this product is this label
 };

@@ -550,6 +550,48 @@ __global__ void __launch_bounds__(kThreads) k_xent_join(const __grid_constant__ 
   }
 }
 
+// The label's element of G from the sums that kEpiGrad left (EpiGrad), a warp
+// per row, the slots in an order fixed by the sizes: into G itself, or as a value
+// for the pieces of G that are still to be written.
+struct LabelPlan {
+  XentRows rows;
+  const float* sums;         // [n][slots]
+  const float* at;           // [n] exp(l - lse) at the label
+  const float* row_scale;    // or null (1)
+  uint16_t* g;               // [parts][n][ldg]
+  int64_t ldg;
+  uint32_t slots, parts;
+  float* label_g;            // [n], or null: into g
+};
+
+__global__ void __launch_bounds__(kRowsThreads) k_xent_label(const __grid_constant__ LabelPlan p) {
+  pdl_trigger();
+  const uint32_t lane = threadIdx.x & 31, r = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
+  pdl_wait();
+  if (r >= p.rows.n) return;
+  const int64_t y = row_label(p.rows, r);
+  // Left out: zeros.  No class: the row is NaN.
+  if (y == p.rows.ignore_index || y < 0 || y >= p.rows.vocab) return;
+  const float* q = p.sums + uint64_t(r) * p.slots;
+  float s = 0.f;
+#pragma unroll 4
+  for (uint32_t i = lane; i < p.slots; i += 32) s += q[i];
+  s = warp_sum(s);
+  if (lane != 0) return;
+  float v = -__fdiv_rn(s, s + p.at[r]);
+  if (p.label_g) {
+    p.label_g[r] = v;
+    return;
+  }
+  if (p.row_scale) v *= p.row_scale[r];
+  uint16_t* g = p.g + int64_t(r) * p.ldg + y;
+  for (uint32_t part = 0; part < p.parts; ++part, g += int64_t(p.rows.n) * p.ldg) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+    *g = *reinterpret_cast<const uint16_t*>(&h);
+    v -= __bfloat162float(h);
+  }
+}
+
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;  // G of one piece of the vocabulary, about
 
 struct XentSet {
@@ -565,6 +607,11 @@ struct XentSet {
   size_t ws_partial = 0, ws_at = 0, ws_row = 0, ws_ticket = 0;
   // backward
   size_t ws_common = 0, ws_g = 0, ws_acc[2] = {0, 0};
+  // Where the label's element comes from: 0 exp(l - lse) - 1, 1 the sums that
+  // are left with G, 2 sums of their own before it (LabelPlan).
+  int label_pass = 0;
+  uint32_t label_slots = 0;
+  size_t ws_sums = 0, ws_label = 0;
   int64_t piece = 0, n_piece = 0;
   uint32_t slices[2] = {1, 1};  // of grad_x's and grad_w's k (plan_slices)
 };
@@ -744,6 +791,18 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     S->n_piece = (vocab + S->piece - 1) / S->piece;
     const int64_t wide = std::min<int64_t>(S->piece, (vocab + 63) / 64 * 64);
     S->ws_g = take(&at, N * size_t(wide) * 2 * S->parts);
+    // Over several pieces the sums are known when the label's piece is long
+    // gone.  binary32 then sums once before (a fourth more products).  bfloat16
+    // does without: lse's rounding, some 1e-6 of p, is beside the 2^-9 that G
+    // itself is rounded by until p is within 5e-4 of 1.
+    S->label_pass = S->n_piece == 1 ? 1 : (S->es == 4 ? 2 : 0);
+    if (S->label_pass) {
+      const int64_t tn = widest(*S, pick_cg(S->x.rows));
+      S->label_slots = 2 * uint32_t((vocab + tn - 1) / tn);
+      S->ws_sums = take(&at, N * S->label_slots * sizeof(float));
+      S->ws_at = take(&at, N * 4);
+      if (S->label_pass == 2) S->ws_label = take(&at, N * 4);
+    }
     plan_slices(S, dim);
     const size_t lda = size_t(dim + 3) / 4 * 4;
     if (S->n_piece > 1 || S->slices[0] > 1) S->ws_acc[0] = take(&at, S->slices[0] * N * lda * 4);
@@ -1014,23 +1073,58 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
   };
   const int64_t lda = (D + 3) / 4 * 4;
   const int per16 = 16 / S.es;
+  LabelPlan label = {};
+  label.rows = r;
+  label.sums = reinterpret_cast<const float*>(ws + S.ws_sums);
+  label.at = reinterpret_cast<const float*>(ws + S.ws_at);
+  label.row_scale = r.reduction == ZR_NONE ? grad_loss : nullptr;
+  label.g = G;
+  label.slots = S.label_slots;
+  label.parts = S.parts;
+  auto launch_label = [&](float* label_g, int64_t ldg) {
+    label.label_g = label_g;
+    label.ldg = ldg;
+    return launch_k(k_xent_label, unsigned((N + kRowsThreads / 32 - 1) / (kRowsThreads / 32)), kRowsThreads, 0, s,
+                    label);
+  };
+  auto grad_logits = [&](int64_t v0, int64_t n, int cg, GemmPlan* g) {
+    g->lse = lse;
+    g->labels = r.labels;
+    g->label_stride = r.label_stride;
+    g->label_i64 = r.label_i64;
+    g->ignore_index = r.ignore_index;
+    g->vocab = V;
+    g->row_scale = label.row_scale;
+    g->label_base = v0;
+    return logits_problem(S, ws, v0, n, cg, g);
+  };
+  float* label_g = nullptr;
+  if (S.label_pass == 2) {
+    label_g = reinterpret_cast<float*>(ws + S.ws_label);
+    GemmPlan g = {};
+    g.sums = reinterpret_cast<float*>(ws + S.ws_sums);
+    g.at = reinterpret_cast<float*>(ws + S.ws_at);
+    const int cg = pick_cg(N);
+    if ((e = grad_logits(0, V, cg, &g)) != cudaSuccess) return cuda_status(e);
+    if ((e = launch_product(S, kEpiGrad, cg, &g, s)) != cudaSuccess) return cuda_status(e);
+    if ((e = launch_label(label_g, 0)) != cudaSuccess) return cuda_status(e);
+  }
   for (int64_t k = 0; k < S.n_piece; ++k) {
     const int64_t v0 = k * S.piece, n = std::min(S.piece, V - v0);
     const int64_t ldg = (n + 63) / 64 * 64;
     int cg = pick_cg(N);
     GemmPlan g = {};
-    if ((e = logits_problem(S, ws, v0, n, cg, &g)) != cudaSuccess) return cuda_status(e);
-    g.lse = lse;
-    g.labels = r.labels;
-    g.label_stride = r.label_stride;
-    g.label_i64 = r.label_i64;
-    g.ignore_index = r.ignore_index;
-    g.vocab = V;
-    g.row_scale = r.reduction == ZR_NONE ? grad_loss : nullptr;
-    g.label_base = v0;
+    if (S.label_pass == 1) {
+      g.sums = reinterpret_cast<float*>(ws + S.ws_sums);
+      g.at = reinterpret_cast<float*>(ws + S.ws_at);
+    }
+    g.label_g = label_g;
+    if ((e = grad_logits(v0, n, cg, &g)) != cudaSuccess) return cuda_status(e);
+    g.pr[0].tma_out = 1;
     if ((e = output_map(&g.pr[0].c, G, 2, ldg, N, ldg, S.parts, N * ldg)) != cudaSuccess)
       return cuda_status(e);
     if ((e = launch_product(S, kEpiGrad, cg, &g, s)) != cudaSuccess) return cuda_status(e);
+    if (S.label_pass == 1 && (e = launch_label(nullptr, ldg)) != cudaSuccess) return cuda_status(e);
 
     cg = pick_cg(std::min(N, n));
     GemmPlan o = {};
@@ -1110,7 +1204,7 @@ std::string xent_json(const XentSet& S) {
          std::to_string(S.parts) + ",\"pack_x\":" + std::to_string(S.x.pack) + ",\"pack_w\":" +
          std::to_string(S.w.pack) + ",\"piece\":" + std::to_string(S.piece) + ",\"n_piece\":" +
          std::to_string(S.n_piece) + ",\"slices_x\":" + std::to_string(S.slices[0]) +
-         ",\"slices_w\":" + std::to_string(S.slices[1]) + ",\"ws\":" + std::to_string(S.ws) + "}";
+         ",\"slices_w\":" + std::to_string(S.slices[1]) + ",\"label_pass\":" + std::to_string(S.label_pass) + ",\"ws\":" + std::to_string(S.ws) + "}";
 }
 
 int check_all(std::initializer_list<const void*> ps) {
