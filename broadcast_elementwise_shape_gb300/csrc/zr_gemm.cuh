@@ -383,7 +383,10 @@ __device__ __forceinline__ void epi_store_f32(const CUtensorMap* map, const EpiP
 }
 
 // Running maximum and sum of exponentials over the lane's columns, in one
-// walk: a chunk's maximum rescales the sum once.
+// walk: a chunk's maximum rescales the sum once.  The maximum (in EpiGrad, lse)
+// is subtracted before the factor log2(e): near it, where terms count, that
+// difference is exact, while one fused step from the rounded product
+// max * log2(e) would put its rounding, 1e-6 at 20, into every term.
 struct EpiLse {
   int64_t at;                // column of the label in this tile
   float m, s;
@@ -416,20 +419,20 @@ struct EpiLse {
         top[j] = i + 4 + j < 64 ? fmaxf(fmaxf(top[j], v[i + j]), v[i + 4 + j]) : fmaxf(top[j], v[i + j]);
     }
     const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    const float ms = mn == -INFINITY ? 0.f : mn * kLog2e;
-    const F2 k = f2_splat(kLog2e), off = f2_splat(-ms);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const F2 k = f2_splat(kLog2e), off = f2_splat(-base);
     F2 add[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) add[i] = f2_splat(0.f);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       float lo, hi;
-      f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), k, off), lo, hi);
+      f2_unpack(f2_mul(f2_add(f2_pack(v[2 * i], v[2 * i + 1]), off), k), lo, hi);
       add[i & 3] = f2_add(add[i & 3], f2_pack(ex2(lo), ex2(hi)));
     }
     float lo, hi;
     f2_unpack(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
-    s = __fmaf_rn(s, ex2(__fmaf_rn(m, kLog2e, -ms)), lo + hi);
+    s = __fmaf_rn(s, ex2((m - base) * kLog2e), lo + hi);
     m = mn;
   }
   __device__ __forceinline__ void end(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
@@ -454,13 +457,13 @@ struct EpiLse {
 // for the label's, and k_xent_label puts -sum / (sum + the label's) in its place.
 template <int PARTS>
 struct EpiGrad {
-  float scale, lse2, sum;
+  float scale, lse, sum;
   int64_t at;
   bool out;                  // the row is left out: zeros, whatever its products are
 
   __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem&, const EpiPos& e) {
     scale = 1.f;
-    lse2 = sum = 0.f;
+    lse = sum = 0.f;
     at = -1;
     out = true;
     if (e.live) {
@@ -468,7 +471,7 @@ struct EpiGrad {
       out = label == p.ignore_index;
       if (!out) {
         if (p.row_scale) scale = p.row_scale[e.row];
-        lse2 = p.lse[e.row] * kLog2e;
+        lse = p.lse[e.row];
         if (label < 0 || label >= p.vocab) scale = qnan();  // no class: NaN, not a guess
         else at = label - p.label_base - int64_t(e.n0);
       }
@@ -476,11 +479,11 @@ struct EpiGrad {
   }
   __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
                                         uint32_t c, float* v) {
-    const F2 k = f2_splat(kLog2e), off = f2_splat(-lse2);
+    const F2 k = f2_splat(kLog2e), off = f2_splat(-lse);
     float low = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), k, off), v[2 * i], v[2 * i + 1]);
+      f2_unpack(f2_mul(f2_add(f2_pack(v[2 * i], v[2 * i + 1]), off), k), v[2 * i], v[2 * i + 1]);
       low = fminf(fminf(low, v[2 * i]), v[2 * i + 1]);
     }
     // The short exponential flushes subnormal results; the gradient of a class

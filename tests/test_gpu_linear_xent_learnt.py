@@ -115,3 +115,20 @@ def test_one_row_gradient_norm():
             for a, b in zip(got, (G @ w.double(), G.t() @ x.double())):
                 # Terms of logits of both signs: |x| |w| is about 13 times 20 / 12 of them.
                 assert float((a.double() - b).norm() / b.norm()) <= proportion(384, torch.float32), (N, seed)
+
+
+def test_lse_near_its_maximum():
+    """A row's lse where one logit is nearly all of it: l's error, whatever it
+    is, is one logit's, so lse - l shows the sum's own error: exponentials of
+    2^-22, their sum and logarithm, 8u, and one rounding of lse, u |lse|."""
+    for dtype in (torch.float32, torch.bfloat16):
+        for level in (20.0, 75.0):
+            g = torch.Generator("cuda").manual_seed(int(level))
+            x = torch.zeros(4096, 64, device="cuda")
+            x[:, 0] = level * (1 + torch.rand(4096, generator=g, device="cuda") / 8)
+            w = torch.zeros(300, 64, device="cuda")
+            w[7, 0] = 1
+            x, w = x.to(dtype), w.to(dtype)
+            _, lse = zr.zr_linear_xent_fwd(x, w, torch.full((4096,), 7, device="cuda"), "none")
+            want = torch.logsumexp(x.double() @ w.double().t(), 1)
+            assert ((lse.double() - want).abs() <= 2.0 ** -22 + 8 * U + U * want).all(), (dtype, level)
