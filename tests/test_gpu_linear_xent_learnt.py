@@ -132,3 +132,18 @@ def test_lse_near_its_maximum():
             _, lse = zr.zr_linear_xent_fwd(x, w, torch.full((4096,), 7, device="cuda"), "none")
             want = torch.logsumexp(x.double() @ w.double().t(), 1)
             assert ((lse.double() - want).abs() <= 2.0 ** -22 + 8 * U + U * want).all(), (dtype, level)
+
+
+def test_bf16_label_over_pieces():
+    """A bfloat16 vocabulary in two pieces: the label's element is p - 1 from
+    lse, off by lse's rounding (u |lse|), two exponentials of 2^-22, their sums
+    and the logits' errors in proportion, besides the roundings to bfloat16."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 60e9:
+        pytest.skip("needs 60 GB")
+    x, w, y, G = learnt(256, 64, torch.bfloat16, V=2100001, others=-4.0)
+    _, lse = zr.zr_linear_xent_fwd(x, w, y, "none")
+    _, gw = zr.zr_linear_xent_bwd(torch.ones(256, device="cuda"), x, w, y, lse, "none")
+    err = (gw[1, 64:].double() - G[:, 1]).abs()
+    bound = proportion(320, torch.bfloat16) * G[:, 1].abs() + 20 * U + 2.0 ** -21 + 16 * U
+    assert (err <= bound).all(), float((err / bound).max())
