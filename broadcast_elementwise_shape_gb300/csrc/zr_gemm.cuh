@@ -30,15 +30,21 @@ constexpr uint32_t kGemmK = 64;        // k per block (128 bytes)
 constexpr uint32_t kABytes = kGemmM * kGemmK * 2;
 constexpr uint64_t kWaitNs = 2000000000ull, kStepNs = 1000000ull;
 
-// PARTS = 3: a stage holds all three parts of both operands, which its six
-// products share; half the traffic of loading a pair of parts for each.  Tiles
-// of a single CTA are then at most 128 columns wide.  (Four stages of half the
-// k instead of two: [2048, 1024] x [8192, 1024] f32 backward 434 us against 405.)
-template <int CG, int PARTS>
+// Parts of the operands A and B, and the products of parts that make up theirs.
+// PARTS = 3 (binary32 tensors): a stage holds all three parts of both operands,
+// which its six products share; half the traffic of loading a pair of parts for
+// each.  Tiles of a single CTA are then at most 128 columns wide.  (Four stages
+// of half the k instead of two: [2048, 1024] x [8192, 1024] f32 backward 434 us
+// against 405.)
+// PARTS = 2 (bfloat16 tensors, G in two parts): A of the gradients' products.
+template <int EPI, int CG, int PARTS>
 struct GemmCfg {
+  static constexpr uint32_t kA = PARTS == 2 && EPI != kEpiOut ? 1 : PARTS;
+  static constexpr uint32_t kB = PARTS == 3 ? 3 : 1;
+  static constexpr int kPairs = PARTS == 3 ? 6 : kA;
   static constexpr uint32_t kBBytes = (PARTS == 3 ? 128 : 256 / CG) * kGemmK * 2;
-  static constexpr uint32_t kStageBytes = PARTS * (kABytes + kBBytes);
-  static constexpr int kStages = PARTS == 3 ? 2 : (CG == 1 ? 4 : 6);
+  static constexpr uint32_t kStageBytes = kA * kABytes + kB * kBBytes;
+  static constexpr int kStages = 192 * 1024 / kStageBytes;
   // The ring, 4 KB of output staging per epilogue warp, alignment.
   static constexpr uint32_t kOutAt = kStages * kStageBytes;
   static constexpr uint32_t kSmem = kOutAt + 8 * 4096 + 1024;
@@ -288,9 +294,9 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmPlan& p, uint32_t t) {
 // The pairs of parts (a, b) of a block of k in the order they are added:
 // smallest products first, so that the sum is small until the last, largest
 // pair (parts 0, 0).
-template <int PARTS>
+template <int PAIRS>
 __device__ __forceinline__ constexpr uint32_t gemm_pair(int i, int operand) {
-  if (PARTS == 1) return 0;
+  if (PAIRS < 6) return operand == 0 ? PAIRS - 1 - i : 0;
   constexpr uint32_t pairs[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
   return pairs[i][operand];
 }
@@ -443,12 +449,17 @@ struct EpiLse {
 };
 
 // G = scale * (exp(l - lse) - [column is the label]).  G is the operand of
-// the two gradient products, so it is stored as their operand type: rounded
-// once to bfloat16 (2^-8 relative per element at most, the size of the
-// rounding of the bfloat16 results that average over it), or, for binary32
-// tensors, as three bfloat16 parts that hold it to 2^-24.  A factor that all
-// rows share is left to the products' epilogue: then the label's element of a
-// row that is not yet learnt, the largest by far, is -1 and rounds to itself.
+// the two gradient products, so it is stored as their operand type: for binary32
+// tensors as three bfloat16 parts that hold it to 2^-24, for bfloat16 ones
+// rounded once (2^-8 of an element at most) or, for few rows, in two parts.  One
+// part's rounding is as large as that of the bfloat16 results and independent of
+// it.  A result that averages over many elements shows little of it, but a class
+// that is one row's label has that row's G as its main factor however many rows
+// there are: over all of a gradient the error grew from 0.0017 of it, the
+// results' rounding, to 0.0019 or 0.0020.  A second part costs half of the step
+// again where the tensor cores bound it (kTwoPartRows).  A factor that all rows
+// share is left to the products' epilogue: then the label's element of a row that
+// is not yet learnt, the largest by far, is -1 and rounds to itself.
 //
 // The label's element, p - 1, is a small difference where the row is learnt:
 // lse's rounding alone (2^-25 of it) was 1.7e-5 of a whole binary32 gradient of
@@ -589,7 +600,7 @@ struct EpiOut {
       return;
     }
     if (q.tma_out) {
-      if constexpr (PARTS == 1) {
+      if constexpr (PARTS != 3) {
         epi_store(&q.c, e, c, 0, v);
       } else {
         epi_store_f32(&q.c, e, c, v);
@@ -630,7 +641,7 @@ struct EpiOf<kEpiOut, PARTS> { using type = EpiOut<PARTS>; };
 // some hundred thousand.
 template <int EPI, int CG, bool SUM, int PARTS>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant__ GemmPlan p) {
-  using Cfg = GemmCfg<CG, PARTS>;
+  using Cfg = GemmCfg<EPI, CG, PARTS>;
   constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint64_t s_full[S], s_empty[S], s_tfull[2], s_tempty[2];
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
       const uint32_t m0 = (g.mt * CG + rank) * kGemmM;
       const uint32_t n0 = g.n0 + rank * (g.tn / CG);
       // Whole boxes, whatever part of them is inside the operand.
-      const uint32_t bytes = (kABytes + q.tn / CG * kGemmK * 2) * PARTS * CG;
+      const uint32_t bytes = (Cfg::kA * kABytes + Cfg::kB * (q.tn / CG * kGemmK * 2)) * CG;
       const uint32_t end = g.kb0 + g.n_kb, a_mn = q.a_mn, b_mn = q.b_mn;
       for (uint32_t kb = g.kb0; kb < end; ++kb) {
         ok = warp_wait(smem_u32(&s_empty[stage]), phase ^ 1, abort);
@@ -684,7 +695,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
           const uint32_t local = smem_u32(&s_full[stage]);
           if (rank == 0) mbar_expect(local, bytes);
           const uint32_t bar = CG == 1 ? local : cluster_addr(local, 0);
-          const uint32_t sa = ring + stage * Cfg::kStageBytes, sb = sa + PARTS * kABytes;
+          const uint32_t sa = ring + stage * Cfg::kStageBytes, sb = sa + Cfg::kA * kABytes;
           tma_load<CG>(sa, &q.a, bar, a_mn ? kb * kGemmK : m0, a_mn ? m0 / 64 : kb);
           tma_load<CG>(sb, &q.b, bar, b_mn ? kb * kGemmK : n0, b_mn ? n0 / 64 : kb);
         }
@@ -714,7 +725,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
                              ((g.tn >> 3) << 17) | (uint32_t(kGemmM * CG / 16) << 24);
       const uint32_t ka = q.a_mn ? 2048 >> 4 : 32 >> 4, kb16 = q.b_mn ? 2048 >> 4 : 32 >> 4;
       const uint64_t da = operand_desc(ring, q.a_mn);
-      const uint64_t db = operand_desc(ring + PARTS * kABytes, q.b_mn);
+      const uint64_t db = operand_desc(ring + Cfg::kA * kABytes, q.b_mn);
       const uint32_t n_kb = g.n_kb, chunk = q.chunk;
       for (uint32_t k1 = 0; k1 < n_kb && ok; k1 += chunk, ++it) {
         const uint32_t buf = it & 1;
@@ -730,9 +741,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm(const __grid_constant_
           if (leader) {
             const uint64_t at = stage * (Cfg::kStageBytes >> 4);
 #pragma unroll
-            for (int i = 0; i < (PARTS == 3 ? 6 : 1); ++i) {
-              const uint64_t pa = da + at + gemm_pair<PARTS>(i, 0) * (kABytes >> 4);
-              const uint64_t pb = db + at + gemm_pair<PARTS>(i, 1) * (Cfg::kBBytes >> 4);
+            for (int i = 0; i < Cfg::kPairs; ++i) {
+              const uint64_t pa = da + at + gemm_pair<Cfg::kPairs>(i, 0) * (kABytes >> 4);
+              const uint64_t pb = db + at + gemm_pair<Cfg::kPairs>(i, 1) * (Cfg::kBBytes >> 4);
 #pragma unroll
               for (uint32_t j = 0; j < kGemmK / 16; ++j)
                 tc_mma<CG>(d, pa + j * ka, pb + j * kb16, idesc, (kb | i | j) != 0);

@@ -17,7 +17,8 @@ namespace zr {
 // operand and stage: two of 8 KB instead of one of 16 KB cost MN-major products
 // 12 % ([4096, 32000] x [32000, 1024]: 193 against 172 us).
 // Parts: one, or the three that a binary32 operand is split into (zr_xent.cu),
-// whose product is the sum of six.
+// whose product is the sum of six; G of bfloat16 tensors may have two, whose
+// product with one is the sum of both.
 struct GemmProblem {
   CUtensorMap a, b;
   uint32_t m, n, k;
@@ -52,7 +53,7 @@ enum GemmEpilogue : int {
 
 struct GemmPlan {
   GemmProblem pr[2];
-  uint32_t n_prob, parts;
+  uint32_t n_prob, parts;    // parts: of both operands; 2: of G alone
   uint32_t tiles0, tiles;    // tiles of problem 0, of both
   uint32_t m_fast;           // consecutive tiles walk m first
   // Two problems' tiles over `workers` clusters (GemmWalk).

@@ -8,15 +8,17 @@ namespace {
 template <int EPI, int CG, bool SUM, int PARTS>
 cudaError_t go(const GemmPlan& p, unsigned grid, cudaStream_t s) {
   auto* k = k_gemm<EPI, CG, SUM, PARTS>;
-  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), int(GemmCfg<CG, PARTS>::kSmem));
+  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), int(GemmCfg<EPI, CG, PARTS>::kSmem));
   if (e != cudaSuccess) return e;
-  if (CG == 1) return launch_k(k, grid, kGemmThreads, GemmCfg<CG, PARTS>::kSmem, s, p);
-  return launch_k_cluster(k, grid, kGemmThreads, GemmCfg<CG, PARTS>::kSmem, s, CG, p);
+  if (CG == 1) return launch_k(k, grid, kGemmThreads, GemmCfg<EPI, CG, PARTS>::kSmem, s, p);
+  return launch_k_cluster(k, grid, kGemmThreads, GemmCfg<EPI, CG, PARTS>::kSmem, s, CG, p);
 }
 
 template <int EPI, int CG>
 cudaError_t pick(bool sum, const GemmPlan& p, unsigned grid, cudaStream_t s) {
   if (p.parts == 3) return go<EPI, CG, true, 3>(p, grid, s);
+  if constexpr (EPI != kEpiLse && CG == 1)  // G in two parts is for up to 128 rows
+    if (p.parts == 2) return sum ? go<EPI, CG, true, 2>(p, grid, s) : go<EPI, CG, false, 2>(p, grid, s);
   return sum ? go<EPI, CG, true, 1>(p, grid, s) : go<EPI, CG, false, 1>(p, grid, s);
 }
 
@@ -27,7 +29,8 @@ cudaError_t launch_gemm(int epi, int cg, bool sum, const GemmPlan& p, unsigned g
   if (grid == 0 || (cg != 1 && cg != 2) || grid % unsigned(cg) != 0) return cudaErrorInvalidValue;
   for (uint32_t i = 0; i < p.n_prob; ++i)
     if (p.pr[i].chunk == 0 || (!sum && p.pr[i].chunk < p.pr[i].kb_slice)) return cudaErrorInvalidValue;
-  if ((p.parts != 1 && p.parts != 3) || (p.parts == 3 && !sum)) return cudaErrorInvalidValue;
+  if (p.parts < 1 || p.parts > 3 || (p.parts == 3 && !sum) || (p.parts == 2 && (epi == kEpiLse || cg != 1)))
+    return cudaErrorInvalidValue;
   const uint32_t widest = p.parts == 3 && cg == 1 ? 128 : 256;
   for (uint32_t i = 0; i < p.n_prob; ++i)
     if (p.pr[i].tn > widest) return cudaErrorInvalidValue;

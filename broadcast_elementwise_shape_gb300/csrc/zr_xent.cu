@@ -596,11 +596,22 @@ __global__ void __launch_bounds__(kRowsThreads) k_xent_label(const __grid_consta
   }
 }
 
+// Rows up to which the bfloat16 backward holds G in two parts (to 2^-16) rather
+// than in one (2^-8): one row block, whose calls wait for w and for launches
+// rather than for the tensor cores.  One part shows beside the rounding of the
+// result, most of all where few rows leave nothing to average: relative errors
+// of the gradients are 0.0026 of [1, 512] x [5000, 512], 0.0019 to 0.0021 of 16
+// rows and more; 0.0016 to 0.0017, the result's own rounding, with two.
+// Backward, us, one part and two:
+//   [50001, 768]:  1 row 68, 78; 128 rows 78, 98; 256 rows 86, 118; 1024 rows 165, 268
+//   [32000, 1024]: 16 rows 57, 68; 128 rows 64, 84; 512 rows 89, 133; 4096 rows 444, 763
+//   [5000, 512]:   1 row 24, 30; 128 rows 29, 35; 4096 rows 61, 97
+constexpr int64_t kTwoPartRows = 128;
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;  // G of one piece of the vocabulary, about
 
 struct XentSet {
   int es = 4;
-  uint32_t parts = 1;
+  uint32_t parts = 1, g_parts = 1;  // of the operands, of G
   bool empty = false;        // no rows
   bool few = false;          // forward by k_xent_few
   Operand x, w;
@@ -788,13 +799,14 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     S->ws_row = take(&at, (N + 7) / 8 * 8);  // (float, count) per block of eight rows
     S->ws_ticket = take(&at, 4);
   } else {
+    S->g_parts = S->es == 4 ? 3 : (S->x.rows <= kTwoPartRows ? 2 : 1);
     S->ws_common = take(&at, 4);
-    const int64_t most = std::max<int64_t>(2048, int64_t(kPieceBytes / (2 * S->parts * N)));
+    const int64_t most = std::max<int64_t>(2048, int64_t(kPieceBytes / (2 * S->g_parts * N)));
     S->n_piece = (vocab + most - 1) / most;
     S->piece = ((vocab + S->n_piece - 1) / S->n_piece + 255) / 256 * 256;
     S->n_piece = (vocab + S->piece - 1) / S->piece;
     const int64_t wide = std::min<int64_t>(S->piece, (vocab + 63) / 64 * 64);
-    S->ws_g = take(&at, N * size_t(wide) * 2 * S->parts);
+    S->ws_g = take(&at, N * size_t(wide) * 2 * S->g_parts);
     // Over several pieces the sums are known when the label's piece is long
     // gone.  binary32 then sums once before (a fourth more products).  bfloat16
     // does without: lse's rounding, some 1e-6 of p, is beside the 2^-9 that G
@@ -1084,7 +1096,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
   label.row_scale = r.reduction == ZR_NONE ? grad_loss : nullptr;
   label.g = G;
   label.slots = S.label_slots;
-  label.parts = S.parts;
+  label.parts = S.g_parts;
   auto launch_label = [&](float* label_g, int64_t ldg) {
     label.label_g = label_g;
     label.ldg = ldg;
@@ -1100,7 +1112,9 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     g->vocab = V;
     g->row_scale = label.row_scale;
     g->label_base = v0;
-    return logits_problem(S, ws, v0, n, cg, g);
+    const cudaError_t rc = logits_problem(S, ws, v0, n, cg, g);
+    g->parts = S.g_parts;
+    return rc;
   };
   float* label_g = nullptr;
   if (S.label_pass == 2) {
@@ -1125,14 +1139,14 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     g.label_g = label_g;
     if ((e = grad_logits(v0, n, cg, &g)) != cudaSuccess) return cuda_status(e);
     g.pr[0].tma_out = 1;
-    if ((e = output_map(&g.pr[0].c, G, 2, ldg, N, ldg, S.parts, N * ldg)) != cudaSuccess)
+    if ((e = output_map(&g.pr[0].c, G, 2, ldg, N, ldg, S.g_parts, N * ldg)) != cudaSuccess)
       return cuda_status(e);
     if ((e = launch_product(S, kEpiGrad, cg, &g, s)) != cudaSuccess) return cuda_status(e);
     if (S.label_pass == 1 && (e = launch_label(nullptr, ldg)) != cudaSuccess) return cuda_status(e);
 
     cg = pick_cg(std::min(N, n));
     GemmPlan o = {};
-    o.parts = S.parts;
+    o.parts = S.g_parts;
     o.out_scale = r.common;
     // grad_x += G W: rows of x, k = this piece's vocabulary.
     if (grad_x) {
@@ -1156,7 +1170,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       if (S.slices[0] > 1 && k + 1 == S.n_piece) join_part(&join.p[0], q, S.slices[0], vec);
       if (q.tma_out && (e = output_map(&q.c, grad_x, S.es, D, N, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
-      if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 128, 1)) != cudaSuccess)
+      if ((e = operand_map(&q.a, G, n, N, ldg, S.g_parts, N * ldg, 128, 1)) != cudaSuccess)
         return cuda_status(e);
       if ((e = operand_map(&q.b, operand_base(S.w, ws) + v0 * S.w.pitch * 2, D, n, S.w.pitch, S.parts,
                            S.w.rows * S.w.pitch, 64, q.tn / cg / 64)) != cudaSuccess)
@@ -1183,7 +1197,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       if (q.acc_out) join_part(&join.p[1], q, q.slices, vec);
       if (q.tma_out && (e = output_map(&q.c, q.out, S.es, D, n, D, 1, 0)) != cudaSuccess)
         return cuda_status(e);
-      if ((e = operand_map(&q.a, G, n, N, ldg, S.parts, N * ldg, 64, 2)) != cudaSuccess)
+      if ((e = operand_map(&q.a, G, n, N, ldg, S.g_parts, N * ldg, 64, 2)) != cudaSuccess)
         return cuda_status(e);
       if ((e = operand_map(&q.b, operand_base(S.x, ws), D, N, S.x.pitch, S.parts,
                            S.x.rows * S.x.pitch, 64, q.tn / cg / 64)) != cudaSuccess)
@@ -1205,7 +1219,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
 std::string xent_json(const XentSet& S) {
   return std::string("{\"kernel\":\"") + (S.few ? "xent_few" : "xent") + "\",\"rows\":" + std::to_string(S.x.rows) + ",\"dim\":" +
          std::to_string(S.x.cols) + ",\"vocab\":" + std::to_string(S.w.rows) + ",\"parts\":" +
-         std::to_string(S.parts) + ",\"pack_x\":" + std::to_string(S.x.pack) + ",\"pack_w\":" +
+         std::to_string(S.parts) + ",\"g_parts\":" + std::to_string(S.g_parts) + ",\"pack_x\":" + std::to_string(S.x.pack) + ",\"pack_w\":" +
          std::to_string(S.w.pack) + ",\"piece\":" + std::to_string(S.piece) + ",\"n_piece\":" +
          std::to_string(S.n_piece) + ",\"slices_x\":" + std::to_string(S.slices[0]) +
          ",\"slices_w\":" + std::to_string(S.slices[1]) + ",\"label_pass\":" + std::to_string(S.label_pass) + ",\"ws\":" + std::to_string(S.ws) + "}";

@@ -492,7 +492,7 @@ int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, voi
  *
  * Numerics.  Products accumulate in binary32 on the tensor cores; statistics
  * and losses are binary32.  ZR_BF16: operands as stored, G rounded once to
- * bfloat16 as an operand, gradients rounded once.  ZR_F32: each operand is
+ * bfloat16 as an operand (up to 128 rows: held to 2^-16), gradients rounded once.  ZR_F32: each operand is
  * split into three bfloat16 parts, whose products reach binary32 accuracy.
  * A row with an infinite logit has a NaN loss.  Results are reproducible run
  * to run (no atomics).
