@@ -572,8 +572,12 @@ template <int PARTS>
 struct EpiOut {
   float scale;
 
-  __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem& q, const EpiPos&) {
+  bool out;                  // the row is left out: an infinite factor makes no NaN of its zeros
+
+  __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
     scale = p.out_scale && !q.acc_out ? *p.out_scale : 1.f;
+    out = q.by_row && e.live &&
+          xent_label(p.labels, p.label_stride, p.label_i64, e.row) == p.ignore_index;
   }
   __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
                                         uint32_t c, float* v) {
@@ -589,7 +593,7 @@ struct EpiOut {
       }
     }
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = e.ok ? v[i] * scale : qnan();
+    for (int i = 0; i < 64; ++i) v[i] = e.ok ? (out ? 0.f : v[i] * scale) : qnan();
     if (q.acc_out) {
       if (e.live) {
 #pragma unroll

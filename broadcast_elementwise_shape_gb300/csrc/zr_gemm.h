@@ -42,6 +42,9 @@ struct GemmProblem {
   float* acc;
   int64_t ldo, lda;
   uint32_t acc_in, acc_out;
+  // Epilogue kEpiOut: rows are those of the labels; left-out ones become 0
+  // whatever the product and the factor are.
+  uint32_t by_row;
 };
 
 enum GemmEpilogue : int {
@@ -59,7 +62,7 @@ struct GemmPlan {
   // Two problems' tiles over `workers` clusters (GemmWalk).
   uint32_t workers, head, extra, late_first;
   const float* out_scale;    // kEpiOut: multiplies the finished product, or null (1)
-  // kEpiLse, kEpiGrad
+  // kEpiLse, kEpiGrad; kEpiOut by_row
   const void* labels;        // label of row r: labels[r * label_stride]
   int64_t label_stride;
   uint32_t label_i64;

@@ -513,8 +513,9 @@ struct JoinPart {
   uint32_t blocks;
 };
 struct JoinPlan {
-  JoinPart p[2];
+  JoinPart p[2];             // of grad_x, grad_w
   const float* scale;        // or null (1)
+  XentRows rows;             // left-out rows of part 0 become 0 whatever the factor is
 };
 
 __device__ __forceinline__ uint32_t join_bf16(float lo, float hi) {
@@ -533,13 +534,15 @@ __global__ void __launch_bounds__(kThreads) k_xent_join(const __grid_constant__ 
   const float* a = q.acc + uint64_t(i) * 4;
   pdl_wait();
   const float scale = p.scale ? *p.scale : 1.f;
+  const bool left_out = !second && row_label(p.rows, row) == p.rows.ignore_index;
   float4 v = *reinterpret_cast<const float4*>(a);
 #pragma unroll 4
   for (uint32_t k = 1; k < q.slices; ++k) {
     const float4 o = *reinterpret_cast<const float4*>(a + k * q.plane);
     v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
   }
-  const float r[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+  float r[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+  if (left_out) r[0] = r[1] = r[2] = r[3] = 0.f;
   E* out = static_cast<E*>(q.out) + uint64_t(row) * q.cols + c;
   if (q.vec) {
     if constexpr (sizeof(E) == 4) {
@@ -1080,6 +1083,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
                    reinterpret_cast<float*>(ws + S.ws_acc[1])};
   JoinPlan join = {};
   join.scale = r.common;
+  join.rows = r;
   auto join_part = [&](JoinPart* j, const GemmProblem& q, uint32_t slices, bool vec) {
     j->acc = q.acc;
     j->plane = q.plane;
@@ -1152,6 +1156,10 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     GemmPlan o = {};
     o.parts = S.g_parts;
     o.out_scale = r.common;
+    o.labels = r.labels;
+    o.label_stride = r.label_stride;
+    o.label_i64 = r.label_i64;
+    o.ignore_index = r.ignore_index;
     // grad_x += G W: rows of x, k = this piece's vocabulary.
     if (grad_x) {
       GemmProblem& q = o.pr[o.n_prob++];
@@ -1164,6 +1172,7 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
       set_tiles(&q, cg, S.slices[0]);
       q.out = grad_x;
       q.ldo = D;
+      q.by_row = 1;
       q.acc = acc[0];
       q.lda = lda;
       q.plane = N * lda;
