@@ -471,7 +471,7 @@ int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, voi
  *   labels      x's leading shape, int32 or int64 (label_type), with strides
  *               that walk it row-major at one step (else ZR_ERR_LAYOUT).
  *   ignore_index  rows with this label are left out: their loss is 0, their
- *               gradients are 0 whatever x holds there (infinities and NaN
+ *               gradients are 0 whatever x, w and grad_loss hold (infinities and NaN
  *               included), and a mean does not count them.  Any other label
  *               outside [0, V) makes the row's loss and gradients NaN.
  *   reduction   ZR_NONE: loss holds N floats; ZR_SUM, ZR_MEAN: one.  The mean
