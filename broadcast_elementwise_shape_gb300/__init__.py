@@ -376,6 +376,18 @@ def zr_unary_bwd(op, grad_out, x, alpha=1.0, grad_x=None):
     return grad_x
 
 
+# The training operators' binding imports torch; the package itself does not.
+_TRAIN = ("zr_layer_norm_fwd", "zr_layer_norm_bwd", "zr_dropout_fwd", "zr_dropout_bwd",
+          "zr_linear_xent_fwd", "zr_linear_xent_bwd")
 
-from .train import (zr_dropout_bwd, zr_dropout_fwd, zr_layer_norm_bwd,  # noqa: E402,F401
-                    zr_layer_norm_fwd, zr_linear_xent_bwd, zr_linear_xent_fwd)
+
+def __getattr__(name):
+    if name not in _TRAIN:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import train
+    globals().update((n, getattr(train, n)) for n in _TRAIN)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_TRAIN})

@@ -1,6 +1,7 @@
 """Build the zr CUDA library in-tree: ``_build/libzr.so`` (sm_103a only), and the
 training operators' torch binding beside it (``csrc/zr_torch.cpp``, one CPython
-module linked against the library and the installed torch).
+module linked against the library and the installed torch; the library neither
+needs it nor torch).
 
 Each translation unit compiles in parallel with nvcc; the objects link into
 one shared library with the CUDA runtime linked statically, so the library
@@ -10,7 +11,9 @@ subnormals preserved (``-ftz=false``).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -44,45 +47,76 @@ def _inputs():
     return files + [os.path.abspath(__file__)]
 
 
+def _torch_root():
+    """The installed torch package's folder, without importing it; None if there is none."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
 def _torch_version() -> str:
     from importlib.metadata import version
     return version("torch")
 
 
-def stale() -> bool:
-    if not all(os.path.exists(f) for f in (LIB, TORCH_LIB, TORCH_STAMP)):
+def _older(target: str) -> bool:
+    """Whether `target` is missing or older than any source."""
+    if not os.path.exists(target):
         return True
-    with open(TORCH_STAMP) as f:
-        if f.read() != _torch_version():
-            return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
-def _build_binding(obj: str) -> None:
-    """Link the binding's object against libzr.so and torch."""
-    root = _torch_root()
-    tmp = f"{TORCH_LIB}.{os.getpid()}.tmp"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(root, "lib"), "-ltorch_python",
-           "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libzr.so",
-           "-Wl,-rpath,$ORIGIN"]
+def _binding_stale() -> bool:
+    """The binding needs torch; without it there is none to build."""
+    if _torch_root() is None:
+        return False
+    if not os.path.exists(TORCH_STAMP) or _older(TORCH_LIB):
+        return True
+    with open(TORCH_STAMP) as f:
+        return f.read() != _torch_version()
+
+
+def stale() -> bool:
+    return _older(LIB) or _binding_stale()
+
+
+def _run(cmd, what: str) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link of the torch binding failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
+def _compile_binding(nvcc: str) -> str:
+    """The binding's object file."""
+    found = shutil.which(nvcc)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(found or nvcc)))
+    inc = os.path.join(_torch_root(), "include")
+    obj = os.path.join(BUILD, "zr_torch.o")
+    _run(["g++", "-std=c++17", "-O2", "-fPIC", "-I", inc, "-I",
+          os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+          "-I", os.path.join(cuda, "include"), "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj],
+         f"compilation of {TORCH_SOURCE}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    """Link the binding's object against libzr.so and torch."""
+    tmp = f"{TORCH_LIB}.{os.getpid()}.tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_root(), "lib"), "-ltorch_python",
+          "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libzr.so",
+          "-Wl,-rpath,$ORIGIN"], "link of the torch binding")
     os.replace(tmp, TORCH_LIB)
     with open(TORCH_STAMP, "w") as f:
         f.write(_torch_version())
 
 
-def _torch_root() -> str:
-    """The installed torch package's folder, without importing it."""
-    import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
-
-
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link ``libzr.so`` if missing or older than its sources."""
-    if not force and not stale():
+    """Compile and link ``libzr.so`` if missing or older than its sources, and
+    where torch is installed the binding.  The library does not wait for the
+    binding: it is in place when the binding's errors are raised."""
+    lib, binding = force or _older(LIB), _torch_root() is not None and (force or _binding_stale())
+    if not lib and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -90,30 +124,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        cmd = [nvcc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        if src == TORCH_SOURCE:
-            inc = os.path.join(_torch_root(), "include")
-            cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
-            cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-I", inc, "-I",
-                   os.path.join(inc, "torch", "csrc", "api", "include"), "-I",
-                   sysconfig.get_paths()["include"], "-I", cuda, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"compiler failed on {src}:\n{r.stdout}\n{r.stderr}")
+        said = _run([nvcc, *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj],
+                    f"compilation of {src}")
         if verbose or ptxas_info:
-            sys.stderr.write(r.stdout + r.stderr)
+            sys.stderr.write(said)
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        objs = list(ex.map(compile_one, [*SOURCES, TORCH_SOURCE]))
-    binding = objs.pop()
-    tmp = f"{LIB}.{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _build_binding(binding)
+        torch_obj = ex.submit(_compile_binding, nvcc) if binding else None
+        objs = [ex.submit(compile_one, s) for s in SOURCES] if lib else []
+    if lib:
+        tmp = f"{LIB}.{os.getpid()}.tmp"
+        _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *(o.result() for o in objs)], "link")
+        os.replace(tmp, LIB)
+    if binding:
+        _link_binding(torch_obj.result())
     return LIB
 
 
