@@ -317,12 +317,6 @@ __device__ __forceinline__ float ex2_full(float x) {
 }
 __device__ __forceinline__ float qnan() { return __uint_as_float(0x7FFFFFFFu); }
 
-__device__ __forceinline__ int64_t xent_label(const void* labels, int64_t stride, uint32_t i64,
-                                              uint32_t row) {
-  return i64 ? static_cast<const int64_t*>(labels)[int64_t(row) * stride]
-             : int64_t(static_cast<const int32_t*>(labels)[int64_t(row) * stride]);
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -398,8 +392,7 @@ struct EpiLse {
   float m, s;
 
   __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem&, const EpiPos& e) {
-    const int64_t label =
-        e.live ? xent_label(p.labels, p.label_stride, p.label_i64, e.row) : int64_t(-1);
+    const int64_t label = e.live ? row_label(p.labels, e.row) : int64_t(-1);
     at = e.live ? label - int64_t(e.n0) : int64_t(-1);
     m = -INFINITY;
     s = 0.f;
@@ -478,7 +471,7 @@ struct EpiGrad {
     at = -1;
     out = true;
     if (e.live) {
-      const int64_t label = xent_label(p.labels, p.label_stride, p.label_i64, e.row);
+      const int64_t label = row_label(p.labels, e.row);
       out = label == p.ignore_index;
       if (!out) {
         if (p.row_scale) scale = p.row_scale[e.row];
@@ -570,14 +563,13 @@ struct EpiGrad {
 // Results in the operands' type: binary32 where they come in three parts.
 template <int PARTS>
 struct EpiOut {
+  // -0: the row is left out, and an infinite factor makes no NaN of its zeros
+  // (a sentinel and not a flag beside it: the tile's values take the registers).
   float scale;
-
-  bool out;                  // the row is left out: an infinite factor makes no NaN of its zeros
 
   __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem& q, const EpiPos& e) {
     scale = p.out_scale && !q.acc_out ? *p.out_scale : 1.f;
-    out = q.by_row && e.live &&
-          xent_label(p.labels, p.label_stride, p.label_i64, e.row) == p.ignore_index;
+    if (q.by_row && e.live && row_label(p.labels, e.row) == p.ignore_index) scale = -0.f;
   }
   __device__ __forceinline__ void chunk(const GemmPlan& p, const GemmProblem& q, const EpiPos& e,
                                         uint32_t c, float* v) {
@@ -592,8 +584,9 @@ struct EpiOut {
         }
       }
     }
+    const bool left_out = __float_as_uint(scale) == 0x80000000u;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = e.ok ? (out ? 0.f : v[i] * scale) : qnan();
+    for (int i = 0; i < 64; ++i) v[i] = e.ok ? (left_out ? 0.f : v[i] * scale) : qnan();
     if (q.acc_out) {
       if (e.live) {
 #pragma unroll

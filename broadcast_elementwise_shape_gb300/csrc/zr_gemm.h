@@ -6,7 +6,33 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "zr_internal.h"
+
 namespace zr {
+
+// The labels of the rows, int32 or int64: a row's index is split over the
+// labels' dims (merged where they allow it, innermost first; mostly one).
+struct RowLabels {
+  const void* p;
+  uint32_t i64, n;
+  FastDiv div[kMaxDims];
+  int64_t stride[kMaxDims];
+};
+#if defined(__CUDACC__)
+__device__ __forceinline__ int64_t row_label(const RowLabels& l, uint32_t row) {
+  int64_t off = 0;
+  uint32_t i = 0;
+#pragma unroll 1
+  for (; i + 1 < l.n; ++i) {
+    const uint32_t q = fd_div(l.div[i], row);
+    off += int64_t(row - q * l.div[i].d) * l.stride[i];
+    row = q;
+  }
+  off += int64_t(row) * l.stride[i];
+  return l.i64 ? static_cast<const int64_t*>(l.p)[off]
+               : int64_t(static_cast<const int32_t*>(l.p)[off]);
+}
+#endif
 
 // One product out[m, n] = sum_k A[m, k] B[n, k] of bfloat16 operands, binary32
 // accumulation.  K-major operands have k as their contiguous dim, MN-major ones
@@ -63,9 +89,7 @@ struct GemmPlan {
   uint32_t workers, head, extra, late_first;
   const float* out_scale;    // kEpiOut: multiplies the finished product, or null (1)
   // kEpiLse, kEpiGrad; kEpiOut by_row
-  const void* labels;        // label of row r: labels[r * label_stride]
-  int64_t label_stride;
-  uint32_t label_i64;
+  RowLabels labels;
   // kEpiLse
   uint32_t* ticket;          // set to 0
   float2* partial;           // [m][2 * n_tiles] (maximum, sum)

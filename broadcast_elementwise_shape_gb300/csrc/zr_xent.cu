@@ -42,9 +42,7 @@ struct PackPlan {
 };
 
 struct XentRows {
-  const void* labels;
-  int64_t label_stride;
-  uint32_t label_i64;
+  RowLabels labels;
   int64_t ignore_index, vocab;
   uint32_t n;
   int reduction;
@@ -71,11 +69,6 @@ struct PrepPlan {
 
 namespace {
 
-__device__ __forceinline__ int64_t row_label(const XentRows& p, uint32_t r) {
-  return p.label_i64 ? static_cast<const int64_t*>(p.labels)[int64_t(r) * p.label_stride]
-                     : int64_t(static_cast<const int32_t*>(p.labels)[int64_t(r) * p.label_stride]);
-}
-
 template <typename E, int PARTS>
 __device__ __forceinline__ void xent_pack(const PackPlan& p, const XentRows* zero, uint64_t i) {
   if (i >= p.items) return;
@@ -83,7 +76,7 @@ __device__ __forceinline__ void xent_pack(const PackPlan& p, const XentRows* zer
   const uint32_t row = uint32_t(i / nvec);
   const uint32_t c = uint32_t(i - uint64_t(row) * nvec) * 8;
   float v[8];
-  if (zero && row_label(*zero, row) == zero->ignore_index) {
+  if (zero && row_label(zero->labels, row) == zero->ignore_index) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
   } else {
@@ -157,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) k_xent_prep(const __grid_constant__ 
   uint32_t cnt = 0;
   if (r.reduction == ZR_MEAN) {
 #pragma unroll 8
-    for (uint32_t i = threadIdx.x; i < r.n; i += kThreads) cnt += row_label(r, i) != r.ignore_index;
+    for (uint32_t i = threadIdx.x; i < r.n; i += kThreads) cnt += row_label(r.labels, i) != r.ignore_index;
     cnt = block_count<kThreads>(cnt, s_cnt);
   }
   if (threadIdx.x == 0)
@@ -181,7 +174,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // One warp joins a row's partial maxima and sums in a fixed order.  Returns the
 // row's loss (0 when it is left out), *used: whether it takes part.
 __device__ __forceinline__ float xent_row(const XentRows& p, uint32_t r, uint32_t lane, bool* used) {
-  const int64_t y = row_label(p, r);
+  const int64_t y = row_label(p.labels, r);
   const bool known = y >= 0 && y < p.vocab;
   *used = y != p.ignore_index;
   const float at = known ? p.at[r] : __uint_as_float(0x7FFFFFFFu);  // no class: NaN
@@ -316,9 +309,7 @@ struct FewPlan {
   int64_t xp, wp;
   uint32_t n, vocab, dim;
   uint32_t groups, slots;    // of NT rows; blocks of each
-  const void* labels;
-  int64_t label_stride;
-  uint32_t label_i64;
+  RowLabels labels;
   float2* partial;           // [n][slots]
   float* at;
 };
@@ -381,10 +372,7 @@ k_xent_few(const __grid_constant__ FewPlan p) {
   }
   const uint32_t mine = lane / kLanes, my_r = mine / NT, my_t = t0 + mine % NT;
   int64_t label = -1;
-  if (my_t < p.n)
-    label = p.label_i64
-                ? static_cast<const int64_t*>(p.labels)[int64_t(my_t) * p.label_stride]
-                : int64_t(static_cast<const int32_t*>(p.labels)[int64_t(my_t) * p.label_stride]);
+  if (my_t < p.n) label = row_label(p.labels, my_t);
   float m = -INFINITY, s = 0.f;
   __syncthreads();
   F2 acc[N];
@@ -534,7 +522,7 @@ __global__ void __launch_bounds__(kThreads) k_xent_join(const __grid_constant__ 
   const float* a = q.acc + uint64_t(i) * 4;
   pdl_wait();
   const float scale = p.scale ? *p.scale : 1.f;
-  const bool left_out = !second && row_label(p.rows, row) == p.rows.ignore_index;
+  const bool left_out = !second && row_label(p.rows.labels, row) == p.rows.ignore_index;
   float4 v = *reinterpret_cast<const float4*>(a);
 #pragma unroll 4
   for (uint32_t k = 1; k < q.slices; ++k) {
@@ -576,7 +564,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_xent_label(const __grid_consta
   const uint32_t lane = threadIdx.x & 31, r = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
   pdl_wait();
   if (r >= p.rows.n) return;
-  const int64_t y = row_label(p.rows, r);
+  const int64_t y = row_label(p.rows.labels, r);
   // Left out: zeros.  No class: the row is NaN.
   if (y == p.rows.ignore_index || y < 0 || y >= p.rows.vocab) return;
   const float* q = p.sums + uint64_t(r) * p.slots;
@@ -780,11 +768,17 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
     for (int d = 0; d < n - 1; ++d) st[0][d] = S->labels.stride[d];
     Prob P;
     if ((rc = coalesce(n - 1, S->labels.size, st, 1u, -1, &P))) return rc;
-    if (P.n != 1) return ZR_ERR_LAYOUT;
-    r.label_stride = P.st[0][0];
+    // Pitched (a slice of a longer row of labels) and expanded dims, in order.
+    for (int d = 0; d + 1 < P.n; ++d)
+      if (P.st[0][d] != 0 && P.st[0][d] < P.st[0][d + 1] * P.size[d + 1]) return ZR_ERR_LAYOUT;
+    r.labels.n = uint32_t(P.n);
+    for (int i = 0; i < P.n; ++i) {
+      r.labels.div[i] = make_fastdiv(uint32_t(P.size[P.n - 1 - i]));
+      r.labels.stride[i] = P.st[0][P.n - 1 - i];
+    }
   }
-  r.labels = S->labels.ptr;
-  r.label_i64 = it == ZR_I64;
+  r.labels.p = S->labels.ptr;
+  r.labels.i64 = it == ZR_I64;
   r.ignore_index = ignore;
   r.vocab = vocab;
   r.n = uint32_t(S->x.rows);
@@ -1033,8 +1027,6 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
     p.vocab = uint32_t(S.w.rows);
     p.dim = uint32_t(S.x.cols);
     p.labels = r.labels;
-    p.label_stride = r.label_stride;
-    p.label_i64 = r.label_i64;
     p.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
     p.at = reinterpret_cast<float*>(ws + S.ws_at);
     e = S.es == 4 ? launch_few<float>(p, s) : launch_few<__nv_bfloat16>(p, s);
@@ -1058,8 +1050,6 @@ int run_fwd(const XentSet& S, float* loss, float* lse, char* ws, cudaStream_t s)
   r.row_loss = r.reduction == ZR_NONE ? loss : reinterpret_cast<float*>(ws + S.ws_row);
   r.loss = loss;
   g.labels = r.labels;
-  g.label_stride = r.label_stride;
-  g.label_i64 = r.label_i64;
   g.partial = reinterpret_cast<float2*>(ws + S.ws_partial);
   g.at = reinterpret_cast<float*>(ws + S.ws_at);
   r.ticket = g.ticket = reinterpret_cast<uint32_t*>(ws + S.ws_ticket);
@@ -1114,8 +1104,6 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
   auto grad_logits = [&](int64_t v0, int64_t n, int cg, GemmPlan* g) {
     g->lse = lse;
     g->labels = r.labels;
-    g->label_stride = r.label_stride;
-    g->label_i64 = r.label_i64;
     g->ignore_index = r.ignore_index;
     g->vocab = V;
     g->row_scale = label.row_scale;
@@ -1157,8 +1145,6 @@ int run_bwd(const XentSet& S, const float* grad_loss, const float* lse, void* gr
     o.parts = S.g_parts;
     o.out_scale = r.common;
     o.labels = r.labels;
-    o.label_stride = r.label_stride;
-    o.label_i64 = r.label_i64;
     o.ignore_index = r.ignore_index;
     // grad_x += G W: rows of x, k = this piece's vocabulary.
     if (grad_x) {
@@ -1255,7 +1241,7 @@ int64_t loss_count(const XentSet& S, int red) {
 int check_spans(const XentSet& S, std::initializer_list<Span> outs, std::initializer_list<Span> ins,
                 const Span& ws) {
   const Span fixed[3] = {span_of(S.x.t.ptr, S.x.t.extent, S.es), span_of(S.w.t.ptr, S.w.t.extent, S.es),
-                         span_of(S.labels.ptr, S.labels.extent, S.rows.label_i64 ? 8 : 4)};
+                         span_of(S.labels.ptr, S.labels.extent, S.rows.labels.i64 ? 8 : 4)};
   for (const Span& f : fixed)
     if (overlaps(f, ws)) return ZR_ERR_LAYOUT;
   for (const Span& i : ins)

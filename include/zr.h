@@ -468,8 +468,9 @@ int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, voi
  *               product (rank 1: N = 1).
  *   w           [V, D], any strides, x's element type (a weight-tied head is
  *               the embedding itself).
- *   labels      x's leading shape, int32 or int64 (label_type), with strides
- *               that walk it row-major at one step (else ZR_ERR_LAYOUT).
+ *   labels      x's leading shape, int32 or int64 (label_type); dims may be
+ *               pitched (ids[:, 1:], the next-token labels of ids) or expanded,
+ *               but not permuted (ZR_ERR_LAYOUT).
  *   ignore_index  rows with this label are left out: their loss is 0, their
  *               gradients are 0 whatever x, w and grad_loss hold (infinities and NaN
  *               included), and a mean does not count them.  Any other label
