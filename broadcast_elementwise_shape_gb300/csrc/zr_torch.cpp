@@ -57,12 +57,15 @@ void dense(const Tensor& t, at::IntArrayRef shape, const char* what) {
   if (!t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", what);
 }
 // A float32 CUDA tensor, dense over `shape`.
-const float* stats(PyObject* o, at::IntArrayRef shape, const char* what) {
-  const Tensor& t = tensor(o, what);
+const float* stats(const Tensor& t, at::IntArrayRef shape, const char* what) {
   if (t.scalar_type() != at::kFloat) fail(PyExc_TypeError, "%s must be float32", what);
   if (!t.is_cuda()) fail(PyExc_ValueError, "%s must be a CUDA tensor", what);
   dense(t, shape, what);
   return static_cast<const float*>(t.data_ptr());
+}
+
+const float* stats(PyObject* o, at::IntArrayRef shape, const char* what) {
+  return stats(tensor(o, what), shape, what);
 }
 
 zr_tensor desc(const Tensor& t) {
@@ -277,7 +280,7 @@ PyObject* linear_xent_fwd(PyObject* const* a, Py_ssize_t n) {
 // workspace -> (grad_x, grad_w)
 PyObject* linear_xent_bwd(PyObject* const* a, Py_ssize_t n) {
   count(n, 12);
-  const Tensor &gl = tensor(a[0], "grad_loss"), &x = tensor(a[1], "x"), &w = tensor(a[2], "w");
+  const Tensor &given = tensor(a[0], "grad_loss"), &x = tensor(a[1], "x"), &w = tensor(a[2], "w");
   const Tensor& labels = tensor(a[3], "labels");
   const auto red = static_cast<zr_reduction>(integer(a[5]));
   const int64_t ignore = integer(a[6]);
@@ -286,7 +289,9 @@ PyObject* linear_xent_bwd(PyObject* const* a, Py_ssize_t n) {
   const auto lead = x.dim() ? x.sizes().slice(0, x.dim() - 1) : x.sizes();
   const zr_index it = label_type(labels, lead);
   const float* lse = stats(a[4], lead, "lse");
-  const float* grad_loss = stats(a[0], gl.sizes(), "grad_loss");
+  // A view, as loss.sum() hands down an expanded one, is copied: one float per row.
+  const Tensor gl = given.contiguous();
+  const float* grad_loss = stats(gl, gl.sizes(), "grad_loss");
   if (gl.numel() != (red == ZR_NONE ? labels.numel() : 1))
     fail(PyExc_ValueError, "%s has the wrong number of elements", "grad_loss");
   if (ox) dense(*ox, x.sizes(), "grad_x");

@@ -98,7 +98,8 @@ def zr_linear_xent_fwd(x, w, labels, reduction="mean", ignore_index=-100, worksp
 def zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction="mean", ignore_index=-100,
                        want=(True, True), grads=(None, None), workspace=None):
     """(grad_x, grad_w) of zr_linear_xent_fwd's loss given grad_loss (float32,
-    one element, or one per row with reduction "none") and the forward's lse.
+    one element, or one per row with reduction "none", views too) and the
+    forward's lse.
     ``grads`` may hold preallocated contiguous outputs."""
     wx, ww = want
     return _out(_c().linear_xent_bwd(grad_loss, x, w, labels, lse, _reduction(reduction), ignore_index,

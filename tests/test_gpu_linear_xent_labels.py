@@ -1,5 +1,5 @@
-"""GPU tests of the linear head's cross entropy: labels that are views
-give what their copies give, bit for bit."""
+"""GPU tests of the linear head's cross entropy: labels and upstream gradients
+that are views give what their copies give, bit for bit."""
 import pytest
 import torch
 
@@ -45,3 +45,16 @@ def test_labels_are_views(dtype, itype):
                     loss, lse = zr.zr_linear_xent_fwd(x, w, labels, reduction)
                     both.append((loss, lse, *zr.zr_linear_xent_bwd(grad, x, w, labels, lse, reduction)))
                 assert all(torch.equal(a, b) for a, b in zip(*both)), (what, D, reduction)
+
+
+@pytest.mark.parametrize("N", [3, 200])
+def test_upstream_gradient_is_a_view(N):
+    """loss.sum()'s gradient is an expanded one; others have a step."""
+    g = torch.Generator("cuda").manual_seed(4)
+    x, w = torch.randn(N, 64, generator=g, device="cuda"), torch.randn(300, 64, generator=g, device="cuda")
+    y = torch.randint(0, 300, (N,), generator=g, device="cuda")
+    _, lse = zr.zr_linear_xent_fwd(x, w, y, "none")
+    for grad in (torch.tensor(0.5, device="cuda").expand(N), torch.rand(2 * N, generator=g, device="cuda")[::2]):
+        got = zr.zr_linear_xent_bwd(grad, x, w, y, lse, "none")
+        want = zr.zr_linear_xent_bwd(grad.contiguous(), x, w, y, lse, "none")
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
