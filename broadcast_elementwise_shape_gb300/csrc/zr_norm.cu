@@ -251,11 +251,13 @@ int plan_norm_bwd(zr_dtype dtype, const zr_tensor& g, const zr_tensor& x, const 
     const uint32_t sums = p.group == kNormThreads ? 0 : kNormThreads * p.ni * uint32_t(S->vec) * 4;
     pick_ring(&p, S->es, S->vec, 2, uint32_t(norm_bwd_occ(int(p.ni) * S->vec)), sums);
   } else {
-    // k_norm_sums: rows split so that the column blocks fill the GPU, at
-    // least 64 rows to a split.
+    // k_norm_sums: rows split so that the column blocks fill the GPU, and so
+    // that a lane adds 128 rows at most (its error grows with them, the second
+    // pass is compensated); at least 64 rows to a split.
     const uint32_t cb = (p.dim + kNormSumCols - 1) / kNormSumCols;
-    const uint32_t want = (kSms * 8 + cb - 1) / cb;
-    p.n_cta = std::max<uint32_t>(1, std::min<uint32_t>(want, p.nrow / 64));
+    const uint32_t fill = (kSms * 8 + cb - 1) / cb, lanes = 128 * (kNormThreads / 32);
+    const uint32_t want = std::max(fill, (p.nrow + lanes - 1) / lanes);
+    p.n_cta = std::max<uint32_t>(1, std::min(std::min<uint32_t>(want, p.nrow / 64), 65535u));
   }
   if (p.want_gamma || p.want_beta) S->ws = size_t(p.n_cta) * (p.want_gamma + p.want_beta) * size_t(dim) * sizeof(float);
   return ZR_OK;
