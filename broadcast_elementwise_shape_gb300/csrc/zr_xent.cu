@@ -353,7 +353,7 @@ k_xent_few(const __grid_constant__ FewPlan p) {
         if (c + V <= p.dim) {
           q[u][r] = __ldg(reinterpret_cast<const uint4*>(row + c));
         } else if (c < p.dim) {
-          E tail[V];
+          alignas(16) E tail[V];  // read as one 16-byte word
 #pragma unroll
           for (int j = 0; j < V; ++j) tail[j] = c + j < p.dim ? row[c + j] : E(0.f);
           q[u][r] = *reinterpret_cast<const uint4*>(tail);
