@@ -67,3 +67,20 @@ def test_rows_that_end_inside_an_access(N, dtype):
         # What lies past a row's end is not read into it.
         w._base[:, D:] = float("nan")
         check(x, w, y)
+
+
+@pytest.mark.parametrize("dtype,N,D,few", [(torch.float32, 16, 6144, True), (torch.float32, 16, 6148, False),
+                                           (torch.float32, 4, 12288, True), (torch.float32, 4, 12292, False),
+                                           (torch.float32, 2, 24576, True), (torch.float32, 2, 24580, False),
+                                           (torch.float32, 1, 49152, True), (torch.float32, 1, 49156, False),
+                                           (torch.float32, 9, 6144, True), (torch.float32, 17, 64, False),
+                                           (torch.bfloat16, 4, 12288, True), (torch.bfloat16, 4, 12296, False),
+                                           (torch.bfloat16, 1, 49152, True), (torch.bfloat16, 1, 49160, False)])
+def test_around_the_shared_memory_limit(dtype, N, D, few):
+    """Widths that w's rows allow on both sides of what x may take in shared memory."""
+    g = torch.Generator("cuda").manual_seed(D)
+    w = (torch.randn(301, D, generator=g, device="cuda") / D ** 0.5).to(dtype)
+    x = torch.randn(N, D, generator=g, device="cuda").to(dtype)
+    y = torch.randint(0, 301, (N,), generator=g, device="cuda")
+    assert kernel(x, w, y) == ("xent_few" if few else "xent")
+    check(x, w, y)
