@@ -35,6 +35,7 @@ void norm_cases(F f) {
 #undef ZR_NORM_CASE
 }
 
+// 16-byte units that a row takes in the ring.
 uint32_t ring_slot(const NormPlan& p, int es, int vec) {
   return vec > 1 ? p.group * p.ni : (p.dim * uint32_t(es) + 16 - uint32_t(es) + 15) / 16;
 }
@@ -71,7 +72,7 @@ void pick_group(NormPlan* p, int vec) {
 void pick_ring(NormPlan* p, int es, int vec, uint32_t streams, uint32_t per_sm, uint32_t at_least) {
   const uint32_t rpb = kNormThreads / p->group;
   p->n_cta = (p->nrow + rpb - 1) / rpb;
-  p->slot = vec > 1 ? p->group * p->ni : (p->dim * uint32_t(es) + 16 - uint32_t(es) + 15) / 16;
+  p->slot = ring_slot(*p, es, vec);
   const uint32_t ring = streams * rpb * p->slot * 16;  // one stage
   const uint32_t most = uint32_t(kNormSmemMax);
   p->stages = 3 * ring * per_sm <= most ? 3 : 2;
@@ -198,7 +199,7 @@ int plan_norm_fwd(zr_dtype dtype, const zr_tensor& x, const zr_tensor& gamma, co
   p.rstd = rstd;
   p.eps = eps;
   if ((rc = plan_rows(S, 1, y))) return rc;
-  if (p.group) pick_ring(&p, S->es, S->vec, 1, uint32_t(norm_fwd_occ(int(p.ni) * S->vec)), 0);
+  if (p.group) pick_ring(&p, S->es, S->vec, 1, uint32_t(norm_occ(int(p.ni) * S->vec)), 0);
   else p.n_cta = p.nrow;
   return ZR_OK;
 }
@@ -249,7 +250,7 @@ int plan_norm_bwd(zr_dtype dtype, const zr_tensor& g, const zr_tensor& x, const 
   if (p.group) {
     // After the rows the ring holds every row group's column sums.
     const uint32_t sums = p.group == kNormThreads ? 0 : kNormThreads * p.ni * uint32_t(S->vec) * 4;
-    pick_ring(&p, S->es, S->vec, 2, uint32_t(norm_bwd_occ(int(p.ni) * S->vec)), sums);
+    pick_ring(&p, S->es, S->vec, 2, uint32_t(norm_occ(int(p.ni) * S->vec)), sums);
   } else {
     // k_norm_sums: rows split so that the column blocks fill the GPU, and so
     // that a lane adds 128 rows at most (its error grows with them, the second

@@ -275,7 +275,7 @@ __device__ __forceinline__ float f2_sum(F2 a) {
 }
 
 template <typename E, int VEC, int G, int NI>
-__global__ void __launch_bounds__(kNormThreads, norm_fwd_occ(NI * VEC))
+__global__ void __launch_bounds__(kNormThreads, norm_occ(NI * VEC))
 k_norm_fwd(const __grid_constant__ NormPlan p) {
   pdl_trigger();
   constexpr int RPB = kNormThreads / G;           // rows per block per step
@@ -453,7 +453,7 @@ k_norm_fwd_long(const __grid_constant__ NormPlan p) {
 // and the column sums, once for grad_x: kept in registers instead it took 222
 // of them, 8 warps per SM, and [65536, 1024] bf16 137 us; 60 now.
 template <typename E, int VEC, int G, int NI>
-__global__ void __launch_bounds__(kNormThreads, norm_bwd_occ(NI * VEC))
+__global__ void __launch_bounds__(kNormThreads, norm_occ(NI * VEC))
 k_norm_bwd(const __grid_constant__ NormPlan p) {
   pdl_trigger();
   constexpr int T = kNormThreads;

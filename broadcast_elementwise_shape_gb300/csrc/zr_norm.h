@@ -38,9 +38,8 @@ struct NormPlan {
 
 constexpr int kNormThreads = 256;
 // CTAs per SM that the kernels' registers allow without spills, by columns per
-// lane.
-ZR_CX int norm_fwd_occ(int cols) { return cols > 16 ? 2 : (cols > 8 ? 3 : 4); }
-ZR_CX int norm_bwd_occ(int cols) { return cols > 16 ? 2 : (cols > 8 ? 3 : 4); }
+// lane, forward and backward alike.
+ZR_CX int norm_occ(int cols) { return cols > 16 ? 2 : (cols > 8 ? 3 : 4); }
 constexpr int kNormSmemMax = 224 * 1024; // dynamic shared memory of all CTAs of an SM
 constexpr uint32_t kNormLongThreads = 1024;
 constexpr uint32_t kNormSumCols = 32;    // k_norm_sums: columns per CTA
