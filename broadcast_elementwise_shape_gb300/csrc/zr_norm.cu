@@ -312,9 +312,13 @@ int zr_layer_norm_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor x, zr_tensor
   if (S.ws) {
     if (!aligned(workspace, 16)) return ZR_ERR_WORKSPACE;
     const Span sw = span_of(workspace, int64_t(S.ws), 1);
-    for (int k = 0; k < 2; ++k)
-      if (overlaps(sw, span_of(S.in[k].ptr, S.in[k].extent, S.es))) return ZR_ERR_LAYOUT;
-    if (overlaps(sw, span_of(grad_x, S.out.extent, S.es))) return ZR_ERR_LAYOUT;
+    const int64_t rows = S.p.nrow;
+    const Span others[] = {span_of(S.in[0].ptr, S.in[0].extent, S.es), span_of(S.in[1].ptr, S.in[1].extent, S.es),
+                           span_of(S.gamma.ptr, S.gamma.extent, S.es), span_of(mean, rows), span_of(rstd, rows),
+                           span_of(grad_x, S.out.extent, S.es), span_of(grad_gamma, int64_t(dim), S.es),
+                           span_of(grad_beta, int64_t(dim), S.es)};
+    for (const Span& o : others)
+      if (overlaps(sw, o)) return ZR_ERR_LAYOUT;
   }
   if (trace_on()) trace("zr_layer_norm_bwd", norm_json(S, "norm_bwd"));
   const void* need[9] = {S.p.in[0], S.p.in[1], S.p.gamma, mean, rstd, grad_x, grad_gamma, grad_beta,
