@@ -486,17 +486,34 @@ int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, voi
  * ZR_MEAN: divided by the count of rows that take part) and
  * G[n, v] = c_n (exp(l[n, v] - lse_n) - [v = label_n]):
  *   grad_x = G W and grad_w = G^T X, dense row-major, either may be NULL.
- * The logits are computed again, a piece of the vocabulary at a time; the
- * workspace holds one piece of G (about 1 GiB at most, or 2048 classes'
- * worth for very many rows) and, where a gradient's long sum over few outputs
- * is cut into slices, their results (1 GiB at most per gradient).
+ * The label's element is taken as what the row's others sum to, so that of a
+ * learnt row, whose p is near 1, it is as exact as they are (ZR_BF16 with G in
+ * several pieces: exp(l - lse) - 1, off by lse's rounding).
+ * The logits are computed again, a piece of the vocabulary at a time.
  *
- * Numerics.  Products accumulate in binary32 on the tensor cores; statistics
- * and losses are binary32.  ZR_BF16: operands as stored, G rounded once to
- * bfloat16 as an operand (up to 128 rows: held to 2^-16), gradients rounded once.  ZR_F32: each operand is
- * split into three bfloat16 parts, whose products reach binary32 accuracy.
- * A row with an infinite logit has a NaN loss.  Results are reproducible run
- * to run (no atomics).
+ * Workspace, in bytes:
+ *   operands that the tensor cores cannot read as they are, copied by rows of
+ *   whole 64 columns: ZR_F32 x and w, 6 per element (1.6e9 for w of [130000,
+ *   2048]); ZR_BF16 those whose D is no multiple of 64, whose rows are no
+ *   multiple of 8 elements apart or not 16-byte aligned, 2 per element, and x
+ *   whenever grad_w is wanted.  The forward of a few rows copies none.
+ *   Forward: 8 per row and 128 classes (ZR_F32 up to 128 rows: per 64 classes).
+ *   Backward: one piece of G, 2 per element (ZR_F32 6; ZR_BF16 up to 128 rows
+ *   4), about 1 GiB at most, or 2048 classes' worth for very many rows; 4 per row
+ *   and 128 classes (64, as above) for the rows' sums; where there are several pieces, N x D
+ *   floats that grad_x adds up in; where a gradient's long sum over few outputs is
+ *   cut into slices, their results, 1 GiB at most per gradient.
+ *
+ * Numerics.  Products accumulate in binary32 on the tensor cores, whose sums
+ * truncate: at most 1024 terms of a logit (ZR_F32 64) and 8192 of a gradient
+ * (64) in one go, which are then added with rounding.  Statistics and losses are
+ * binary32.  ZR_BF16: operands as stored, G rounded once to bfloat16 as an
+ * operand (up to 128 rows: held to 2^-16), gradients rounded once.  ZR_F32: each
+ * operand is split into three bfloat16 parts, and a product is the sum of the
+ * six products of parts that reach 2^-24 of it.
+ * A row with a logit of +infinity or NaN has a NaN loss; so has, in ZR_F32, one
+ * with -infinity, which has no parts (the forward of a few rows takes it as 0).
+ * Results are reproducible run to run (no atomics).
  * Sizes: D < 2^24, V and N < 2^30 (else ZR_ERR_SIZE); D, V >= 1.  N = 0: loss
  * (sum, mean) and grad_w become 0.  Errors as zr_binary_bwd, plus ZR_ERR_DTYPE.
  */
