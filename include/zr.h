@@ -500,9 +500,9 @@ int zr_dropout_bwd(zr_dtype dtype, zr_tensor grad_out, double p, zr_rng rng, voi
  *   Forward: 8 per row and 128 classes (ZR_F32 up to 128 rows: per 64 classes).
  *   Backward: one piece of G, 2 per element (ZR_F32 6; ZR_BF16 up to 128 rows
  *   4), about 1 GiB at most, or 2048 classes' worth for very many rows; 4 per row
- *   and 128 classes (64, as above) for the rows' sums; where there are several pieces, N x D
- *   floats that grad_x adds up in; where a gradient's long sum over few outputs is
- *   cut into slices, their results, 1 GiB at most per gradient.
+ *   and 128 classes (64, as above) for the rows' sums; where there are several
+ *   pieces, N x D floats that grad_x adds up in; where a gradient's long sum over
+ *   few outputs is cut into slices, their results, 1 GiB at most per gradient.
  *
  * Numerics.  Products accumulate in binary32 on the tensor cores, whose sums
  * truncate: at most 1024 terms of a logit (ZR_F32 64) and 8192 of a gradient
