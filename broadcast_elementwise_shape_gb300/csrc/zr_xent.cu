@@ -934,14 +934,17 @@ constexpr uint32_t kChunkF32 = 1, kChunkBf16 = 64;
 constexpr uint32_t kLongK = 128;
 
 // The logits of bfloat16 rows give binary32 results: at most 1024 terms in one
-// go, so that only longer rows pay for the registers.  Longer or shorter, the
-// forward: [4096, 2048] x [20000, 2048], 171 us and a loss off by 1.6e-6 in one
-// go, 174 us and 0.8e-6 in two; [4096, 1024], 88 us and 0.9e-6 in one, 106 us
-// and 0.5e-6 in two.  The backward's logits go the same way, for
+// go, so that only longer rows pay for the registers.  Forward of 4096 rows and
+// 20000 classes, us and the loss's error: 1024 columns in one go 89, 4.5e-7 (in
+// two 106); in one go and in chunks 1088 columns 95, 4.5e-7
+// and 111, 2.3e-7; 1280 columns 110, 6.0e-7 and 119, 3.1e-7; 2048 columns 172,
+// 9.0e-7 and 177, 4.6e-7; 4096 columns 336, 1.8e-6 and 340, 3.8e-7.  The
+// backward's logits go the same way, for
 // exp(l - lse) - 1 of a row that is learnt shows every difference between them
 // and those that lse was summed from: rows of 4096 positive terms, l = 20, had
 // the label's gradient off by 1.2 times its size at 1 - p = 1.5e-4 when the
-// backward added them in one go.
+// backward added them in one go.  Backward, in one go and in chunks: 1088 columns
+// 343 and 397, 2048 585 and 590, 4096 1154 and 1178.
 constexpr uint32_t kChunkLse = 16;
 
 bool sum_chunks(const XentSet& S, int epi, GemmPlan* g) {
