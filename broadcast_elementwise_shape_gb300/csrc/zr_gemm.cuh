@@ -458,11 +458,11 @@ struct EpiLse {
 // lse's rounding alone (2^-25 of it) was 1.7e-5 of a whole binary32 gradient of
 // one row.  So it is taken as what the other elements sum to, which is as exact
 // as they are: with p.sums every half tile leaves its sum of exp(l - lse) but
-// for the label's, and k_xent_label puts -sum / (sum + the label's) in its place.
+// for the label's, and -sum / (sum + the label's) takes its place (k_xent_label).
 template <int PARTS>
 struct EpiGrad {
   float scale, lse, sum;
-  int64_t at;
+  int64_t at;                // column of the label in this tile
   bool out;                  // the row is left out: zeros, whatever its products are
 
   __device__ __forceinline__ void begin(const GemmPlan& p, const GemmProblem&, const EpiPos& e) {
@@ -506,7 +506,7 @@ struct EpiGrad {
     }
     const bool mine = at >= int64_t(c) && at < int64_t(c) + 64;
     if (__any_sync(0xFFFFFFFFu, mine)) {
-      if (p.sums) {          // what is stored in its place is overwritten
+      if (p.sums) {
         float own = 0.f;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
@@ -516,11 +516,6 @@ struct EpiGrad {
           }
         }
         if (mine) p.at[e.row] = e.ok ? own : qnan();
-      } else if (p.label_g) {
-        const float g = mine ? p.label_g[e.row] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (at == int64_t(c) + i) v[i] = g;
       } else {
 #pragma unroll
         for (int i = 0; i < 64; ++i)
@@ -528,15 +523,10 @@ struct EpiGrad {
       }
     }
     if (p.sums) {
-      F2 add[4];
+      float lo = 0.f, hi = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) add[i] = f2_pack(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-      for (int i = 4; i < 32; ++i) add[i & 3] = f2_add(add[i & 3], f2_pack(v[2 * i], v[2 * i + 1]));
-      float lo, hi;
-      f2_unpack(f2_add(f2_add(add[0], add[1]), f2_add(add[2], add[3])), lo, hi);
+      for (int i = 0; i < 64; i += 2) { lo += v[i]; hi += v[i + 1]; }
       sum += lo + hi;
-      if (!q.tma_out) return;
     }
     if (__any_sync(0xFFFFFFFFu, scale != 1.f)) {
 #pragma unroll
@@ -584,9 +574,12 @@ struct EpiOut {
         }
       }
     }
-    const bool left_out = __float_as_uint(scale) == 0x80000000u;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = e.ok ? (left_out ? 0.f : v[i] * scale) : qnan();
+    for (int i = 0; i < 64; ++i) v[i] *= scale;
+    if (__float_as_uint(scale) == 0x80000000u || !e.ok) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = e.ok ? 0.f : qnan();
+    }
     if (q.acc_out) {
       if (e.live) {
 #pragma unroll

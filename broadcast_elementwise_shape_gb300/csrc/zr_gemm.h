@@ -59,7 +59,7 @@ struct GemmProblem {
   int64_t plane;
   uint32_t chunk;            // k blocks per accumulation in TMEM
   // Epilogues kEpiGrad and kEpiOut with tma_out: results leave through this map,
-  // in boxes of 128 bytes by 32 rows.  kEpiGrad without it: not stored.
+  // in boxes of 128 bytes by 32 rows.
   CUtensorMap c;
   uint32_t tma_out;
   // Epilogue kEpiOut: out = [acc_in +] product, in the operands' type with row
@@ -97,8 +97,8 @@ struct GemmPlan {
   // kEpiGrad
   const float* lse;          // [m]
   const float* row_scale;    // [m], or null (1)
-  float* sums;               // [m][2 * n_tiles] sum of exp(product - lse) but for the label, or null
-  const float* label_g;      // [m] the label's element less its factor, or null (exp(...) - 1)
+  float* sums;               // [m][2 * n_tiles] sum of exp(product - lse) but for the label,
+                             // whose element is stored as 0; or null
   int64_t ignore_index, vocab;
   int64_t label_base;        // column 0 of this product is this label
 };
