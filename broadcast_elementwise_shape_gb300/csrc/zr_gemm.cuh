@@ -499,7 +499,9 @@ struct EpiGrad {
 #pragma unroll
       for (int i = 0; i < 64; ++i) v[i] = ex2(v[i]);
     }
-    if (e.n0 + c + 64 > q.n) {  // G's rows are padded with zeros to whole blocks of 64
+    // G's rows are padded with zeros to whole blocks of 64.
+    const bool ragged = e.n0 + c + 64 > q.n;
+    if (ragged) {
 #pragma unroll
       for (int i = 0; i < 64; ++i)
         if (e.n0 + c + i >= q.n) v[i] = 0.f;
@@ -531,6 +533,11 @@ struct EpiGrad {
     if (__any_sync(0xFFFFFFFFu, scale != 1.f)) {
 #pragma unroll
       for (int i = 0; i < 64; ++i) v[i] *= scale;
+      if (ragged || (p.sums && mine)) {  // an infinite factor leaves what is no element 0
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (e.n0 + c + i >= q.n || (p.sums && at == int64_t(c) + i)) v[i] = 0.f;
+      }
     }
     if (out || !e.ok) {
 #pragma unroll

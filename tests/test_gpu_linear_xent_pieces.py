@@ -106,3 +106,17 @@ def test_repeats_itself():
     a = zr.zr_linear_xent_bwd(one, x, w, y, lse)
     b = zr.zr_linear_xent_bwd(one, x, w, y, lse)
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_infinite_upstream_gradient():
+    """One row's upstream gradient overflowed: its label's row of grad_w is
+    infinite with the sign of -x, and rows it has no part in stay finite."""
+    x, w, y = make(300, 700001, 8)
+    y[5] = 17
+    y[torch.arange(300, device="cuda") != 5] = 700000
+    grad = torch.ones(300, device="cuda")
+    grad[5] = float("inf")
+    _, lse = zr.zr_linear_xent_fwd(x, w, y, "none")
+    gx, gw = zr.zr_linear_xent_bwd(grad, x, w, y, lse, "none")
+    assert bool((gw[17] == -x[5].sign() * float("inf")).all())
+    assert bool(torch.isfinite(gx[:5]).all()) and bool(torch.isfinite(gx[6:]).all())
