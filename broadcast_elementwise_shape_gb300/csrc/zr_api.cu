@@ -465,7 +465,7 @@ static int binary_fwd_es(int es, zr_op op, zr_tensor a, zr_tensor b, float* out,
   S.es = es;
   int rc = plan_fwd(op, a, b, out, out_strides, &S);
   if (rc) return rc;
-  if (trace_on()) trace("zr_binary_fwd", fwd_json(S));
+  trace("zr_binary_fwd", [&] { return fwd_json(S); });
   if (S.empty) return ZR_OK;
   for (const void* p : {static_cast<const void*>(S.a.ptr), static_cast<const void*>(S.b.ptr),
                         static_cast<const void*>(out)}) {
@@ -490,7 +490,7 @@ static int binary_bwd_es(int es, zr_op op, zr_tensor grad_out, zr_tensor a, zr_t
     *workspace_bytes = S.ws_query;
     return ZR_OK;
   }
-  if (trace_on()) trace("zr_binary_bwd", bwd_json(S));
+  trace("zr_binary_bwd", [&] { return bwd_json(S); });
   if (S.nothing) return ZR_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (S.empty) {
@@ -610,7 +610,7 @@ int zr_binary_bwd_noalloc(zr_op op, zr_tensor grad_out, zr_tensor a, zr_tensor b
   BwdSet S;
   int rc = plan_bwd(op, grad_out, a, b, grad_a, grad_b, &S);
   if (rc) return rc;
-  if (trace_on()) trace("zr_binary_bwd_noalloc", bwd_json(S));
+  trace("zr_binary_bwd_noalloc", [&] { return bwd_json(S); });
   if (S.nothing) return ZR_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (S.empty) {
@@ -656,7 +656,7 @@ static int sum_to_shape_es(int es, zr_tensor in, int32_t ndim_out, const int64_t
     *workspace_bytes = S.ws_query;
     return ZR_OK;
   }
-  if (trace_on()) trace("zr_sum_to_shape", sum_json(S));
+  trace("zr_sum_to_shape", [&] { return sum_json(S); });
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (S.empty) {
     if (!S.zero_ptr) return ZR_OK;
@@ -1785,7 +1785,7 @@ int zr_unary_fwd_t(zr_dtype dtype, zr_unary op, float alpha, zr_tensor x, void* 
   S.es = dtype == ZR_BF16 ? 2 : 4;
   int rc = plan_unary(op, alpha, x, nullptr, out, out_strides, &S);
   if (rc || S.empty) return rc;
-  if (trace_on()) trace("zr_unary_fwd", describe_ew(S.eb));
+  trace("zr_unary_fwd", [&] { return describe_ew(S.eb); });
   for (const void* p : {static_cast<const void*>(S.g.ptr), static_cast<const void*>(out)}) {
     rc = check_device_ptr(p);
     if (rc) return rc;
@@ -1808,7 +1808,7 @@ int zr_unary_bwd_t(zr_dtype dtype, zr_unary op, float alpha, zr_tensor grad_out,
   int rc = plan_unary(op, alpha, grad_out, op == UN_GELU ? &x : nullptr, grad_x, grad_x_strides,
                       &S);
   if (rc || S.empty) return rc;
-  if (trace_on()) trace("zr_unary_bwd", describe_ew(S.eb));
+  trace("zr_unary_bwd", [&] { return describe_ew(S.eb); });
   if (op != UN_GELU) {
     if (x.ndim != grad_out.ndim || (x.ndim > 0 && !x.sizes)) return ZR_ERR_SHAPE;
     for (int d = 0; d < x.ndim; ++d)

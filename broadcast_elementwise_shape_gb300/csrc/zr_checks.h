@@ -101,8 +101,15 @@ inline bool trace_on() {
   return on;
 }
 
-inline void trace(const char* entry, const std::string& json) {
-  std::fprintf(stderr, "zr_trace %s %s\n", entry, json.c_str());
+// json(): the plan.  It allocates, and the C entry points raise nothing: where
+// there is no memory for the line, the call goes on without it.
+template <typename F>
+inline void trace(const char* entry, F json) noexcept {
+  if (!trace_on()) return;
+  try {
+    std::fprintf(stderr, "zr_trace %s %s\n", entry, json().c_str());
+  } catch (...) {
+  }
 }
 
 }  // namespace zr

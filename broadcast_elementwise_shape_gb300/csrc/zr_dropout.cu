@@ -312,10 +312,10 @@ int run_dropout(const char* name, zr_dtype dtype, const zr_tensor& x, const zr_t
   DropSet S;
   int rc = plan_dropout(dtype, x, residual, prob, rng, out, out_strides, &S);
   if (rc || S.empty) return rc;
-  if (trace_on())
-    trace(name, std::string("{\"kernel\":\"dropout\",\"vec\":") + std::to_string(S.vec) +
-                    ",\"items\":" + std::to_string(S.p.nitems) +
-                    ",\"n_cta\":" + std::to_string(S.n_cta) + "}");
+  trace(name, [&] {
+    return std::string("{\"kernel\":\"dropout\",\"vec\":") + std::to_string(S.vec) +
+           ",\"items\":" + std::to_string(S.p.nitems) + ",\"n_cta\":" + std::to_string(S.n_cta) + "}";
+  });
   const void* need[4] = {S.p.x, S.p.residual, out, rng.device_offset};
   for (const void* q : need)
     if (q && (rc = check_device_ptr(q))) return rc;

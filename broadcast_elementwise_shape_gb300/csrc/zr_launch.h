@@ -5,8 +5,6 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
-#include <utility>
-#include <vector>
 
 #include "zr_plan.h"
 
@@ -66,18 +64,19 @@ inline cudaError_t launch_k_cluster(void (*kernel)(KArgs...), unsigned grid, uns
 // Kernels whose dynamic shared memory may exceed the default 48 KB limit:
 // raise_smem_limit sets the kernel's limit to `bytes` (the most a CTA may use,
 // for kernels without static shared memory), once per kernel and device
-// (remembered in a small table under a lock).
+// (remembered in a small table under a lock; once it is full, every time).
 inline cudaError_t raise_smem_limit(const void* kernel, int bytes = 227 * 1024) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static std::mutex mu;
-  static std::vector<std::pair<const void*, int>> done;
+  static struct { const void* kernel; int dev; } done[256];
+  static int n = 0;
   std::lock_guard<std::mutex> lock(mu);
-  for (const auto& d : done)
-    if (d.first == kernel && d.second == dev) return cudaSuccess;
+  for (int i = 0; i < n; ++i)
+    if (done[i].kernel == kernel && done[i].dev == dev) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.emplace_back(kernel, dev);
+  if (e == cudaSuccess && n < 256) done[n++] = {kernel, dev};
   return e;
 }
 // The kernel itself when `smem` bytes are allowed for it, null otherwise (the

@@ -277,7 +277,7 @@ int zr_layer_norm_fwd(zr_dtype dtype, zr_tensor x, zr_tensor gamma, zr_tensor be
   NormSet S;
   int rc = plan_norm_fwd(dtype, x, gamma, beta, eps, y, y_strides, mean, rstd, &S);
   if (rc || S.empty) return rc;
-  if (trace_on()) trace("zr_layer_norm_fwd", norm_json(S, "norm_fwd"));
+  trace("zr_layer_norm_fwd", [&] { return norm_json(S, "norm_fwd"); });
   const void* need[6] = {S.p.in[0], y, S.p.gamma, S.p.beta, mean, rstd};
   for (const void* q : need)
     if (q && (rc = check_device_ptr(q))) return rc;
@@ -320,7 +320,7 @@ int zr_layer_norm_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor x, zr_tensor
     for (const Span& o : others)
       if (overlaps(sw, o)) return ZR_ERR_LAYOUT;
   }
-  if (trace_on()) trace("zr_layer_norm_bwd", norm_json(S, "norm_bwd"));
+  trace("zr_layer_norm_bwd", [&] { return norm_json(S, "norm_bwd"); });
   const void* need[9] = {S.p.in[0], S.p.in[1], S.p.gamma, mean, rstd, grad_x, grad_gamma, grad_beta,
                          S.ws ? workspace : nullptr};
   for (const void* q : need)

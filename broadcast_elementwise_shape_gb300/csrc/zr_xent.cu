@@ -1407,7 +1407,7 @@ int zr_linear_xent_fwd(zr_dtype dtype, zr_tensor x, zr_tensor w, zr_index label_
     if ((rc = check_all({loss}))) return rc;
     return cuda_status(cudaMemsetAsync(loss, 0, sizeof(float), st));
   }
-  if (trace_on()) trace("zr_linear_xent_fwd", xent_json(S));
+  trace("zr_linear_xent_fwd", [&] { return xent_json(S); });
   if ((rc = check_all({S.x.t.ptr, S.w.t.ptr, S.labels.ptr, loss, lse, workspace}))) return rc;
   return run_fwd(S, loss, lse, static_cast<char*>(workspace), st);
 }
@@ -1443,7 +1443,7 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
     return cuda_status(cudaMemsetAsync(grad_w, 0, size_t(vocab) * dim * S.es, st));
   }
   if (!grad_x && !grad_w) return ZR_OK;
-  if (trace_on()) trace("zr_linear_xent_bwd", xent_json(S));
+  trace("zr_linear_xent_bwd", [&] { return xent_json(S); });
   if ((rc = check_all({grad_loss, S.x.t.ptr, S.w.t.ptr, S.labels.ptr, lse, grad_x, grad_w, workspace})))
     return rc;
   return run_bwd(S, grad_loss, lse, grad_x, grad_w, static_cast<char*>(workspace), st);
