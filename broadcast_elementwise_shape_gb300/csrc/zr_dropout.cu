@@ -17,6 +17,7 @@
 #include "zr_checks.h"
 #include "zr_kernels.cuh"
 #include "zr_launch.h"
+#include "zr_philox.cuh"
 
 namespace zr {
 
@@ -41,20 +42,8 @@ struct DropPlan {
 
 namespace {
 
-// The four words of one counter: ten rounds of two 32 x 32 -> 64
-// multiplications.  The key's schedule (the paper's Weyl constants added from
-// round to round) is the same for every element, so the host computes it.
 __device__ __forceinline__ void philox(uint64_t counter, const uint32_t* key, uint32_t* w) {
-  uint32_t c0 = uint32_t(counter), c1 = uint32_t(counter >> 32), c2 = 0, c3 = 0;
-#pragma unroll
-  for (int r = 0; r < 10; ++r) {
-    const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;
-    c0 = uint32_t(b >> 32) ^ c1 ^ key[2 * r];
-    c1 = uint32_t(b);
-    c2 = uint32_t(a >> 32) ^ c3 ^ key[2 * r + 1];
-    c3 = uint32_t(a);
-  }
-  w[0] = c0; w[1] = c1; w[2] = c2; w[3] = c3;
+  zr::philox(uint32_t(counter), uint32_t(counter >> 32), 0, 0, key, w);
 }
 
 template <typename E, bool RES>
@@ -239,11 +228,7 @@ int plan_dropout(zr_dtype dtype, const zr_tensor& x, const zr_tensor* residual, 
   p.residual = res ? S->r.ptr : nullptr;
   p.out = out;
   p.device_offset = rng.device_offset;
-  uint32_t k0 = uint32_t(rng.seed), k1 = uint32_t(rng.seed >> 32);
-  for (int r = 0; r < 10; ++r, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
-    p.key[2 * r] = k0;
-    p.key[2 * r + 1] = k1;
-  }
+  philox_keys(rng.seed, p.key);
   p.offset = rng.offset;
   p.numel = uint64_t(S->x.numel);
   const double thr = std::nearbyint(prob * 4294967296.0);

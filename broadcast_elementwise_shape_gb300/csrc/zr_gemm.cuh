@@ -21,6 +21,7 @@
 
 #include "zr_gemm.h"
 #include "zr_kernels.cuh"
+#include "zr_tc.cuh"
 
 namespace zr {
 
@@ -28,7 +29,6 @@ constexpr int kGemmThreads = 320;      // 8 epilogue warps, producer, issuer
 constexpr uint32_t kGemmM = 128;       // rows per CTA
 constexpr uint32_t kGemmK = 64;        // k per block (128 bytes)
 constexpr uint32_t kABytes = kGemmM * kGemmK * 2;
-constexpr uint64_t kWaitNs = 2000000000ull, kStepNs = 1000000ull;
 
 // Parts of the operands A and B, and the products of parts that make up theirs.
 // PARTS = 3 (binary32 tensors): a stage holds all three parts of both operands,
@@ -49,211 +49,6 @@ struct GemmCfg {
   static constexpr uint32_t kOutAt = kStages * kStageBytes;
   static constexpr uint32_t kSmem = kOutAt + 8 * 4096 + 1024;
 };
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ uint64_t timer_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-// ------------------------------------------------------------------ mbarrier
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Waits for the phase of the given parity; false when the CTA has aborted or
-// the limit ran out (which aborts it).  A step of the clock that is longer than
-// the tries between two looks at it can take is time the GPU spent elsewhere
-// (another process's turn), and counts as no more than kStepNs.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-  if (mbar_try(bar, parity)) return true;
-  uint64_t last = timer_ns(), waited = 0;
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try(bar, parity)) return true;
-    if (*abort) return false;
-    const uint64_t now = timer_ns();
-    waited += now - last < kStepNs ? now - last : kStepNs;
-    last = now;
-    if (waited > kWaitNs) {
-      *abort = 1;
-      return false;
-    }
-  }
-}
-// The same by a whole warp: true when all its lanes saw the phase.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-  const bool ok = mbar_wait(bar, parity, abort);
-  return __all_sync(0xFFFFFFFFu, ok);
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-// The address of `local` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
-               : "memory");
-}
-
-// ------------------------------------------------------------------ TMA, tcgen05
-template <int CG>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t row,
-                                         uint32_t block) {
-  if constexpr (CG == 1) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(0), "r"(row), "r"(block), "r"(0)
-        : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(0), "r"(row), "r"(block), "r"(0)
-        : "memory");
-  }
-}
-
-template <int CG>
-__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
-  if constexpr (CG == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
-}
-template <int CG>
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-template <int CG>
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-  if constexpr (CG == 1) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
-}
-// Arrives on `bar` (of both CTAs of a pair) once the instructions issued so
-// far are done.
-template <int CG>
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  if constexpr (CG == 1) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-  } else {
-    const uint16_t both = 3;
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"(both)
-        : "memory");
-  }
-}
-// 32 columns of this warp's 32 TMEM lanes; tc_wait_load() before their use.
-__device__ __forceinline__ void tc_load32_async(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tc_wait_load() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc_load32(uint32_t addr, float* v) {
-  uint32_t r[32];
-  tc_load32_async(addr, r);
-  tc_wait_load();
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tc_load64(uint32_t addr, float* v) {
-  uint32_t r[64];
-  tc_load32_async(addr, r);
-  tc_load32_async(addr + 32, r + 32);
-  tc_wait_load();
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// Shared-memory operand descriptor, 128-byte swizzle.  Both kinds of block
-// hold 128-byte rows in groups of 8 (1024 bytes apart, the stride offset).
-// K-major: a row is one m or n with 64 k.  MN-major: a row is one k with 64 m
-// or n, and further 64-wide columns of rows follow after 8192 bytes (64 k
-// rows; the leading offset).
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t mn_major) {
-  uint64_t d = uint64_t((addr & 0x3FFFFu) >> 4);
-  d |= uint64_t(mn_major ? 8192 >> 4 : 1) << 16;
-  d |= uint64_t(1024 >> 4) << 32;
-  d |= uint64_t(1) << 46;
-  d |= uint64_t(2) << 61;
-  return d;
-}
-
-// A value that every lane of the warp holds, in a form the compiler knows to be
-// the same: operands of the copy engine and the tensor core are then kept in
-// uniform registers.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
-// True in one lane of the warp, the same each time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok));
-  return ok != 0;
-}
 
 struct GemmTile {
   uint32_t prob, mt, nt, n0, tn;
@@ -302,25 +97,6 @@ __device__ __forceinline__ constexpr uint32_t gemm_pair(int i, int operand) {
 }
 
 // ------------------------------------------------------------------ epilogues
-
-constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// The same with subnormal results kept, at some more instructions.
-__device__ __forceinline__ float ex2_full(float x) {
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float qnan() { return __uint_as_float(0x7FFFFFFFu); }
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // Where one epilogue warp's lane stands: row `row` (live: inside the product)
 // of the warp's 32 from row0, columns c0, c0 + 128, ... of the tile in chunks
