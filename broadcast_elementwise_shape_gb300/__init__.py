@@ -19,6 +19,10 @@ Entry points mirror the C names:
   ``zr_dropout_bwd(grad_out, p, seed, offset) -> grad_x``
 * ``zr_linear_xent_fwd(x, w, labels, reduction) -> (loss, lse)`` and
   ``zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction) -> (grad_x, grad_w)``
+* ``zr_rotary_plan(part, base, ...) -> plan``, ``zr_rotary_fwd(x, plan, positions) -> out`` and
+  ``zr_rotary_bwd(grad_out, plan, positions) -> grad_x``
+* ``zr_adamw_step(params, grads, ms, vs, step, lr, ...)`` in place, and
+  ``zr_adamw_state(ms, vs, m_scales, v_scales) -> (m values, v values)`` of 8-bit states
 
 ``op`` is one of ``"add" "sub" "mul" "div"`` or the ``ZR_*`` integer codes.
 """
@@ -60,6 +64,22 @@ class ZrRng(ctypes.Structure):
                 ("device_offset", ctypes.c_void_p)]
 
 
+class ZrRotary(ctypes.Structure):
+    _fields_ = [("part", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 256)]
+
+
+class ZrAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "copy", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float)]
+
+
+class ZrAdamw(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)] + [
+        (n, ctypes.c_void_p) for n in ("device_step", "device_lr", "device_grad_scale")]
+
+
 def lib() -> ctypes.CDLL:
     """The loaded ``libzr.so``; raises if it has not been built."""
     global _lib
@@ -98,13 +118,21 @@ def lib() -> ctypes.CDLL:
                                          ctypes.c_int64, c_int, vp, vp, vp, szp, vp]
         L.zr_linear_xent_bwd.argtypes = [c_int, vp, ZrTensor, ZrTensor, c_int, ZrTensor,
                                          ctypes.c_int64, c_int, vp, vp, vp, vp, szp, vp]
+        rotp, i64 = ctypes.POINTER(ZrRotary), ctypes.c_int64
+        L.zr_rotary_plan.argtypes = [i32, i32, *[ctypes.c_double] * 6, rotp]
+        L.zr_rotary_fwd.argtypes = [c_int, ZrTensor, rotp, c_int, ZrTensor, i64, vp, i64p, vp]
+        L.zr_rotary_bwd.argtypes = L.zr_rotary_fwd.argtypes
+        adam = ctypes.POINTER(ZrAdamwTensor)
+        L.zr_adamw_step.argtypes = [c_int, i32, i32, adam, ctypes.POINTER(ZrAdamw), vp]
+        L.zr_adamw_state.argtypes = [i32, adam, ctypes.POINTER(vp), ctypes.POINTER(vp), vp]
         L.zr_status_string.argtypes = [c_int]
         L.zr_status_string.restype = ctypes.c_char_p
         for f in ("zr_broadcast_shape", "zr_binary_fwd", "zr_binary_bwd", "zr_sum_to_shape",
                   "zr_chain_fwd", "zr_chain_bwd", "zr_binary_bwd_ex", "zr_unary_fwd", "zr_unary_bwd",
                   "zr_binary_fwd_t", "zr_binary_bwd_t", "zr_sum_to_shape_t", "zr_unary_fwd_t",
                   "zr_unary_bwd_t", "zr_layer_norm_fwd", "zr_layer_norm_bwd", "zr_dropout_fwd",
-                  "zr_dropout_bwd", "zr_linear_xent_fwd", "zr_linear_xent_bwd"):
+                  "zr_dropout_bwd", "zr_linear_xent_fwd", "zr_linear_xent_bwd", "zr_rotary_plan",
+                  "zr_rotary_fwd", "zr_rotary_bwd", "zr_adamw_step", "zr_adamw_state"):
             getattr(L, f).restype = c_int
         _lib = L
     return _lib
@@ -378,7 +406,8 @@ def zr_unary_bwd(op, grad_out, x, alpha=1.0, grad_x=None):
 
 # The training operators' binding imports torch; the package itself does not.
 _TRAIN = ("zr_layer_norm_fwd", "zr_layer_norm_bwd", "zr_dropout_fwd", "zr_dropout_bwd",
-          "zr_linear_xent_fwd", "zr_linear_xent_bwd")
+          "zr_linear_xent_fwd", "zr_linear_xent_bwd", "zr_rotary_plan", "zr_rotary_fwd", "zr_rotary_bwd",
+          "zr_adamw_step", "zr_adamw_state")
 
 
 def __getattr__(name):

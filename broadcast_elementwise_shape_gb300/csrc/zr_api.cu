@@ -732,6 +732,7 @@ const char* zr_status_string(int status) {
     case ZR_ERR_DEVICE: return "ZR_ERR_DEVICE: pointer not addressable by the current device";
     case ZR_ERR_WORKSPACE: return "ZR_ERR_WORKSPACE: workspace too small or misaligned";
     case ZR_ERR_CUDA: return "ZR_ERR_CUDA: CUDA call or kernel launch failed";
+    case ZR_ERR_MEMORY: return "ZR_ERR_MEMORY: no host memory for the call's lists";
     default: return "unknown zr status";
   }
 }

@@ -13,6 +13,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
+#include <memory>
+#include <vector>
+
 #include "../../include/zr.h"
 
 namespace {
@@ -307,10 +311,201 @@ PyObject* linear_xent_bwd(PyObject* const* a, Py_ssize_t n) {
   return result(rc, gx, gw);
 }
 
+// part, interleaved, base, factor, original, low, high, magnitude -> the plan's bytes
+PyObject* rotary_plan(PyObject* const* a, Py_ssize_t n) {
+  count(n, 8);
+  zr_rotary plan;
+  const int64_t part = integer(a[0]);
+  const int rc = zr_rotary_plan(part < 0 || part > (1 << 30) ? -1 : int32_t(part), PyObject_IsTrue(a[1]) == 1, real(a[2]),
+                                real(a[3]), real(a[4]), real(a[5]), real(a[6]), real(a[7]), &plan);
+  if (rc) return PyLong_FromLong(rc);
+  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&plan), sizeof plan);
+}
+
+// x, plan, positions, start, out, backward -> out
+PyObject* rotary(PyObject* const* a, Py_ssize_t n) {
+  count(n, 6);
+  const Tensor& x = tensor(a[0], "x");
+  if (!PyBytes_Check(a[1]) || PyBytes_GET_SIZE(a[1]) != Py_ssize_t(sizeof(zr_rotary)))
+    fail(PyExc_TypeError, "%s must come from zr_rotary_plan", "plan");
+  zr_rotary plan;
+  std::memcpy(&plan, PyBytes_AS_STRING(a[1]), sizeof plan);
+  const Tensor *positions = maybe(a[2], "positions"), *out = maybe(a[4], "out");
+  const int64_t start = integer(a[3]);
+  const zr_dtype dt = dtype_of({&x, out});
+  zr_index type = ZR_I64;
+  if (positions) {
+    const auto pt = positions->scalar_type();
+    if (pt != at::kLong && pt != at::kInt) fail(PyExc_TypeError, "%s must be int32 or int64", "positions");
+    if (!positions->is_cuda()) fail(PyExc_ValueError, "%s must be a CUDA tensor", "positions");
+    if (x.dim() >= 2) same_shape(*positions, x.sizes().slice(0, x.dim() - 2), "positions");
+    type = pt == at::kLong ? ZR_I64 : ZR_I32;
+  }
+  const Tensor y = output(out, x.sizes(), x, "out");
+  const int rc = (a[5] == Py_True ? zr_rotary_bwd : zr_rotary_fwd)(dt, desc(x), &plan, type, desc(positions), start,
+                                                                   y.data_ptr(), y.strides().data(), stream_of(x));
+  return result(rc, y);
+}
+
+// The items of a list or tuple.
+struct Items {
+  PyObject* fast;
+  Items(PyObject* o, const char* what) : fast(PySequence_Fast(o, what)) {
+    if (!fast) throw Failed();
+  }
+  Items(const Items&) = delete;
+  ~Items() { Py_DECREF(fast); }
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(fast); }
+  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast, i); }
+};
+
+// The data of a contiguous CUDA tensor of `numel` elements on `like`'s device.
+void* flat(const Tensor& t, at::ScalarType dt, int64_t numel, const Tensor& like, const char* what) {
+  if (t.scalar_type() != dt) {
+    PyErr_Format(PyExc_TypeError, "%s must be %s", what, c10::toString(dt));
+    throw Failed();
+  }
+  if (!t.is_cuda() || t.device() != like.device()) fail(PyExc_ValueError, "%s must be CUDA tensors of one device", what);
+  if (t.numel() != numel) fail(PyExc_ValueError, "%s has the wrong number of elements", what);
+  if (!t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", what);
+  return t.data_ptr();
+}
+void* flat(PyObject* o, at::ScalarType dt, int64_t numel, const Tensor& like, const char* what) {
+  return flat(tensor(o, what), dt, numel, like, what);
+}
+int64_t blocks_of(int64_t n) { return (n + ZR_ADAMW_BLOCK - 1) / ZR_ADAMW_BLOCK; }
+const void* one(PyObject* o, at::ScalarType dt, const Tensor& like, const char* what) {
+  return o == Py_None ? nullptr : flat(o, dt, 1, like, what);
+}
+
+// params, grads, ms, vs, step, lr, beta1, beta2, eps, weight_decay, copies, m_scales, v_scales, seed,
+// device_step, device_lr, grad_scale -> the status
+PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
+  count(n, 17);
+  const Items params(a[0], "params must be a sequence"), grads(a[1], "grads must be a sequence"),
+      ms(a[2], "ms must be a sequence"), vs(a[3], "vs must be a sequence");
+  const Py_ssize_t k = params.size();
+  const auto same = [&](const Items& x, const char* what) {
+    if (x.size() != k) fail(PyExc_ValueError, "%s must have one entry per parameter", what);
+  };
+  const auto optional = [&](PyObject* o, const char* what) {
+    std::unique_ptr<Items> x;
+    if (o != Py_None) {
+      x = std::make_unique<Items>(o, what);
+      same(*x, what);
+    }
+    return x;
+  };
+  same(grads, "grads");
+  same(ms, "ms");
+  same(vs, "vs");
+  const bool decays = !PyNumber_Check(a[9]);
+  const auto wd = decays ? optional(a[9], "weight_decay") : nullptr;
+  const double decay = decays ? 0 : real(a[9]);
+  const auto copies = optional(a[10], "copies"), msc = optional(a[11], "m_scales"), vsc = optional(a[12], "v_scales");
+  if (!msc != !vsc) fail(PyExc_ValueError, "%s come together", "m_scales and v_scales");
+  if (k > 0x7FFFFFFF) fail(PyExc_ValueError, "too many tensors%s", "");
+  zr_adamw how{};
+  how.step = integer(a[4]);
+  how.lr = real(a[5]);
+  how.beta1 = real(a[6]);
+  how.beta2 = real(a[7]);
+  how.eps = real(a[8]);
+  how.seed = word(a[13]);
+  std::vector<zr_adamw_tensor> list(size_t(k), zr_adamw_tensor{});
+  auto gt = at::kFloat;
+  const auto st = msc ? at::kByte : at::kFloat;
+  zr_stream_t stream = nullptr;
+  for (Py_ssize_t i = 0; i < k; ++i) {
+    const Tensor& p = tensor(params[i], "params");
+    const Tensor& g = tensor(grads[i], "grads");
+    if (i == 0) {
+      gt = g.scalar_type();
+      if (gt != at::kFloat && gt != at::kBFloat16) fail(PyExc_TypeError, "%s must be float32 or bfloat16", "grads");
+      if (!p.is_cuda()) fail(PyExc_ValueError, "%s must be CUDA tensors", "params");
+      stream = stream_of(p);
+      how.device_step = static_cast<const int64_t*>(one(a[14], at::kLong, p, "device_step"));
+      how.device_lr = static_cast<const float*>(one(a[15], at::kFloat, p, "device_lr"));
+      how.device_grad_scale = static_cast<const float*>(one(a[16], at::kFloat, p, "grad_scale"));
+    }
+    const Tensor& first = tensor(params[0], "params");
+    const int64_t m = p.numel();
+    zr_adamw_tensor& t = list[size_t(i)];
+    t.n = m;
+    t.param = static_cast<float*>(flat(p, at::kFloat, m, first, "params"));
+    t.grad = flat(g, gt, m, first, "grads");
+    t.m = flat(ms[i], st, m, first, "ms");
+    t.v = flat(vs[i], st, m, first, "vs");
+    if (copies && (*copies)[i] != Py_None) t.copy = flat((*copies)[i], at::kBFloat16, m, first, "copies");
+    if (msc) {
+      t.m_scale = static_cast<float*>(flat((*msc)[i], at::kFloat, blocks_of(m), first, "m_scales"));
+      t.v_scale = static_cast<float*>(flat((*vsc)[i], at::kFloat, blocks_of(m), first, "v_scales"));
+    }
+    t.weight_decay = float(wd ? real((*wd)[i]) : decay);
+  }
+  return PyLong_FromLong(zr_adamw_step(gt == at::kBFloat16 ? ZR_BF16 : ZR_F32, msc ? 8 : 32, int32_t(k), list.data(), &how, stream));
+}
+
+// ms, vs, m_scales, v_scales, out (None, or two sequences) -> (m values, v values)
+PyObject* adamw_state(PyObject* const* a, Py_ssize_t n) {
+  count(n, 5);
+  const Items ms(a[0], "ms must be a sequence"), vs(a[1], "vs must be a sequence"),
+      msc(a[2], "m_scales must be a sequence"), vsc(a[3], "v_scales must be a sequence");
+  const Py_ssize_t k = ms.size();
+  if (vs.size() != k || msc.size() != k || vsc.size() != k)
+    fail(PyExc_ValueError, "%s must have as many entries", "vs, m_scales and v_scales");
+  std::unique_ptr<Items> out[2];
+  if (a[4] != Py_None) {
+    const Items both(a[4], "out must hold two sequences");
+    if (both.size() != 2) fail(PyExc_ValueError, "%s must hold two sequences", "out");
+    for (int i = 0; i < 2; ++i) {
+      out[i] = std::make_unique<Items>(both[i], "out must hold two sequences");
+      if (out[i]->size() != k) fail(PyExc_ValueError, "%s must have as many entries", "out");
+    }
+  }
+  std::vector<zr_adamw_tensor> list(size_t(k), zr_adamw_tensor{});
+  std::vector<void*> to[2];
+  std::vector<Tensor> made[2];
+  zr_stream_t stream = nullptr;
+  for (Py_ssize_t i = 0; i < k; ++i) {
+    const Tensor &m = tensor(ms[i], "ms"), &v = tensor(vs[i], "vs"), &first = tensor(ms[0], "ms");
+    if (i == 0) {
+      if (!m.is_cuda()) fail(PyExc_ValueError, "%s must be CUDA tensors", "ms");
+      stream = stream_of(m);
+    }
+    zr_adamw_tensor& t = list[size_t(i)];
+    t.n = m.numel();
+    t.m = flat(m, at::kByte, t.n, first, "ms");
+    t.v = flat(v, at::kByte, t.n, first, "vs");
+    t.m_scale = static_cast<float*>(flat(msc[i], at::kFloat, blocks_of(t.n), first, "m_scales"));
+    t.v_scale = static_cast<float*>(flat(vsc[i], at::kFloat, blocks_of(t.n), first, "v_scales"));
+    for (int j = 0; j < 2; ++j) {
+      made[j].push_back(out[j] ? tensor((*out[j])[i], "out") : empty(m.sizes(), m, at::kBFloat16));
+      to[j].push_back(flat(made[j].back(), at::kBFloat16, t.n, first, "out"));
+    }
+  }
+  const int rc = zr_adamw_state(int32_t(k), list.data(), to[0].data(), to[1].data(), stream);
+  if (rc) return PyLong_FromLong(rc);
+  PyObject* both = PyTuple_New(2);
+  if (!both) throw Failed();
+  for (int j = 0; j < 2; ++j) {
+    PyObject* l = PyList_New(k);
+    if (!l) {
+      Py_DECREF(both);
+      throw Failed();
+    }
+    for (Py_ssize_t i = 0; i < k; ++i) PyList_SET_ITEM(l, i, wrap(made[j][size_t(i)]));
+    PyTuple_SET_ITEM(both, j, l);
+  }
+  return both;
+}
+
 #define ZR_METHOD(F) {#F, reinterpret_cast<PyCFunction>(entry<F>), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ZR_METHOD(layer_norm_fwd),  ZR_METHOD(layer_norm_bwd),
                          ZR_METHOD(dropout_fwd),     ZR_METHOD(dropout_bwd),
                          ZR_METHOD(linear_xent_fwd), ZR_METHOD(linear_xent_bwd),
+                         ZR_METHOD(rotary_plan),     ZR_METHOD(rotary),
+                         ZR_METHOD(adamw_step),      ZR_METHOD(adamw_state),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "zr_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

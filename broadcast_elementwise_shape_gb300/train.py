@@ -104,3 +104,55 @@ def zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction="mean", ignore_in
     wx, ww = want
     return _out(_c().linear_xent_bwd(grad_loss, x, w, labels, lse, _reduction(reduction), ignore_index,
                                      bool(wx), bool(ww), *grads, workspace), "zr_linear_xent_bwd")
+
+
+class RotaryPlan(bytes):
+    """The turning rates of a head's pairs (zr_rotary of include/zr.h)."""
+    __slots__ = ()
+
+
+def zr_rotary_plan(part, base=10000.0, interleaved=False, factor=1.0, original=None, low=1.0, high=32.0,
+                   magnitude=1.0):
+    """The plan of zr_rotary_fwd and zr_rotary_bwd for the first ``part``
+    elements of a head: pair j turns by base^(-2j / part) a position, divided by
+    ``factor``; with ``original`` (the trained length) pairs that turn ``high``
+    times over it are left as they are, those that turn ``low`` times are
+    divided, and those between are blended.  Made once, on the host."""
+    made = _c().rotary_plan(part, interleaved, base, factor, 0.0 if original is None else original, low, high,
+                            magnitude)
+    return RotaryPlan(_out(made, "zr_rotary_plan"))
+
+
+def zr_rotary_fwd(x, plan, positions=None, start=0, out=None):
+    """x [..., H, D] with the pairs of each head turned by their token's
+    position: ``start`` + ``positions`` (int32 or int64, of the leading shape),
+    or ``start`` + the index in the last leading dim.  ``out`` may be a
+    preallocated (strided) tensor of x's shape, or x itself."""
+    return _out(_c().rotary(x, plan, positions, start, out, False), "zr_rotary_fwd")
+
+
+def zr_rotary_bwd(grad_out, plan, positions=None, start=0, grad_x=None):
+    """grad_x of zr_rotary_fwd given grad_out: the turn back."""
+    return _out(_c().rotary(grad_out, plan, positions, start, grad_x, True), "zr_rotary_bwd")
+
+
+def zr_adamw_step(params, grads, ms, vs, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, copies=None,
+                  m_scales=None, v_scales=None, seed=0, device_step=None, device_lr=None, grad_scale=None):
+    """One AdamW step over lists of contiguous tensors, in place: ``params``
+    float32, ``grads`` float32 or bfloat16, the states ``ms`` and ``vs`` float32,
+    or uint8 with ``m_scales`` and ``v_scales`` (float32, one per 256 elements;
+    all zeros at the start).  ``copies`` (bfloat16, entries may be None) get the
+    new parameters.  ``weight_decay`` is one number or one per tensor.  ``seed``
+    draws the rounding of 8-bit states.  ``device_step`` (int64, added to
+    ``step``), ``device_lr`` and ``grad_scale`` (float32) are one element each on
+    the device, read when the kernel runs."""
+    rc = _c().adamw_step(params, grads, ms, vs, step, lr, *betas, eps, weight_decay, copies, m_scales, v_scales, seed,
+                         device_step, device_lr, grad_scale)
+    if rc:
+        raise _zr.ZrError(rc, "zr_adamw_step")
+
+
+def zr_adamw_state(ms, vs, m_scales, v_scales, out=None):
+    """(m values, v values) of 8-bit states as lists of bfloat16 tensors, which
+    hold them exactly.  ``out`` may hold two lists of preallocated ones."""
+    return _out(_c().adamw_state(ms, vs, m_scales, v_scales, out), "zr_adamw_state")

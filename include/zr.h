@@ -86,7 +86,8 @@ typedef enum {
   ZR_ERR_WORKSPACE = -7, /* workspace smaller than required                    */
   ZR_ERR_CUDA = -8,      /* a CUDA call or kernel launch failed                */
   ZR_ERR_DTYPE = -9,     /* unknown element type (the _t entry points)         */
-  ZR_ERR_VALUE = -10     /* a scalar argument is outside its range             */
+  ZR_ERR_VALUE = -10,    /* a scalar argument is outside its range             */
+  ZR_ERR_MEMORY = -11    /* no host memory for the call's own lists (AdamW)    */
 } zr_status;
 
 /*
@@ -527,6 +528,143 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
                        zr_index label_type, zr_tensor labels, int64_t ignore_index,
                        zr_reduction reduction, const float* lse, void* grad_x, void* grad_w,
                        void* workspace, size_t* workspace_bytes, zr_stream_t stream);
+
+/*
+ * Rotary positions: pairs of elements of a head are turned by an angle that
+ * grows with the token's position.
+ *
+ * zr_rotary_plan — the pairs' turning rates; host only, launches nothing.  The
+ * caller keeps the plan and passes it to each call (it goes to the kernel by
+ * value).
+ *   part        elements of a head that are turned, even, 2 to
+ *               2 * ZR_ROTARY_PAIRS; those behind them pass through.
+ *   interleaved 0: element j is paired with j + part / 2; 1: 2j with 2j + 1.
+ *   base        pair j turns by base^(-2j / part) a position; finite, >= 1.
+ *   factor      finite, > 0: the rates are divided by it (a longer context seen
+ *               as if it had the trained length), all of them with original = 0.
+ *   original    the trained length, >= 0: then pairs that turn at least `high`
+ *               times over it keep their rate, those that turn at most `low`
+ *               times are divided, between the two the rate is a blend, linear
+ *               in the count of turns (NTK-by-parts of Peng, Quesnelle, Fan and
+ *               Shippole, "YaRN", 2023).  0 <= low < high, finite.
+ *   magnitude   finite; the turned elements are multiplied by it.
+ * Errors: ZR_ERR_NULL, ZR_ERR_SIZE (part), ZR_ERR_VALUE.
+ *
+ * zr_rotary_fwd — with angle a = position * rate_j:
+ *   out_i = m (x_i cos a - x_k sin a), out_k = m (x_k cos a + x_i sin a)
+ * for each pair (i, k) of each head.
+ *   x           [..., H, D], rank 2 to 8, any strides, D >= part; the leading
+ *               dims count tokens.
+ *   positions   int32 or int64 (position_type) of the leading sizes, any
+ *               strides, negative ones too; data == NULL: `start` plus the index
+ *               in the last leading dim (rank 2: start).  `start` is added to
+ *               given positions too.
+ *   out         x's shape in out_strides (NULL: dense); it may alias x exactly.
+ * zr_rotary_bwd — grad_x given grad_out: the turn by -a, magnitude included.
+ *
+ * Numerics.  The angle is a fraction of a turn in 64-bit fixed point, the
+ * position times the rate modulo 2^64: exact to 2^-52 of a turn per position of
+ * the rate, however far the position.  Sine, cosine and the products are
+ * binary32, a stored element is rounded once.  Errors as zr_binary_fwd, plus
+ * ZR_ERR_DTYPE.
+ */
+#define ZR_ROTARY_PAIRS 256
+typedef struct {
+  int32_t part;
+  int32_t interleaved;
+  float magnitude;
+  int32_t reserved;                 /* 0 */
+  uint64_t turns[ZR_ROTARY_PAIRS];  /* per pair: turns a position, times 2^64 */
+} zr_rotary;
+
+int zr_rotary_plan(int32_t part, int32_t interleaved, double base, double factor, double original,
+                   double low, double high, double magnitude, zr_rotary* plan);
+int zr_rotary_fwd(zr_dtype dtype, zr_tensor x, const zr_rotary* plan, zr_index position_type,
+                  zr_tensor positions, int64_t start, void* out, const int64_t* out_strides,
+                  zr_stream_t stream);
+int zr_rotary_bwd(zr_dtype dtype, zr_tensor grad_out, const zr_rotary* plan, zr_index position_type,
+                  zr_tensor positions, int64_t start, void* grad_x, const int64_t* grad_x_strides,
+                  zr_stream_t stream);
+
+/*
+ * AdamW over many tensors at once (the book's AdamW).  Per element, with
+ * g = grad * grad_scale and t the step:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   param -= lr (weight_decay param + (m / (1 - beta1^t)) /
+ *                (sqrt(v / (1 - beta2^t)) + eps)).
+ *
+ * zr_adamw_step — `count` tensors, each n dense elements:
+ *   param       float, read and written.
+ *   copy        bfloat16, or NULL: the new parameter, rounded once (what the
+ *               forward computes with).
+ *   grad        grad_type; binary32 or bfloat16.
+ *   m, v        state_bits 32: float, read and written.
+ *               state_bits 8: one byte per element, with m_scale and v_scale,
+ *               one float per block of ZR_ADAMW_BLOCK elements (the last block
+ *               may be short); zeros are the state before the first step.
+ *   weight_decay  of this tensor, finite.
+ *   n           >= 0; with states of 8 bits < 2^34 (else ZR_ERR_SIZE).
+ * how:
+ *   lr, beta1, beta2, eps   lr finite, betas in [0, 1), eps finite, >= 0.
+ *   step        t >= 1.
+ *   seed        of the random rounding of 8-bit states.
+ *   device_step, device_lr, device_grad_scale   device memory read when the
+ *               kernel runs, or NULL: added to step (the sum is t, >= 1); used
+ *               instead of lr; 1.  A
+ *               captured graph that advances them goes on training.
+ * No buffer that is written may overlap another (ZR_ERR_LAYOUT).  Errors as
+ * zr_binary_fwd, plus ZR_ERR_DTYPE and ZR_ERR_VALUE.  count = 0, or no
+ * elements: nothing is launched.
+ *
+ * States of 8 bits.  A block's scale is the power of two at or below its
+ * largest magnitude (2^-90 at least).  m is a sign, 4 bits of exponent and 3 of
+ * mantissa, v has no sign and 5 bits of exponent; both fields as in IEEE
+ * formats, subnormals included, with no infinities, and the block's largest is
+ * in the last binade but one: m = scale 2^(E - 14) 1.f, v = scale 2^(E - 30)
+ * 1.f.  A new value is rounded up with the probability of what is cut off.
+ * Rounded to nearest, a v that loses one part in a thousand a step would never
+ * move; rounded so, its mean does.  The draw is 16 bits of word i mod 4 (low
+ * half: m, high half: v) of Philox4x32-10 at counter (i / 4, tensor's index in
+ * the call, t, t >> 32) under the key (seed, seed >> 32).  A block that holds
+ * an infinity or NaN, or a magnitude of 2^127 or more, has the scale NaN, and so
+ * its values from then on.
+ *
+ * zr_adamw_state — the values that 8-bit states stand for, as bfloat16, which
+ * holds them exactly: m_out[k] and v_out[k] of tensors[k], dense (either array,
+ * or any of its pointers, may be NULL).  param, grad and copy are not used.
+ *
+ * Numerics.  Each operation of the formulas is one binary32 operation, in the
+ * order beta1 * m + (1 - beta1) * g, beta2 * v + (1 - beta2) * (g * g),
+ * d = sqrt(v) * (1 - beta2^t)^-1/2 + eps,
+ * param - ((lr * weight_decay) * param + (lr / (1 - beta1^t)) * (m / d)), the
+ * factors computed in binary64 from the step (from device memory: in binary32)
+ * and rounded.
+ */
+#define ZR_ADAMW_BLOCK 256
+typedef struct {
+  float* param;
+  void* copy;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float weight_decay;
+} zr_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint64_t seed;
+  const int64_t* device_step;
+  const float* device_lr;
+  const float* device_grad_scale;
+} zr_adamw;
+
+int zr_adamw_step(zr_dtype grad_type, int32_t state_bits, int32_t count,
+                  const zr_adamw_tensor* tensors, const zr_adamw* how, zr_stream_t stream);
+int zr_adamw_state(int32_t count, const zr_adamw_tensor* tensors, void* const* m_out,
+                   void* const* v_out, zr_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* zr_status_string(int status);
