@@ -19,6 +19,8 @@ Entry points mirror the C names:
   ``zr_dropout_bwd(grad_out, p, seed, offset) -> grad_x``
 * ``zr_linear_xent_fwd(x, w, labels, reduction) -> (loss, lse)`` and
   ``zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction) -> (grad_x, grad_w)``
+* ``zr_attention_fwd(q, k, v, scale, offsets) -> (out, lse, low)`` and
+  ``zr_attention_bwd(grad_out, q, k, v, out, lse, low, scale, offsets) -> (grad_q, grad_k, grad_v)``
 * ``zr_rotary_plan(part, base, ...) -> plan``, ``zr_rotary_fwd(x, plan, positions) -> out`` and
   ``zr_rotary_bwd(grad_out, plan, positions) -> grad_x``
 * ``zr_adamw_step(params, grads, ms, vs, step, lr, ...)`` in place, and
@@ -118,6 +120,9 @@ def lib() -> ctypes.CDLL:
                                          ctypes.c_int64, c_int, vp, vp, vp, szp, vp]
         L.zr_linear_xent_bwd.argtypes = [c_int, vp, ZrTensor, ZrTensor, c_int, ZrTensor,
                                          ctypes.c_int64, c_int, vp, vp, vp, vp, szp, vp]
+        L.zr_attention_fwd.argtypes = [c_int, ZrTensor, ZrTensor, ZrTensor, ctypes.c_float, vp, i32, vp, i64p, vp, vp, vp]
+        L.zr_attention_bwd.argtypes = [c_int, *[ZrTensor] * 5, vp, vp, ctypes.c_float, vp, i32, vp, i64p, vp, i64p, vp,
+                                       i64p, vp, szp, vp]
         rotp, i64 = ctypes.POINTER(ZrRotary), ctypes.c_int64
         L.zr_rotary_plan.argtypes = [i32, i32, *[ctypes.c_double] * 6, rotp]
         L.zr_rotary_fwd.argtypes = [c_int, ZrTensor, rotp, c_int, ZrTensor, i64, vp, i64p, vp]
@@ -131,8 +136,8 @@ def lib() -> ctypes.CDLL:
                   "zr_chain_fwd", "zr_chain_bwd", "zr_binary_bwd_ex", "zr_unary_fwd", "zr_unary_bwd",
                   "zr_binary_fwd_t", "zr_binary_bwd_t", "zr_sum_to_shape_t", "zr_unary_fwd_t",
                   "zr_unary_bwd_t", "zr_layer_norm_fwd", "zr_layer_norm_bwd", "zr_dropout_fwd",
-                  "zr_dropout_bwd", "zr_linear_xent_fwd", "zr_linear_xent_bwd", "zr_rotary_plan",
-                  "zr_rotary_fwd", "zr_rotary_bwd", "zr_adamw_step", "zr_adamw_state"):
+                  "zr_dropout_bwd", "zr_linear_xent_fwd", "zr_linear_xent_bwd", "zr_attention_fwd",
+                  "zr_attention_bwd", "zr_rotary_plan", "zr_rotary_fwd", "zr_rotary_bwd", "zr_adamw_step", "zr_adamw_state"):
             getattr(L, f).restype = c_int
         _lib = L
     return _lib
@@ -406,7 +411,8 @@ def zr_unary_bwd(op, grad_out, x, alpha=1.0, grad_x=None):
 
 # The training operators' binding imports torch; the package itself does not.
 _TRAIN = ("zr_layer_norm_fwd", "zr_layer_norm_bwd", "zr_dropout_fwd", "zr_dropout_bwd",
-          "zr_linear_xent_fwd", "zr_linear_xent_bwd", "zr_rotary_plan", "zr_rotary_fwd", "zr_rotary_bwd",
+          "zr_linear_xent_fwd", "zr_linear_xent_bwd", "zr_attention_fwd", "zr_attention_bwd",
+          "zr_rotary_plan", "zr_rotary_fwd", "zr_rotary_bwd",
           "zr_adamw_step", "zr_adamw_state")
 
 

@@ -1,0 +1,266 @@
+// zr_attn.cu — causal attention: plan and C entry points.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "zr_attn.h"
+#include "zr_checks.h"
+#include "zr_launch.h"
+
+namespace zr {
+namespace {
+
+constexpr float kLog2eHost = 1.4426950408889634f;
+
+struct AttnSet {
+  AttnPlan p;
+  TDesc q, k, v, o, go, gq, gk, gv;
+  int es = 4;
+  bool empty = false;
+  size_t ws = 0;
+};
+
+AttnView view_of(const TDesc& t) {
+  const int n = t.nd;
+  return {t.ptr, n == 4 ? t.stride[0] : 0, t.stride[n - 3], t.stride[n - 2], t.stride[n - 1]};
+}
+
+// Everything that both directions share.  Leaves S->empty where there is
+// nothing to do.
+int plan_attn(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_tensor& v, float scale,
+              const int32_t* offsets, int32_t sequences, AttnSet* S) {
+  if (dtype != ZR_F32 && dtype != ZR_BF16) return ZR_ERR_DTYPE;
+  S->es = dtype == ZR_BF16 ? 2 : 4;
+  AttnPlan& p = S->p;
+  p = AttnPlan{};
+  int rc;
+  if ((rc = read_tensor(q, &S->q)) || (rc = read_tensor(k, &S->k)) || (rc = read_tensor(v, &S->v))) return rc;
+  const int n = S->q.nd;
+  if (n < 3 || n > 4 || S->k.nd != n || S->v.nd != n) return ZR_ERR_RANK;
+  if (offsets && n != 3) return ZR_ERR_RANK;
+  if (sequences < 0) return ZR_ERR_SIZE;
+  if (!std::isfinite(scale)) return ZR_ERR_VALUE;
+  const int64_t* sq = S->q.size;
+  for (int d = 0; d < n; ++d) {
+    if (S->k.size[d] != S->v.size[d]) return ZR_ERR_SHAPE;
+    if (d != n - 2 && S->k.size[d] != sq[d]) return ZR_ERR_SHAPE;
+  }
+  const int64_t B = n == 4 ? sq[0] : 1, T = sq[n - 3], H = sq[n - 2], K = S->k.size[n - 2], D = sq[n - 1];
+  if (H < 1 || K < 1 || H % K != 0 || D < 1) return ZR_ERR_SHAPE;
+  if (D > 256) return ZR_ERR_SIZE;
+  if (reinterpret_cast<uintptr_t>(offsets) % 4) return ZR_ERR_LAYOUT;
+  if (B == 0 || T == 0 || (offsets && sequences == 0)) {
+    S->empty = true;
+    return ZR_OK;
+  }
+  // Rows and tiles of all heads are counted in 31 bits.
+  if (T >= (int64_t(1) << 30) || H >= (int64_t(1) << 20) || B >= (int64_t(1) << 30) ||
+      B * H >= (int64_t(1) << 31) || (T + 127) / 128 * 128 >= (int64_t(1) << 33) / (B * H))
+    return ZR_ERR_SIZE;
+  const int64_t tiles = offsets ? T / 64 + std::min<int64_t>(sequences, T) : (T + 63) / 64 * B;
+  if (tiles >= (int64_t(1) << 31) / H) return ZR_ERR_SIZE;
+  p.offsets = offsets;
+  p.sequences = uint32_t(sequences);
+  p.batch = uint32_t(B);
+  p.tokens = uint32_t(T);
+  p.heads = uint32_t(H);
+  p.kv_heads = uint32_t(K);
+  p.group = uint32_t(H / K);
+  p.dim = uint32_t(D);
+  p.row_pitch = uint32_t((T + 127) / 128 * 128);
+  p.tile_rows = 64;
+  p.slots = uint32_t(tiles);
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2eHost;
+  p.q = view_of(S->q);
+  p.k = view_of(S->k);
+  p.v = view_of(S->v);
+  return ZR_OK;
+}
+
+// A written tensor of `like`'s shape.
+int plan_out(const TDesc& like, void* data, const int64_t* strides, TDesc* t) {
+  const int rc = read_tensor(zr_tensor{data, like.nd, like.size, strides}, t);
+  if (rc) return rc;
+  return data && !non_overlapping(*t) ? ZR_ERR_LAYOUT : ZR_OK;
+}
+
+// 16-byte accesses along the elements.
+bool wide(const TDesc& t, int es) {
+  const int n = t.nd;
+  if (!t.ptr) return true;
+  if (t.size[n - 1] * es % 16 != 0 || (t.size[n - 1] > 1 && t.stride[n - 1] != 1)) return false;
+  if (reinterpret_cast<uintptr_t>(t.ptr) % 16) return false;
+  for (int d = 0; d + 1 < n; ++d)
+    if (t.size[d] > 1 && t.stride[d] * es % 16) return false;
+  return true;
+}
+
+// Whether two tensors whose spans meet share no element: both have unit
+// elements and the same batch and token strides, and within a token's stride
+// their heads lie in separate runs, as the parts of a projection's rows do.
+bool interleaved(const TDesc& x, const TDesc& y, int es) {
+  const int n = x.nd;
+  int64_t run[2], pitch = 0;  // a token's run; tokens are at least this far apart
+  const TDesc* t[2] = {&x, &y};
+  for (int i = 0; i < 2; ++i) {
+    const TDesc& a = *t[i];
+    if (a.size[n - 1] > 1 && a.stride[n - 1] != 1) return false;
+    if (a.size[n - 2] > 1 && a.stride[n - 2] < a.size[n - 1]) return false;
+    run[i] = (a.size[n - 2] - 1) * a.stride[n - 2] + a.size[n - 1];
+  }
+  for (int d = 0; d + 2 < n; ++d) {
+    if (x.size[d] <= 1) continue;
+    if (x.stride[d] != y.stride[d]) return false;
+    pitch = pitch ? std::min(pitch, x.stride[d]) : x.stride[d];
+    // Every other leading dim's stride is a multiple of the smallest.
+  }
+  if (!pitch) return false;
+  for (int d = 0; d + 2 < n; ++d)
+    if (x.size[d] > 1 && x.stride[d] % pitch) return false;
+  const int64_t apart = int64_t(reinterpret_cast<intptr_t>(y.ptr) - reinterpret_cast<intptr_t>(x.ptr));
+  if (apart % es) return false;
+  // Offsets of a token's run modulo the pitch: [0, run x) and [at, at + run y).
+  const int64_t at = ((apart / es) % pitch + pitch) % pitch;
+  return run[0] <= at && at + run[1] <= pitch;
+}
+
+// No written buffer may overlap another, or an input.
+int check_overlaps(const Span* in, int n_in, const Span* out, int n_out) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (overlaps(out[i], in[j])) return ZR_ERR_LAYOUT;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i], out[j])) return ZR_ERR_LAYOUT;
+  }
+  return ZR_OK;
+}
+
+std::string plan_json(const AttnSet& S, const char* kernel) {
+  const AttnPlan& p = S.p;
+  return std::string("{\"kernel\":\"") + kernel + "\",\"tile\":" + std::to_string(p.tile_rows) +
+         ",\"slots\":" + std::to_string(p.slots) + ",\"dim\":" + std::to_string(p.dim) +
+         ",\"workspace\":" + std::to_string(S.ws) + "}";
+}
+
+int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_tensor& v, float scale,
+             const int32_t* offsets, int32_t sequences, void* out, const int64_t* out_strides, void* low,
+             float* lse, zr_stream_t stream) {
+  AttnSet S;
+  int rc = plan_attn(dtype, q, k, v, scale, offsets, sequences, &S);
+  if (rc) return rc;
+  if ((rc = plan_out(S.q, out, out_strides, &S.o))) return rc;
+  if (low && dtype != ZR_BF16) return ZR_ERR_DTYPE;
+  if (S.empty) return ZR_OK;
+  if (!S.q.ptr || !S.k.ptr || !S.v.ptr || !out) return ZR_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(low) % S.es || reinterpret_cast<uintptr_t>(lse) % 4) return ZR_ERR_LAYOUT;
+  AttnPlan& p = S.p;
+  const Span in[] = {span_of(S.q.ptr, S.q.extent, S.es), span_of(S.k.ptr, S.k.extent, S.es),
+                     span_of(S.v.ptr, S.v.extent, S.es), span_of(offsets, int64_t(sequences) + 1, 4)};
+  const Span outs[] = {span_of(out, S.o.extent, S.es), span_of(low, S.q.numel, S.es),
+                       span_of(lse, S.q.numel / p.dim, 4)};
+  if ((rc = check_overlaps(in, 4, outs, 3))) return rc;
+  p.o = view_of(S.o);
+  p.low = low;
+  p.lse = lse;
+  p.vec = wide(S.q, S.es) && wide(S.k, S.es) && wide(S.v, S.es);
+  trace("zr_attention_fwd", [&] { return plan_json(S, "any"); });
+  for (const void* x : {p.q.p, p.k.p, p.v.p, static_cast<const void*>(out), static_cast<const void*>(low),
+                        static_cast<const void*>(lse), static_cast<const void*>(offsets)})
+    if (x && (rc = check_device_ptr(x))) return rc;
+  return cuda_status(launch_attn_any_fwd(S.es, p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, const zr_tensor& k,
+             const zr_tensor& v, const zr_tensor& out, const void* low, const float* lse, float scale,
+             const int32_t* offsets, int32_t sequences, void* grad_q, const int64_t* grad_q_strides,
+             void* grad_k, const int64_t* grad_k_strides, void* grad_v, const int64_t* grad_v_strides,
+             void* workspace, size_t* workspace_bytes, zr_stream_t stream) {
+  if (!workspace_bytes) return ZR_ERR_NULL;
+  AttnSet S;
+  int rc = plan_attn(dtype, q, k, v, scale, offsets, sequences, &S);
+  if (rc) return rc;
+  if ((rc = read_tensor(grad_out, &S.go)) || (rc = read_tensor(out, &S.o))) return rc;
+  for (const TDesc* t : {&S.go, &S.o}) {
+    if (t->nd != S.q.nd) return ZR_ERR_RANK;
+    for (int d = 0; d < t->nd; ++d)
+      if (t->size[d] != S.q.size[d]) return ZR_ERR_SHAPE;
+  }
+  if ((rc = plan_out(S.q, grad_q, grad_q_strides, &S.gq)) || (rc = plan_out(S.k, grad_k, grad_k_strides, &S.gk)) ||
+      (rc = plan_out(S.v, grad_v, grad_v_strides, &S.gv)))
+    return rc;
+  if (low && dtype != ZR_BF16) return ZR_ERR_DTYPE;
+  AttnPlan& p = S.p;
+  const size_t rows = S.empty ? 0 : size_t(p.batch) * p.heads * p.row_pitch;
+  S.ws = 2 * rows * sizeof(float);
+  if (!workspace) {
+    *workspace_bytes = S.ws;
+    return ZR_OK;
+  }
+  if (S.empty || (!grad_q && !grad_k && !grad_v)) return ZR_OK;
+  if (!S.q.ptr || !S.k.ptr || !S.v.ptr || !S.go.ptr || !S.o.ptr || !lse) return ZR_ERR_NULL;
+  if (*workspace_bytes < S.ws || reinterpret_cast<uintptr_t>(workspace) % 16) return ZR_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(low) % S.es || reinterpret_cast<uintptr_t>(lse) % 4) return ZR_ERR_LAYOUT;
+  const Span in[] = {span_of(S.q.ptr, S.q.extent, S.es),   span_of(S.k.ptr, S.k.extent, S.es),
+                     span_of(S.v.ptr, S.v.extent, S.es),   span_of(S.go.ptr, S.go.extent, S.es),
+                     span_of(S.o.ptr, S.o.extent, S.es),   span_of(low, S.q.numel, S.es),
+                     span_of(lse, S.q.numel / p.dim, 4),   span_of(offsets, int64_t(sequences) + 1, 4)};
+  const Span outs[] = {span_of(grad_q, S.gq.extent, S.es), span_of(grad_k, S.gk.extent, S.es),
+                       span_of(grad_v, S.gv.extent, S.es), span_of(workspace, int64_t(S.ws), 1)};
+  // The gradients may be views that lie between one another, as those of one
+  // projection's rows do: then their spans meet and their elements do not.
+  const TDesc* grads[] = {&S.gq, &S.gk, &S.gv};
+  for (int i = 0; i < 4; ++i)
+    for (const Span& x : in)
+      if (overlaps(outs[i], x)) return ZR_ERR_LAYOUT;
+  for (int i = 0; i < 3; ++i) {
+    if (overlaps(outs[i], outs[3])) return ZR_ERR_LAYOUT;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outs[j]) && !interleaved(*grads[i], *grads[j], S.es)) return ZR_ERR_LAYOUT;
+  }
+  p.go = view_of(S.go);
+  p.o = view_of(S.o);
+  p.gq = view_of(S.gq);
+  p.gk = view_of(S.gk);
+  p.gv = view_of(S.gv);
+  p.low = const_cast<void*>(low);
+  p.lse = const_cast<float*>(lse);
+  p.lse2 = static_cast<float*>(workspace);
+  p.delta = p.lse2 + rows;
+  p.want = (grad_q ? 1u : 0u) | (grad_k ? 2u : 0u) | (grad_v ? 4u : 0u);
+  p.vec = wide(S.q, S.es) && wide(S.k, S.es) && wide(S.v, S.es) && wide(S.go, S.es);
+  trace("zr_attention_bwd", [&] { return plan_json(S, "any"); });
+  for (const void* x : {p.q.p, p.k.p, p.v.p, p.go.p, p.o.p, static_cast<const void*>(low),
+                        static_cast<const void*>(lse), static_cast<const void*>(offsets),
+                        static_cast<const void*>(grad_q), static_cast<const void*>(grad_k),
+                        static_cast<const void*>(grad_v), static_cast<const void*>(workspace)})
+    if (x && (rc = check_device_ptr(x))) return rc;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_attn_rows(S.es, p, st);
+  if (e == cudaSuccess) e = launch_attn_any_bwd(S.es, p, st);
+  return cuda_status(e);
+}
+
+}  // namespace
+}  // namespace zr
+
+extern "C" {
+
+int zr_attention_fwd(zr_dtype dtype, zr_tensor q, zr_tensor k, zr_tensor v, float scale,
+                     const int32_t* offsets, int32_t sequences, void* out, const int64_t* out_strides,
+                     void* low, float* lse, zr_stream_t stream) {
+  return zr::fwd_impl(dtype, q, k, v, scale, offsets, sequences, out, out_strides, low, lse, stream);
+}
+
+int zr_attention_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor q, zr_tensor k, zr_tensor v,
+                     zr_tensor out, const void* low, const float* lse, float scale,
+                     const int32_t* offsets, int32_t sequences, void* grad_q,
+                     const int64_t* grad_q_strides, void* grad_k, const int64_t* grad_k_strides,
+                     void* grad_v, const int64_t* grad_v_strides, void* workspace,
+                     size_t* workspace_bytes, zr_stream_t stream) {
+  return zr::bwd_impl(dtype, grad_out, q, k, v, out, low, lse, scale, offsets, sequences, grad_q, grad_q_strides,
+                      grad_k, grad_k_strides, grad_v, grad_v_strides, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

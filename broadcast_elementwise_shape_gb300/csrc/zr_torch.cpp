@@ -13,6 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstring>
 #include <memory>
 #include <vector>
@@ -311,6 +312,69 @@ PyObject* linear_xent_bwd(PyObject* const* a, Py_ssize_t n) {
   return result(rc, gx, gw);
 }
 
+// The scale argument, D^-1/2 where it is None.
+float scale_of(PyObject* o, const Tensor& q) {
+  if (o != Py_None) return float(real(o));
+  return q.dim() && q.size(-1) > 0 ? float(1.0 / std::sqrt(double(q.size(-1)))) : 1.f;
+}
+struct Offsets {
+  const int32_t* p = nullptr;
+  int32_t sequences = 0;
+};
+Offsets offsets_of(PyObject* o, const Tensor& q) {
+  if (o == Py_None) return {};
+  const Tensor& t = tensor(o, "offsets");
+  if (t.scalar_type() != at::kInt) fail(PyExc_TypeError, "%s must be int32", "offsets");
+  if (!t.is_cuda() || t.device() != q.device()) fail(PyExc_ValueError, "%s must be on the operands' device", "offsets");
+  if (t.dim() != 1 || t.numel() < 1 || t.numel() > (int64_t(1) << 30) || !t.is_contiguous())
+    fail(PyExc_ValueError, "%s must be a contiguous vector of at least one border", "offsets");
+  return {static_cast<const int32_t*>(t.data_ptr()), int32_t(t.numel() - 1)};
+}
+
+// q, k, v, scale, offsets, out, keep_lse, keep_low -> (out, lse, low)
+PyObject* attention_fwd(PyObject* const* a, Py_ssize_t n) {
+  count(n, 8);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+  const Tensor* out = maybe(a[5], "out");
+  const zr_dtype dt = dtype_of({&q, &k, &v, out});
+  const float scale = scale_of(a[3], q);
+  const Offsets off = offsets_of(a[4], q);
+  const Tensor y = output(out, q.sizes(), q, "out");
+  Tensor lse, low;
+  if (PyObject_IsTrue(a[6]) == 1) lse = empty(q.dim() ? q.sizes().slice(0, q.dim() - 1) : q.sizes(), q, at::kFloat);
+  if (PyObject_IsTrue(a[7]) == 1 && dt == ZR_BF16) low = empty(q.sizes(), q, at::kBFloat16);
+  const int rc = zr_attention_fwd(dt, desc(q), desc(k), desc(v), scale, off.p, off.sequences, y.data_ptr(),
+                                  y.strides().data(), ptr(low), static_cast<float*>(ptr(lse)), stream_of(q));
+  return result(rc, y, lse, low);
+}
+
+// grad_out, q, k, v, out, lse, low, scale, offsets, want_q, want_k, want_v, grad_q, grad_k, grad_v,
+// workspace -> (grad_q, grad_k, grad_v)
+PyObject* attention_bwd(PyObject* const* a, Py_ssize_t n) {
+  count(n, 16);
+  const Tensor &g = tensor(a[0], "grad_out"), &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  const Tensor& o = tensor(a[4], "out");
+  const Tensor *low = maybe(a[6], "low"), *oq = maybe(a[12], "grad_q"), *ok = maybe(a[13], "grad_k"), *ov = maybe(a[14], "grad_v");
+  const Tensor* ws = maybe(a[15], "workspace");
+  const zr_dtype dt = dtype_of({&q, &k, &v, &g, &o, low, oq, ok, ov});
+  const float* lse = stats(a[5], q.dim() ? q.sizes().slice(0, q.dim() - 1) : q.sizes(), "lse");
+  if (low) dense(*low, q.sizes(), "low");
+  const float scale = scale_of(a[7], q);
+  const Offsets off = offsets_of(a[8], q);
+  Tensor gq, gk, gv;
+  if (oq || a[9] == Py_True) gq = output(oq, q.sizes(), q, "grad_q");
+  if (ok || a[10] == Py_True) gk = output(ok, k.sizes(), q, "grad_k");
+  if (ov || a[11] == Py_True) gv = output(ov, v.sizes(), q, "grad_v");
+  const auto strides = [](const Tensor& t) { return t.defined() ? t.strides().data() : nullptr; };
+  const zr_stream_t st = stream_of(q);
+  const int rc = with_workspace(ws, q, [&](void* w, size_t* bytes) {
+    return zr_attention_bwd(dt, desc(g), desc(q), desc(k), desc(v), desc(o), low ? low->data_ptr() : nullptr, lse,
+                            scale, off.p, off.sequences, ptr(gq), strides(gq), ptr(gk), strides(gk), ptr(gv),
+                            strides(gv), w, bytes, st);
+  });
+  return result(rc, gq, gk, gv);
+}
+
 // part, interleaved, base, factor, original, low, high, magnitude -> the plan's bytes
 PyObject* rotary_plan(PyObject* const* a, Py_ssize_t n) {
   count(n, 8);
@@ -504,6 +568,7 @@ PyObject* adamw_state(PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {ZR_METHOD(layer_norm_fwd),  ZR_METHOD(layer_norm_bwd),
                          ZR_METHOD(dropout_fwd),     ZR_METHOD(dropout_bwd),
                          ZR_METHOD(linear_xent_fwd), ZR_METHOD(linear_xent_bwd),
+                         ZR_METHOD(attention_fwd),   ZR_METHOD(attention_bwd),
                          ZR_METHOD(rotary_plan),     ZR_METHOD(rotary),
                          ZR_METHOD(adamw_step),      ZR_METHOD(adamw_state),
                          {nullptr, nullptr, 0, nullptr}};

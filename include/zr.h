@@ -530,6 +530,64 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
                        void* workspace, size_t* workspace_bytes, zr_stream_t stream);
 
 /*
+ * Causal attention (the book's fused attention, whose backward computes the
+ * scores again): with query head h reading key and value head h * K / H,
+ *   s_ij = scale * q_i . k_j for the tokens j <= i of i's own sequence,
+ *   lse_i = log(sum over j of exp(s_ij)), p_ij = exp(s_ij - lse_i),
+ *   out_i = sum over j of p_ij v_j.
+ *
+ * zr_attention_fwd
+ *   q           [B, T, H, D], or [T, H, D], any strides; 1 <= D <= 256.
+ *   k, v        the same with K heads, H a multiple of K.
+ *   offsets     NULL: each batch entry is one sequence of T tokens.  Otherwise
+ *               (rank 3) device memory, `sequences` + 1 int32, read when the
+ *               kernel runs: sequence i is the tokens [offsets[i],
+ *               offsets[i + 1]).  They do not decrease and lie in [0, T]; what
+ *               lies outside is cut off, and where they decrease results are
+ *               unspecified (no access leaves the tensors).  Rows in no sequence are
+ *               left as they were.
+ *   out         q's shape in out_strides (NULL: dense).
+ *   low         ZR_BF16: out's rounding error, dense in q's shape, for the
+ *               backward; or NULL.
+ *   lse         float per (token, head), dense in the order of q's leading
+ *               dims, for the backward; or NULL.
+ *
+ * zr_attention_bwd — with delta_i = sum over the elements of grad_out_i out_i:
+ *   dp_ij = grad_out_i . v_j,  ds_ij = scale p_ij (dp_ij - delta_i),
+ *   grad_q_i = sum over j of ds_ij k_j, grad_k_j = sum over i of ds_ij q_i,
+ *   grad_v_j = sum over i of p_ij grad_out_i, the last two over the queries of
+ *   all heads that read the head.
+ *   out, low, lse   the forward's.  low may be NULL: delta then carries out's
+ *               rounding, which shows in the gradients of rows whose weight is
+ *               almost all on one token.
+ *   grad_q, grad_k, grad_v   of q's, k's and v's shape in their strides (NULL:
+ *               dense), any of them NULL: not wanted.  They may be parts of one
+ *               projection's rows [.., T, H + 2 K, D].
+ *   workspace   NULL queries the size (8 bytes per row of T rounded up to 128,
+ *               for each batch entry and head); 16-byte aligned.
+ *
+ * Numerics.  Scores, sums and statistics are binary32, gradients are summed in
+ * a fixed order (no atomics), results are rounded once.  ZR_F32: products of
+ * binary32 multiply-adds.  ZR_BF16 on the tensor cores (D <= 128, a multiple of
+ * 8, 16-byte aligned rows): products accumulate in binary32, weights and ds are
+ * rounded to bfloat16 as operands.  A token whose q, k or v holds an infinity or
+ * NaN makes NaN of rows that see it, and may of others of its sequence; never of another
+ * sequence's.
+ * Sizes: T < 2^30 (else ZR_ERR_SIZE); ranks differ or offsets with rank 4:
+ * ZR_ERR_RANK.  Outputs overlap no input.  Errors as zr_binary_bwd, plus
+ * ZR_ERR_DTYPE (low with ZR_F32 too) and ZR_ERR_VALUE (scale not finite).
+ */
+int zr_attention_fwd(zr_dtype dtype, zr_tensor q, zr_tensor k, zr_tensor v, float scale,
+                     const int32_t* offsets, int32_t sequences, void* out, const int64_t* out_strides,
+                     void* low, float* lse, zr_stream_t stream);
+int zr_attention_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor q, zr_tensor k, zr_tensor v,
+                     zr_tensor out, const void* low, const float* lse, float scale,
+                     const int32_t* offsets, int32_t sequences, void* grad_q,
+                     const int64_t* grad_q_strides, void* grad_k, const int64_t* grad_k_strides,
+                     void* grad_v, const int64_t* grad_v_strides, void* workspace,
+                     size_t* workspace_bytes, zr_stream_t stream);
+
+/*
  * Rotary positions: pairs of elements of a head are turned by an angle that
  * grows with the token's position.
  *
