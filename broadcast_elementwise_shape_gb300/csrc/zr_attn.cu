@@ -7,6 +7,7 @@
 #include "zr_attn.h"
 #include "zr_checks.h"
 #include "zr_launch.h"
+#include "zr_maps.h"
 
 namespace zr {
 namespace {
@@ -137,6 +138,41 @@ int check_overlaps(const Span* in, int n_in, const Span* out, int n_out) {
   return ZR_OK;
 }
 
+// What the tensor-core kernels read by TMA: unit elements, rows that start on 16
+// bytes and whose strides are positive multiples of them.
+bool mappable(const TDesc& t, int es) {
+  if (!wide(t, es)) return false;
+  for (int d = 0; d + 1 < t.nd; ++d)
+    if (t.size[d] > 1 && (t.stride[d] <= 0 || t.stride[d] * es >= (int64_t(1) << 40))) return false;
+  return true;
+}
+// The tensor cores take bfloat16 heads of up to 128 elements, and a positive
+// scale: a row's maximum is that of its products.
+bool tensor_cores(const AttnSet& S, float scale) {
+  return S.es == 2 && S.p.dim <= 128 && S.p.dim % 8 == 0 && scale > 0 && mappable(S.q, 2) && mappable(S.k, 2) &&
+         mappable(S.v, 2);
+}
+// Boxes of 64 elements x 128 tokens; what is out of range reads as zero.
+bool tile_map(CUtensorMap* m, const TDesc& t) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const int n = t.nd;
+  const auto stride = [&](int d) { return cuuint64_t(t.size[d] > 1 ? t.stride[d] * 2 : 16); };
+  const cuuint64_t dims[4] = {cuuint64_t(t.size[n - 1]), cuuint64_t(t.size[n - 2]), cuuint64_t(t.size[n - 3]),
+                              cuuint64_t(n == 4 ? t.size[0] : 1)};
+  const cuuint64_t strides[3] = {stride(n - 2), stride(n - 3), n == 4 ? stride(0) : 16};
+  const cuuint32_t box[4] = {64, 1, 128, 1}, step[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<float*>(t.ptr), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Tiles of `rows` rows.
+void set_tiles(AttnPlan* p, uint32_t rows) {
+  p->tile_rows = rows;
+  p->slots = p->offsets ? p->tokens / rows + (p->sequences < p->tokens ? p->sequences : p->tokens)
+                        : (p->tokens + rows - 1) / rows * p->batch;
+}
+
 std::string plan_json(const AttnSet& S, const char* kernel) {
   const AttnPlan& p = S.p;
   return std::string("{\"kernel\":\"") + kernel + "\",\"tile\":" + std::to_string(p.tile_rows) +
@@ -165,11 +201,20 @@ int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_te
   p.low = low;
   p.lse = lse;
   p.vec = wide(S.q, S.es) && wide(S.k, S.es) && wide(S.v, S.es);
-  trace("zr_attention_fwd", [&] { return plan_json(S, "any"); });
+  p.o_wide = wide(S.o, S.es);
+  p.low_wide = reinterpret_cast<uintptr_t>(low) % 16 == 0;
+  const bool tc = tensor_cores(S, scale);
+  if (tc) set_tiles(&p, 256);
+  trace("zr_attention_fwd", [&] { return plan_json(S, tc ? "tensor" : "any"); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, static_cast<const void*>(out), static_cast<const void*>(low),
                         static_cast<const void*>(lse), static_cast<const void*>(offsets)})
     if (x && (rc = check_device_ptr(x))) return rc;
-  return cuda_status(launch_attn_any_fwd(S.es, p, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!tc) return cuda_status(launch_attn_any_fwd(S.es, p, st));
+  AttnMaps maps;
+  if (!tile_map(&maps.q, S.q) || !tile_map(&maps.k, S.k) || !tile_map(&maps.v, S.v)) return ZR_ERR_CUDA;
+  maps.go = maps.q;
+  return cuda_status(launch_attn_fwd(p, maps, st));
 }
 
 int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, const zr_tensor& k,

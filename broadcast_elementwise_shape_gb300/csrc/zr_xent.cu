@@ -25,6 +25,7 @@
 #include "zr_gemm.h"
 #include "zr_kernels.cuh"
 #include "zr_launch.h"
+#include "zr_maps.h"
 
 namespace zr {
 
@@ -941,24 +942,6 @@ int plan_xent(zr_dtype dtype, const zr_tensor& x, const zr_tensor& w, zr_index i
 }
 
 // ------------------------------------------------------------------ launches
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                              CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
 
 // Map of an operand [parts][rows][cols] of bfloat16 (zr_gemm.h): rows `pitch`
 // elements apart that hold whole blocks of 64 columns, parts `part` apart;
