@@ -275,7 +275,11 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   p.delta = p.lse2 + rows;
   p.want = (grad_q ? 1u : 0u) | (grad_k ? 2u : 0u) | (grad_v ? 4u : 0u);
   p.vec = wide(S.q, S.es) && wide(S.k, S.es) && wide(S.v, S.es) && wide(S.go, S.es);
-  trace("zr_attention_bwd", [&] { return plan_json(S, "any"); });
+  p.o_wide = wide(S.o, S.es) && wide(S.go, S.es) && reinterpret_cast<uintptr_t>(low) % 16 == 0;
+  p.g_wide = (wide(S.gq, S.es) ? 1u : 0u) | (wide(S.gk, S.es) ? 2u : 0u) | (wide(S.gv, S.es) ? 4u : 0u);
+  const bool tc = tensor_cores(S, scale) && mappable(S.go, S.es);
+  if (tc) set_tiles(&p, 128);
+  trace("zr_attention_bwd", [&] { return plan_json(S, tc ? "tensor" : "any"); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, p.go.p, p.o.p, static_cast<const void*>(low),
                         static_cast<const void*>(lse), static_cast<const void*>(offsets),
                         static_cast<const void*>(grad_q), static_cast<const void*>(grad_k),
@@ -283,8 +287,12 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
     if (x && (rc = check_device_ptr(x))) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_attn_rows(S.es, p, st);
-  if (e == cudaSuccess) e = launch_attn_any_bwd(S.es, p, st);
-  return cuda_status(e);
+  if (e != cudaSuccess) return ZR_ERR_CUDA;
+  if (!tc) return cuda_status(launch_attn_any_bwd(S.es, p, st));
+  AttnMaps maps;
+  if (!tile_map(&maps.q, S.q) || !tile_map(&maps.k, S.k) || !tile_map(&maps.v, S.v) || !tile_map(&maps.go, S.go))
+    return ZR_ERR_CUDA;
+  return cuda_status(launch_attn_bwd(p, maps, st));
 }
 
 }  // namespace

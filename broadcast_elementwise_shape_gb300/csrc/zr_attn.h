@@ -30,7 +30,8 @@ struct AttnPlan {
   uint32_t tile_rows;        // rows of a tile
   uint32_t want;             // bit 0: grad_q, bits 1 and 2: grad_k, grad_v
   uint32_t vec;              // 16-byte reads of every operand
-  uint32_t o_wide, low_wide; // tensor-core forward: 16-byte stores of o and low
+  uint32_t o_wide, low_wide; // tensor-core forward: 16-byte stores of o and low;
+                             // backward, o_wide: 16-byte reads of o, low and go
   uint32_t g_wide;           // tensor-core backward: bits as `want`, of the gradients
   float scale, scale_log2;   // scale, scale * log2(e)
 };
@@ -105,6 +106,8 @@ cudaError_t launch_attn_any_fwd(int es, const AttnPlan& p, cudaStream_t s);
 // On the tensor cores, bfloat16, dim <= 128 and a multiple of 8; p.tile_rows and
 // p.slots for tiles of 256 queries.
 cudaError_t launch_attn_fwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
+// The same of tiles of 128; after launch_attn_rows.
+cudaError_t launch_attn_bwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
 cudaError_t launch_attn_any_bwd(int es, const AttnPlan& p, cudaStream_t s);
 // lse2 and delta of every row that a sequence holds.
 cudaError_t launch_attn_rows(int es, const AttnPlan& p, cudaStream_t s);

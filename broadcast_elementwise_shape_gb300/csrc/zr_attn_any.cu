@@ -32,6 +32,17 @@ __device__ __forceinline__ float any_load(const __nv_bfloat16* p) { return __bfl
 __device__ __forceinline__ void any_store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void any_store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+__device__ __forceinline__ void rows_load(const float* p, float (&x)[4]) {
+  const float4 w = *reinterpret_cast<const float4*>(p);
+  x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+}
+__device__ __forceinline__ void rows_load(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+}
+
 // ROWS rows from `row0` of a head into shared memory, DP elements each, zero
 // behind the sequence's end and the head's.
 template <typename E, int DP, int ROWS>
@@ -247,29 +258,49 @@ __global__ void __launch_bounds__(kThreads) k_attn_any_fwd(const __grid_constant
   any_write<E, DP>(p, p.o, p.low, t.batch, head, p.heads, t.start, row0, t.len, acc, by);
 }
 
-// delta = sum of grad_out * out, a warp per row and head.
+// delta = sum of grad_out * out, and lse2: eight lanes per row and head, which read
+// 16 bytes each where the tensors allow it.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) k_attn_rows(const __grid_constant__ AttnPlan p) {
   pdl_trigger();
   pdl_wait();
-  const uint32_t lane = threadIdx.x % 32;
-  const uint64_t i = uint64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  const uint32_t lane = threadIdx.x % 8;
+  const uint64_t i = uint64_t(blockIdx.x) * (kThreads / 8) + threadIdx.x / 8;
   const uint64_t n = uint64_t(p.batch) * p.tokens * p.heads;
-  if (i >= n) return;
-  const uint64_t row = i / p.heads;
-  const uint32_t head = uint32_t(i - row * p.heads), b = uint32_t(row / p.tokens), t = uint32_t(row - uint64_t(b) * p.tokens);
+  const bool live = i < n;
+  const uint64_t row = live ? i / p.heads : 0;
+  const uint32_t head = live ? uint32_t(i - row * p.heads) : 0, b = uint32_t(row / p.tokens);
+  const uint32_t t = uint32_t(row - uint64_t(b) * p.tokens);
   const E* o = static_cast<const E*>(p.o.p) + int64_t(b) * p.o.batch + int64_t(t) * p.o.token + int64_t(head) * p.o.head;
   const E* g = static_cast<const E*>(p.go.p) + int64_t(b) * p.go.batch + int64_t(t) * p.go.token + int64_t(head) * p.go.head;
-  const E* l = static_cast<const E*>(p.low) + i * p.dim;
+  const E* l = static_cast<const E*>(p.low) + (live ? i : 0) * p.dim;
+  const bool low = sizeof(E) == 2 && p.low;
   float sum = 0.f;
-  for (uint32_t d = lane; d < p.dim; d += 32) {
-    float x = any_load(o + int64_t(d) * p.o.elem);
-    if (sizeof(E) == 2 && p.low) x += any_load(l + d);
-    sum = __fmaf_rn(x, any_load(g + int64_t(d) * p.go.elem), sum);
+  if (live && p.o_wide) {
+    constexpr uint32_t V = 16 / sizeof(E);
+    for (uint32_t d = lane * V; d < p.dim; d += 8 * V) {
+      float x[V], y[V];
+      rows_load(o + d, x);
+      rows_load(g + d, y);
+      if (low) {
+        float z[V];
+        rows_load(l + d, z);
+#pragma unroll
+        for (uint32_t k = 0; k < V; ++k) x[k] += z[k];
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < V; ++k) sum = __fmaf_rn(x[k], y[k], sum);
+    }
+  } else if (live) {
+    for (uint32_t d = lane; d < p.dim; d += 8) {
+      float x = any_load(o + int64_t(d) * p.o.elem);
+      if (low) x += any_load(l + d);
+      sum = __fmaf_rn(x, any_load(g + int64_t(d) * p.go.elem), sum);
+    }
   }
 #pragma unroll
-  for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  if (lane == 0) {
+  for (int d = 4; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (live && lane == 0) {
     const int64_t at = (int64_t(b) * p.heads + head) * p.row_pitch + t;
     p.delta[at] = sum;
     p.lse2[at] = p.lse[i] * kLog2e;
@@ -445,7 +476,7 @@ cudaError_t launch_attn_any_bwd(int es, const AttnPlan& p, cudaStream_t s) {
 
 cudaError_t launch_attn_rows(int es, const AttnPlan& p, cudaStream_t s) {
   const uint64_t n = uint64_t(p.batch) * p.tokens * p.heads;
-  const unsigned cta = unsigned((n + kThreads / 32 - 1) / (kThreads / 32));
+  const unsigned cta = unsigned((n + kThreads / 8 - 1) / (kThreads / 8));
   return es == 2 ? launch_k(k_attn_rows<__nv_bfloat16>, cta, kThreads, 0, s, p)
                  : launch_k(k_attn_rows<float>, cta, kThreads, 0, s, p);
 }
