@@ -570,7 +570,7 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
  * a fixed order (no atomics), results are rounded once.  ZR_F32: products of
  * binary32 multiply-adds.  ZR_BF16 on the tensor cores (D <= 128, a multiple of
  * 8, 16-byte aligned rows): products accumulate in binary32, weights and ds are
- * rounded to bfloat16 as operands.  A token whose q, k or v holds an infinity or
+ * rounded to bfloat16 as operands, weights below 2^-126 are 0.  A token whose q, k or v holds an infinity or
  * NaN makes NaN of rows that see it, and may of others of its sequence; never of another
  * sequence's.
  * Sizes: T < 2^30 (else ZR_ERR_SIZE); ranks differ or offsets with rank 4:

@@ -9,11 +9,13 @@ tensors: 0), e = 2^-24 and A_ij = |scale| sum |q k|:
 * grad_v: the same of sum p |grad_out|;
 * ds = p (dp - delta): p's factor w, dp's (D + 4) e sum |grad_out v|, delta's: out's own error and (D + 4) e,
   of sum |grad_out| |out|, and where low is not given out's rounding; ds is rounded to u as an operand.
+* Weights below 2^-126 may be taken as 0 (the exponential flushes them): a weight is off by F = 2^-126 besides, which adds
+  F sum |grad_out| to grad_v, and to ds F |scale| (|dp| + |delta|) + F (ds itself may flush).
 The tensor core truncates where it adds, at most 2 e per 16 terms, which (D + 4) e and (T + 4) e cover.
 """
 import torch
 
-E = 2.0 ** -24
+E, F = 2.0 ** -24, 2.0 ** -126
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
 
 
@@ -49,12 +51,13 @@ def heads(q, k, v, scale, go, u, rows_low):
         o_size = (go.abs() * out.abs()).sum(-1, keepdim=True)
         e_delta = (go.abs() * raw).sum(-1, keepdim=True) + (d + 4) * E * o_size + rows_low * o_size
         e_ds = abs(scale) * p * (w[..., None] * (dp.abs() + delta.abs()) + (1 + w[..., None]) * ((d + 4) * E * size + e_delta) + 4 * E * (dp.abs() + delta.abs()))
+        e_ds = e_ds + F * (abs(scale) * (dp.abs() + delta.abs()) + 1).masked_fill(mask, 0)
         e_ds = e_ds + (u + 2 * E) * (ds.abs() + e_ds)
         fold = lambda x: x.unflatten(0, (-1, g)).sum(1)  # noqa: E731
         val |= {"gq": ds @ k, "gk": fold(ds.transpose(1, 2) @ q), "gv": fold(p.transpose(1, 2) @ go)}
         n = (t * g + 4) * E
         off |= {"gq": e_ds @ k.abs() + n * (ds.abs() @ k.abs()), "gk": fold(e_ds.transpose(1, 2) @ q.abs() + n * (ds.abs().transpose(1, 2) @ q.abs())),
-                "gv": fold(((u + n + w[..., None]) * p).transpose(1, 2) @ go.abs())}
+                "gv": fold(((u + n + w[..., None]) * p + F * ~mask).transpose(1, 2) @ go.abs())}
     turn = lambda x: x.transpose(0, 1)  # noqa: E731
     return {n: turn(x) for n, x in val.items()}, {n: turn(x) for n, x in off.items()}
 
