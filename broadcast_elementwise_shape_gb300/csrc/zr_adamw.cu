@@ -98,13 +98,23 @@ __device__ __forceinline__ uint32_t adam_find(const AdamPlan<N>& p) {
   return lo;
 }
 
+// The root and the quotient are the hardware's approximate ones, within 2^-22: of
+// the update, which is small beside the parameter, 2^-22 is far below the
+// parameter's own rounding, and the exact forms take a quarter of the 8-bit
+// step's instructions, which bound it.  (The states, whose codes depend on every bit,
+// use neither.)
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ void adam_one(float& param, float& m, float& v, float g, const AdamFactors& f,
                                          float b1, float c1, float b2, float c2, float eps) {
   g = __fmul_rn(g, f.grad);
   m = __fadd_rn(__fmul_rn(b1, m), __fmul_rn(c1, g));
   v = __fadd_rn(__fmul_rn(b2, v), __fmul_rn(c2, __fmul_rn(g, g)));
-  const float d = __fadd_rn(__fmul_rn(__fsqrt_rn(v), f.root), eps);
-  param = __fsub_rn(param, __fadd_rn(__fmul_rn(f.decay, param), __fmul_rn(f.rate, __fdiv_rn(m, d))));
+  const float d = __fadd_rn(__fmul_rn(sqrt_approx(v), f.root), eps);
+  param = __fsub_rn(param, __fadd_rn(__fmul_rn(f.decay, param), __fmul_rn(f.rate, __fmul_rn(m, rcp_approx(d)))));
 }
 
 // The scale of a block whose largest magnitude has the pattern `top`, and its
@@ -267,7 +277,7 @@ __device__ __forceinline__ void adam_block(const AdamPlan<N>& p, const AdamTenso
 }
 
 template <typename G, int BITS, int N>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ AdamPlan<N> p) {
+__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ AdamPlan<N> p) {
   __shared__ __align__(16) uint32_t s_words[BITS == 8 ? kAdamRun : 4];
   pdl_trigger();
   const uint32_t i = adam_find(p);
@@ -302,16 +312,26 @@ __global__ void __launch_bounds__(kThreads) k_adamw_state(const __grid_constant_
     if (!out) continue;
     const uint8_t* in = static_cast<const uint8_t*>(which ? t.v : t.m) + at;
     const float s = (which ? t.v_scale : t.m_scale)[at / ZR_ADAMW_BLOCK];
-    const bool wide = ((reinterpret_cast<uintptr_t>(out) * 2 | reinterpret_cast<uintptr_t>(in) * 4) % 16) == 0;
-    uint8_t c[8];
-    uint16_t o[8];
-    if (wide) adam_load<uint8_t, 4>(in, n, lane, c);
-    else adam_load<uint8_t, 1>(in, n, lane, c);
+    const auto value = [&](uint32_t c) {
+      return uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(which ? adam_v(c, s) : adam_m(c, s))));
+    };
+    if (n == 256 && (reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(in) * 2) % 16 == 0) {
+      const uint2 c = *reinterpret_cast<const uint2*>(in + lane * 8);
+      uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      o[k] = __bfloat16_as_ushort(__float2bfloat16_rn(which ? adam_v(c[k], s) : adam_m(c[k], s)));
-    if (wide) adam_store<uint16_t, 4>(out + at, n, lane, o);
-    else adam_store<uint16_t, 1>(out + at, n, lane, o);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t two = (k < 2 ? c.x : c.y) >> (k % 2 * 16);
+        o[k] = value(two & 255) | value(two >> 8 & 255) << 16;
+      }
+      *reinterpret_cast<uint4*>(out + at + lane * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+      uint8_t c[8];
+      uint16_t o[8];
+      adam_load<uint8_t, 1>(in, n, lane, c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = uint16_t(value(c[k]));
+      adam_store<uint16_t, 1>(out + at, n, lane, o);
+    }
   }
 }
 
@@ -324,9 +344,26 @@ struct AdamSpan {
 // No written buffer may share a byte with another; every buffer is memory that
 // the device addresses.  Sorted, both take one walk; buffers out of one
 // allocation are looked up once (a lookup costs some hundred ns, a call has up
-// to seven buffers a tensor).
+// to seven buffers a tensor).  The buffers of one kind mostly ascend already, as
+// views of one large buffer do, so the sort merges the runs it finds.
 int check_spans(std::vector<AdamSpan>& s) {
-  std::sort(s.begin(), s.end(), [](const AdamSpan& x, const AdamSpan& y) { return x.lo < y.lo; });
+  const auto before = [](const AdamSpan& x, const AdamSpan& y) { return x.lo < y.lo; };
+  std::vector<size_t> run{0};
+  for (size_t i = 1; i < s.size(); ++i)
+    if (before(s[i], s[i - 1])) run.push_back(i);
+  run.push_back(s.size());
+  std::vector<AdamSpan> to(s.size());
+  while (run.size() > 2) {
+    std::vector<size_t> next;
+    for (size_t r = 0; r + 1 < run.size(); r += 2) {
+      const auto from = [&](size_t k) { return s.begin() + std::ptrdiff_t(run[std::min(r + k, run.size() - 1)]); };
+      std::merge(from(0), from(1), from(1), from(2), to.begin() + std::ptrdiff_t(run[r]), before);
+      next.push_back(run[r]);
+    }
+    next.push_back(s.size());
+    run.swap(next);
+    s.swap(to);
+  }
   uintptr_t any = 0, written = 0;
   for (const AdamSpan& x : s) {
     if (x.lo < written || (x.written && x.lo < any)) return ZR_ERR_LAYOUT;
@@ -359,12 +396,11 @@ int check_devices(const std::vector<AdamSpan>& s) {
   return ZR_OK;
 }
 
-bool add_span(std::vector<AdamSpan>& s, const void* p, int64_t n, int es, bool written) {
+void add_span(std::vector<AdamSpan>& s, const void* p, int64_t n, int es, bool written) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  if (lo == 0) return false;
-  s.push_back({lo, lo + uintptr_t(n) * uintptr_t(es), written});
-  return true;
+  if (lo) s.push_back({lo, lo + uintptr_t(n) * uintptr_t(es), written});
 }
+int64_t scales_of(int64_t n) { return (n + ZR_ADAMW_BLOCK - 1) / ZR_ADAMW_BLOCK; }
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
 // Launches `run` for the tensors' elements, kAdamMany tensors at a time.
@@ -423,26 +459,28 @@ int step_impl(zr_dtype grad_type, int32_t state_bits, int32_t count, const zr_ad
   std::vector<AdamSpan> spans;
   list.reserve(size_t(count));
   spans.reserve(size_t(count) * 7 + 3);
+  const int ss = state_bits / 8;
   for (int32_t i = 0; i < count; ++i) {
     const zr_adamw_tensor& t = tensors[i];
     if (t.n < 0 || t.n >= (state_bits == 8 ? int64_t(1) << 34 : kMostElements)) return ZR_ERR_SIZE;
     if (!std::isfinite(t.weight_decay)) return ZR_ERR_VALUE;
     if (t.n == 0) continue;
-    const int ss = state_bits / 8;
-    if (!add_span(spans, t.param, t.n, 4, true) || !add_span(spans, t.grad, t.n, gs, false) ||
-        !add_span(spans, t.m, t.n, ss, true) || !add_span(spans, t.v, t.n, ss, true))
-      return ZR_ERR_NULL;
-    if (t.copy) add_span(spans, t.copy, t.n, 2, true);
-    if (!aligned(t.param, 4) || !aligned(t.grad, gs) || !aligned(t.m, ss) || !aligned(t.v, ss) || !aligned(t.copy, 2))
+    if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scale || !t.v_scale))) return ZR_ERR_NULL;
+    if (!aligned(t.param, 4) || !aligned(t.grad, gs) || !aligned(t.m, ss) || !aligned(t.v, ss) || !aligned(t.copy, 2) ||
+        (state_bits == 8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
       return ZR_ERR_LAYOUT;
-    if (state_bits == 8) {
-      const int64_t blocks = (t.n + ZR_ADAMW_BLOCK - 1) / ZR_ADAMW_BLOCK;
-      if (!add_span(spans, t.m_scale, blocks, 4, true) || !add_span(spans, t.v_scale, blocks, 4, true)) return ZR_ERR_NULL;
-      if (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4)) return ZR_ERR_LAYOUT;
-    }
     const float decay = how->device_lr ? t.weight_decay : float(how->lr * double(t.weight_decay));
     list.push_back({t.param, static_cast<__nv_bfloat16*>(t.copy), t.grad, t.m, t.v, t.m_scale, t.v_scale, t.n,
                     uint32_t(i), decay});
+  }
+  for (const AdamTensor& t : list) add_span(spans, t.param, t.n, 4, true);
+  for (const AdamTensor& t : list) add_span(spans, t.grad, t.n, gs, false);
+  for (const AdamTensor& t : list) add_span(spans, t.m, t.n, ss, true);
+  for (const AdamTensor& t : list) add_span(spans, t.v, t.n, ss, true);
+  for (const AdamTensor& t : list) add_span(spans, t.copy, t.n, 2, true);
+  if (state_bits == 8) {
+    for (const AdamTensor& t : list) add_span(spans, t.m_scale, scales_of(t.n), 4, true);
+    for (const AdamTensor& t : list) add_span(spans, t.v_scale, scales_of(t.n), 4, true);
   }
   if (list.empty()) return ZR_OK;
   if (how->device_step) add_span(spans, how->device_step, 1, 8, false);
@@ -498,18 +536,21 @@ int state_impl(int32_t count, const zr_adamw_tensor* tensors, void* const* m_out
     void* om = m_out ? m_out[i] : nullptr;
     void* ov = v_out ? v_out[i] : nullptr;
     if (t.n == 0 || (!om && !ov)) continue;
-    const int64_t blocks = (t.n + ZR_ADAMW_BLOCK - 1) / ZR_ADAMW_BLOCK;
-    const struct { void* out; const void* code; const float* scale; } part[2] = {{om, t.m, t.m_scale}, {ov, t.v, t.v_scale}};
-    for (const auto& x : part) {
-      if (!x.out) continue;
-      add_span(spans, x.out, t.n, 2, true);
-      if (!add_span(spans, x.code, t.n, 1, false) || !add_span(spans, x.scale, blocks, 4, false)) return ZR_ERR_NULL;
-      if (!aligned(x.out, 2) || !aligned(x.scale, 4)) return ZR_ERR_LAYOUT;
-    }
+    if ((om && (!t.m || !t.m_scale)) || (ov && (!t.v || !t.v_scale))) return ZR_ERR_NULL;
+    if (!aligned(om, 2) || !aligned(ov, 2) || (om && !aligned(t.m_scale, 4)) || (ov && !aligned(t.v_scale, 4)))
+      return ZR_ERR_LAYOUT;
     list.push_back({static_cast<float*>(om), static_cast<__nv_bfloat16*>(ov), nullptr, t.m, t.v, t.m_scale,
                     t.v_scale, t.n, uint32_t(i), 0.f});
   }
   if (list.empty()) return ZR_OK;
+  for (int which = 0; which < 2; ++which) {
+    const auto out = [&](const AdamTensor& t) { return which ? static_cast<void*>(t.copy) : static_cast<void*>(t.param); };
+    for (const AdamTensor& t : list) add_span(spans, out(t), t.n, 2, true);
+    for (const AdamTensor& t : list)
+      if (out(t)) add_span(spans, which ? t.v : t.m, t.n, 1, false);
+    for (const AdamTensor& t : list)
+      if (out(t)) add_span(spans, which ? t.v_scale : t.m_scale, scales_of(t.n), 4, false);
+  }
   int rc = check_spans(spans);
   if (rc) return rc;
   trace("zr_adamw_state", [&] {

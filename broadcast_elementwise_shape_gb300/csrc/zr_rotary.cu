@@ -32,12 +32,13 @@ struct RotPlan {
   Decomp lead;               // a token's offsets
   FastDiv last;              // without positions: size of the last leading dim
   FastDiv per_token;         // items of a token
-  FastDiv per_head;          // items of a head
+  FastDiv per_head;          // places of a head
+  uint32_t heads, share;     // heads; of an item
   int64_t head[2];           // stride of a head: x, out
   int64_t inner[2];          // of an element (element-wise plans)
   uint32_t tokens, tile;     // tokens in all; per CTA
   uint32_t pairs;
-  uint32_t turned;           // items of a head that turn; those behind pass through
+  uint32_t turned;           // places of a head that turn; those behind pass through
   uint32_t i64, interleaved, backward;
   float magnitude;
   uint64_t turns[ZR_ROTARY_PAIRS];
@@ -46,6 +47,7 @@ struct RotPlan {
 namespace {
 
 constexpr uint32_t kRotAngles = 2048;  // (cos, sin) of a tile, 16 KB
+constexpr int kRotHeads = 4;
 
 __device__ __forceinline__ float2 rot_angle(const RotPlan& p, int64_t position, uint32_t pair) {
   const uint64_t turn = uint64_t(position) * p.turns[pair];
@@ -91,12 +93,15 @@ struct RotVec {
   }
 };
 
-// WIDE: an item is 16 bytes of neighbouring pairs (half layout: 16 bytes of each
-// half), V elements.  Otherwise one pair, or one element that passes through.
+// An item is a place in the head and a group of up to kRotHeads heads: its angles
+// are read from shared memory once, and nothing but an addition lies between one
+// head and the next.  WIDE: the place is 16 bytes of neighbouring pairs (half
+// layout: 16 bytes of each half), V elements.  Otherwise one pair, or one element
+// that passes through.
 template <typename E, bool WIDE>
 __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ RotPlan p) {
   constexpr int V = WIDE ? 16 / int(sizeof(E)) : 1;
-  constexpr int U = 4;                      // items in flight per thread
+  constexpr int A = WIDE ? V : 1;           // angles of an item, at most
   extern __shared__ float2 s_angle[];       // [token][pair]
   __shared__ int64_t s_at[2 * 32];
   pdl_trigger();
@@ -123,61 +128,66 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Rot
     s_angle[i] = rot_angle(p, position + p.start, pair);
   }
   __syncthreads();
-  const E* x = static_cast<const E*>(p.x);
-  E* out = static_cast<E*>(p.out);
   const uint32_t total = n * p.per_token.d;
-  for (uint32_t base = threadIdx.x; base < total; base += kThreads * U) {
-    uint4 w[U][2];
-    float f[U][2];
-    int64_t to[U];
-    uint32_t ang[U], kind[U];               // kind: distance to the pair's other half, 0 passes through
+  for (uint32_t i = threadIdx.x; i < total; i += kThreads) {
+    const uint32_t t = fd_div(p.per_token, i), j = i - t * p.per_token.d;
+    const uint32_t group = fd_div(p.per_head, j), k = j - group * p.per_head.d;
+    const uint32_t h0 = group * p.share, heads = p.heads - h0 < p.share ? p.heads - h0 : p.share;
+    const bool turn = k < p.turned;
+    const uint32_t e = WIDE ? (turn || p.interleaved ? k * V : 2 * p.pairs + (k - p.turned) * V)
+                            : (turn ? (p.interleaved ? 2 * k : k) : p.pairs + k);
+    const uint32_t apart = p.interleaved ? 1 : p.pairs;  // from a pair's first element to its second
+    const int64_t si = WIDE ? 1 : p.inner[0], so = WIDE ? 1 : p.inner[1];
+    const E* x = static_cast<const E*>(p.x) + s_at[2 * t] + int64_t(h0) * p.head[0] + int64_t(e) * si;
+    E* out = static_cast<E*>(p.out) + s_at[2 * t + 1] + int64_t(h0) * p.head[1] + int64_t(e) * so;
+    float2 angle[A];
+    if (turn) {
+      const float2* from = s_angle + t * p.pairs + (WIDE ? (p.interleaved ? k * (V / 2) : k * V) : k);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t i = base + u * kThreads;
-      if (i >= total) continue;
-      const uint32_t t = fd_div(p.per_token, i), j = i - t * p.per_token.d;
-      const uint32_t h = fd_div(p.per_head, j), k = j - h * p.per_head.d;
-      const bool turn = k < p.turned;
-      const int64_t from = s_at[2 * t] + int64_t(h) * p.head[0];
-      to[u] = s_at[2 * t + 1] + int64_t(h) * p.head[1];
+      for (int a = 0; a < A; ++a)
+        if (!WIDE || a < V / 2 || !p.interleaved) angle[a] = from[a];
+    }
+    uint4 w[kRotHeads][2];
+    float f[kRotHeads][2];
+    const bool both = turn && (!WIDE || !p.interleaved);
+#pragma unroll
+    for (int u = 0; u < kRotHeads; ++u) {
+      if (uint32_t(u) >= heads) continue;
+      const E* from = x + u * p.head[0];
       if constexpr (WIDE) {
-        const uint32_t e = turn || p.interleaved ? k * V : 2 * p.pairs + (k - p.turned) * V;
-        ang[u] = t * p.pairs + (p.interleaved ? k * (V / 2) : k * V);
-        kind[u] = turn ? (p.interleaved ? 1 : p.pairs) : 0;
-        to[u] += e;
-        w[u][0] = *reinterpret_cast<const uint4*>(x + from + e);
-        if (turn && !p.interleaved) w[u][1] = *reinterpret_cast<const uint4*>(x + from + e + p.pairs);
+        w[u][0] = *reinterpret_cast<const uint4*>(from);
+        if (both) w[u][1] = *reinterpret_cast<const uint4*>(from + apart);
       } else {
-        const uint32_t e = turn ? (p.interleaved ? 2 * k : k) : p.pairs + k;
-        ang[u] = t * p.pairs + k;
-        kind[u] = turn ? (p.interleaved ? 1 : p.pairs) : 0;
-        to[u] += int64_t(e) * p.inner[1];
-        f[u][0] = ld1(x + from + int64_t(e) * p.inner[0], false);
-        if (turn) f[u][1] = ld1(x + from + int64_t(e + kind[u]) * p.inner[0], false);
+        f[u][0] = ld1(from, false);
+        if (both) f[u][1] = ld1(from + apart * si, false);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (base + u * kThreads >= total) continue;
+    for (int u = 0; u < kRotHeads; ++u) {
+      if (uint32_t(u) >= heads) continue;
+      E* to = out + u * p.head[1];
       if constexpr (WIDE) {
         RotVec<E, V> a, b;
-        a.unpack(w[u][0]);
-        if (kind[u] && p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) rot_turn(a.v[2 * i], a.v[2 * i + 1], s_angle[ang[u] + i]);
-        } else if (kind[u]) {
+        if (both) {
+          a.unpack(w[u][0]);
           b.unpack(w[u][1]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) rot_turn(a.v[i], b.v[i], s_angle[ang[u] + i]);
-          *reinterpret_cast<uint4*>(out + to[u] + kind[u]) = b.pack();
+          for (int v = 0; v < V; ++v) rot_turn(a.v[v], b.v[v], angle[v]);
+          *reinterpret_cast<uint4*>(to + apart) = b.pack();
+          w[u][0] = a.pack();
+        } else if (turn) {
+          a.unpack(w[u][0]);
+#pragma unroll
+          for (int v = 0; v < V / 2; ++v) rot_turn(a.v[2 * v], a.v[2 * v + 1], angle[v]);
+          w[u][0] = a.pack();
         }
-        *reinterpret_cast<uint4*>(out + to[u]) = kind[u] ? a.pack() : w[u][0];
+        *reinterpret_cast<uint4*>(to) = w[u][0];
       } else {
-        if (kind[u]) {
-          rot_turn(f[u][0], f[u][1], s_angle[ang[u]]);
-          st1(out + to[u] + int64_t(kind[u]) * p.inner[1], f[u][1]);
+        if (both) {
+          rot_turn(f[u][0], f[u][1], angle[0]);
+          st1(to + apart * so, f[u][1]);
         }
-        st1(out + to[u], f[u][0]);
+        st1(to, f[u][0]);
       }
     }
   }
@@ -280,11 +290,16 @@ int plan_rotary(zr_dtype dtype, const zr_tensor& x, const zr_rotary* plan, zr_in
   p.turned = wide ? (p.interleaved ? uint32_t(plan->part) : p.pairs) / v : p.pairs;
   const uint32_t per_head = p.turned + uint32_t(D - plan->part) / v;
   if (uint64_t(per_head) * uint64_t(H) >= (uint64_t(1) << 26)) return ZR_ERR_SIZE;
+  // Heads of an item: one where there are few items, for latency, up to four, so
+  // that a thread has that many loads under way and reads its angles once.
+  p.heads = uint32_t(H);
+  const uint64_t items = uint64_t(per_head) * uint64_t(H) * p.tokens;
+  p.share = uint32_t(std::min<uint64_t>(kRotHeads, 1 + items / (kSms * 2 * kThreads)));
   p.per_head = make_fastdiv(per_head);
-  p.per_token = make_fastdiv(per_head * uint32_t(H));
-  // Tokens of a CTA: eight items a thread, but no fewer CTAs than four a SM, at
-  // most 32 tokens, and their angles in 16 KB.
-  uint32_t tile = (8 * kThreads + p.per_token.d - 1) / p.per_token.d;
+  p.per_token = make_fastdiv(per_head * ((p.heads + p.share - 1) / p.share));
+  // Tokens of a CTA: two items a thread, but no fewer CTAs than four a SM, at most
+  // 32 tokens, and their angles in 16 KB.
+  uint32_t tile = (2 * kThreads + p.per_token.d - 1) / p.per_token.d;
   tile = std::min({tile, 32u, kRotAngles / p.pairs, std::max(1u, p.tokens / (4 * kSms))});
   p.tile = std::max(1u, tile);
   S->n_cta = (p.tokens + p.tile - 1) / p.tile;

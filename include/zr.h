@@ -696,7 +696,7 @@ int zr_rotary_bwd(zr_dtype dtype, zr_tensor grad_out, const zr_rotary* plan, zr_
  * d = sqrt(v) * (1 - beta2^t)^-1/2 + eps,
  * param - ((lr * weight_decay) * param + (lr / (1 - beta1^t)) * (m / d)), the
  * factors computed in binary64 from the step (from device memory: in binary32)
- * and rounded.
+ * and rounded; the root and the quotient are within 2^-22.
  */
 #define ZR_ADAMW_BLOCK 256
 typedef struct {
