@@ -120,7 +120,8 @@ def lib() -> ctypes.CDLL:
                                          ctypes.c_int64, c_int, vp, vp, vp, szp, vp]
         L.zr_linear_xent_bwd.argtypes = [c_int, vp, ZrTensor, ZrTensor, c_int, ZrTensor,
                                          ctypes.c_int64, c_int, vp, vp, vp, vp, szp, vp]
-        L.zr_attention_fwd.argtypes = [c_int, ZrTensor, ZrTensor, ZrTensor, ctypes.c_float, vp, i32, vp, i64p, vp, vp, vp]
+        L.zr_attention_fwd.argtypes = [c_int, ZrTensor, ZrTensor, ZrTensor, ctypes.c_float, vp, i32, vp, i64p, vp, vp, vp,
+                                       szp, vp]
         L.zr_attention_bwd.argtypes = [c_int, *[ZrTensor] * 5, vp, vp, ctypes.c_float, vp, i32, vp, i64p, vp, i64p, vp,
                                        i64p, vp, szp, vp]
         rotp, i64 = ctypes.POINTER(ZrRotary), ctypes.c_int64

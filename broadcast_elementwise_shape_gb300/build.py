@@ -29,7 +29,8 @@ SOURCES = ["zr_api.cu", "zr_plan.cpp", "zr_launch_ew.cu", "zr_launch_red.cu", "z
            "zr_launch_chain.cu", "zr_launch_bf16.cu", "zr_norm.cu", "zr_launch_norm_fwd.cu",
            "zr_launch_norm_bwd.cu", "zr_dropout.cu", "zr_xent.cu", "zr_launch_gemm.cu",
            "zr_rotary.cu", "zr_adamw.cu", "zr_attn.cu", "zr_attn_any.cu",
-           "zr_attn_fwd.cu", "zr_attn_bwd.cu"]
+           "zr_attn_fwd.cu", "zr_attn_bwd.cu",
+           "zr_attn_f32.cu"]
 TORCH_SOURCE = "zr_torch.cpp"
 TORCH_LIB = os.path.join(BUILD, "zr_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
 TORCH_STAMP = os.path.join(BUILD, "zr_torch.version")  # the torch it was built against

@@ -166,6 +166,50 @@ bool tile_map(CUtensorMap* m, const TDesc& t) {
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// binary32 heads that the tensor cores take in parts (zr_attn_f32.cu).
+bool in_parts(const AttnSet& S, float scale) { return S.es == 4 && S.p.dim <= 64 && scale > 0; }
+
+// The parts of q, k, v and (count 4) grad_out behind `at` bytes of workspace.
+struct Parts {
+  uint64_t rows[4];
+  size_t at[4], end;
+};
+Parts parts_of(const AttnPlan& p, int count, size_t at) {
+  Parts x{};
+  for (int i = 0; i < count; ++i) {
+    x.rows[i] = uint64_t(p.batch) * p.tokens * (i == 1 || i == 2 ? p.kv_heads : p.heads);
+    x.at[i] = at = (at + 255) / 256 * 256;
+    at += size_t(x.rows[i]) * 64 * 2 * 3;
+  }
+  x.end = at;
+  return x;
+}
+// Boxes of all three parts of 128 tokens.
+bool part_map(CUtensorMap* m, const AttnPlan& p, void* base, uint64_t rows, uint32_t heads) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[5] = {64, heads, p.tokens, p.batch, 3};
+  const cuuint64_t token = cuuint64_t(heads) * 128;
+  const cuuint64_t strides[4] = {128, token, token * p.tokens, cuuint64_t(rows) * 128};
+  const cuuint32_t box[5] = {64, 1, 128, 1, 3}, step[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Splits the operands and maps their parts.
+cudaError_t split(const AttnSet& S, const Parts& x, int count, void* workspace, AttnMaps* maps, cudaStream_t s) {
+  const AttnPlan& p = S.p;
+  CUtensorMap* m[4] = {&maps->q, &maps->k, &maps->v, &maps->go};
+  const TDesc* t[4] = {&S.q, &S.k, &S.v, &S.go};
+  uint16_t* out[4] = {};
+  uint32_t w = 0;
+  for (int i = 0; i < count; ++i) {
+    out[i] = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + x.at[i]);
+    if (!part_map(m[i], p, out[i], x.rows[i], i == 1 || i == 2 ? p.kv_heads : p.heads)) return cudaErrorInvalidValue;
+    if (wide(*t[i], 4)) w |= 1u << i;
+  }
+  if (count == 3) maps->go = maps->q;
+  return launch_attn_split(p, out, uint32_t(count), w, s);
+}
 // Tiles of `rows` rows.
 void set_tiles(AttnPlan* p, uint32_t rows) {
   p->tile_rows = rows;
@@ -182,21 +226,30 @@ std::string plan_json(const AttnSet& S, const char* kernel) {
 
 int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_tensor& v, float scale,
              const int32_t* offsets, int32_t sequences, void* out, const int64_t* out_strides, void* low,
-             float* lse, zr_stream_t stream) {
+             float* lse, void* workspace, size_t* workspace_bytes, zr_stream_t stream) {
+  if (!workspace_bytes) return ZR_ERR_NULL;
   AttnSet S;
   int rc = plan_attn(dtype, q, k, v, scale, offsets, sequences, &S);
   if (rc) return rc;
   if ((rc = plan_out(S.q, out, out_strides, &S.o))) return rc;
   if (low && dtype != ZR_BF16) return ZR_ERR_DTYPE;
+  const bool parts = !S.empty && in_parts(S, scale);
+  const Parts split_at = parts ? parts_of(S.p, 3, 0) : Parts{};
+  S.ws = split_at.end;
+  if (!workspace) {
+    *workspace_bytes = S.ws;
+    return ZR_OK;
+  }
   if (S.empty) return ZR_OK;
   if (!S.q.ptr || !S.k.ptr || !S.v.ptr || !out) return ZR_ERR_NULL;
+  if (*workspace_bytes < S.ws || reinterpret_cast<uintptr_t>(workspace) % 16) return ZR_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(low) % S.es || reinterpret_cast<uintptr_t>(lse) % 4) return ZR_ERR_LAYOUT;
   AttnPlan& p = S.p;
   const Span in[] = {span_of(S.q.ptr, S.q.extent, S.es), span_of(S.k.ptr, S.k.extent, S.es),
                      span_of(S.v.ptr, S.v.extent, S.es), span_of(offsets, int64_t(sequences) + 1, 4)};
   const Span outs[] = {span_of(out, S.o.extent, S.es), span_of(low, S.q.numel, S.es),
-                       span_of(lse, S.q.numel / p.dim, 4)};
-  if ((rc = check_overlaps(in, 4, outs, 3))) return rc;
+                       span_of(lse, S.q.numel / p.dim, 4), span_of(workspace, int64_t(S.ws), 1)};
+  if ((rc = check_overlaps(in, 4, outs, 4))) return rc;
   p.o = view_of(S.o);
   p.low = low;
   p.lse = lse;
@@ -204,12 +257,18 @@ int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_te
   p.o_wide = wide(S.o, S.es);
   p.low_wide = reinterpret_cast<uintptr_t>(low) % 16 == 0;
   const bool tc = tensor_cores(S, scale);
-  if (tc) set_tiles(&p, 256);
-  trace("zr_attention_fwd", [&] { return plan_json(S, tc ? "tensor" : "any"); });
+  if (tc || parts) set_tiles(&p, 256);
+  trace("zr_attention_fwd", [&] { return plan_json(S, tc ? "tensor" : parts ? "parts" : "any"); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, static_cast<const void*>(out), static_cast<const void*>(low),
-                        static_cast<const void*>(lse), static_cast<const void*>(offsets)})
+                        static_cast<const void*>(lse), static_cast<const void*>(offsets),
+                        static_cast<const void*>(S.ws ? workspace : nullptr)})
     if (x && (rc = check_device_ptr(x))) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (parts) {
+    AttnMaps maps;
+    const cudaError_t e = split(S, split_at, 3, workspace, &maps, st);
+    return cuda_status(e == cudaSuccess ? launch_attn_f32_fwd(p, maps, st) : e);
+  }
   if (!tc) return cuda_status(launch_attn_any_fwd(S.es, p, st));
   AttnMaps maps;
   if (!tile_map(&maps.q, S.q) || !tile_map(&maps.k, S.k) || !tile_map(&maps.v, S.v)) return ZR_ERR_CUDA;
@@ -238,7 +297,9 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   if (low && dtype != ZR_BF16) return ZR_ERR_DTYPE;
   AttnPlan& p = S.p;
   const size_t rows = S.empty ? 0 : size_t(p.batch) * p.heads * p.row_pitch;
-  S.ws = 2 * rows * sizeof(float);
+  const bool parts = !S.empty && in_parts(S, scale);
+  const Parts split_at = parts ? parts_of(p, 4, 2 * rows * sizeof(float)) : Parts{};
+  S.ws = parts ? split_at.end : 2 * rows * sizeof(float);
   if (!workspace) {
     *workspace_bytes = S.ws;
     return ZR_OK;
@@ -278,8 +339,8 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   p.o_wide = wide(S.o, S.es) && wide(S.go, S.es) && reinterpret_cast<uintptr_t>(low) % 16 == 0;
   p.g_wide = (wide(S.gq, S.es) ? 1u : 0u) | (wide(S.gk, S.es) ? 2u : 0u) | (wide(S.gv, S.es) ? 4u : 0u);
   const bool tc = tensor_cores(S, scale) && mappable(S.go, S.es);
-  if (tc) set_tiles(&p, 128);
-  trace("zr_attention_bwd", [&] { return plan_json(S, tc ? "tensor" : "any"); });
+  if (tc || parts) set_tiles(&p, 128);
+  trace("zr_attention_bwd", [&] { return plan_json(S, tc ? "tensor" : parts ? "parts" : "any"); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, p.go.p, p.o.p, static_cast<const void*>(low),
                         static_cast<const void*>(lse), static_cast<const void*>(offsets),
                         static_cast<const void*>(grad_q), static_cast<const void*>(grad_k),
@@ -288,6 +349,11 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_attn_rows(S.es, p, st);
   if (e != cudaSuccess) return ZR_ERR_CUDA;
+  if (parts) {
+    AttnMaps maps;
+    e = split(S, split_at, 4, workspace, &maps, st);
+    return cuda_status(e == cudaSuccess ? launch_attn_f32_bwd(p, maps, st) : e);
+  }
   if (!tc) return cuda_status(launch_attn_any_bwd(S.es, p, st));
   AttnMaps maps;
   if (!tile_map(&maps.q, S.q) || !tile_map(&maps.k, S.k) || !tile_map(&maps.v, S.v) || !tile_map(&maps.go, S.go))
@@ -302,8 +368,9 @@ extern "C" {
 
 int zr_attention_fwd(zr_dtype dtype, zr_tensor q, zr_tensor k, zr_tensor v, float scale,
                      const int32_t* offsets, int32_t sequences, void* out, const int64_t* out_strides,
-                     void* low, float* lse, zr_stream_t stream) {
-  return zr::fwd_impl(dtype, q, k, v, scale, offsets, sequences, out, out_strides, low, lse, stream);
+                     void* low, float* lse, void* workspace, size_t* workspace_bytes, zr_stream_t stream) {
+  return zr::fwd_impl(dtype, q, k, v, scale, offsets, sequences, out, out_strides, low, lse, workspace,
+                      workspace_bytes, stream);
 }
 
 int zr_attention_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor q, zr_tensor k, zr_tensor v,

@@ -109,6 +109,12 @@ cudaError_t launch_attn_fwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_
 // The same of tiles of 128; after launch_attn_rows.
 cudaError_t launch_attn_bwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
 cudaError_t launch_attn_any_bwd(int es, const AttnPlan& p, cudaStream_t s);
+// binary32, dim <= 64: launch_attn_split brings q, k, v (and go; count = 3 or 4)
+// into parts, [part][batch][token][head][64], which the maps are over; wide: bit i, 16-byte
+// reads.  Tiles of 256 queries forward, of 128 backward.
+cudaError_t launch_attn_split(const AttnPlan& p, uint16_t* const* out, uint32_t count, uint32_t wide, cudaStream_t s);
+cudaError_t launch_attn_f32_fwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
+cudaError_t launch_attn_f32_bwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
 // lse2 and delta of every row that a sequence holds.
 cudaError_t launch_attn_rows(int es, const AttnPlan& p, cudaStream_t s);
 

@@ -15,7 +15,7 @@ constexpr uint32_t kAtBlock = kAtRows * 128;  // bytes of 64 elements of its row
 
 // Registers per thread from here on, by a whole warpgroup.  384 threads are
 // launched with 168 each: 216 for two warpgroups and 72 for the third are as
-// many, so the wait for them ends.
+// many (or 200 and 104), so the wait for them ends.
 template <int N>
 __device__ __forceinline__ void regs_give() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -24,7 +24,7 @@ template <int N>
 __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-static_assert(2 * 216 + 72 == 3 * 168, "registers");
+static_assert(2 * 216 + 72 == 3 * 168 && 2 * 200 + 104 == 3 * 168, "registers");
 
 // 64 elements (block * 64 on) of 128 tokens of a head, 128-byte swizzle; tokens
 // and elements out of range read as zero.

@@ -118,11 +118,11 @@ int with_workspace(const Tensor* given, const Tensor& like, F call) {
   Tensor own;
   if (given && (given->scalar_type() != at::kByte || !given->is_cuda() || !given->is_contiguous()))
     fail(PyExc_TypeError, "%s must be a contiguous uint8 CUDA tensor", "workspace");
-  if (!given || size_t(given->numel()) < need) {
+  if (need && (!given || size_t(given->numel()) < need)) {
     own = empty({int64_t(need > 16 ? need : 16)}, like, at::kByte);
     given = &own;
   }
-  size_t bytes = size_t(given->numel());
+  size_t bytes = given ? size_t(given->numel()) : 0;
   // Not NULL even where nothing is needed: that would ask for the size.
   void* ws = bytes ? given->data_ptr() : reinterpret_cast<void*>(uintptr_t(16));
   return call(ws, &bytes);
@@ -331,11 +331,11 @@ Offsets offsets_of(PyObject* o, const Tensor& q) {
   return {static_cast<const int32_t*>(t.data_ptr()), int32_t(t.numel() - 1)};
 }
 
-// q, k, v, scale, offsets, out, keep_lse, keep_low -> (out, lse, low)
+// q, k, v, scale, offsets, out, keep_lse, keep_low, workspace -> (out, lse, low)
 PyObject* attention_fwd(PyObject* const* a, Py_ssize_t n) {
-  count(n, 8);
+  count(n, 9);
   const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
-  const Tensor* out = maybe(a[5], "out");
+  const Tensor *out = maybe(a[5], "out"), *ws = maybe(a[8], "workspace");
   const zr_dtype dt = dtype_of({&q, &k, &v, out});
   const float scale = scale_of(a[3], q);
   const Offsets off = offsets_of(a[4], q);
@@ -343,8 +343,11 @@ PyObject* attention_fwd(PyObject* const* a, Py_ssize_t n) {
   Tensor lse, low;
   if (PyObject_IsTrue(a[6]) == 1) lse = empty(q.dim() ? q.sizes().slice(0, q.dim() - 1) : q.sizes(), q, at::kFloat);
   if (PyObject_IsTrue(a[7]) == 1 && dt == ZR_BF16) low = empty(q.sizes(), q, at::kBFloat16);
-  const int rc = zr_attention_fwd(dt, desc(q), desc(k), desc(v), scale, off.p, off.sequences, y.data_ptr(),
-                                  y.strides().data(), ptr(low), static_cast<float*>(ptr(lse)), stream_of(q));
+  const zr_stream_t st = stream_of(q);
+  const int rc = with_workspace(ws, q, [&](void* w, size_t* bytes) {
+    return zr_attention_fwd(dt, desc(q), desc(k), desc(v), scale, off.p, off.sequences, y.data_ptr(), y.strides().data(),
+                            ptr(low), static_cast<float*>(ptr(lse)), w, bytes, st);
+  });
   return result(rc, y, lse, low);
 }
 

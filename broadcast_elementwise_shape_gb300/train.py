@@ -105,14 +105,16 @@ def zr_linear_xent_bwd(grad_loss, x, w, labels, lse, reduction="mean", ignore_in
     return _out(_c().linear_xent_bwd(grad_loss, x, w, labels, lse, _reduction(reduction), ignore_index,
                                      bool(wx), bool(ww), *grads, workspace), "zr_linear_xent_bwd")
 
-def zr_attention_fwd(q, k, v, scale=None, offsets=None, out=None, keep_lse=True, keep_low=False):
+def zr_attention_fwd(q, k, v, scale=None, offsets=None, out=None, keep_lse=True, keep_low=False,
+                     workspace=None):
     """(out, lse, low) of causal attention: q [B, T, H, D], k and v [B, T, K, D],
     H a multiple of K, or without B, and then with ``offsets`` (int32 on the
     device, one more than there are sequences) for sequences packed one behind
     the other.  ``scale`` is D^-0.5 unless given.  lse [.., T, H] and, of
     bfloat16 tensors, low (what rounding took from out) are for the backward:
     None unless kept.  ``out`` may be a preallocated (strided) tensor."""
-    return _out(_c().attention_fwd(q, k, v, scale, offsets, out, keep_lse, keep_low), "zr_attention_fwd")
+    return _out(_c().attention_fwd(q, k, v, scale, offsets, out, keep_lse, keep_low, workspace),
+                "zr_attention_fwd")
 
 
 def zr_attention_bwd(grad_out, q, k, v, out, lse, low=None, scale=None, offsets=None, want=(True, True, True),

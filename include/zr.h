@@ -563,13 +563,19 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
  *   grad_q, grad_k, grad_v   of q's, k's and v's shape in their strides (NULL:
  *               dense), any of them NULL: not wanted.  They may be parts of one
  *               projection's rows [.., T, H + 2 K, D].
- *   workspace   NULL queries the size (8 bytes per row of T rounded up to 128,
- *               for each batch entry and head); 16-byte aligned.
+ *
+ * workspace (both)  NULL queries the size; 16-byte aligned, contents irrelevant,
+ *               used in stream order.  Backward: 8 bytes per row of T rounded up to
+ *               128, for each batch entry and head.  ZR_F32 with D <= 64: 384 bytes
+ *               per row of q, k, v and (backward) grad_out besides.
  *
  * Numerics.  Scores, sums and statistics are binary32, gradients are summed in
- * a fixed order (no atomics), results are rounded once.  ZR_F32: products of
- * binary32 multiply-adds.  ZR_BF16 on the tensor cores (D <= 128, a multiple of
- * 8, 16-byte aligned rows): products accumulate in binary32, weights and ds are
+ * a fixed order (no atomics), results are rounded once.  ZR_F32 with D <= 64 and
+ * scale > 0 on the tensor cores: each operand, weights and ds among them, is
+ * split into three bfloat16 parts, and a product is the sum of the six products
+ * of parts that reach 2^-24 of it; other ZR_F32 by binary32 multiply-adds.
+ * ZR_BF16 on the tensor cores (D <= 128, a multiple of
+ * 8, 16-byte aligned rows, scale > 0; others as ZR_F32 by multiply-adds): products accumulate in binary32, weights and ds are
  * rounded to bfloat16 as operands, weights below 2^-126 are 0.  A token whose q, k or v holds an infinity or
  * NaN makes NaN of rows that see it, and may of others of its sequence; never of another
  * sequence's.
@@ -579,7 +585,8 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
  */
 int zr_attention_fwd(zr_dtype dtype, zr_tensor q, zr_tensor k, zr_tensor v, float scale,
                      const int32_t* offsets, int32_t sequences, void* out, const int64_t* out_strides,
-                     void* low, float* lse, zr_stream_t stream);
+                     void* low, float* lse, void* workspace, size_t* workspace_bytes,
+                     zr_stream_t stream);
 int zr_attention_bwd(zr_dtype dtype, zr_tensor grad_out, zr_tensor q, zr_tensor k, zr_tensor v,
                      zr_tensor out, const void* low, const float* lse, float scale,
                      const int32_t* offsets, int32_t sequences, void* grad_q,

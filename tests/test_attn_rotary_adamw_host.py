@@ -36,8 +36,18 @@ NONE = ZrTensor(None, 0, None, None)
 def test_attention_forward_refusals(L):
     q, kv = (2, 10, 4, 64), (2, 10, 2, 64)
 
-    def fwd(q=TT(T, q), k=TT(2 * T, kv), v=TT(3 * T, kv), scale=0.1, off=None, n=0, out=4 * T, os=None, low=None, lse=5 * T, dt=BF16):
-        return L.zr_attention_fwd(dt, q.desc, k.desc, v.desc, scale, off, n, out, os, low, lse, None)
+    nb = ctypes.c_size_t(0)
+
+    def fwd(q=TT(T, q), k=TT(2 * T, kv), v=TT(3 * T, kv), scale=0.1, off=None, n=0, out=4 * T, os=None, low=None, lse=5 * T, dt=BF16, ws=8 * T,
+            size=1 << 24):
+        nb.value = size
+        return L.zr_attention_fwd(dt, q.desc, k.desc, v.desc, scale, off, n, out, os, low, lse, ws, ctypes.byref(nb), None)
+
+    need = 384 * 2 * 10 * (4 + 2 + 2)  # three parts of 64 elements per row of q, k and v
+    assert fwd(ws=None) == 0 and nb.value == 0 and fwd(ws=None, dt=F32) == 0 and nb.value == need
+    assert fwd(dt=F32) == DEVICE and fwd(dt=F32, size=need - 1) == WORKSPACE and fwd(dt=F32, ws=8 * T + 8) == WORKSPACE
+    assert fwd(dt=F32, ws=4 * T) == LAYOUT and fwd(ws=16, size=0) == DEVICE
+    assert L.zr_attention_fwd(BF16, TT(T, q).desc, TT(2 * T, kv).desc, TT(3 * T, kv).desc, 0.1, None, 0, 4 * T, None, None, None, None, None, None) == NULL
 
     assert fwd() == DEVICE  # nothing but the addresses is wrong
     assert fwd(dt=5) == DTYPE and fwd(dt=F32, low=6 * T) == DTYPE
