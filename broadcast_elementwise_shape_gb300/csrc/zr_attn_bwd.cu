@@ -9,11 +9,9 @@
 // that weights and their gradients lie in tensor memory as the products need them:
 // as A operands, written over the scores they come from.
 //
-// Warp 16 brings operands by TMA, warp 17 issues, warp 18 brings the rows' lse
-// and delta (k_attn_kv), and four groups of four warps take 32 of a tile's 128
-// columns each, a lane per thread: what they do, not the products, bounds heads
-// of 64, and with two groups of 64 columns a scheduler's two warps waited
-// together.  With s the scores and d the products grad_out . v of a step:
+// Warp 8 brings operands by TMA, warp 9 issues, warp 10 brings the rows' lse and
+// delta (k_attn_kv), and the warps 0-3 and 4-7 take 64 of a tile's 128 columns each, a lane
+// per thread.  With s the scores and d the products grad_out . v of a step:
 //   tensor core:  dV(i) += P(i) dO   s(i+1) | dK(i) += dS(i) Q   d(i+1)
 //   warps:        dS(i) from d(i), P(i)     | P(i+1) from s(i+1)
 // so that both work at all times; in k_attn_q likewise, with s(i+1) as soon as
@@ -25,11 +23,7 @@
 namespace zr {
 namespace {
 
-constexpr int kBwdThreads = 640;
-constexpr uint32_t kWarps = 16;     // that turn scores into weights
-// Registers per thread: 640 threads are launched with 96 each.
-constexpr int kRegsGive = 56, kRegsTake = 104;
-static_assert(4 * kRegsTake + kRegsGive <= 5 * 96, "registers");
+constexpr int kBwdThreads = 384;
 
 template <int DP>
 struct BwdCfg {
@@ -39,20 +33,28 @@ struct BwdCfg {
   static constexpr uint32_t kS = 0, kD = 128, kAcc = 256, kCols = 512;
 };
 
-// W [128, 128] as bfloat16 in four runs of 16 columns, 32 columns apart.
+// W [128, 128] as bfloat16 in two halves of 32 columns, 64 columns apart.
 template <int DP>
 __device__ __forceinline__ void bwd_sum(uint32_t d, uint32_t w, uint32_t b, bool accumulate) {
   const uint64_t db = at_desc(b, true);
 #pragma unroll
   for (uint32_t j = 0; j < kAtRows / 16; ++j)
-    tc_mma_ts(d, w + (j / 2) * 32 + (j % 2) * 8, db + j * (2048 >> 4), at_idesc(DP, true), accumulate || j != 0);
+    tc_mma_ts(d, w + (j / 4) * 64 + (j % 4) * 8, db + j * (2048 >> 4), at_idesc(DP, true), accumulate || j != 0);
 }
 
-__device__ __forceinline__ void bwd_write32(uint32_t addr, const float* v) {
-  uint32_t r[16];
+__device__ __forceinline__ void bwd_read64(uint32_t addr, float* v) {
+  uint32_t r[64];
+  tc_load32_async(addr, r);
+  tc_load32_async(addr + 32, r + 32);
+  tc_wait_load();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  tc_store16(addr, r);
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void bwd_write64(uint32_t addr, const float* v) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  tc_store32(addr, r);
   tc_wait_store();
 }
 // By a whole warp: what it read and wrote in tensor memory is done.
@@ -62,21 +64,20 @@ __device__ __forceinline__ void bwd_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 // The rows of a gradient out of tensor memory, times `by`.
-// Elements [from, from + N).
-template <int N>
+template <int DP>
 __device__ __forceinline__ void bwd_store(const AttnPlan& p, const AttnView& x, uint32_t addr, const AttnTile& t, uint32_t row,
-                                          uint32_t head, float by, bool is_wide, uint32_t from) {
+                                          uint32_t head, float by, bool is_wide) {
   const bool live = row < t.len && x.p != nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(const_cast<void*>(x.p)) + int64_t(t.batch) * x.batch +
                      (int64_t(t.start) + row) * x.token + int64_t(head) * x.head;
 #pragma unroll
-  for (int j = 0; j < N; j += 32) {
+  for (int j = 0; j < DP; j += 32) {
     float v[32];
     __syncwarp();
-    tc_load32(addr + from + j, v);
+    tc_load32(addr + j, v);
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] *= by;
-    if (live) at_store_row(o, x.elem, is_wide, v, from + j, p.dim);
+    if (live) at_store_row(o, x.elem, is_wide, v, j, p.dim);
   }
 }
 
@@ -106,18 +107,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(smem_u32(&s_landed), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_rfull[i]), 1);
-      mbar_init(smem_u32(&s_rempty[i]), kWarps);
+      mbar_init(smem_u32(&s_rempty[i]), 8);
     }
     mbar_init(smem_u32(&s_sfull), 1);
-    mbar_init(smem_u32(&s_pfull), kWarps);
+    mbar_init(smem_u32(&s_pfull), 8);
     mbar_init(smem_u32(&s_dfull), 1);
-    mbar_init(smem_u32(&s_wfull), kWarps);
+    mbar_init(smem_u32(&s_wfull), 8);
     mbar_init(smem_u32(&s_accfull), 1);
-    mbar_init(smem_u32(&s_accempty), kWarps);
+    mbar_init(smem_u32(&s_accempty), 8);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 17) tmem_alloc<1>(smem_u32(&s_tmem), Cfg::kCols);
+  if (warp == 9) tmem_alloc<1>(smem_u32(&s_tmem), Cfg::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -125,19 +126,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t items = p.slots * p.kv_heads;
   pdl_wait();
 
-  if (warp >= kWarps) {
-    regs_give<kRegsGive>();
+  if (warp >= 8) {
+    regs_give<72>();
     const bool leader = elect_one();
     bool ok = true;
     uint32_t n_item = 0, n_step = 0, landed = 0;
-    for (uint32_t round = 0; warp < 19 && ok && round * gridDim.x < items; ++round) {
+    for (uint32_t round = 0; warp < 11 && ok && round * gridDim.x < items; ++round) {
       const uint32_t w = at_item(round);
       if (w >= items) continue;
       const uint32_t slot = w / p.kv_heads, kvh = w - slot * p.kv_heads;
       const AttnTile t = attn_tile(p, slot, true);
       if (!t.live) continue;
       const uint32_t tiles = (t.len + 127) / 128, per = tiles - t.tile, steps = per * p.group;
-      if (warp == 16) {
+      if (warp == 8) {
         ok = warp_wait(smem_u32(&s_kvempty), (n_item & 1) ^ 1, abort);
         if (!ok) break;
         if (leader) {
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ++head;
           }
         }
-      } else if (warp == 17) {
+      } else if (warp == 9) {
         ok = warp_wait(smem_u32(&s_kvfull), n_item & 1, abort);
         auto stage_at = [&](uint32_t i) { return ring + (n_step + i) % S * 2 * kTile; };
         auto scores = [&](uint32_t i) {  // of step i, when its operands are there
@@ -248,8 +249,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ++n_item;
     }
   } else {
-    regs_take<kRegsTake>();
-    const uint32_t part = warp >> 2, quad = warp & 3, mine = quad * 32 + lane;
+    regs_take<216>();
+    const uint32_t half = warp >> 2, quad = warp & 3, mine = quad * 32 + lane;
     const uint32_t lanes = tmem + (quad << 21);
     const F2 c2 = f2_splat(p.scale_log2);
     bool ok = true;
@@ -264,40 +265,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint32_t q = 0;
       for (uint32_t i = 0; i < steps; ++i, ++n_step) {
         const uint32_t stage = n_step & 1;
-        const float* rows = s_rows[stage] + part * 32;
+        const float* rows = s_rows[stage] + half * 64;
         ok = ok && warp_wait(smem_u32(&s_rfull[stage]), (n_step / 2) & 1, abort);
         ok = ok && warp_wait(smem_u32(&s_sfull), n_step & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        float v[32], d[32];
-        tc_load32(lanes + Cfg::kS + part * 32, v);
+        float v[64], d[64];
+        bwd_read64(lanes + Cfg::kS + half * 64, v);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 64; j += 4) {
           const float4 l = *reinterpret_cast<const float4*>(rows + j);
           f2_unpack(f2_fma(f2_pack(v[j], v[j + 1]), c2, f2_pack(l.x, l.y)), v[j], v[j + 1]);
           f2_unpack(f2_fma(f2_pack(v[j + 2], v[j + 3]), c2, f2_pack(l.z, l.w)), v[j + 2], v[j + 3]);
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = ex2(v[j]);
+        for (int j = 0; j < 64; ++j) v[j] = ex2(v[j]);
         if (q == 0) {  // the tile on the diagonal
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (part * 32 + j < mine) v[j] = 0.f;
+          for (int j = 0; j < 64; ++j)
+            if (half * 64 + j < mine) v[j] = 0.f;
         }
-        bwd_write32(lanes + Cfg::kS + part * 32, v);
+        bwd_write64(lanes + Cfg::kS + half * 64, v);
         bwd_arrive(smem_u32(&s_pfull));
         ok = warp_wait(smem_u32(&s_dfull), n_step & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        tc_load32(lanes + Cfg::kD + part * 32, d);
+        bwd_read64(lanes + Cfg::kD + half * 64, d);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 64; j += 4) {
           const float4 l = *reinterpret_cast<const float4*>(rows + 128 + j);
           f2_unpack(f2_mul(f2_add(f2_pack(d[j], d[j + 1]), f2_pack(l.x, l.y)), f2_pack(v[j], v[j + 1])), d[j], d[j + 1]);
           f2_unpack(f2_mul(f2_add(f2_pack(d[j + 2], d[j + 3]), f2_pack(l.z, l.w)), f2_pack(v[j + 2], v[j + 3])), d[j + 2],
                     d[j + 3]);
         }
-        bwd_write32(lanes + Cfg::kD + part * 32, d);
+        bwd_write64(lanes + Cfg::kD + half * 64, d);
         bwd_arrive(smem_u32(&s_wfull));
         if (lane == 0) mbar_arrive(smem_u32(&s_rempty[stage]));
         if (++q == per) q = 0;
@@ -306,11 +307,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ++n_item;
       tc_fence_after();
       const uint32_t row = t.tile * 128 + mine;
-      const uint32_t from = (part & 1) * (DP / 2);
-      if (part < 2)
-        bwd_store<DP / 2>(p, p.gv, lanes + Cfg::kAcc, t, row, kvh, ok ? 1.f : qnan(), p.g_wide & 4, from);
+      if (half == 0)
+        bwd_store<DP>(p, p.gv, lanes + Cfg::kAcc, t, row, kvh, ok ? 1.f : qnan(), p.g_wide & 4);
       else
-        bwd_store<DP / 2>(p, p.gk, lanes + Cfg::kAcc + DP, t, row, kvh, ok ? p.scale : qnan(), p.g_wide & 2, from);
+        bwd_store<DP>(p, p.gk, lanes + Cfg::kAcc + DP, t, row, kvh, ok ? p.scale : qnan(), p.g_wide & 2);
       bwd_arrive(smem_u32(&s_accempty));
     }
   }
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tmem_free<1>(tmem, Cfg::kCols);
+  if (warp == 9) tmem_free<1>(tmem, Cfg::kCols);
 }
 
 // Items: query tiles (as slots) times heads.
@@ -351,15 +351,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     mbar_init(smem_u32(&s_landed), 1);
     mbar_init(smem_u32(&s_sfull), 1);
-    mbar_init(smem_u32(&s_sread), kWarps);
+    mbar_init(smem_u32(&s_sread), 8);
     mbar_init(smem_u32(&s_dfull), 1);
-    mbar_init(smem_u32(&s_wfull), kWarps);
+    mbar_init(smem_u32(&s_wfull), 8);
     mbar_init(smem_u32(&s_accfull), 1);
-    mbar_init(smem_u32(&s_accempty), kWarps);
+    mbar_init(smem_u32(&s_accempty), 8);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 17) tmem_alloc<1>(smem_u32(&s_tmem), Cfg::kCols);
+  if (warp == 9) tmem_alloc<1>(smem_u32(&s_tmem), Cfg::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -367,19 +367,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t items = p.slots * p.heads;
   pdl_wait();
 
-  if (warp >= kWarps) {
-    regs_give<kRegsGive>();
+  if (warp >= 8) {
+    regs_give<72>();
     const bool leader = elect_one();
     bool ok = true;
     uint32_t n_item = 0, n_step = 0, landed = 0;
-    for (uint32_t round = 0; warp < 18 && ok && round * gridDim.x < items; ++round) {
+    for (uint32_t round = 0; warp < 10 && ok && round * gridDim.x < items; ++round) {
       const uint32_t w = at_item(round);
       if (w >= items) continue;
       const uint32_t slot = w / p.heads, head = w - slot * p.heads, kvh = head / p.group;
       const AttnTile t = attn_tile(p, slot, false);
       if (!t.live) continue;
       const uint32_t steps = t.tile + 1;
-      if (warp == 16) {
+      if (warp == 8) {
         ok = warp_wait(smem_u32(&s_qempty), (n_item & 1) ^ 1, abort);
         if (!ok) break;
         if (leader) {
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ++n_item;
     }
   } else {
-    regs_take<kRegsTake>();
-    const uint32_t part = warp >> 2, quad = warp & 3, mine = quad * 32 + lane;
+    regs_take<216>();
+    const uint32_t half = warp >> 2, quad = warp & 3, mine = quad * 32 + lane;
     const uint32_t lanes = tmem + (quad << 21);
     const F2 c2 = f2_splat(p.scale_log2);
     bool ok = true;
@@ -479,33 +479,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ok = ok && warp_wait(smem_u32(&s_sfull), n_step & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        float v[32], d[32];
-        tc_load32(lanes + Cfg::kS + part * 32, v);
+        float v[64], d[64];
+        bwd_read64(lanes + Cfg::kS + half * 64, v);
         bwd_arrive(smem_u32(&s_sread));
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) f2_unpack(f2_fma(f2_pack(v[j], v[j + 1]), c2, lse), v[j], v[j + 1]);
+        for (int j = 0; j < 64; j += 2) f2_unpack(f2_fma(f2_pack(v[j], v[j + 1]), c2, lse), v[j], v[j + 1]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = ex2(v[j]);
+        for (int j = 0; j < 64; ++j) v[j] = ex2(v[j]);
         ok = warp_wait(smem_u32(&s_dfull), n_step & 1, abort);
         if (!ok) break;
         tc_fence_after();
-        tc_load32(lanes + Cfg::kD + part * 32, d);
+        bwd_read64(lanes + Cfg::kD + half * 64, d);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2)
+        for (int j = 0; j < 64; j += 2)
           f2_unpack(f2_mul(f2_add(f2_pack(d[j], d[j + 1]), delta), f2_pack(v[j], v[j + 1])), d[j], d[j + 1]);
         if (i == t.tile) {  // the tile on the diagonal
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (part * 32 + j > mine) d[j] = 0.f;
+          for (int j = 0; j < 64; ++j)
+            if (half * 64 + j > mine) d[j] = 0.f;
         }
-        bwd_write32(lanes + Cfg::kD + part * 32, d);
+        bwd_write64(lanes + Cfg::kD + half * 64, d);
         bwd_arrive(smem_u32(&s_wfull));
       }
       ok = ok && warp_wait(smem_u32(&s_accfull), n_item & 1, abort);
       ++n_item;
       tc_fence_after();
-      if (part < 2)
-        bwd_store<DP / 2>(p, p.gq, lanes + Cfg::kAcc, t, row, head, ok ? p.scale : qnan(), p.g_wide & 1, part * (DP / 2));
+      // Each half stores its share of the elements.
+      const float by = ok ? p.scale : qnan();
+      const bool live = row < t.len;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(const_cast<void*>(p.gq.p)) + int64_t(t.batch) * p.gq.batch +
+                         (int64_t(t.start) + row) * p.gq.token + int64_t(head) * p.gq.head;
+#pragma unroll
+      for (int j = 0; j < DP / 2; j += 32) {
+        float x[32];
+        const uint32_t e = half * (DP / 2) + j;
+        __syncwarp();
+        tc_load32(lanes + Cfg::kAcc + e, x);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] *= by;
+        if (live) at_store_row(o, p.gq.elem, p.g_wide & 1, x, e, p.dim);
+      }
       bwd_arrive(smem_u32(&s_accempty));
     }
   }
@@ -519,7 +532,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 17) tmem_free<1>(tmem, Cfg::kCols);
+  if (warp == 9) tmem_free<1>(tmem, Cfg::kCols);
 }
 
 template <typename K>

@@ -66,6 +66,14 @@ __device__ __forceinline__ void sum_of(uint32_t d, uint32_t s, uint32_t more, ui
       tc_mma_ts(d, weights_at(s, more, pair_of(i, 0), j / 2) + (j % 2) * 8,
                 db + pair_of(i, 1) * (kAtBlock >> 4) + j * (2048 >> 4), at_idesc(64, true), (i | j) != 0);
 }
+__device__ __forceinline__ void tc_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // 32 columns' weights in parts; tc_wait_store() before others read.
 __device__ __forceinline__ void write_parts(uint32_t s, uint32_t more, uint32_t chunk, const float* x) {
   float v[32];
