@@ -55,9 +55,9 @@ int plan_attn(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_t
     S->empty = true;
     return ZR_OK;
   }
-  // Rows and tiles of all heads are counted in 31 bits.
+  // Rows (batch, token, head) and tiles are counted in 31 bits.
   if (T >= (int64_t(1) << 30) || H >= (int64_t(1) << 20) || B >= (int64_t(1) << 30) ||
-      B * H >= (int64_t(1) << 31) || (T + 127) / 128 * 128 >= (int64_t(1) << 33) / (B * H))
+      B * H >= (int64_t(1) << 31) || (T + 127) / 128 * 128 >= (int64_t(1) << 31) / (B * H))
     return ZR_ERR_SIZE;
   const int64_t tiles = offsets ? T / 64 + std::min<int64_t>(sequences, T) : (T + 63) / 64 * B;
   if (tiles >= (int64_t(1) << 31) / H) return ZR_ERR_SIZE;

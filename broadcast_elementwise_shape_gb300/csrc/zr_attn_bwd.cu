@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __shared__ uint64_t s_kvfull, s_kvempty, s_full[S], s_empty[S], s_landed, s_rfull[2], s_rempty[2];
   __shared__ uint64_t s_sfull, s_pfull, s_dfull, s_wfull, s_accfull, s_accempty;
   __shared__ uint32_t s_tmem, s_abort;
-  pdl_trigger();
   const uint32_t warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t sk = (smem_u32(s_raw) + 1023u) & ~1023u, sv = sk + kTile, ring = sv + kTile;
   volatile uint32_t* abort = &s_abort;
@@ -125,6 +124,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = uniform(s_tmem);
   const uint32_t items = p.slots * p.kv_heads;
   pdl_wait();
+  pdl_trigger();  // behind the wait: k_attn_q may start beside this one, the rows are done
 
   if (warp >= 8) {
     regs_give<72>();
@@ -365,7 +365,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(s_tmem);
   const uint32_t items = p.slots * p.heads;
-  pdl_wait();
+  // Behind k_attn_kv, of which nothing here depends, this kernel takes the SMs that
+  // one leaves: by then the rows' kernel, whose results both read, is done (k_attn_kv
+  // has waited for it).  It waits at its end instead, so that whatever comes
+  // next finds both done.
+  const bool beside = p.want & 6;
+  if (!beside) pdl_wait();
 
   if (warp >= 8) {
     regs_give<72>();
@@ -474,7 +479,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!t.live) continue;
       const uint32_t row = t.tile * 128 + mine;
       const int64_t at = (int64_t(t.batch) * p.heads + head) * p.row_pitch + t.start + row;
-      const F2 lse = f2_splat(row < t.len ? -p.lse2[at] : 0.f), delta = f2_splat(row < t.len ? -p.delta[at] : 0.f);
+      const F2 lse = f2_splat(row < t.len ? -__ldcg(p.lse2 + at) : 0.f),
+               delta = f2_splat(row < t.len ? -__ldcg(p.delta + at) : 0.f);
       for (uint32_t i = 0; i <= t.tile; ++i, ++n_step) {
         ok = ok && warp_wait(smem_u32(&s_sfull), n_step & 1, abort);
         if (!ok) break;
@@ -533,6 +539,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_free<1>(tmem, Cfg::kCols);
+  if (beside) pdl_wait();
 }
 
 template <typename K>

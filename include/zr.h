@@ -579,7 +579,8 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
  * rounded to bfloat16 as operands, weights below 2^-126 are 0.  A token whose q, k or v holds an infinity or
  * NaN makes NaN of rows that see it, and may of others of its sequence; never of another
  * sequence's.
- * Sizes: T < 2^30 (else ZR_ERR_SIZE); ranks differ or offsets with rank 4:
+ * Sizes: B times T (rounded up to 128) times H < 2^31, T < 2^30 (else
+ * ZR_ERR_SIZE); ranks differ or offsets with rank 4:
  * ZR_ERR_RANK.  Outputs overlap no input.  Errors as zr_binary_bwd, plus
  * ZR_ERR_DTYPE (low with ZR_F32 too) and ZR_ERR_VALUE (scale not finite).
  */
