@@ -29,7 +29,10 @@ template <int DP>
 struct BwdCfg {
   static constexpr uint32_t kTile = DP / 64 * kAtBlock;
   static constexpr int kStages = DP == 64 ? 3 : 2;  // of two tiles
-  static constexpr uint32_t kSmem = (2 + 2 * kStages) * kTile + 1024;
+  // Room for the tiles that stay: heads of 64 have it for the next item's too, which
+  // arrive while this one is at work.
+  static constexpr int kStay = DP == 64 ? 2 : 1;
+  static constexpr uint32_t kSmem = 2 * (kStay + kStages) * kTile + 1024;
   static constexpr uint32_t kS = 0, kD = 128, kAcc = 256, kCols = 512;
 };
 
@@ -90,15 +93,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr uint32_t kTile = Cfg::kTile;
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(16) float s_rows[2][256];  // -lse2 and -delta of a tile of queries
-  __shared__ uint64_t s_kvfull, s_kvempty, s_full[S], s_empty[S], s_landed, s_rfull[2], s_rempty[2];
+  __shared__ uint64_t s_kvfull[Cfg::kStay], s_kvempty[Cfg::kStay], s_full[S], s_empty[S], s_landed, s_rfull[2], s_rempty[2];
   __shared__ uint64_t s_sfull, s_pfull, s_dfull, s_wfull, s_accfull, s_accempty;
   __shared__ uint32_t s_tmem, s_abort;
   const uint32_t warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const uint32_t sk = (smem_u32(s_raw) + 1023u) & ~1023u, sv = sk + kTile, ring = sv + kTile;
+  const uint32_t stay = (smem_u32(s_raw) + 1023u) & ~1023u, ring = stay + Cfg::kStay * 2 * kTile;
   volatile uint32_t* abort = &s_abort;
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&s_kvfull), 1);
-    mbar_init(smem_u32(&s_kvempty), 1);
+    for (int i = 0; i < Cfg::kStay; ++i) {
+      mbar_init(smem_u32(&s_kvfull[i]), 1);
+      mbar_init(smem_u32(&s_kvempty[i]), 1);
+    }
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_empty[i]), 1);
@@ -138,11 +143,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const AttnTile t = attn_tile(p, slot, true);
       if (!t.live) continue;
       const uint32_t tiles = (t.len + 127) / 128, per = tiles - t.tile, steps = per * p.group;
+      const uint32_t sk = stay + n_item % Cfg::kStay * 2 * kTile, sv = sk + kTile;
       if (warp == 8) {
-        ok = warp_wait(smem_u32(&s_kvempty), (n_item & 1) ^ 1, abort);
+        ok = warp_wait(smem_u32(&s_kvempty[n_item % Cfg::kStay]), ((n_item / Cfg::kStay) & 1) ^ 1, abort);
         if (!ok) break;
         if (leader) {
-          const uint32_t bar = smem_u32(&s_kvfull);
+          const uint32_t bar = smem_u32(&s_kvfull[n_item % Cfg::kStay]);
           mbar_expect(bar, 2 * kTile);
           for (uint32_t b = 0; b < DP / 64; ++b) {
             at_load(sk + b * kAtBlock, &maps.k, bar, b, kvh, t.start + t.tile * 128, t.batch);
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
       } else if (warp == 9) {
-        ok = warp_wait(smem_u32(&s_kvfull), n_item & 1, abort);
+        ok = warp_wait(smem_u32(&s_kvfull[n_item % Cfg::kStay]), (n_item / Cfg::kStay) & 1, abort);
         auto stage_at = [&](uint32_t i) { return ring + (n_step + i) % S * 2 * kTile; };
         auto scores = [&](uint32_t i) {  // of step i, when its operands are there
           ok = ok && warp_wait(smem_u32(&s_full[(n_step + i) % S]), ((n_step + i) / S) & 1, abort);
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_commit<1>(smem_u32(&s_empty[(n_step + i) % S]));
             if (i + 1 == steps) {
               tc_commit<1>(smem_u32(&s_accfull));
-              tc_commit<1>(smem_u32(&s_kvempty));
+              tc_commit<1>(smem_u32(&s_kvempty[n_item % Cfg::kStay]));
             }
           }
           __syncwarp();
@@ -335,16 +341,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr int S = Cfg::kStages;
   constexpr uint32_t kTile = Cfg::kTile;
   extern __shared__ uint8_t s_raw[];
-  __shared__ uint64_t s_qfull, s_qempty, s_full[S], s_empty[S], s_landed;
+  __shared__ uint64_t s_qfull[Cfg::kStay], s_qempty[Cfg::kStay], s_full[S], s_empty[S], s_landed;
   __shared__ uint64_t s_sfull, s_sread, s_dfull, s_wfull, s_accfull, s_accempty;
   __shared__ uint32_t s_tmem, s_abort;
   pdl_trigger();
   const uint32_t warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const uint32_t sq = (smem_u32(s_raw) + 1023u) & ~1023u, sg = sq + kTile, ring = sg + kTile;
+  const uint32_t stay = (smem_u32(s_raw) + 1023u) & ~1023u, ring = stay + Cfg::kStay * 2 * kTile;
   volatile uint32_t* abort = &s_abort;
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&s_qfull), 1);
-    mbar_init(smem_u32(&s_qempty), 1);
+    for (int i = 0; i < Cfg::kStay; ++i) {
+      mbar_init(smem_u32(&s_qfull[i]), 1);
+      mbar_init(smem_u32(&s_qempty[i]), 1);
+    }
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_empty[i]), 1);
@@ -384,11 +392,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const AttnTile t = attn_tile(p, slot, false);
       if (!t.live) continue;
       const uint32_t steps = t.tile + 1;
+      const uint32_t sq = stay + n_item % Cfg::kStay * 2 * kTile, sg = sq + kTile;
       if (warp == 8) {
-        ok = warp_wait(smem_u32(&s_qempty), (n_item & 1) ^ 1, abort);
+        ok = warp_wait(smem_u32(&s_qempty[n_item % Cfg::kStay]), ((n_item / Cfg::kStay) & 1) ^ 1, abort);
         if (!ok) break;
         if (leader) {
-          const uint32_t bar = smem_u32(&s_qfull);
+          const uint32_t bar = smem_u32(&s_qfull[n_item % Cfg::kStay]);
           mbar_expect(bar, 2 * kTile);
           for (uint32_t b = 0; b < DP / 64; ++b) {
             at_load(sq + b * kAtBlock, &maps.q, bar, b, head, t.start + t.tile * 128, t.batch);
@@ -420,7 +429,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
       } else {
-        ok = warp_wait(smem_u32(&s_qfull), n_item & 1, abort);
+        ok = warp_wait(smem_u32(&s_qfull[n_item % Cfg::kStay]), (n_item / Cfg::kStay) & 1, abort);
         auto stage_at = [&](uint32_t i) { return ring + (n_step + i) % S * 2 * kTile; };
         auto scores = [&](uint32_t i) {  // of step i, when its operands are there
           ok = ok && warp_wait(smem_u32(&s_full[(n_step + i) % S]), ((n_step + i) / S) & 1, abort);
@@ -454,7 +463,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_commit<1>(smem_u32(&s_empty[(n_step + i) % S]));
             if (i + 1 == steps) {
               tc_commit<1>(smem_u32(&s_accfull));
-              tc_commit<1>(smem_u32(&s_qempty));
+              tc_commit<1>(smem_u32(&s_qempty[n_item % Cfg::kStay]));
             }
           }
           __syncwarp();

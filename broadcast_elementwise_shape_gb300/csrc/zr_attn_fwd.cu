@@ -28,7 +28,10 @@ template <int DP>
 struct FwdCfg {
   static constexpr uint32_t kTile = DP / 64 * kAtBlock;  // bytes of 128 rows
   static constexpr int kStages = DP == 64 ? 4 : 2;       // of keys, and of values
-  static constexpr uint32_t kSmem = (2 + 2 * kStages) * kTile + 1024;
+  // Room for the queries: heads of 64 have it for the next item's too, which arrive
+  // while this one is at work.
+  static constexpr int kStay = DP == 64 ? 2 : 1;
+  static constexpr uint32_t kSmem = 2 * (kStay + kStages) * kTile + 1024;
   static constexpr uint32_t kO = 256;                    // columns: S0, S1, O0, O1
   static constexpr uint32_t kCols = 512;
 };
@@ -40,18 +43,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   constexpr int S = Cfg::kStages;
   constexpr uint32_t kTile = Cfg::kTile;
   extern __shared__ uint8_t s_raw[];
-  __shared__ uint64_t s_qfull[2], s_qempty[2], s_kfull[S], s_kempty[S], s_vfull[S], s_vempty[S], s_landed;
+  __shared__ uint64_t s_qfull[2 * Cfg::kStay], s_qempty[2 * Cfg::kStay], s_kfull[S], s_kempty[S], s_vfull[S], s_vempty[S], s_landed;
   __shared__ uint64_t s_sfull[2], s_pfull[2], s_ofull[2], s_oempty[2];
   __shared__ uint32_t s_tmem, s_abort;
   pdl_trigger();
   const uint32_t warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
-  const uint32_t sq = base, sk = base + 2 * kTile, sv = sk + S * kTile;
+  const uint32_t sq = base, sk = base + 2 * Cfg::kStay * kTile, sv = sk + S * kTile;
   volatile uint32_t* abort = &s_abort;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * Cfg::kStay; ++i) {
       mbar_init(smem_u32(&s_qfull[i]), 1);
       mbar_init(smem_u32(&s_qempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_sfull[i]), 1);
       mbar_init(smem_u32(&s_pfull[i]), 4);
       mbar_init(smem_u32(&s_ofull[i]), 1);
@@ -95,13 +100,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           // Queries with the first keys: each tile's when the last item's scores are done.
           if (i == 0) {
             for (uint32_t h = 0; h < tiles && ok; ++h) {
-              ok = warp_wait(smem_u32(&s_qempty[h]), (nq[h] & 1) ^ 1, abort);
+              const uint32_t room = h + nq[h] % Cfg::kStay * 2;
+              ok = warp_wait(smem_u32(&s_qempty[room]), ((nq[h] / Cfg::kStay) & 1) ^ 1, abort);
               ++nq[h];
               if (ok && leader) {
-                const uint32_t bar = smem_u32(&s_qfull[h]);
+                const uint32_t bar = smem_u32(&s_qfull[room]);
                 mbar_expect(bar, kTile);
                 for (uint32_t b = 0; b < DP / 64; ++b)
-                  at_load(sq + h * kTile + b * kAtBlock, &maps.q, bar, b, head, t.start + row0 + h * 128, t.batch);
+                  at_load(sq + room * kTile + b * kAtBlock, &maps.q, bar, b, head, t.start + row0 + h * 128, t.batch);
               }
               __syncwarp();
             }
@@ -147,15 +153,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t tiles = t.tile * kFwdRows + 128 < t.len ? 2 : 1;
         // Scores of tile h with key tile i, whose stage goes back with the last tile that reads it.
         auto scores = [&](uint32_t h, uint32_t i) {
-          const uint32_t at = n_key + i, stage = at % S;
+          const uint32_t at = n_key + i, stage = at % S, room = h + items_of[h] % Cfg::kStay * 2;
           ok = ok && warp_wait(smem_u32(&s_kfull[stage]), (at / S) & 1, abort);
-          if (i == 0) ok = ok && warp_wait(smem_u32(&s_qfull[h]), items_of[h] & 1, abort);
+          if (i == 0) ok = ok && warp_wait(smem_u32(&s_qfull[room]), (items_of[h] / Cfg::kStay) & 1, abort);
           if (!ok) return;
           tc_fence_after();
           if (leader) {
-            at_scores<DP>(tmem + h * 128, sq + h * kTile, sk + stage * kTile);
+            at_scores<DP>(tmem + h * 128, sq + room * kTile, sk + stage * kTile);
             tc_commit<1>(smem_u32(&s_sfull[h]));
-            if (i == 2 * t.tile + h) tc_commit<1>(smem_u32(&s_qempty[h]));
+            if (i == 2 * t.tile + h) tc_commit<1>(smem_u32(&s_qempty[room]));
             if (h + 1 == tiles) tc_commit<1>(smem_u32(&s_kempty[stage]));
           }
           __syncwarp();
