@@ -217,6 +217,17 @@ void set_tiles(AttnPlan* p, uint32_t rows) {
                         : (p->tokens + rows - 1) / rows * p->batch;
 }
 
+// Shares of a key tile's steps in the backward (bfloat16 on the tensor cores).
+// Tiles are dealt out whole, heaviest first, which evens out with some three tiles
+// for each SM; with fewer (few key heads, short batches) each is cut, up to
+// eight times, and the shares' sums are added at the end: [1, 4096], 8 heads on one key head, D =
+// 128, grad_k and grad_v 328 us in one share.  A share has four steps of the average tile at least.
+uint32_t shares(const AttnPlan& p) {
+  const uint64_t tiles = (uint64_t(p.tokens) + 127) / 128, items = tiles * p.batch * p.kv_heads;
+  const uint64_t average = std::max<uint64_t>(1, (tiles + 1) / 2 * p.group);
+  return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({8, 3 * kSms / items, average / 4})));
+}
+
 std::string plan_json(const AttnSet& S, const char* kernel) {
   const AttnPlan& p = S.p;
   return std::string("{\"kernel\":\"") + kernel + "\",\"tile\":" + std::to_string(p.tile_rows) +
@@ -300,6 +311,12 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   const bool parts = !S.empty && in_parts(S, scale);
   const Parts split_at = parts ? parts_of(p, 4, 2 * rows * sizeof(float)) : Parts{};
   S.ws = parts ? split_at.end : 2 * rows * sizeof(float);
+  // The alignment of what the call is given does not change the size it asks for.
+  const bool shared = !S.empty && S.es == 2 && p.dim <= 128 && p.dim % 8 == 0 && scale > 0 && (grad_k || grad_v);
+  p.splits = shared ? shares(p) : 1;
+  const size_t part_at = S.ws;
+  if (p.splits > 1)
+    S.ws += size_t(p.splits) * p.batch * p.tokens * p.kv_heads * 2 * (p.dim <= 64 ? 64 : 128) * sizeof(float);
   if (!workspace) {
     *workspace_bytes = S.ws;
     return ZR_OK;
@@ -340,6 +357,8 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   p.g_wide = (wide(S.gq, S.es) ? 1u : 0u) | (wide(S.gk, S.es) ? 2u : 0u) | (wide(S.gv, S.es) ? 4u : 0u);
   const bool tc = tensor_cores(S, scale) && mappable(S.go, S.es);
   if (tc || parts) set_tiles(&p, 128);
+  if (!tc) p.splits = 1;
+  p.part = p.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_at) : nullptr;
   trace("zr_attention_bwd", [&] { return plan_json(S, tc ? "tensor" : parts ? "parts" : "any"); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, p.go.p, p.o.p, static_cast<const void*>(low),
                         static_cast<const void*>(lse), static_cast<const void*>(offsets),

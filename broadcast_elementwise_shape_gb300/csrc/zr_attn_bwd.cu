@@ -84,7 +84,24 @@ __device__ __forceinline__ void bwd_store(const AttnPlan& p, const AttnView& x, 
   }
 }
 
-// Items: key tiles (as slots) times kv_heads.
+// The steps of one share of a key tile: queries' tiles of the group's heads, counted through.
+struct KvSteps {
+  uint32_t per, first, count;  // steps of a head; the share's first, how many
+};
+__device__ __forceinline__ KvSteps kv_steps(const AttnPlan& p, const AttnTile& t, uint32_t split) {
+  const uint32_t per = (t.len + 127) / 128 - t.tile, all = per * p.group;
+  const uint32_t first = uint32_t(uint64_t(all) * split / p.splits);
+  return {per, first, uint32_t(uint64_t(all) * (split + 1) / p.splits) - first};
+}
+// A row's sums of one share in the workspace: grad_v, then grad_k, DP each.
+template <int DP>
+__device__ __forceinline__ float* part_row(const AttnPlan& p, uint32_t split, const AttnTile& t, uint32_t row, uint32_t kvh) {
+  const int64_t at = (int64_t(t.batch) * p.tokens + t.start + row) * p.kv_heads + kvh;
+  return p.part + (int64_t(split) * p.batch * p.tokens * p.kv_heads + at) * (2 * DP);
+}
+
+// Items: key tiles (as slots) times kv_heads, or with p.splits shares of their steps,
+// whose sums k_attn_join adds.
 template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_attn_kv(const __grid_constant__ AttnPlan p, const __grid_constant__ AttnMaps maps) {
@@ -127,7 +144,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(s_tmem);
-  const uint32_t items = p.slots * p.kv_heads;
+  const uint32_t items = p.slots * p.splits * p.kv_heads;
   pdl_wait();
   pdl_trigger();  // behind the wait: k_attn_q may start beside this one, the rows are done
 
@@ -139,10 +156,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (uint32_t round = 0; warp < 11 && ok && round * gridDim.x < items; ++round) {
       const uint32_t w = at_item(round);
       if (w >= items) continue;
-      const uint32_t slot = w / p.kv_heads, kvh = w - slot * p.kv_heads;
+      const uint32_t share = w / p.kv_heads, kvh = w - share * p.kv_heads, slot = share / p.splits;
       const AttnTile t = attn_tile(p, slot, true);
       if (!t.live) continue;
-      const uint32_t tiles = (t.len + 127) / 128, per = tiles - t.tile, steps = per * p.group;
+      const uint32_t tiles = (t.len + 127) / 128;
+      const KvSteps run = kv_steps(p, t, share - slot * p.splits);
+      const uint32_t steps = run.count;
+      if (steps == 0) continue;
       const uint32_t sk = stay + n_item % Cfg::kStay * 2 * kTile, sv = sk + kTile;
       if (warp == 8) {
         ok = warp_wait(smem_u32(&s_kvempty[n_item % Cfg::kStay]), ((n_item / Cfg::kStay) & 1) ^ 1, abort);
@@ -156,7 +176,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
         __syncwarp();
-        uint32_t head = kvh * p.group, q = t.tile;
+        uint32_t head = kvh * p.group + run.first / run.per, q = t.tile + run.first % run.per;
         for (uint32_t i = 0; i < steps; ++i, ++n_step) {
           const uint32_t stage = n_step % S, sq = ring + stage * 2 * kTile;
           ok = warp_wait(smem_u32(&s_empty[stage]), ((n_step / S) & 1) ^ 1, abort);
@@ -231,7 +251,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         n_step += steps;
       } else {
-        uint32_t head = kvh * p.group, q = t.tile;
+        uint32_t head = kvh * p.group + run.first / run.per, q = t.tile + run.first % run.per;
         for (uint32_t i = 0; i < steps; ++i, ++n_step) {
           const uint32_t stage = n_step & 1;
           ok = warp_wait(smem_u32(&s_rempty[stage]), ((n_step / 2) & 1) ^ 1, abort);
@@ -264,11 +284,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (uint32_t round = 0; round * gridDim.x < items; ++round) {
       const uint32_t w = at_item(round);
       if (w >= items) continue;
-      const uint32_t slot = w / p.kv_heads, kvh = w - slot * p.kv_heads;
+      const uint32_t share = w / p.kv_heads, kvh = w - share * p.kv_heads, slot = share / p.splits;
       const AttnTile t = attn_tile(p, slot, true);
       if (!t.live) continue;
-      const uint32_t per = (t.len + 127) / 128 - t.tile, steps = per * p.group;
-      uint32_t q = 0;
+      const uint32_t split = share - slot * p.splits;
+      const KvSteps run = kv_steps(p, t, split);
+      const uint32_t per = run.per, steps = run.count;
+      if (steps == 0) continue;  // k_attn_join knows
+      uint32_t q = run.first % per;
       for (uint32_t i = 0; i < steps; ++i, ++n_step) {
         const uint32_t stage = n_step & 1;
         const float* rows = s_rows[stage] + half * 64;
@@ -313,10 +336,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ++n_item;
       tc_fence_after();
       const uint32_t row = t.tile * 128 + mine;
-      if (half == 0)
+      if (p.splits > 1) {
+        float* to = part_row<DP>(p, split, t, row, kvh) + half * DP;
+#pragma unroll
+        for (int j = 0; j < DP; j += 32) {
+          float x[32];
+          __syncwarp();
+          tc_load32(lanes + Cfg::kAcc + half * DP + j, x);
+          if (row < t.len) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(to + j + k) =
+                  ok ? make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]) : make_float4(qnan(), qnan(), qnan(), qnan());
+          }
+        }
+      } else if (half == 0) {
         bwd_store<DP>(p, p.gv, lanes + Cfg::kAcc, t, row, kvh, ok ? 1.f : qnan(), p.g_wide & 4);
-      else
+      } else {
         bwd_store<DP>(p, p.gk, lanes + Cfg::kAcc + DP, t, row, kvh, ok ? p.scale : qnan(), p.g_wide & 2);
+      }
       bwd_arrive(smem_u32(&s_accempty));
     }
   }
@@ -331,6 +369,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_free<1>(tmem, Cfg::kCols);
+}
+
+// Adds the shares' sums in their order: blockIdx.x = (slot * kv_heads + kv head) *
+// 16 + eighth rows, four elements a thread.
+template <int DP>
+__global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ AttnPlan p) {
+  pdl_wait();
+  const uint32_t tile = blockIdx.x / 16, slot = tile / p.kv_heads, kvh = tile - slot * p.kv_heads;
+  const AttnTile t = attn_tile(p, slot, true);
+  if (!t.live) return;
+  for (uint32_t i = threadIdx.x; i < 8 * 2 * DP / 4; i += kThreads) {
+    const uint32_t e = i % (2 * DP / 4) * 4, d = e % DP, row = t.tile * 128 + blockIdx.x % 16 * 8 + i / (2 * DP / 4);
+    if (row >= t.len || d >= p.dim) continue;
+    float4 x[8];
+#pragma unroll
+    for (uint32_t split = 0; split < 8; ++split)
+      x[split] = split < p.splits && kv_steps(p, t, split).count
+                     ? *reinterpret_cast<const float4*>(part_row<DP>(p, split, t, row, kvh) + e)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int split = 0; split < 8; ++split) {
+      sum[0] += x[split].x; sum[1] += x[split].y; sum[2] += x[split].z; sum[3] += x[split].w;
+    }
+    const AttnView& g = e < DP ? p.gv : p.gk;
+    if (!g.p) continue;
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(const_cast<void*>(g.p)) + int64_t(t.batch) * g.batch +
+                        (int64_t(t.start) + row) * g.token + int64_t(kvh) * g.head + int64_t(d) * g.elem;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)  // dim is a multiple of 8
+      to[k * g.elem] = __float2bfloat16_rn(e < DP ? sum[k] : sum[k] * p.scale);
+  }
 }
 
 // Items: query tiles (as slots) times heads.
@@ -377,7 +447,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // one leaves: by then the rows' kernel, whose results both read, is done (k_attn_kv
   // has waited for it).  It waits at its end instead, so that whatever comes
   // next finds both done.
-  const bool beside = p.want & 6;
+  const bool beside = (p.want & 6) && p.splits == 1;
   if (!beside) pdl_wait();
 
   if (warp >= 8) {
@@ -561,7 +631,8 @@ cudaError_t go(K k, uint32_t items, uint32_t smem, const AttnPlan& p, const Attn
 template <int DP>
 cudaError_t launch(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  if (p.want & 6) e = go(k_attn_kv<DP>, p.slots * p.kv_heads, BwdCfg<DP>::kSmem, p, maps, s);
+  if (p.want & 6) e = go(k_attn_kv<DP>, p.slots * p.splits * p.kv_heads, BwdCfg<DP>::kSmem, p, maps, s);
+  if (e == cudaSuccess && p.splits > 1) e = launch_k(k_attn_join<DP>, p.slots * p.kv_heads * 16, kThreads, 0, s, p);
   if (e == cudaSuccess && (p.want & 1)) e = go(k_attn_q<DP>, p.slots * p.heads, BwdCfg<DP>::kSmem, p, maps, s);
   return e;
 }

@@ -566,8 +566,10 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
  *
  * workspace (both)  NULL queries the size; 16-byte aligned, contents irrelevant,
  *               used in stream order.  Backward: 8 bytes per row of T rounded up to
- *               128, for each batch entry and head.  ZR_F32 with D <= 64: 384 bytes
- *               per row of q, k, v and (backward) grad_out besides.
+ *               128, for each batch entry and head; ZR_BF16 with few key tiles and heads
+ *               for the GPU up to 8 times 1024 bytes (D <= 64: 512) per token and
+ *               key head besides.  ZR_F32 with D <= 64, both: 384 bytes per row of
+ *               q, k, v and (backward) grad_out.
  *
  * Numerics.  Scores, sums and statistics are binary32, gradients are summed in
  * a fixed order (no atomics), results are rounded once.  ZR_F32 with D <= 64 and

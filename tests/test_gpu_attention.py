@@ -46,6 +46,25 @@ def test_grouped_heads(h, kv, d, dtype):
     run(zr, q, k, v, go=go)
 
 
+@pytest.mark.parametrize("d", [64, 80, 128])
+@pytest.mark.parametrize("lengths", [None, [1, 700, 0, 129, 255], [30] * 40])
+def test_shares_of_a_key_tile(lengths, d):
+    """Few key tiles for the GPU: each is worked on in shares, some of them empty."""
+    t = sum(lengths) if lengths else 1100
+    lead = (t,) if lengths else (1, t)
+    q, k, v, go = make(lead, 8, 1, d, BF16)
+    off = packed(lengths) if lengths else None
+    full = run(zr, q, k, v, offsets=off, go=go)
+    out, lse, low = zr.zr_attention_fwd(q, k, v, None, off, keep_low=True)
+    gk = zr.zr_attention_bwd(go, q, k, v, out, lse, low, None, off, want=(False, True, False))[1]
+    assert torch.equal(gk, full[3])
+    if lengths:  # rows in no sequence stay as they are
+        off = off[:-1].contiguous()
+        grads = [torch.full_like(x, 7.0) for x in (q, k, v)]
+        zr.zr_attention_bwd(go, q, k, v, out, lse, low, None, off, grads=grads)
+        assert all(bool((x[int(off[-1]):] == 7).all()) for x in grads) and torch.equal(grads[1][:int(off[-1])], full[3][:int(off[-1])])
+
+
 LENGTHS = [[5, 1, 17, 64], [128, 128], [1] * 40, [129, 0, 0, 255, 1, 300], [1000], [0, 0, 7], [64, 63, 65, 127, 128, 129, 2, 256, 257]]
 
 
