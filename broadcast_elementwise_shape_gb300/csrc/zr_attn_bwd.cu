@@ -14,7 +14,9 @@
 // per thread.  With s the scores and d the products grad_out . v of a step:
 //   tensor core:  dV(i) += P(i) dO   s(i+1) | dK(i) += dS(i) Q   d(i+1)
 //   warps:        dS(i) from d(i), P(i)     | P(i+1) from s(i+1)
-// so that both work at all times; in k_attn_q likewise, with s(i+1) as soon as
+// so that both work at all times ([2, 8192] tokens of 16 heads of 128, 1470 us: the
+// products that are computed at 1.3 PFLOP/s; four groups of 32 columns instead
+// of two of 64, for more warps, took 1 to 3 % longer); in k_attn_q likewise, with s(i+1) as soon as
 // s(i) has been read.  Every wait has a limit (zr_tc.cuh); when one runs out the
 // CTA's remaining rows become NaN.
 #include "zr_attn_tc.cuh"

@@ -1,5 +1,5 @@
 """Binding of the training operators: layer norm, dropout with its residual,
-cross entropy of a linear head.
+cross entropy of a linear head, causal attention, rotary positions, AdamW.
 
 The functions pass their arguments on to the CPython module built from
 ``csrc/zr_torch.cpp``, which reads the tensors, allocates outputs and
