@@ -146,11 +146,18 @@ bool mappable(const TDesc& t, int es) {
     if (t.size[d] > 1 && (t.stride[d] <= 0 || t.stride[d] * es >= (int64_t(1) << 40))) return false;
   return true;
 }
-// The tensor cores take bfloat16 heads of up to 128 elements, and a positive
-// scale: a row's maximum is that of its products.
+// The tensor cores take bfloat16 heads of up to 128 elements, and binary32 ones
+// of up to 64 in parts (zr_attn_f32.cu), with a positive scale: a row's maximum is that
+// of its products.  Up to 64 tokens the copy into parts costs more than it gains: [64, 64]
+// tokens of 12 heads of 64, forward 53 us, by multiply-adds 36; [4, 128] 13.8 and 20.9.
 bool tensor_cores(const AttnSet& S, float scale) {
-  return S.es == 2 && S.p.dim <= 128 && S.p.dim % 8 == 0 && scale > 0 && mappable(S.q, 2) && mappable(S.k, 2) &&
-         mappable(S.v, 2);
+  return scale > 0 && (S.es == 2 ? S.p.dim <= 128 : S.p.dim <= 64 && S.p.tokens > 64);
+}
+// Whether the operands are copied for it: binary32 always (into parts), bfloat16
+// rows that no tensor map describes (odd addresses, head sizes or strides): [2048]
+// tokens of 16 heads of 81, 88 us with their copy.
+bool copied(const AttnSet& S, bool backward) {
+  return S.es == 4 || !mappable(S.q, 2) || !mappable(S.k, 2) || !mappable(S.v, 2) || (backward && !mappable(S.go, 2));
 }
 // Boxes of 64 elements x 128 tokens; what is out of range reads as zero.
 bool tile_map(CUtensorMap* m, const TDesc& t) {
@@ -166,49 +173,55 @@ bool tile_map(CUtensorMap* m, const TDesc& t) {
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// binary32 heads that the tensor cores take in parts (zr_attn_f32.cu).
-bool in_parts(const AttnSet& S, float scale) { return S.es == 4 && S.p.dim <= 64 && scale > 0; }
-
-// The parts of q, k, v and (count 4) grad_out behind `at` bytes of workspace.
-struct Parts {
+// The copies of q, k, v and (count 4) grad_out behind `at` bytes of workspace.
+struct Copies {
   uint64_t rows[4];
   size_t at[4], end;
 };
-Parts parts_of(const AttnPlan& p, int count, size_t at) {
-  Parts x{};
+Copies copies_of(const AttnSet& S, int count, size_t at) {
+  const AttnPlan& p = S.p;
+  Copies x{};
+  const size_t row = S.es == 4 ? 3 * 128 : p.dim <= 64 ? 128 : 256;  // bytes
   for (int i = 0; i < count; ++i) {
     x.rows[i] = uint64_t(p.batch) * p.tokens * (i == 1 || i == 2 ? p.kv_heads : p.heads);
     x.at[i] = at = (at + 255) / 256 * 256;
-    at += size_t(x.rows[i]) * 64 * 2 * 3;
+    at += size_t(x.rows[i]) * row;
   }
   x.end = at;
   return x;
 }
-// Boxes of all three parts of 128 tokens.
-bool part_map(CUtensorMap* m, const AttnPlan& p, void* base, uint64_t rows, uint32_t heads) {
+// Boxes of 64 elements of 128 tokens, all parts of binary32 ones.
+bool copy_map(CUtensorMap* m, const AttnSet& S, void* base, uint64_t rows, uint32_t heads) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[5] = {64, heads, p.tokens, p.batch, 3};
-  const cuuint64_t token = cuuint64_t(heads) * 128;
-  const cuuint64_t strides[4] = {128, token, token * p.tokens, cuuint64_t(rows) * 128};
-  const cuuint32_t box[5] = {64, 1, 128, 1, 3}, step[5] = {1, 1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const AttnPlan& p = S.p;
+  const cuuint32_t parts = S.es == 4 ? 3 : 1;
+  const cuuint64_t width = p.dim <= 64 ? 64 : 128, token = heads * width * 2;
+  const cuuint64_t dims[5] = {width, heads, p.tokens, p.batch, parts};
+  const cuuint64_t strides[4] = {width * 2, token, token * p.tokens, cuuint64_t(rows) * width * 2};
+  const cuuint32_t box[5] = {64, 1, 128, 1, parts}, step[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, parts == 3 ? 5 : 4, base, dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// Splits the operands and maps their parts.
-cudaError_t split(const AttnSet& S, const Parts& x, int count, void* workspace, AttnMaps* maps, cudaStream_t s) {
+// The kernels' maps, over the operands or over their copies, which this makes.
+cudaError_t operands(const AttnSet& S, bool copy, const Copies& x, int count, void* workspace, AttnMaps* maps, cudaStream_t s) {
   const AttnPlan& p = S.p;
   CUtensorMap* m[4] = {&maps->q, &maps->k, &maps->v, &maps->go};
   const TDesc* t[4] = {&S.q, &S.k, &S.v, &S.go};
   uint16_t* out[4] = {};
   uint32_t w = 0;
   for (int i = 0; i < count; ++i) {
+    if (!copy) {
+      if (!tile_map(m[i], *t[i])) return cudaErrorInvalidValue;
+      continue;
+    }
     out[i] = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + x.at[i]);
-    if (!part_map(m[i], p, out[i], x.rows[i], i == 1 || i == 2 ? p.kv_heads : p.heads)) return cudaErrorInvalidValue;
-    if (wide(*t[i], 4)) w |= 1u << i;
+    if (!copy_map(m[i], S, out[i], x.rows[i], i == 1 || i == 2 ? p.kv_heads : p.heads)) return cudaErrorInvalidValue;
+    if (wide(*t[i], S.es)) w |= 1u << i;
   }
   if (count == 3) maps->go = maps->q;
-  return launch_attn_split(p, out, uint32_t(count), w, s);
+  return copy ? launch_attn_split(S.es, p, out, uint32_t(count), w, s) : cudaSuccess;
 }
 // Tiles of `rows` rows.
 void set_tiles(AttnPlan* p, uint32_t rows) {
@@ -228,6 +241,8 @@ uint32_t shares(const AttnPlan& p) {
   return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({8, 3 * kSms / items, average / 4})));
 }
 
+const char* kernel_name(bool tc, bool copy, int es) { return !tc ? "any" : es == 4 ? "parts" : copy ? "copied" : "tensor"; }
+
 std::string plan_json(const AttnSet& S, const char* kernel) {
   const AttnPlan& p = S.p;
   return std::string("{\"kernel\":\"") + kernel + "\",\"tile\":" + std::to_string(p.tile_rows) +
@@ -244,9 +259,9 @@ int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_te
   if (rc) return rc;
   if ((rc = plan_out(S.q, out, out_strides, &S.o))) return rc;
   if (low && dtype != ZR_BF16) return ZR_ERR_DTYPE;
-  const bool parts = !S.empty && in_parts(S, scale);
-  const Parts split_at = parts ? parts_of(S.p, 3, 0) : Parts{};
-  S.ws = split_at.end;
+  const bool tc = !S.empty && tensor_cores(S, scale), copy = tc && copied(S, false);
+  const Copies copies = copy ? copies_of(S, 3, 0) : Copies{};
+  S.ws = copies.end;
   if (!workspace) {
     *workspace_bytes = S.ws;
     return ZR_OK;
@@ -266,25 +281,19 @@ int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_te
   p.lse = lse;
   p.vec = wide(S.q, S.es) && wide(S.k, S.es) && wide(S.v, S.es);
   p.o_wide = wide(S.o, S.es);
-  p.low_wide = reinterpret_cast<uintptr_t>(low) % 16 == 0;
-  const bool tc = tensor_cores(S, scale);
-  if (tc || parts) set_tiles(&p, 256);
-  trace("zr_attention_fwd", [&] { return plan_json(S, tc ? "tensor" : parts ? "parts" : "any"); });
+  p.low_wide = reinterpret_cast<uintptr_t>(low) % 16 == 0 && p.dim % 8 == 0;
+  if (tc) set_tiles(&p, 256);
+  trace("zr_attention_fwd", [&] { return plan_json(S, kernel_name(tc, copy, S.es)); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, static_cast<const void*>(out), static_cast<const void*>(low),
                         static_cast<const void*>(lse), static_cast<const void*>(offsets),
                         static_cast<const void*>(S.ws ? workspace : nullptr)})
     if (x && (rc = check_device_ptr(x))) return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (parts) {
-    AttnMaps maps;
-    const cudaError_t e = split(S, split_at, 3, workspace, &maps, st);
-    return cuda_status(e == cudaSuccess ? launch_attn_f32_fwd(p, maps, st) : e);
-  }
   if (!tc) return cuda_status(launch_attn_any_fwd(S.es, p, st));
   AttnMaps maps;
-  if (!tile_map(&maps.q, S.q) || !tile_map(&maps.k, S.k) || !tile_map(&maps.v, S.v)) return ZR_ERR_CUDA;
-  maps.go = maps.q;
-  return cuda_status(launch_attn_fwd(p, maps, st));
+  const cudaError_t e = operands(S, copy, copies, 3, workspace, &maps, st);
+  if (e != cudaSuccess) return ZR_ERR_CUDA;
+  return cuda_status(S.es == 4 ? launch_attn_f32_fwd(p, maps, st) : launch_attn_fwd(p, maps, st));
 }
 
 int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, const zr_tensor& k,
@@ -308,15 +317,13 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   if (low && dtype != ZR_BF16) return ZR_ERR_DTYPE;
   AttnPlan& p = S.p;
   const size_t rows = S.empty ? 0 : size_t(p.batch) * p.heads * p.row_pitch;
-  const bool parts = !S.empty && in_parts(S, scale);
-  const Parts split_at = parts ? parts_of(p, 4, 2 * rows * sizeof(float)) : Parts{};
-  S.ws = parts ? split_at.end : 2 * rows * sizeof(float);
-  // The alignment of what the call is given does not change the size it asks for.
-  const bool shared = !S.empty && S.es == 2 && p.dim <= 128 && p.dim % 8 == 0 && scale > 0 && (grad_k || grad_v);
-  p.splits = shared ? shares(p) : 1;
-  const size_t part_at = S.ws;
+  const bool tc = !S.empty && tensor_cores(S, scale), copy = tc && copied(S, true);
+  const Copies copies = copy ? copies_of(S, 4, 2 * rows * sizeof(float)) : Copies{};
+  S.ws = copy ? copies.end : 2 * rows * sizeof(float);
+  p.splits = tc && S.es == 2 && (grad_k || grad_v) ? shares(p) : 1;
+  const size_t part_at = (S.ws + 255) / 256 * 256;
   if (p.splits > 1)
-    S.ws += size_t(p.splits) * p.batch * p.tokens * p.kv_heads * 2 * (p.dim <= 64 ? 64 : 128) * sizeof(float);
+    S.ws = part_at + size_t(p.splits) * p.batch * p.tokens * p.kv_heads * 2 * (p.dim <= 64 ? 64 : 128) * sizeof(float);
   if (!workspace) {
     *workspace_bytes = S.ws;
     return ZR_OK;
@@ -355,11 +362,9 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   p.vec = wide(S.q, S.es) && wide(S.k, S.es) && wide(S.v, S.es) && wide(S.go, S.es);
   p.o_wide = wide(S.o, S.es) && wide(S.go, S.es) && reinterpret_cast<uintptr_t>(low) % 16 == 0;
   p.g_wide = (wide(S.gq, S.es) ? 1u : 0u) | (wide(S.gk, S.es) ? 2u : 0u) | (wide(S.gv, S.es) ? 4u : 0u);
-  const bool tc = tensor_cores(S, scale) && mappable(S.go, S.es);
-  if (tc || parts) set_tiles(&p, 128);
-  if (!tc) p.splits = 1;
+  if (tc) set_tiles(&p, 128);
   p.part = p.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_at) : nullptr;
-  trace("zr_attention_bwd", [&] { return plan_json(S, tc ? "tensor" : parts ? "parts" : "any"); });
+  trace("zr_attention_bwd", [&] { return plan_json(S, kernel_name(tc, copy, S.es)); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, p.go.p, p.o.p, static_cast<const void*>(low),
                         static_cast<const void*>(lse), static_cast<const void*>(offsets),
                         static_cast<const void*>(grad_q), static_cast<const void*>(grad_k),
@@ -368,16 +373,11 @@ int bwd_impl(zr_dtype dtype, const zr_tensor& grad_out, const zr_tensor& q, cons
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_attn_rows(S.es, p, st);
   if (e != cudaSuccess) return ZR_ERR_CUDA;
-  if (parts) {
-    AttnMaps maps;
-    e = split(S, split_at, 4, workspace, &maps, st);
-    return cuda_status(e == cudaSuccess ? launch_attn_f32_bwd(p, maps, st) : e);
-  }
   if (!tc) return cuda_status(launch_attn_any_bwd(S.es, p, st));
   AttnMaps maps;
-  if (!tile_map(&maps.q, S.q) || !tile_map(&maps.k, S.k) || !tile_map(&maps.v, S.v) || !tile_map(&maps.go, S.go))
-    return ZR_ERR_CUDA;
-  return cuda_status(launch_attn_bwd(p, maps, st));
+  e = operands(S, copy, copies, 4, workspace, &maps, st);
+  if (e != cudaSuccess) return ZR_ERR_CUDA;
+  return cuda_status(S.es == 4 ? launch_attn_f32_bwd(p, maps, st) : launch_attn_bwd(p, maps, st));
 }
 
 }  // namespace

@@ -105,16 +105,18 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnPlan& p, uint32_t slot, 
 
 // es: bytes per element.
 cudaError_t launch_attn_any_fwd(int es, const AttnPlan& p, cudaStream_t s);
-// On the tensor cores, bfloat16, dim <= 128 and a multiple of 8; p.tile_rows and
-// p.slots for tiles of 256 queries.
+// On the tensor cores, bfloat16, dim <= 128; p.tile_rows and p.slots for tiles of
+// 256 queries.
 cudaError_t launch_attn_fwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
 // The same of tiles of 128; after launch_attn_rows.
 cudaError_t launch_attn_bwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
 cudaError_t launch_attn_any_bwd(int es, const AttnPlan& p, cudaStream_t s);
-// binary32, dim <= 64: launch_attn_split brings q, k, v (and go; count = 3 or 4)
-// into parts, [part][batch][token][head][64], which the maps are over; wide: bit i, 16-byte
-// reads.  Tiles of 256 queries forward, of 128 backward.
-cudaError_t launch_attn_split(const AttnPlan& p, uint16_t* const* out, uint32_t count, uint32_t wide, cudaStream_t s);
+// launch_attn_split copies q, k, v (and go; count = 3 or 4) to rows that the maps
+// are over: binary32 with dim <= 64 into parts, [part][batch][token][head][64]; bfloat16
+// as they are, in rows of 64 or 128.  wide: bit i, 16-byte reads (binary32).
+cudaError_t launch_attn_split(int es, const AttnPlan& p, uint16_t* const* out, uint32_t count, uint32_t wide,
+                              cudaStream_t s);
+// binary32, dim <= 64, in parts.  Tiles of 256 queries forward, of 128 backward.
 cudaError_t launch_attn_f32_fwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
 cudaError_t launch_attn_f32_bwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s);
 // lse2 and delta of every row that a sequence holds.

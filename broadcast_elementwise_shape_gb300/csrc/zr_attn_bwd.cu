@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_join(const __grid_constant__ 
     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(const_cast<void*>(g.p)) + int64_t(t.batch) * g.batch +
                         (int64_t(t.start) + row) * g.token + int64_t(kvh) * g.head + int64_t(d) * g.elem;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)  // dim is a multiple of 8
-      to[k * g.elem] = __float2bfloat16_rn(e < DP ? sum[k] : sum[k] * p.scale);
+    for (int k = 0; k < 4; ++k)
+      if (d + k < p.dim) to[k * g.elem] = __float2bfloat16_rn(e < DP ? sum[k] : sum[k] * p.scale);
   }
 }
 

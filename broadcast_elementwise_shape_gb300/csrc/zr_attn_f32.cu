@@ -134,29 +134,34 @@ __device__ __forceinline__ void wait_in_flight(volatile uint32_t* abort) {
 
 struct SplitPlan {
   AttnView x[4];             // q, k, v, grad_out
-  uint16_t* out[4];          // [part][batch][token][head][64]
+  uint16_t* out[4];          // [part][batch][token][head][W]
   uint32_t heads[4];
   uint64_t first[5];         // first row (batch, token, head) of each, counted through
   uint32_t count, tokens, dim, wide;
 };
 
-// Eight lanes per row, eight elements each.
+__device__ __forceinline__ float split_load(const float* p) { return *p; }
+__device__ __forceinline__ float split_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// Rows of W elements, zero behind the head's, eight elements a thread.  PARTS = 1:
+// bfloat16 rows that no tensor map describes, as they are.
+template <typename E, uint32_t PARTS, uint32_t W>
 __global__ void __launch_bounds__(kThreads) k_attn_split(const __grid_constant__ SplitPlan p) {
+  constexpr uint32_t kLanes = W / 8;
   pdl_trigger();
   pdl_wait();
-  const uint64_t i = uint64_t(blockIdx.x) * (kThreads / 8) + threadIdx.x / 8;
+  const uint64_t i = uint64_t(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
   if (i >= p.first[p.count]) return;
   uint32_t which = 0;
   while (which + 1 < p.count && i >= p.first[which + 1]) ++which;
-  const uint64_t row = i - p.first[which];
-  const uint32_t e0 = threadIdx.x % 8 * 8;
-  const uint64_t token = row / p.heads[which];
-  const uint32_t head = uint32_t(row - token * p.heads[which]), b = uint32_t(token / p.tokens);
+  const uint32_t row = uint32_t(i - p.first[which]);  // rows are counted in 31 bits
+  const uint32_t e0 = threadIdx.x % kLanes * 8;
+  const uint32_t token = row / p.heads[which], head = row - token * p.heads[which], b = token / p.tokens;
   const AttnView& x = p.x[which];
-  const float* from = static_cast<const float*>(x.p) + int64_t(b) * x.batch + int64_t(token - uint64_t(b) * p.tokens) * x.token +
-                      int64_t(head) * x.head;
+  const E* from = static_cast<const E*>(x.p) + int64_t(b) * x.batch + int64_t(token - b * p.tokens) * x.token +
+                  int64_t(head) * x.head;
   float v[8];
-  if (p.wide >> which & 1) {
+  if (sizeof(E) == 4 && p.wide >> which & 1) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -165,11 +170,11 @@ __global__ void __launch_bounds__(kThreads) k_attn_split(const __grid_constant__
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = e0 + k < p.dim ? from[int64_t(e0 + k) * x.elem] : 0.f;
+    for (int k = 0; k < 8; ++k) v[k] = e0 + k < p.dim ? split_load(from + int64_t(e0 + k) * x.elem) : 0.f;
   }
-  const uint64_t plane = (p.first[which + 1] - p.first[which]) * 64;
+  const uint64_t plane = (p.first[which + 1] - p.first[which]) * W;
 #pragma unroll
-  for (uint32_t part = 0; part < kParts; ++part) {
+  for (uint32_t part = 0; part < PARTS; ++part) {
     uint32_t r[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_split(const __grid_constant__
       v[2 * k] -= __uint_as_float(r[k] << 16);
       v[2 * k + 1] -= __uint_as_float(r[k] & 0xFFFF0000u);
     }
-    *reinterpret_cast<uint4*>(p.out[which] + part * plane + row * 64 + e0) = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(p.out[which] + part * plane + uint64_t(row) * W + e0) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -676,7 +681,8 @@ cudaError_t go(K k, uint32_t items, const AttnPlan& p, const AttnMaps& maps, cud
 
 }  // namespace
 
-cudaError_t launch_attn_split(const AttnPlan& p, uint16_t* const* out, uint32_t count, uint32_t wide, cudaStream_t s) {
+cudaError_t launch_attn_split(int es, const AttnPlan& p, uint16_t* const* out, uint32_t count, uint32_t wide,
+                              cudaStream_t s) {
   SplitPlan d{};
   const AttnView* x[4] = {&p.q, &p.k, &p.v, &p.go};
   d.count = count;
@@ -689,8 +695,11 @@ cudaError_t launch_attn_split(const AttnPlan& p, uint16_t* const* out, uint32_t 
     d.heads[i] = i == 1 || i == 2 ? p.kv_heads : p.heads;
     d.first[i + 1] = d.first[i] + uint64_t(p.batch) * p.tokens * d.heads[i];
   }
-  const uint64_t cta = (d.first[count] + kThreads / 8 - 1) / (kThreads / 8);
-  return launch_k(k_attn_split, unsigned(cta), kThreads, 0, s, d);
+  const uint32_t rows = kThreads / (p.dim <= 64 ? 8 : 16);  // of a CTA
+  const unsigned cta = unsigned((d.first[count] + rows - 1) / rows);
+  if (es == 4) return launch_k(k_attn_split<float, kParts, 64>, cta, kThreads, 0, s, d);
+  return p.dim <= 64 ? launch_k(k_attn_split<__nv_bfloat16, 1, 64>, cta, kThreads, 0, s, d)
+                     : launch_k(k_attn_split<__nv_bfloat16, 1, 128>, cta, kThreads, 0, s, d);
 }
 
 cudaError_t launch_attn_f32_fwd(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s) {

@@ -569,19 +569,21 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
  *               used in stream order.  Backward: 8 bytes per row of T rounded up to
  *               128, for each batch entry and head; ZR_BF16 with few key tiles and heads
  *               for the GPU up to 8 times 1024 bytes (D <= 64: 512) per token and
- *               key head besides.  ZR_F32 with D <= 64, both: 384 bytes per row of
- *               q, k, v and (backward) grad_out.
+ *               key head besides.  Both: copies of q, k, v and (backward) grad_out
+ *               that the tensor cores read, 384 bytes per row with ZR_F32, and
+ *               256 (D <= 64: 128) with ZR_BF16 where rows are not aligned
+ *               to 16 bytes or D is no multiple of 8.
  *
  * Numerics.  Scores, sums and statistics are binary32, gradients are summed in
- * a fixed order (no atomics), results are rounded once.  ZR_F32 with D <= 64 and
- * scale > 0 on the tensor cores: each operand, weights and ds among them, is
+ * a fixed order (no atomics), results are rounded once.  ZR_F32 with D <= 64,
+ * T > 64 and scale > 0 on the tensor cores: each operand, weights and ds among them, is
  * split into three bfloat16 parts, and a product is the sum of the six products
  * of parts that reach 2^-24 of it; other ZR_F32 by binary32 multiply-adds.
- * ZR_BF16 on the tensor cores (D <= 128, a multiple of
- * 8, 16-byte aligned rows, scale > 0; others as ZR_F32 by multiply-adds): products accumulate in binary32, weights and ds are
- * rounded to bfloat16 as operands, weights below 2^-126 are 0.  A token whose q, k or v holds an infinity or
- * NaN makes NaN of rows that see it, and may of others of its sequence; never of another
- * sequence's.
+ * ZR_BF16 with D <= 128 and scale > 0 on the tensor cores (others as ZR_F32 by
+ * multiply-adds): products accumulate in binary32, weights and ds are rounded to
+ * bfloat16 as operands, weights below 2^-126 are 0.  A token whose q, k or v holds
+ * an infinity or NaN makes NaN of rows that see it, and may of others of its
+ * sequence; never of another sequence's.
  * Sizes: B times T (rounded up to 128) times H < 2^31, T < 2^30 (else
  * ZR_ERR_SIZE); ranks differ or offsets with rank 4:
  * ZR_ERR_RANK.  Outputs overlap no input.  Errors as zr_binary_bwd, plus

@@ -43,10 +43,14 @@ def test_attention_forward_refusals(L):
         nb.value = size
         return L.zr_attention_fwd(dt, q.desc, k.desc, v.desc, scale, off, n, out, os, low, lse, ws, ctypes.byref(nb), None)
 
-    need = 384 * 2 * 10 * (4 + 2 + 2)  # three parts of 64 elements per row of q, k and v
-    assert fwd(ws=None) == 0 and nb.value == 0 and fwd(ws=None, dt=F32) == 0 and nb.value == need
-    assert fwd(dt=F32) == DEVICE and fwd(dt=F32, size=need - 1) == WORKSPACE and fwd(dt=F32, ws=8 * T + 8) == WORKSPACE
-    assert fwd(dt=F32, ws=4 * T) == LAYOUT and fwd(ws=16, size=0) == DEVICE
+    assert fwd(ws=None) == 0 and nb.value == 0 and fwd(ws=None, dt=F32) == 0 and nb.value == 0 and fwd(ws=16, size=0) == DEVICE
+    need = 384 * 2 * 100 * (4 + 2 + 2)  # three parts of 64 elements per row of q, k and v
+    f32 = dict(q=TT(T, (2, 100, 4, 64)), k=TT(2 * T, (2, 100, 2, 64)), v=TT(3 * T, (2, 100, 2, 64)), dt=F32)
+    assert fwd(**f32, ws=None) == 0 and nb.value == need
+    assert fwd(**f32) == DEVICE and fwd(**f32, size=need - 1) == WORKSPACE and fwd(**f32, ws=8 * T + 8) == WORKSPACE
+    assert fwd(**f32, ws=4 * T) == LAYOUT
+    odd = [TT(i * T, (2, 100, 1, d)) for i, d in ((1, 33), (2, 33), (3, 33))]  # rows of 64 elements: copies
+    assert fwd(*odd, ws=None) == 0 and nb.value >= 128 * 2 * 100 * 3
     assert L.zr_attention_fwd(BF16, TT(T, q).desc, TT(2 * T, kv).desc, TT(3 * T, kv).desc, 0.1, None, 0, 4 * T, None, None, None, None, None, None) == NULL
 
     assert fwd() == DEVICE  # nothing but the addresses is wrong
