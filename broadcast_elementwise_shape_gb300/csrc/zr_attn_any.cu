@@ -267,8 +267,8 @@ constexpr int kRowsEach = 4;
 template <typename E>
 __global__ void __launch_bounds__(kThreads) k_attn_rows(const __grid_constant__ AttnPlan p) {
   constexpr uint32_t V = 16 / sizeof(E);
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // behind the wait: k_attn_split may start beside this kernel, its operands are there
   const uint32_t lane = threadIdx.x % 8;
   const uint32_t n = p.batch * p.tokens * p.heads;
   const uint32_t first = (blockIdx.x * (kThreads / 8) + threadIdx.x / 8) * kRowsEach;

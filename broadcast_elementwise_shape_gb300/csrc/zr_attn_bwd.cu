@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int k = 0; k < 4; ++k) {
             const uint32_t r = lane + 32 * k;
             const bool in = q * 128 + r < t.len;  // behind the end the weight is 0
-            s_rows[stage][r] = in ? -p.lse2[at + r] : -INFINITY;
-            s_rows[stage][128 + r] = in ? -p.delta[at + r] : 0.f;
+            s_rows[stage][r] = in ? -__ldcg(p.lse2 + at + r) : -INFINITY;
+            s_rows[stage][128 + r] = in ? -__ldcg(p.delta + at + r) : 0.f;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s_rfull[stage]));

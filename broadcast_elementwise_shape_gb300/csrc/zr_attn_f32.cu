@@ -138,6 +138,7 @@ struct SplitPlan {
   uint32_t heads[4];
   uint64_t first[5];         // first row (batch, token, head) of each, counted through
   uint32_t count, tokens, dim, wide;
+  uint32_t beside;           // behind k_attn_rows, on which it does not depend: waits at its end
 };
 
 __device__ __forceinline__ float split_load(const float* p) { return *p; }
@@ -149,9 +150,12 @@ template <typename E, uint32_t PARTS, uint32_t W>
 __global__ void __launch_bounds__(kThreads) k_attn_split(const __grid_constant__ SplitPlan p) {
   constexpr uint32_t kLanes = W / 8;
   pdl_trigger();
-  pdl_wait();
+  if (!p.beside) pdl_wait();
   const uint64_t i = uint64_t(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-  if (i >= p.first[p.count]) return;
+  if (i >= p.first[p.count]) {
+    if (p.beside) pdl_wait();
+    return;
+  }
   uint32_t which = 0;
   while (which + 1 < p.count && i >= p.first[which + 1]) ++which;
   const uint32_t row = uint32_t(i - p.first[which]);  // rows are counted in 31 bits
@@ -184,6 +188,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_split(const __grid_constant__
     }
     *reinterpret_cast<uint4*>(p.out[which] + part * plane + uint64_t(row) * W + e0) = make_uint4(r[0], r[1], r[2], r[3]);
   }
+  if (p.beside) pdl_wait();  // what comes next finds both done
 }
 
 // ------------------------------------------------------------------ forward
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kF32Threads, 1)
   __shared__ uint32_t s_tmem, s_abort;
   // Columns: s, d, the sums of the first and of the second weights, third parts of both.
   constexpr uint32_t kD = 128, kAccP = 256, kAccW = 320, kMoreP = 384, kMoreW = 448;
-  pdl_trigger();
+  if (!KV) pdl_trigger();
   const uint32_t warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t stay = (smem_u32(s_raw) + 1023u) & ~1023u, past = stay + 2 * kTile;
   volatile uint32_t* abort = &s_abort;
@@ -448,7 +453,11 @@ __global__ void __launch_bounds__(kF32Threads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(s_tmem);
   const uint32_t per_slot = KV ? p.kv_heads : p.heads, items = p.slots * per_slot;
-  pdl_wait();
+  // The kernel for grad_q starts on the SMs that the other one leaves, and waits for
+  // it at its end (zr_attn_bwd.cu, k_attn_q).
+  const bool beside = !KV && (p.want & 6);
+  if (!beside) pdl_wait();
+  if (KV) pdl_trigger();
 
   if (warp >= 8) {
     regs_give<104>();
@@ -545,8 +554,8 @@ __global__ void __launch_bounds__(kF32Threads, 1)
           for (int k = 0; k < 4; ++k) {
             const uint32_t r = lane + 32 * k;
             const bool in = at * 128 + r < t.len;  // behind the end the weight is 0
-            s_rows[stage][r] = in ? -p.lse[first + int64_t(r) * p.heads] : -INFINITY;
-            s_rows[stage][128 + r] = in ? -p.delta[rows + r] : 0.f;
+            s_rows[stage][r] = in ? -__ldcg(p.lse + first + int64_t(r) * p.heads) : -INFINITY;
+            s_rows[stage][128 + r] = in ? -__ldcg(p.delta + rows + r) : 0.f;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&s_rfull[stage]));
@@ -574,8 +583,8 @@ __global__ void __launch_bounds__(kF32Threads, 1)
       const uint32_t row = t.tile * 128 + own;
       float lse = 0.f, delta = 0.f;
       if (!KV && row < t.len) {
-        lse = -p.lse[(int64_t(t.batch) * p.tokens + t.start + row) * p.heads + head];
-        delta = -p.delta[(int64_t(t.batch) * p.heads + head) * p.row_pitch + t.start + row];
+        lse = -__ldcg(p.lse + (int64_t(t.batch) * p.tokens + t.start + row) * p.heads + head);
+        delta = -__ldcg(p.delta + (int64_t(t.batch) * p.heads + head) * p.row_pitch + t.start + row);
       }
       float acc[kAcc];
 #pragma unroll
@@ -670,6 +679,7 @@ __global__ void __launch_bounds__(kF32Threads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_free<1>(tmem, 512);
+  if (beside) pdl_wait();
 }
 
 template <typename K>
@@ -689,6 +699,7 @@ cudaError_t launch_attn_split(int es, const AttnPlan& p, uint16_t* const* out, u
   d.tokens = p.tokens;
   d.dim = p.dim;
   d.wide = wide;
+  d.beside = count == 4;
   for (uint32_t i = 0; i < count; ++i) {
     d.x[i] = *x[i];
     d.out[i] = out[i];

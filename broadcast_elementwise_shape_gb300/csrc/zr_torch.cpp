@@ -513,7 +513,7 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(zr_adamw_step(gt == at::kBFloat16 ? ZR_BF16 : ZR_F32, msc ? 8 : 32, int32_t(k), list.data(), &how, stream));
 }
 
-// ms, vs, m_scales, v_scales, out (None, or two sequences) -> (m values, v values)
+// ms, vs, m_scales, v_scales, out (None, or two sequences) -> (m values, v values), or out
 PyObject* adamw_state(PyObject* const* a, Py_ssize_t n) {
   count(n, 5);
   const Items ms(a[0], "ms must be a sequence"), vs(a[1], "vs must be a sequence"),
@@ -532,10 +532,10 @@ PyObject* adamw_state(PyObject* const* a, Py_ssize_t n) {
   }
   std::vector<zr_adamw_tensor> list(size_t(k), zr_adamw_tensor{});
   std::vector<void*> to[2];
-  std::vector<Tensor> made[2];
+  std::vector<Tensor> made[2];  // where no out is given
   zr_stream_t stream = nullptr;
   for (Py_ssize_t i = 0; i < k; ++i) {
-    const Tensor &m = tensor(ms[i], "ms"), &v = tensor(vs[i], "vs"), &first = tensor(ms[0], "ms");
+    const Tensor &m = tensor(ms[i], "ms"), &first = tensor(ms[0], "ms");
     if (i == 0) {
       if (!m.is_cuda()) fail(PyExc_ValueError, "%s must be CUDA tensors", "ms");
       stream = stream_of(m);
@@ -543,16 +543,20 @@ PyObject* adamw_state(PyObject* const* a, Py_ssize_t n) {
     zr_adamw_tensor& t = list[size_t(i)];
     t.n = m.numel();
     t.m = flat(m, at::kByte, t.n, first, "ms");
-    t.v = flat(v, at::kByte, t.n, first, "vs");
+    t.v = flat(vs[i], at::kByte, t.n, first, "vs");
     t.m_scale = static_cast<float*>(flat(msc[i], at::kFloat, blocks_of(t.n), first, "m_scales"));
     t.v_scale = static_cast<float*>(flat(vsc[i], at::kFloat, blocks_of(t.n), first, "v_scales"));
     for (int j = 0; j < 2; ++j) {
-      made[j].push_back(out[j] ? tensor((*out[j])[i], "out") : empty(m.sizes(), m, at::kBFloat16));
-      to[j].push_back(flat(made[j].back(), at::kBFloat16, t.n, first, "out"));
+      if (!out[j]) made[j].push_back(empty(m.sizes(), m, at::kBFloat16));
+      to[j].push_back(flat(out[j] ? tensor((*out[j])[i], "out") : made[j].back(), at::kBFloat16, t.n, first, "out"));
     }
   }
   const int rc = zr_adamw_state(int32_t(k), list.data(), to[0].data(), to[1].data(), stream);
   if (rc) return PyLong_FromLong(rc);
+  if (a[4] != Py_None) {
+    Py_INCREF(a[4]);
+    return a[4];
+  }
   PyObject* both = PyTuple_New(2);
   if (!both) throw Failed();
   for (int j = 0; j < 2; ++j) {

@@ -176,5 +176,6 @@ def zr_adamw_step(params, grads, ms, vs, step, lr, betas=(0.9, 0.999), eps=1e-8,
 
 def zr_adamw_state(ms, vs, m_scales, v_scales, out=None):
     """(m values, v values) of 8-bit states as lists of bfloat16 tensors, which
-    hold them exactly.  ``out`` may hold two lists of preallocated ones."""
+    hold them exactly.  ``out`` may hold two lists of preallocated ones, and is
+    returned then."""
     return _out(_c().adamw_state(ms, vs, m_scales, v_scales, out), "zr_adamw_state")
