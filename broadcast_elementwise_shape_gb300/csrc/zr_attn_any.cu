@@ -9,8 +9,8 @@
 // keys for grad_q.  That is seven products for the five it cannot do without,
 // and in return every gradient is summed in one place, in a fixed order.
 //
-// Bound by the binary32 multiply-adds ([2, 2048] tokens of 16 heads of 128, 1000
-// us forward: 34 TFLOP/s of 74).  256 threads hold a 64 x 64 tile of
+// Bound by the binary32 multiply-adds and the reads from shared memory that feed
+// them ([1, 2048] tokens of 16 heads of 128, 467 us forward: 37 TFLOP/s of 74).  256 threads hold a 64 x 64 tile of
 // scores as 4 x 4 each, rows and columns 16 apart, so that the 16-byte reads of
 // the operands along the elements meet no bank twice (rows are padded by 16
 // bytes); 16 reads feed 64 multiply-adds, in pairs (two per instruction).  What
@@ -185,13 +185,18 @@ __device__ __forceinline__ float any_add16(float x) {
   return x;
 }
 
+// Heads of 65 to 128 elements bring keys and values through one room in shared
+// memory, one after the other: two CTAs fit an SM, and one computes while the other
+// loads ([1, 2048] tokens of 16 heads of 128, 488 us with a room each).
+template <int DP>
+constexpr bool kOneRoom = DP == 128;
 // blockIdx.x = slot * heads + head.
 template <typename E, int DP>
-__global__ void __launch_bounds__(kThreads) k_attn_any_fwd(const __grid_constant__ AttnPlan p) {
+__global__ void __launch_bounds__(kThreads, DP == 128 ? 2 : 1) k_attn_any_fwd(const __grid_constant__ AttnPlan p) {
   extern __shared__ float s_f[];
   float* sq = s_f;
   float* sk = sq + kAnyRows * (DP + 4);
-  float* sv = sk + 64 * (DP + 4);
+  float* sv = kOneRoom<DP> ? sk : sk + 64 * (DP + 4);
   float* sw = sv + 64 * (DP + 4);
   pdl_trigger();
   pdl_wait();
@@ -213,10 +218,14 @@ __global__ void __launch_bounds__(kThreads) k_attn_any_fwd(const __grid_constant
   for (uint32_t k0 = 0; k0 <= row0; k0 += 64) {
     __syncthreads();
     any_fetch<E, DP, 64>(sk, p, p.k, t.batch, kvh, t.start, k0, t.len);
-    any_fetch<E, DP, 64>(sv, p, p.v, t.batch, kvh, t.start, k0, t.len);
+    if (!kOneRoom<DP>) any_fetch<E, DP, 64>(sv, p, p.v, t.batch, kvh, t.start, k0, t.len);
     __syncthreads();
     float s[4][4];
     any_scores<DP>(sq, sk, s);
+    if (kOneRoom<DP>) {
+      __syncthreads();
+      any_fetch<E, DP, 64>(sv, p, p.v, t.batch, kvh, t.start, k0, t.len);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t r = row0 + ty + 16 * i;
@@ -246,7 +255,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_any_fwd(const __grid_constant
         acc[i][c][1] = f2_mul(acc[i][c][1], f);
       }
     }
-    __syncwarp();
+    if (kOneRoom<DP>) __syncthreads();
+    else __syncwarp();
     any_sum<DP, 4, 64>(sw, sv, acc);
   }
   float by[4];
@@ -459,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) k_attn_any_q(const __grid_constant__
 
 template <typename E, int DP>
 cudaError_t any_fwd(const AttnPlan& p, cudaStream_t s) {
-  constexpr size_t smem = (3 * 64 * (DP + 4) + 64 * 68) * sizeof(float);
+  constexpr size_t smem = ((kOneRoom<DP> ? 2 : 3) * 64 * (DP + 4) + 64 * 68) * sizeof(float);
   const auto k = with_smem(k_attn_any_fwd<E, DP>, smem);
   return k ? launch_k(k, p.slots * p.heads, kThreads, smem, s, p) : cudaErrorInvalidValue;
 }
