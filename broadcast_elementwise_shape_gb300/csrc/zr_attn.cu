@@ -243,6 +243,13 @@ uint32_t shares(const AttnPlan& p) {
 
 const char* kernel_name(bool tc, bool copy, int es) { return !tc ? "any" : es == 4 ? "parts" : copy ? "copied" : "tensor"; }
 
+// The forward's pairs of query tiles likewise, along their keys; a share has
+// eight key tiles of the average pair at least.
+uint32_t fwd_shares(const AttnPlan& p) {
+  const uint64_t tiles = (uint64_t(p.tokens) + 255) / 256, items = tiles * p.batch * p.heads;
+  return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({8, 3 * kSms / items, (tiles + 1) / 8})));
+}
+
 std::string plan_json(const AttnSet& S, const char* kernel) {
   const AttnPlan& p = S.p;
   return std::string("{\"kernel\":\"") + kernel + "\",\"tile\":" + std::to_string(p.tile_rows) +
@@ -262,6 +269,10 @@ int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_te
   const bool tc = !S.empty && tensor_cores(S, scale), copy = tc && copied(S, false);
   const Copies copies = copy ? copies_of(S, 3, 0) : Copies{};
   S.ws = copies.end;
+  S.p.splits = tc && S.es == 2 ? fwd_shares(S.p) : 1;
+  const size_t part_at = (S.ws + 255) / 256 * 256;
+  if (S.p.splits > 1)
+    S.ws = part_at + size_t(S.p.splits) * S.p.batch * S.p.tokens * S.p.heads * ((S.p.dim <= 64 ? 64 : 128) + 1) * sizeof(float);
   if (!workspace) {
     *workspace_bytes = S.ws;
     return ZR_OK;
@@ -283,6 +294,7 @@ int fwd_impl(zr_dtype dtype, const zr_tensor& q, const zr_tensor& k, const zr_te
   p.o_wide = wide(S.o, S.es);
   p.low_wide = reinterpret_cast<uintptr_t>(low) % 16 == 0 && p.dim % 8 == 0;
   if (tc) set_tiles(&p, 256);
+  p.part = p.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_at) : nullptr;
   trace("zr_attention_fwd", [&] { return plan_json(S, kernel_name(tc, copy, S.es)); });
   for (const void* x : {p.q.p, p.k.p, p.v.p, static_cast<const void*>(out), static_cast<const void*>(low),
                         static_cast<const void*>(lse), static_cast<const void*>(offsets),

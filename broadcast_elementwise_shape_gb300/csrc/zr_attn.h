@@ -28,8 +28,10 @@ struct AttnPlan {
   uint32_t row_pitch;        // tokens rounded up to 128
   uint32_t slots;            // tiles of one head, all sequences (packed: at most)
   uint32_t tile_rows;        // rows of a tile
-  uint32_t splits;           // tensor-core backward: shares of a key tile's steps
-  float* part;               // with splits > 1, workspace: [split][batch][token][kv head][grad_v, grad_k]
+  uint32_t splits;           // tensor cores, bfloat16: shares of a pair of query tiles' keys (forward),
+                             // of a key tile's steps (backward), 1 to 8
+  float* part;               // with splits > 1, workspace: [split][batch][token][head] of results, then of
+                             // lse; backward [split][batch][token][kv head][grad_v, grad_k]
   uint32_t want;             // bit 0: grad_q, bits 1 and 2: grad_k, grad_v
   uint32_t vec;              // 16-byte reads of every operand
   uint32_t o_wide, low_wide; // tensor-core forward: 16-byte stores of o and low;

@@ -44,7 +44,35 @@ struct FwdCfg {
   static constexpr uint32_t kCols = 512;
 };
 
-template <int DP>
+// One share of a pair of tiles' keys: tile h takes the key tiles [first, end(h)),
+// of which the one on the diagonal, 2 * tile + h, is its last.
+struct FwdRange {
+  uint32_t tiles, h0;        // the tiles [h0, tiles) have something in this share
+  uint32_t first, end0, end1;
+  __device__ __forceinline__ uint32_t end(uint32_t h) const { return h ? end1 : end0; }
+};
+template <bool SHARES>
+__device__ __forceinline__ FwdRange fwd_range(const AttnPlan& p, const AttnTile& t, uint32_t split) {
+  FwdRange r;
+  r.tiles = t.tile * kFwdRows + 128 < t.len ? 2 : 1;
+  if (!SHARES) {
+    r.h0 = r.first = 0;
+    r.end0 = 2 * t.tile + 1;
+    r.end1 = r.tiles == 2 ? r.end0 + 1 : 0;
+    return r;
+  }
+  const uint32_t n = 2 * t.tile + r.tiles;
+  r.first = uint32_t(uint64_t(n) * split / p.splits);
+  const uint32_t end = uint32_t(uint64_t(n) * (split + 1) / p.splits);
+  r.end0 = end < 2 * t.tile + 1 ? end : 2 * t.tile + 1;
+  r.end1 = r.tiles == 2 ? end : 0;
+  r.h0 = r.end0 > r.first ? 0 : r.end1 > r.first ? 1 : 2;
+  return r;
+}
+
+// Items: pairs of query tiles (as slots) times heads, or with p.splits shares of
+// their keys (SHARES), whose results k_attn_fwd_join weighs.
+template <int DP, bool SHARES>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     k_attn_fwd(const __grid_constant__ AttnPlan p, const __grid_constant__ AttnMaps maps) {
   using Cfg = FwdCfg<DP>;
@@ -85,7 +113,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(s_tmem);
-  const uint32_t items = p.slots * p.heads;
+  const uint32_t items = p.slots * (SHARES ? p.splits : 1) * p.heads;
   pdl_wait();
 
   if (warp >= 8) {
@@ -97,17 +125,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (uint32_t round = 0; ok && round * gridDim.x < items; ++round) {
         const uint32_t w = at_item(round);
         if (w >= items) continue;
-        const uint32_t slot = w / p.heads, head = w - slot * p.heads, kvh = head / p.group;
+        const uint32_t share = w / p.heads, head = w - share * p.heads, kvh = head / p.group, slot = SHARES ? share / p.splits : share;
         const AttnTile t = attn_tile(p, slot, false);
         if (!t.live) continue;
-        const uint32_t row0 = t.tile * kFwdRows;
-        const uint32_t tiles = row0 + 128 < t.len ? 2 : 1, n = 2 * t.tile + tiles;
-        for (uint32_t i = 0; i < n && ok; ++i) {
+        const FwdRange run = fwd_range<SHARES>(p, t, share - slot * p.splits);
+        if (run.h0 >= run.tiles) continue;
+        const uint32_t row0 = t.tile * kFwdRows, end = run.end(run.tiles - 1);
+        for (uint32_t i = run.first; i < end && ok; ++i) {
           const uint32_t stage = nk % S, phase = (nk / S) & 1;
           ++nk;
           // Queries with the first keys: each tile's when the last item's scores are done.
-          if (i == 0) {
-            for (uint32_t h = 0; h < tiles && ok; ++h) {
+          if (i == run.first) {
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+              if (!ok || h < run.h0 || h >= run.tiles) continue;
               const uint32_t room = h + nq[h] % Cfg::kStay * 2;
               ok = warp_wait(smem_u32(&s_qempty[room]), ((nq[h] / Cfg::kStay) & 1) ^ 1, abort);
               ++nq[h];
@@ -156,48 +187,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (uint32_t round = 0; ok && round * gridDim.x < items; ++round) {
         const uint32_t w = at_item(round);
         if (w >= items) continue;
-        const AttnTile t = attn_tile(p, w / p.heads, false);
+        const uint32_t share = w / p.heads, slot = SHARES ? share / p.splits : share;
+        const AttnTile t = attn_tile(p, slot, false);
         if (!t.live) continue;
-        const uint32_t tiles = t.tile * kFwdRows + 128 < t.len ? 2 : 1;
+        const FwdRange run = fwd_range<SHARES>(p, t, share - slot * p.splits);
+        if (run.h0 >= run.tiles) continue;
         // Scores of tile h with key tile i, whose stage goes back with the last tile that reads it.
         auto scores = [&](uint32_t h, uint32_t i) {
-          const uint32_t at = n_key + i, stage = at % S, room = h + items_of[h] % Cfg::kStay * 2;
+          const uint32_t at = n_key + i - run.first, stage = at % S, room = h + items_of[h] % Cfg::kStay * 2;
           ok = ok && warp_wait(smem_u32(&s_kfull[stage]), (at / S) & 1, abort);
-          if (i == 0) ok = ok && warp_wait(smem_u32(&s_qfull[room]), (items_of[h] / Cfg::kStay) & 1, abort);
+          if (i == run.first) ok = ok && warp_wait(smem_u32(&s_qfull[room]), (items_of[h] / Cfg::kStay) & 1, abort);
           if (!ok) return;
           tc_fence_after();
           if (leader) {
             at_scores<DP>(tmem + h * 128, sq + room * kTile, sk + stage * kTile);
             tc_commit<1>(smem_u32(&s_sfull[h]));
-            if (i == 2 * t.tile + h) tc_commit<1>(smem_u32(&s_qempty[room]));
-            if (h + 1 == tiles) tc_commit<1>(smem_u32(&s_kempty[stage]));
+            if (i + 1 == run.end(h)) tc_commit<1>(smem_u32(&s_qempty[room]));
+            if (h + 1 == run.tiles) tc_commit<1>(smem_u32(&s_kempty[stage]));
           }
           __syncwarp();
         };
-        for (uint32_t h = 0; h < tiles; ++h) scores(h, 0);
-        const uint32_t n = 2 * t.tile + tiles;
-        for (uint32_t i = 0; i < n && ok; ++i) {
-          const uint32_t at = n_key + i, stage = at % S;
-          for (uint32_t h = 0; h < tiles && ok; ++h) {
-            const uint32_t last = 2 * t.tile + h;  // the tile on the diagonal
-            if (i > last) continue;
-            if (i == 0) ok = warp_wait(smem_u32(&s_oempty[h]), (items_of[h] & 1) ^ 1, abort);
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+          if (h >= run.h0 && h < run.tiles) scores(h, run.first);
+        const uint32_t end = run.end(run.tiles - 1);
+        for (uint32_t i = run.first; i < end && ok; ++i) {
+          const uint32_t at = n_key + i - run.first, stage = at % S;
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h) {
+            if (!ok || h < run.h0 || h >= run.tiles || i >= run.end(h)) continue;
+            if (i == run.first) ok = warp_wait(smem_u32(&s_oempty[h]), (items_of[h] & 1) ^ 1, abort);
             ok = ok && warp_wait(smem_u32(&s_vfull[stage]), (at / S) & 1, abort);
             ok = ok && warp_wait(smem_u32(&s_pfull[h]), tiles_of[h] & 1, abort);
-            if (!ok) break;
+            if (!ok) continue;
             ++tiles_of[h];
             tc_fence_after();
             if (leader) {
-              at_sum<DP>(tmem + Cfg::kO + h * DP, tmem + h * 128, sv + stage * kTile, i != 0);
-              if (i == last) tc_commit<1>(smem_u32(&s_ofull[h]));
-              if (h + 1 == tiles) tc_commit<1>(smem_u32(&s_vempty[stage]));
+              at_sum<DP>(tmem + Cfg::kO + h * DP, tmem + h * 128, sv + stage * kTile, i != run.first);
+              if (i + 1 == run.end(h)) tc_commit<1>(smem_u32(&s_ofull[h]));
+              if (h + 1 == run.tiles) tc_commit<1>(smem_u32(&s_vempty[stage]));
             }
             __syncwarp();
-            if (i < last) scores(h, i + 1);
+            if (i + 1 < run.end(h)) scores(h, i + 1);
           }
         }
-        n_key += n;
-        for (uint32_t h = 0; h < tiles; ++h) ++items_of[h];
+        n_key += end - run.first;
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+          if (h >= run.h0 && h < run.tiles) ++items_of[h];
       }
     }
   } else {
@@ -210,13 +247,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     for (uint32_t round = 0; round * gridDim.x < items; ++round) {
       const uint32_t w = at_item(round);
       if (w >= items) continue;
-      const uint32_t slot = w / p.heads, head = w - slot * p.heads;
+      const uint32_t share = w / p.heads, head = w - share * p.heads, slot = SHARES ? share / p.splits : share;
       const AttnTile t = attn_tile(p, slot, false);
-      if (!t.live || t.tile * kFwdRows + h * 128 >= t.len) continue;
+      if (!t.live) continue;
+      const uint32_t split = SHARES ? share - slot * p.splits : 0;
+      const FwdRange run = fwd_range<SHARES>(p, t, split);
+      if (h < run.h0 || h >= run.tiles) continue;  // k_attn_fwd_join knows
       const uint32_t row = t.tile * kFwdRows + h * 128 + mine, last = 2 * t.tile + h;
       float top = -INFINITY, off = 0.f;  // the row's maximum so far; -top * scale * log2(e)
       float sum = 0.f;
-      for (uint32_t i = 0; i <= last; ++i, ++n_tile) {
+      for (uint32_t i = run.first; i < run.end(h); ++i, ++n_tile) {
         ok = ok && warp_wait(smem_u32(&s_sfull[h]), n_tile & 1, abort);
         if (!ok) break;
         tc_fence_after();
@@ -243,7 +283,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         m[0] = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), v[127]);
         const float off_new = m[0] == -INFINITY ? 0.f : -(m[0] * p.scale_log2);
-        if (i > 0 && __any_sync(0xFFFFFFFFu, m[0] > top)) {
+        if (i > run.first && __any_sync(0xFFFFFFFFu, m[0] > top)) {
           const float keep = m[0] > top ? ex2(__fmaf_rn(top, p.scale_log2, off_new)) : 1.f;
           sum *= keep;
           const F2 f = f2_splat(keep);
@@ -296,6 +336,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float by = ok ? 1.f / sum : qnan();
       const int64_t token = int64_t(t.start) + row;
       const int64_t flat = (int64_t(t.batch) * p.tokens + token) * p.heads + head;
+      const float lse = ok ? (log2f(sum) - off) * 0.6931471805599453f : qnan();
+      const int64_t rows = int64_t(p.batch) * p.tokens * p.heads;
+      float* part = p.part + (split * rows + flat) * DP;
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(const_cast<void*>(p.o.p)) + int64_t(t.batch) * p.o.batch +
                          token * p.o.token + int64_t(head) * p.o.head;
       __nv_bfloat16* low = p.low ? static_cast<__nv_bfloat16*>(p.low) + flat * p.dim : nullptr;
@@ -311,7 +354,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] *= by;
-        if (row < t.len) {
+        if (SHARES) {
+          if (row < t.len) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(part + j + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+          }
+        } else if (row < t.len) {
           at_store_row(o, p.o.elem, p.o_wide, x, j, p.dim);
           if (low) {
 #pragma unroll
@@ -320,7 +369,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
       }
-      if (p.lse && row < t.len) p.lse[flat] = ok ? (log2f(sum) - off) * 0.6931471805599453f : qnan();
+      if (row < t.len) {
+        if (SHARES) p.part[p.splits * rows * DP + split * rows + flat] = lse;
+        else if (p.lse) p.lse[flat] = lse;
+      }
     }
   }
   __syncthreads();
@@ -336,13 +388,66 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (warp == 9) tmem_free<1>(tmem, Cfg::kCols);
 }
 
+// Weighs the shares' results by their sums: four elements a thread, blockIdx.x =
+// (slot * heads + head) * (blocks of a pair of tiles) + block.
+template <int DP>
+__global__ void __launch_bounds__(kThreads) k_attn_fwd_join(const __grid_constant__ AttnPlan p) {
+  constexpr uint32_t kRows = kThreads / (DP / 4), kBlocks = kFwdRows / kRows;
+  pdl_wait();
+  const uint32_t item = blockIdx.x / kBlocks, slot = item / p.heads, head = item - slot * p.heads;
+  const AttnTile t = attn_tile(p, slot, false);
+  const uint32_t in = blockIdx.x % kBlocks * kRows + threadIdx.x / (DP / 4), d = threadIdx.x % (DP / 4) * 4;
+  const uint32_t row = t.tile * kFwdRows + in;
+  if (!t.live || row >= t.len) return;
+  const int64_t rows = int64_t(p.batch) * p.tokens * p.heads;
+  const int64_t flat = (int64_t(t.batch) * p.tokens + t.start + row) * p.heads + head;
+  float4 x[8];
+  float l[8], top = -INFINITY;
+#pragma unroll
+  for (uint32_t split = 0; split < 8; ++split) {
+    l[split] = -INFINITY;
+    x[split] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (split >= p.splits) continue;
+    const FwdRange run = fwd_range<true>(p, t, split);
+    if (in / 128 < run.h0 || in / 128 >= run.tiles) continue;
+    l[split] = p.part[p.splits * rows * DP + split * rows + flat];
+    x[split] = *reinterpret_cast<const float4*>(p.part + (split * rows + flat) * DP + d);
+    top = fmaxf(top, l[split]);
+  }
+  float sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int split = 0; split < 8; ++split) {
+    const float w = l[split] == -INFINITY ? 0.f : ex2_full((l[split] - top) * kLog2e);
+    sum += w;
+    y[0] = __fmaf_rn(w, x[split].x, y[0]);
+    y[1] = __fmaf_rn(w, x[split].y, y[1]);
+    y[2] = __fmaf_rn(w, x[split].z, y[2]);
+    y[3] = __fmaf_rn(w, x[split].w, y[3]);
+  }
+  const float by = 1.f / sum;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(const_cast<void*>(p.o.p)) + int64_t(t.batch) * p.o.batch +
+                     (int64_t(t.start) + row) * p.o.token + int64_t(head) * p.o.head;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (d + k >= p.dim) continue;
+    const float v = y[k] * by;
+    const __nv_bfloat16 r = __float2bfloat16_rn(v);
+    o[int64_t(d + k) * p.o.elem] = r;
+    if (p.low) static_cast<__nv_bfloat16*>(p.low)[flat * p.dim + d + k] = __float2bfloat16_rn(v - __bfloat162float(r));
+  }
+  if (p.lse && d == 0) p.lse[flat] = top + logf(sum);
+}
+
 template <int DP>
 cudaError_t launch(const AttnPlan& p, const AttnMaps& maps, cudaStream_t s) {
   constexpr size_t smem = FwdCfg<DP>::kSmem;
-  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k_attn_fwd<DP>), smem);
+  const auto k = p.splits > 1 ? k_attn_fwd<DP, true> : k_attn_fwd<DP, false>;
+  cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), smem);
   if (e != cudaSuccess) return e;
-  const uint32_t items = p.slots * p.heads;
-  return launch_k(k_attn_fwd<DP>, items < kSms ? items : kSms, kFwdThreads, smem, s, p, maps);
+  const uint32_t items = p.slots * p.splits * p.heads;
+  e = launch_k(k, items < kSms ? items : kSms, kFwdThreads, smem, s, p, maps);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return launch_k(k_attn_fwd_join<DP>, p.slots * p.heads * (DP / 4), kThreads, 0, s, p);
 }
 
 }  // namespace

@@ -569,7 +569,8 @@ int zr_linear_xent_bwd(zr_dtype dtype, const float* grad_loss, zr_tensor x, zr_t
  *               used in stream order.  Backward: 8 bytes per row of T rounded up to
  *               128, for each batch entry and head; ZR_BF16 with few key tiles and heads
  *               for the GPU up to 8 times 1024 bytes (D <= 64: 512) per token and
- *               key head besides.  Both: copies of q, k, v and (backward) grad_out
+ *               key head besides.  Forward: ZR_BF16 with few heads and long sequences up
+ *               to 8 times 516 bytes (D <= 64: 260) per row of q.  Both: copies of q, k, v and (backward) grad_out
  *               that the tensor cores read, 384 bytes per row with ZR_F32, and
  *               256 (D <= 64: 128) with ZR_BF16 where rows are not aligned
  *               to 16 bytes or D is no multiple of 8.

@@ -46,6 +46,22 @@ def test_grouped_heads(h, kv, d, dtype):
     run(zr, q, k, v, go=go)
 
 
+@pytest.mark.parametrize("d", [64, 81, 128])
+@pytest.mark.parametrize("lengths", [None, [1, 4100, 0, 129, 255, 700, 30]])
+def test_shares_of_a_rows_keys(lengths, d):
+    """Few heads and long sequences: a pair of query tiles' keys are worked on in shares, some of them empty."""
+    t = sum(lengths) if lengths else 4133
+    lead = (t,) if lengths else (1, t)
+    q, k, v, go = make(lead, 1, 1, d, BF16, size=2.0)
+    off = packed(lengths) if lengths else None
+    out, lse, *_ = run(zr, q, k, v, offsets=off, go=go)
+    again, _, low = zr.zr_attention_fwd(q, k, v, None, off, keep_lse=False)
+    assert torch.equal(out, again) and low is None
+    wide = torch.full((*q.shape[:-1], d + 3), 7.0, device="cuda", dtype=BF16)
+    zr.zr_attention_fwd(q, k, v, None, off, out=wide[..., 2:d + 2])
+    assert torch.equal(wide[..., 2:d + 2], out) and bool((wide[..., :2] == 7).all()) and bool((wide[..., d + 2:] == 7).all())
+
+
 @pytest.mark.parametrize("d", [64, 80, 128])
 @pytest.mark.parametrize("lengths", [None, [1, 700, 0, 129, 255], [30] * 40])
 def test_shares_of_a_key_tile(lengths, d):
